@@ -17,6 +17,9 @@ decode step -- uploads, the library calls and the download -- as one CUDA graph
 _API = ("indexer_scores", "topk", "mla_sparse_attn_prefill", "mla_sparse_attn_decode",
         "mla_sparse_attn_decode_noalloc", "indexer_scores_paged", "mla_sparse_attn_decode_paged",
         "mla_sparse_attn_prefill_paged", "mla_value_up_proj", "indexer_source_layer",
+        "mla_cache_write_q8", "mla_cache_read_q8", "mla_cache_read_q8_paged",
+        "mla_sparse_attn_prefill_q8", "mla_sparse_attn_prefill_q8_paged", "mla_sparse_attn_decode_q8",
+        "mla_sparse_attn_decode_q8_paged", "indexer_norm_rope",
         "attn_workspace_size", "device_status", "selftest_wait_timeout", "status_string", "load", "lib_path",
         "DsaError")
 

@@ -47,6 +47,17 @@ SIGNATURES = {
                                                       _P, _SZ, _P]),
     "mla_sparse_attn_prefill_paged": (ctypes.c_int32, [_P, _P, _P, _I, _I, _P, _I, _I, _I, _F, _P, _I, _P, _P, _SZ,
                                                        _P]),
+    "mla_cache_write_q8": (ctypes.c_int32, [_P, _I64, _P, _F, _P, _I, _I, _P, _P, _I, _P, _P, _I64, _P]),
+    "mla_cache_read_q8": (ctypes.c_int32, [_P, _P, _I64, _P, _I, _P, _P]),
+    "mla_cache_read_q8_paged": (ctypes.c_int32, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "mla_sparse_attn_prefill_q8": (ctypes.c_int32, [_P, _P, _P, _P, _I, _I, _I, _F, _P, _I, _P, _P, _SZ, _P]),
+    "mla_sparse_attn_prefill_q8_paged": (ctypes.c_int32, [_P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _F, _P, _I, _P, _P,
+                                                          _SZ, _P]),
+    "mla_sparse_attn_decode_q8": (ctypes.c_int32, [_P, _P, _P, _P, _P, _I, _I, _I, _F, _P, _I, _P, _P, _SZ, _P]),
+    "mla_sparse_attn_decode_q8_paged": (ctypes.c_int32, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _I, _I, _I, _F, _P, _I,
+                                                         _P, _P, _SZ, _P]),
+    "dsa_indexer_norm_rope": (ctypes.c_int32, [_P, _I64, _P, _I64, _I, _P, _P, _P, _P, _F, _P, _I, _I, _P, _P, _I, _P,
+                                               _P, _I64, _P]),
     "mla_value_up_proj": (ctypes.c_int32, [_P, _P, _I, _P, _P]),
     "dsa_indexer_source_layer": (ctypes.c_int, [_I, _I, _I]),
     "dsa_device_status": (ctypes.c_int32, [_P, ctypes.POINTER(ctypes.c_int32), _I]),
@@ -291,6 +302,243 @@ def mla_sparse_attn_prefill_paged(q: torch.Tensor, kv_pool: torch.Tensor, block_
                                               _ptr(lse), None, 0, _stream(stream))
     _check("mla_sparse_attn_prefill_paged", rc)
     return (out, lse) if want_lse else out
+
+
+# ----------------------------------------------------------------------------- the 8-bit latent cache
+
+Q8_ROW = 640        # bytes of a cache row: 512 e4m3 latent dims | 64 bf16 rope dims
+NORMS = {"rms": 0, "layer": 1}
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _here(device: torch.device, *tensors: Optional[torch.Tensor]):
+    """The kernels launch on the current device, so every tensor has to live there."""
+    _need(device.index == torch.cuda.current_device(), "the tensors are not on the current CUDA device")
+    for t in tensors:
+        _need(t is None or t.device == device, "the tensors are not all on one CUDA device")
+
+
+def _rows_ptr(t: torch.Tensor, width: int, what: str) -> int:
+    """Pointer of a 16-bit tensor whose rows (one a token, `width` elements) may be strided: a slice
+    of a wider projection's output."""
+    _need(t.is_cuda and _is16(t), f"{what}: a bf16 CUDA tensor is expected")
+    row = t[0]
+    _need(row.numel() == width and row.is_contiguous(), f"{what}: rows of {width} contiguous elements are expected")
+    return t.data_ptr()
+
+
+def _ints(t: torch.Tensor, n: int, what: str):
+    _need(t.dtype == torch.int32 and t.numel() == n, f"{what}: int32 of {n} elements is expected")
+
+
+def _cache_q8(cache: torch.Tensor, cache_scale: torch.Tensor) -> int:
+    """Checks an 8-bit cache (uint8 [..., 640] and float32 [...]) and returns its rows."""
+    _need(cache.dtype == torch.uint8 and cache.shape[-1] == Q8_ROW, "the cache is uint8 with rows of 640 bytes")
+    rows = cache.numel() // Q8_ROW
+    _need(cache_scale.dtype == torch.float32 and cache_scale.numel() == rows, "cache_scale is float32, one a row")
+    return rows
+
+
+def _torch_stream(stream):
+    if stream is None:
+        return torch.cuda.current_stream()
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor for a call on `stream`, from that stream's memory: neither its earlier nor its next user
+    overlaps the call."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_torch_stream(stream)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _cos_sin(t: torch.Tensor) -> int:
+    _need(t.dtype == torch.float32 and t.dim() == 2 and t.shape[1] == 64, "cos_sin is float32 [max_pos, 64]")
+    return t.shape[0]
+
+
+def mla_cache_write_q8(kv_a: torch.Tensor, norm_w: torch.Tensor, eps: float, cos_sin: torch.Tensor, pos: torch.Tensor,
+                       slots: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor, interleave: bool = True,
+                       stream=None) -> None:
+    """Latent rows of new tokens into the 8-bit cache: norm, rotation, quantisation and scatter.
+
+    kv_a [R, 576] bf16 (rows may be strided), norm_w [512] f32, cos_sin [max_pos, 64] f32 (32 cosines |
+    32 sines a position), pos and slots [R] int32 (a negative slot skips the token; slots differ), cache
+    uint8 [..., 640], cache_scale f32 [...]."""
+    R = kv_a.shape[0]
+    p = _rows_ptr(kv_a, 576, "kv_a") if R else None
+    rows = _cache_q8(cache, cache_scale)
+    _need(norm_w.dtype == torch.float32 and norm_w.numel() == 512, "norm_w is float32 [512]")
+    _ints(pos, R, "pos")
+    _ints(slots, R, "slots")
+    _here(cache.device, kv_a, norm_w, cos_sin, pos, slots, cache_scale)
+    rc = load().mla_cache_write_q8(p, kv_a.stride(0) if R > 1 else 576, _ptr(norm_w), eps, _ptr(cos_sin),
+                                   _cos_sin(cos_sin), 1 if interleave else 0, _ptr(pos), _ptr(slots), R, _ptr(cache),
+                                   _ptr(cache_scale), rows, _stream(stream))
+    _check("mla_cache_write_q8", rc)
+
+
+def mla_cache_read_q8(cache: torch.Tensor, cache_scale: torch.Tensor, slots: torch.Tensor,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out [R, 576] bf16: the rows `slots` [R] int32 of the 8-bit cache (zeros for a negative slot)."""
+    R = slots.numel()
+    rows = _cache_q8(cache, cache_scale)
+    _ints(slots, R, "slots")
+    if out is None:
+        out = _new((R, 576), torch.bfloat16, cache.device, stream)
+    _need(_is16(out) and out.numel() == R * 576, "out is bf16 [R, 576]")
+    _here(cache.device, cache_scale, slots, out)
+    rc = load().mla_cache_read_q8(_ptr(cache), _ptr(cache_scale), rows, _ptr(slots), R, _ptr(out), _stream(stream))
+    _check("mla_cache_read_q8", rc)
+    return out
+
+
+def mla_cache_read_q8_paged(cache: torch.Tensor, cache_scale: torch.Tensor, kv_len: torch.Tensor,
+                            block_table: torch.Tensor, page_size: int, Nmax: int,
+                            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out [B, Nmax, 576] bf16: the kv_len[b] rows of each sequence of a paged 8-bit cache; later rows
+    of a given `out` stay as they are (a new one has zeros there)."""
+    B = kv_len.numel()
+    rows = _cache_q8(cache, cache_scale)
+    _ints(kv_len, B, "kv_len")
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B,
+          "block_table is int32 [B, pages]")
+    if out is None:
+        with torch.cuda.stream(_torch_stream(stream)):
+            out = torch.zeros((B, Nmax, 576), dtype=torch.bfloat16, device=cache.device)
+    _need(_is16(out) and out.numel() == B * Nmax * 576, "out is bf16 [B, Nmax, 576]")
+    _here(cache.device, cache_scale, kv_len, block_table, out)
+    rc = load().mla_cache_read_q8_paged(_ptr(cache), _ptr(cache_scale), _ptr(kv_len), _ptr(block_table),
+                                        block_table.shape[1], page_size, rows // page_size if page_size > 0 else 0, B,
+                                        Nmax, _ptr(out), _stream(stream))
+    _check("mla_cache_read_q8_paged", rc)
+    return out
+
+
+def _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream):
+    """Checks and output buffers the 8-bit attention calls share: (rows, top_k, out, lse, cache rows)."""
+    _need(q.dim() == 3 and q.shape[1] == 64 and q.shape[2] == 576 and _is16(q), "q is bf16 [rows, 64, 576]")
+    rows, top_k = q.shape[0], idx.shape[-1]
+    _ints(idx, rows * top_k, "idx")
+    n = _cache_q8(cache, cache_scale)
+    if out is None:
+        _need(out_dtype in (torch.float32, torch.bfloat16), f"attention output must be float32 or bf16, got {out_dtype}")
+        out = _new((rows, 64, 512), out_dtype, q.device, stream)
+    _need(out.numel() == rows * 64 * 512, "out is [rows, 64, 512]")
+    if lse is None and want_lse:
+        lse = _new((rows, 64), torch.float32, q.device, stream)
+    _need(lse is None or (lse.dtype == torch.float32 and lse.numel() == rows * 64), "lse is float32 [rows, 64]")
+    _here(q.device, cache, cache_scale, idx, out, lse)
+    return rows, top_k, out, lse, n
+
+
+def _decode_workspace(workspace, B, top_k, device, stream):
+    if workspace is None:
+        return _new((attn_workspace_size(B, top_k),), torch.uint8, device, stream)
+    _need(workspace.device == device, "the workspace is on another device")
+    return workspace
+
+
+def mla_sparse_attn_prefill_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor, idx: torch.Tensor,
+                               scale: float, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                               want_lse: bool = False, stream=None, out_dtype=torch.float32):
+    """mla_sparse_attn_prefill over an 8-bit cache: cache uint8 [N, 640], cache_scale f32 [N]."""
+    L, top_k, out, lse, N = _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream)
+    rc = load().mla_sparse_attn_prefill_q8(_ptr(q), _ptr(cache), _ptr(cache_scale), _ptr(idx), L, N, top_k, scale,
+                                           _ptr(out), _out_dtype(out), _ptr(lse), None, 0, _stream(stream))
+    _check("mla_sparse_attn_prefill_q8", rc)
+    return (out, lse) if want_lse else out
+
+
+def mla_sparse_attn_prefill_q8_paged(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor,
+                                     block_table: torch.Tensor, page_size: int, idx: torch.Tensor, scale: float, N: int,
+                                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                                     want_lse: bool = False, stream=None, out_dtype=torch.float32):
+    """mla_sparse_attn_prefill_paged over an 8-bit pool: cache uint8 [num_pages * page_size, 640]."""
+    L, top_k, out, lse, n = _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream)
+    _need(block_table.dtype == torch.int32, "block_table is int32")
+    _need(page_size < 1 or block_table.numel() >= -(-N // page_size), "block_table holds ceil(N / page_size) pages")
+    _here(q.device, block_table)
+    rc = load().mla_sparse_attn_prefill_q8_paged(_ptr(q), _ptr(cache), _ptr(cache_scale), _ptr(block_table), page_size,
+                                                 n // page_size if page_size > 0 else 0, _ptr(idx), L, N, top_k, scale,
+                                                 _ptr(out), _out_dtype(out), _ptr(lse), None, 0, _stream(stream))
+    _check("mla_sparse_attn_prefill_q8_paged", rc)
+    return (out, lse) if want_lse else out
+
+
+def mla_sparse_attn_decode_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor, kv_len: torch.Tensor,
+                              idx: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
+                              lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                              want_lse: bool = False, stream=None, out_dtype=torch.float32):
+    """mla_sparse_attn_decode over an 8-bit cache: cache uint8 [B, Nmax, 640], cache_scale f32 [B, Nmax]."""
+    B, top_k, out, lse, n = _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream)
+    _need(cache.dim() == 3 and cache.shape[0] == B, "the cache is uint8 [B, Nmax, 640]")
+    _ints(kv_len, B, "kv_len")
+    workspace = _decode_workspace(workspace, B, top_k, q.device, stream)
+    _here(q.device, kv_len)
+    rc = load().mla_sparse_attn_decode_q8(_ptr(q), _ptr(cache), _ptr(cache_scale), _ptr(kv_len), _ptr(idx), B,
+                                          cache.shape[1], top_k, scale, _ptr(out), _out_dtype(out), _ptr(lse),
+                                          _ptr(workspace), workspace.nbytes, _stream(stream))
+    _check("mla_sparse_attn_decode_q8", rc)
+    return (out, lse) if want_lse else out
+
+
+def mla_sparse_attn_decode_q8_paged(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor,
+                                    kv_len: torch.Tensor, block_table: torch.Tensor, page_size: int, idx: torch.Tensor,
+                                    scale: float, Nmax: int, out: Optional[torch.Tensor] = None,
+                                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                                    want_lse: bool = False, stream=None, out_dtype=torch.float32):
+    """mla_sparse_attn_decode_paged over an 8-bit pool: cache uint8 [num_pages * page_size, 640]."""
+    B, top_k, out, lse, n = _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream)
+    _ints(kv_len, B, "kv_len")
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B,
+          "block_table is int32 [B, pages]")
+    workspace = _decode_workspace(workspace, B, top_k, q.device, stream)
+    _here(q.device, kv_len, block_table)
+    rc = load().mla_sparse_attn_decode_q8_paged(_ptr(q), _ptr(cache), _ptr(cache_scale), _ptr(kv_len),
+                                                _ptr(block_table), block_table.shape[1], page_size,
+                                                n // page_size if page_size > 0 else 0, _ptr(idx), B, Nmax, top_k,
+                                                scale, _ptr(out), _out_dtype(out), _ptr(lse), _ptr(workspace),
+                                                workspace.nbytes, _stream(stream))
+    _check("mla_sparse_attn_decode_q8_paged", rc)
+    return (out, lse) if want_lse else out
+
+
+def indexer_norm_rope(q: torch.Tensor, k: torch.Tensor, k_w: Optional[torch.Tensor], k_b: Optional[torch.Tensor],
+                      eps: float, cos_sin: torch.Tensor, pos: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                      q_w: Optional[torch.Tensor] = None, q_b: Optional[torch.Tensor] = None, norm: str = "layer",
+                      interleave: bool = True, q_out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The indexer's queries and keys of new tokens: norm and rotation of each head, the queries
+    returned as [R, 32, 128] bf16, the keys scattered to k_cache.
+
+    q [R, 32, 128] and k [R, 128] bf16 (rows may be strided), weights and biases f32 [128] or None (not
+    normalised / nothing added), cos_sin [max_pos, 64] f32, pos and slots [R] int32 (a negative slot
+    writes no key; slots differ), k_cache bf16 [..., 128], norm "rms" or "layer"."""
+    R = q.shape[0]
+    _need(k.shape[0] == R, "q and k hold one row a token")
+    qp, kp = (_rows_ptr(q, 4096, "q"), _rows_ptr(k, 128, "k")) if R else (None, None)
+    _need(norm in NORMS, f"norm is one of {sorted(NORMS)}")
+    for w in (q_w, q_b, k_w, k_b):
+        _need(w is None or (w.dtype == torch.float32 and w.numel() == 128), "weights and biases are float32 [128]")
+    _need(_is16(k_cache) and k_cache.shape[-1] == 128, "k_cache is bf16 with rows of 128")
+    _ints(pos, R, "pos")
+    _ints(slots, R, "slots")
+    if q_out is None:
+        q_out = _new((R, 32, 128), torch.bfloat16, q.device, stream)
+    _need(_is16(q_out) and q_out.numel() == R * 4096, "q_out is bf16 [R, 32, 128]")
+    _here(q.device, k, q_w, q_b, k_w, k_b, cos_sin, pos, slots, k_cache, q_out)
+    rc = load().dsa_indexer_norm_rope(qp, q.stride(0) if R > 1 else 4096, kp, k.stride(0) if R > 1 else 128,
+                                      NORMS[norm], _ptr(q_w), _ptr(q_b), _ptr(k_w), _ptr(k_b), eps, _ptr(cos_sin),
+                                      _cos_sin(cos_sin), 1 if interleave else 0, _ptr(pos), _ptr(slots), R,
+                                      _ptr(q_out), _ptr(k_cache), k_cache.numel() // 128, _stream(stream))
+    _check("dsa_indexer_norm_rope", rc)
+    return q_out
 
 
 def mla_value_up_proj(o: torch.Tensor, wv_b: torch.Tensor, v: Optional[torch.Tensor] = None,

@@ -339,6 +339,154 @@ dsa_status_t mla_sparse_attn_decode_noalloc(const void* q, const void* kv, const
                                       lse, static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+// Host checks the 8-bit attention calls share.
+dsa_status_t check_attn_q8(const void* q, const void* cache, const float* cache_scale, const int32_t* idx, int rows,
+                           int N, int top_k, float scale, const void* out, int out_dtype) {
+    if (!q || !cache || !cache_scale || !idx || !out) return DSA_ERR_INVALID_ARG;
+    if (out_dtype != DSA_OUT_F32 && out_dtype != DSA_OUT_BF16) return DSA_ERR_INVALID_ARG;
+    if (rows < 1 || N < 1) return DSA_ERR_INVALID_ARG;
+    if (top_k < 1 || top_k > DSA_MAX_TOPK) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if ((long long)rows * DSA_HEADS > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!(scale > 0.f) || !(scale < 1e30f)) return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+// eps of a norm: finite and not negative
+bool eps_ok(float eps) { return eps >= 0.f && eps < 3.0e38f; }
+}  // namespace
+
+dsa_status_t mla_sparse_attn_prefill_q8(const void* q, const void* cache, const float* cache_scale,
+                                        const int32_t* idx, int L, int N, int top_k, float scale, void* out,
+                                        int out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    (void)workspace;
+    (void)ws_bytes;
+    dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
+    if (st != DSA_OK) return st;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if ((st = check_device()) != DSA_OK) return st;
+    return launch_attn_q8_prefill(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32, lse,
+                                  PageTable{}, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_sparse_attn_prefill_q8_paged(const void* q, const void* cache, const float* cache_scale,
+                                              const int32_t* block_table, int page_size, int num_pages,
+                                              const int32_t* idx, int L, int N, int top_k, float scale, void* out,
+                                              int out_dtype, float* lse, void* workspace, size_t ws_bytes,
+                                              void* stream) {
+    (void)workspace;
+    (void)ws_bytes;
+    dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
+    if (st != DSA_OK) return st;
+    PageTable pt;
+    const int stride = page_size > 0 ? (int)(((long long)N + page_size - 1) / page_size) : 0;
+    if ((st = make_page_table(block_table, stride, page_size, num_pages, N, &pt)) != DSA_OK) return st;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if ((st = check_device()) != DSA_OK) return st;
+    return launch_attn_q8_prefill(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32, lse,
+                                  pt, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_sparse_attn_decode_q8(const void* q, const void* cache, const float* cache_scale,
+                                       const int32_t* kv_len, const int32_t* idx, int B, int Nmax, int top_k,
+                                       float scale, void* out, int out_dtype, float* lse, void* workspace,
+                                       size_t ws_bytes, void* stream) {
+    if (!kv_len || !workspace) return DSA_ERR_INVALID_ARG;
+    dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, B, Nmax, top_k, scale, out, out_dtype);
+    if (st != DSA_OK) return st;
+    if ((long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
+    if (ws_bytes < attn_decode_workspace(B, top_k)) return DSA_ERR_WORKSPACE_TOO_SMALL;
+    if ((st = check_device()) != DSA_OK) return st;
+    return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
+                                 out_dtype == DSA_OUT_F32, lse, workspace, PageTable{},
+                                 static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_sparse_attn_decode_q8_paged(const void* q, const void* cache, const float* cache_scale,
+                                             const int32_t* kv_len, const int32_t* block_table, int bt_stride,
+                                             int page_size, int num_pages, const int32_t* idx, int B, int Nmax,
+                                             int top_k, float scale, void* out, int out_dtype, float* lse,
+                                             void* workspace, size_t ws_bytes, void* stream) {
+    if (!kv_len || !workspace) return DSA_ERR_INVALID_ARG;
+    dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, B, Nmax, top_k, scale, out, out_dtype);
+    if (st != DSA_OK) return st;
+    PageTable pt;
+    if ((st = make_page_table(block_table, bt_stride, page_size, num_pages, Nmax, &pt)) != DSA_OK) return st;
+    if ((long long)B * bt_stride > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
+    if (ws_bytes < attn_decode_workspace(B, top_k)) return DSA_ERR_WORKSPACE_TOO_SMALL;
+    if ((st = check_device()) != DSA_OK) return st;
+    return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
+                                 out_dtype == DSA_OUT_F32, lse, workspace, pt, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_cache_write_q8(const void* kv_a, int64_t kv_a_stride, const float* norm_w, float eps,
+                                const float* cos_sin, int max_pos, int interleave, const int32_t* pos,
+                                const int32_t* slots, int R, void* cache, float* cache_scale, int64_t cache_rows,
+                                void* stream) {
+    if (!kv_a || !norm_w || !cos_sin || !pos || !slots || !cache || !cache_scale) return DSA_ERR_INVALID_ARG;
+    if (R < 1 || max_pos < 1 || cache_rows < 1 || kv_a_stride < DSA_QK_DIM || !eps_ok(eps)) return DSA_ERR_INVALID_ARG;
+    if (interleave != 0 && interleave != 1) return DSA_ERR_INVALID_ARG;
+    if (cache_rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(kv_a) || !aligned16(norm_w) || !aligned16(cos_sin) || !aligned16(cache) || kv_a_stride % 8)
+        return DSA_ERR_MISALIGNED;
+    dsa_status_t st = check_device();
+    if (st != DSA_OK) return st;
+    return launch_cache_write_q8(kv_a, kv_a_stride, norm_w, eps, cos_sin, max_pos, interleave, pos, slots, R, cache,
+                                 cache_scale, (int)cache_rows, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_cache_read_q8(const void* cache, const float* cache_scale, int64_t cache_rows, const int32_t* slots,
+                               int R, void* out, void* stream) {
+    if (!cache || !cache_scale || !slots || !out) return DSA_ERR_INVALID_ARG;
+    if (R < 1 || cache_rows < 1) return DSA_ERR_INVALID_ARG;
+    if (cache_rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    dsa_status_t st = check_device();
+    if (st != DSA_OK) return st;
+    return launch_cache_read_q8(cache, cache_scale, (int)cache_rows, slots, R, out, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_cache_read_q8_paged(const void* cache, const float* cache_scale, const int32_t* kv_len,
+                                     const int32_t* block_table, int bt_stride, int page_size, int num_pages, int B,
+                                     int Nmax, void* out, void* stream) {
+    if (!cache || !cache_scale || !kv_len || !out) return DSA_ERR_INVALID_ARG;
+    if (B < 1 || Nmax < 1) return DSA_ERR_INVALID_ARG;
+    PageTable pt;
+    dsa_status_t st = make_page_table(block_table, bt_stride, page_size, num_pages, Nmax, &pt);
+    if (st != DSA_OK) return st;
+    if ((long long)B * bt_stride > 0x7FFFFFFFLL || (long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if ((st = check_device()) != DSA_OK) return st;
+    return launch_cache_read_q8_paged(cache, cache_scale, kv_len, B, Nmax, out, pt, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t dsa_indexer_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int norm,
+                                   const float* q_w, const float* q_b, const float* k_w, const float* k_b, float eps,
+                                   const float* cos_sin, int max_pos, int interleave, const int32_t* pos,
+                                   const int32_t* slots, int R, void* q_out, void* k_cache, int64_t cache_rows,
+                                   void* stream) {
+    constexpr int kRow = DSA_INDEXER_HEADS * DSA_INDEXER_DIM;
+    if (!q || !k || !cos_sin || !pos || !slots || !q_out || !k_cache) return DSA_ERR_INVALID_ARG;
+    if ((q_b && !q_w) || (k_b && !k_w)) return DSA_ERR_INVALID_ARG;
+    if (R < 1 || max_pos < 1 || cache_rows < 1 || q_stride < kRow || k_stride < DSA_INDEXER_DIM || !eps_ok(eps))
+        return DSA_ERR_INVALID_ARG;
+    if (norm != DSA_NORM_RMS && norm != DSA_NORM_LAYER) return DSA_ERR_INVALID_ARG;
+    if (interleave != 0 && interleave != 1) return DSA_ERR_INVALID_ARG;
+    if (q == q_out && q_stride != kRow) return DSA_ERR_INVALID_ARG;
+    if (cache_rows > 0x7FFFFFFFLL || (long long)R * (DSA_INDEXER_HEADS + 1) > 0x7FFFFFFFLL)
+        return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(cos_sin) || !aligned16(q_out) || !aligned16(k_cache) ||
+        !aligned16(q_w) || !aligned16(q_b) || !aligned16(k_w) || !aligned16(k_b) || q_stride % 8 || k_stride % 8)
+        return DSA_ERR_MISALIGNED;
+    dsa_status_t st = check_device();
+    if (st != DSA_OK) return st;
+    return launch_indexer_norm_rope(q, q_stride, k, k_stride, norm, q_w, q_b, k_w, k_b, eps, cos_sin, max_pos,
+                                    interleave, pos, slots, R, q_out, k_cache, (int)cache_rows,
+                                    static_cast<cudaStream_t>(stream));
+}
+
 dsa_status_t mla_value_up_proj(const void* o, const void* wv_b, int R, void* v, void* stream) {
     if (!o || !wv_b || !v) return DSA_ERR_INVALID_ARG;
     if (R < 1) return DSA_ERR_INVALID_ARG;

@@ -78,6 +78,26 @@ dsa_status_t launch_attn_decode_noalloc(const void* q, const void* kv, const int
 dsa_status_t launch_attn_decode(const void* q, const void* kv, const int32_t* kv_len, const int32_t* idx, int B,
                                 int Nmax, int top_k, float scale, void* out, int out_f32, float* lse,
                                 void* workspace, const PageTable& pages, cudaStream_t stream);
+dsa_status_t launch_cache_write_q8(const void* kv_a, int64_t kv_a_stride, const float* norm_w, float eps,
+                                   const float* cos_sin, int max_pos, int interleave, const int32_t* pos,
+                                   const int32_t* slots, int R, void* cache, float* cache_scale, int cache_rows,
+                                   cudaStream_t stream);
+dsa_status_t launch_cache_read_q8(const void* cache, const float* cache_scale, int cache_rows, const int32_t* slots,
+                                  int R, void* out, cudaStream_t stream);
+dsa_status_t launch_cache_read_q8_paged(const void* cache, const float* cache_scale, const int32_t* kv_len, int B,
+                                        int Nmax, void* out, const PageTable& pages, cudaStream_t stream);
+dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, const int32_t* idx,
+                                    int L, int N, int top_k, float scale, void* out, int out_f32, float* lse,
+                                    const PageTable& pages, cudaStream_t stream);
+dsa_status_t launch_attn_q8_decode(const void* q, const void* cache, const float* cache_scale, const int32_t* kv_len,
+                                   const int32_t* idx, int B, int Nmax, int top_k, float scale, void* out,
+                                   int out_f32, float* lse, void* workspace, const PageTable& pages,
+                                   cudaStream_t stream);
+dsa_status_t launch_indexer_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int norm,
+                                      const float* q_w, const float* q_b, const float* k_w, const float* k_b,
+                                      float eps, const float* cos_sin, int max_pos, int interleave,
+                                      const int32_t* pos, const int32_t* slots, int R, void* q_out, void* k_cache,
+                                      int cache_rows, cudaStream_t stream);
 dsa_status_t launch_value_up_proj(const void* o, const void* wv_b, int R, void* v, cudaStream_t stream);
 
 }  // namespace dsa

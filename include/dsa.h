@@ -44,6 +44,7 @@ extern "C" {
 #define DSA_V_DIM 512
 #define DSA_V_HEAD_DIM 256
 #define DSA_MAX_TOPK 2048
+#define DSA_Q8_ROW_BYTES 640   /* a row of the 8-bit latent cache */
 
 typedef int32_t dsa_status_t;
 
@@ -262,6 +263,138 @@ dsa_status_t mla_sparse_attn_prefill_paged(const void *q, const void *kv_pool,
                                            const int32_t *idx, int L, int N, int top_k, float scale,
                                            void *out, int out_dtype, float *lse, void *workspace,
                                            size_t ws_bytes, void *stream);
+
+/*
+ * The 8-bit latent cache.  A key's row takes 640 bytes instead of 1152:
+ *
+ *   cache[row]        bytes 0..511:   the 512 latent dims, e4m3
+ *                     bytes 512..639: the 64 rotated rope dims, bf16
+ *   cache_scale[row]  f32: the latent dims are e4m3 * cache_scale[row]
+ *
+ * so every row is five whole 128-byte lines.  One scale covers one token's
+ * latent row (the one key/value head every query head shares): e4m3 carries
+ * its own exponent, so finer blocks gain only below 2^-15 of a row's largest
+ * value.  As written by mla_cache_write_q8 the scale is a power of two, which
+ * makes every stored value exactly a bf16 number; readers take any positive
+ * finite scale in [2^-64, 2^64].  The rope dims stay bf16: they carry the
+ * position.  Rows are addressed as in the bf16 cache (dense [B, Nmax] rows or
+ * pages of a pool; rows * 640 may pass 2^32).  No counterpart on the pages,
+ * whose caches hold bf16 or float32 rows.
+ */
+
+/*
+ * mla_cache_write_q8 -- the latent rows of R new tokens into the 8-bit cache:
+ * RMS norm of the 512 latent dims, rotation of the 64 rope dims, quantisation
+ * and the scatter to the cache, in one pass.  Defined on SlimServe
+ * "GLM52_PIPELINE_TRACE.md", section 4 (the projection's 576 outputs split into
+ * [kv_cmpr 512 | k_pe 64], k_pe rotated, kv_cmpr RMS-normalised); the 8-bit
+ * rounding is this library's.
+ *
+ *   u      = kv_a[r, 0:512] * rsqrt(mean(kv_a[r, 0:512]^2) + eps) * norm_w       (float32)
+ *   k      = the smallest integer with max|u| <= 448 * 2^k, clamped to -64..64; 0 for a row of zeros
+ *   latent = e4m3(u * 2^-k), nearest, ties to even, saturating;  cache_scale = 2^k
+ *   rope   = bf16 of the 64 rope dims with pair i turned by the angle of pos[r]:
+ *            (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i), pairs (2i, 2i + 1) when
+ *            interleave is 1, (i, i + 32) when it is 0
+ *   kv_a     bf16, row r at kv_a + r * kv_a_stride (elements; >= 576, a multiple of 8)
+ *   norm_w   f32 [512]
+ *   cos_sin  f32 [max_pos, 64]: cos_0..cos_31 | sin_0..sin_31 of each position
+ *   pos      int32 [R] (device): position of each token, 0 <= pos < max_pos
+ *   slots    int32 [R] (device): cache row each token goes to; a negative slot skips the token (a
+ *            padded batch).  The slots of a call must differ; a slot given twice ends as a mixture.
+ *   cache, cache_scale   cache_rows rows; rows no slot names are left as they are
+ * A position outside the table or a slot >= cache_rows is recorded as
+ * DSA_ERR_DEVICE_BOUNDS and its token skipped.  Inputs must be finite: another
+ * value leaves that token's row unspecified, and no other row.
+ * Errors (host): DSA_ERR_INVALID_ARG for a null pointer, R < 1, max_pos < 1, cache_rows < 1,
+ * kv_a_stride < 576, eps not finite or < 0, interleave not 0 or 1; DSA_ERR_UNSUPPORTED_SHAPE for
+ * cache_rows > 2^31 - 1; DSA_ERR_MISALIGNED for kv_a, norm_w, cos_sin or cache not 16-byte aligned or
+ * kv_a_stride not a multiple of 8.
+ */
+dsa_status_t mla_cache_write_q8(const void *kv_a, int64_t kv_a_stride, const float *norm_w, float eps,
+                                const float *cos_sin, int max_pos, int interleave, const int32_t *pos,
+                                const int32_t *slots, int R, void *cache, float *cache_scale,
+                                int64_t cache_rows, void *stream);
+
+/*
+ * mla_cache_read_q8 -- rows of the 8-bit cache back as the bf16 rows the other
+ * calls take: out[r] = [bf16(e4m3 * scale) | rope] of cache row slots[r]
+ * (exact for power-of-two scales); zeros for a negative slot.  A slot >=
+ * cache_rows is recorded as DSA_ERR_DEVICE_BOUNDS and read as zeros.
+ *   out  bf16 [R, 576]
+ * mla_cache_read_q8_paged does the same for B sequences through a page table:
+ * out[b, j] = row j of sequence b for j < min(kv_len[b], Nmax); later rows of
+ * out are left as they are.  The page table and its checks are those of
+ * mla_sparse_attn_decode_paged (a page outside the pool reads as zeros).
+ *   out  bf16 [B, Nmax, 576]
+ * Errors (host): as mla_cache_write_q8.
+ */
+dsa_status_t mla_cache_read_q8(const void *cache, const float *cache_scale, int64_t cache_rows,
+                               const int32_t *slots, int R, void *out, void *stream);
+dsa_status_t mla_cache_read_q8_paged(const void *cache, const float *cache_scale, const int32_t *kv_len,
+                                     const int32_t *block_table, int bt_stride, int page_size,
+                                     int num_pages, int B, int Nmax, void *out, void *stream);
+
+/*
+ * mla_sparse_attn_*_q8 -- the attention of the mla_sparse_attn_* calls over the
+ * 8-bit cache, read directly: key row [scale * e4m3 | rope], value row scale *
+ * e4m3.  Arguments, checks, workspaces and results are those of the bf16 call
+ * of the same name, with `cache` (640-byte rows) and `cache_scale` in place of
+ * kv.  The cache may be up to 2^31 - 1 rows.
+ */
+dsa_status_t mla_sparse_attn_prefill_q8(const void *q, const void *cache, const float *cache_scale,
+                                        const int32_t *idx, int L, int N, int top_k, float scale,
+                                        void *out, int out_dtype, float *lse, void *workspace,
+                                        size_t ws_bytes, void *stream);
+dsa_status_t mla_sparse_attn_prefill_q8_paged(const void *q, const void *cache, const float *cache_scale,
+                                              const int32_t *block_table, int page_size, int num_pages,
+                                              const int32_t *idx, int L, int N, int top_k, float scale,
+                                              void *out, int out_dtype, float *lse, void *workspace,
+                                              size_t ws_bytes, void *stream);
+dsa_status_t mla_sparse_attn_decode_q8(const void *q, const void *cache, const float *cache_scale,
+                                       const int32_t *kv_len, const int32_t *idx, int B, int Nmax,
+                                       int top_k, float scale, void *out, int out_dtype, float *lse,
+                                       void *workspace, size_t ws_bytes, void *stream);
+dsa_status_t mla_sparse_attn_decode_q8_paged(const void *q, const void *cache, const float *cache_scale,
+                                             const int32_t *kv_len, const int32_t *block_table,
+                                             int bt_stride, int page_size, int num_pages,
+                                             const int32_t *idx, int B, int Nmax, int top_k, float scale,
+                                             void *out, int out_dtype, float *lse, void *workspace,
+                                             size_t ws_bytes, void *stream);
+
+/*
+ * dsa_indexer_norm_rope -- the indexer's queries and keys of R new tokens from
+ * their projections: norm and rotation of each head in one pass, the queries
+ * written as dsa_indexer_scores takes them and the keys scattered to the key
+ * cache.  The rotation is on SlimServe "GLM52_PIPELINE_TRACE.md", section 5
+ * (indexer_rope_interleave); the pages print neither the indexer's norms nor
+ * which of its 128 dims turn: taken here are the first 64.
+ *
+ *   norm DSA_NORM_RMS:    y = x * rsqrt(mean(x^2) + eps) * w + b
+ *   norm DSA_NORM_LAYER:  y = (x - mean(x)) * rsqrt(var(x) + eps) * w + b
+ *   over the 128 dims of a head (float32; a null b adds nothing), then dims 0..63 turned by the
+ *   angle of pos[r] as in mla_cache_write_q8, dims 64..127 kept; rounded to bf16
+ *   q        bf16, token r's 32 heads of 128 at q + r * q_stride (elements; >= 4096, a multiple of 8)
+ *   k        bf16, token r's 128 dims at k + r * k_stride (>= 128, a multiple of 8)
+ *   q_w, q_b f32 [128], the same for every head; a null q_w leaves the queries unnormalised (q_b null too)
+ *   k_w, k_b f32 [128]; a null k_w leaves the keys unnormalised (k_b null too)
+ *   q_out    bf16 [R, 32, 128]; may be q itself when q_stride is 4096
+ *   k_cache  bf16 [cache_rows, 128]; token r's key goes to row slots[r] (negative: only its queries
+ *            are written).  The slots of a call must differ.  k must not lie in k_cache.
+ * A position outside the table is recorded as DSA_ERR_DEVICE_BOUNDS and the token skipped, a slot >=
+ * cache_rows likewise and its key skipped.
+ * Errors (host): DSA_ERR_INVALID_ARG for a null pointer (other than the weights), a bias without its
+ * weight, R < 1, max_pos < 1, cache_rows < 1, a stride below its row, eps not finite or < 0, norm or
+ * interleave not 0 or 1, q_out equal to q with another stride; DSA_ERR_UNSUPPORTED_SHAPE for cache_rows or
+ * R * 33 > 2^31 - 1; DSA_ERR_MISALIGNED for a tensor not 16-byte aligned or a stride not a multiple of 8.
+ */
+#define DSA_NORM_RMS 0
+#define DSA_NORM_LAYER 1
+dsa_status_t dsa_indexer_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                   int norm, const float *q_w, const float *q_b, const float *k_w,
+                                   const float *k_b, float eps, const float *cos_sin, int max_pos,
+                                   int interleave, const int32_t *pos, const int32_t *slots, int R,
+                                   void *q_out, void *k_cache, int64_t cache_rows, void *stream);
 
 /*
  * mla_value_up_proj -- the value up-projection (wv_b) after the attention.
