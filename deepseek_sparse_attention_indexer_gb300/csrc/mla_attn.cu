@@ -67,16 +67,14 @@
 
 #include "dsa_internal.h"
 #include "dsa_ptx.cuh"
+#include "mla_attn_common.cuh"
 
 namespace dsa {
 
 namespace {
 
-constexpr int kH = DSA_HEADS;          // 64
 constexpr int kD = DSA_QK_DIM;         // 576
-constexpr int kDv = DSA_V_DIM;         // 512
 constexpr int kRowBytes = kD * 2;      // 1152
-constexpr int kTile = 128;             // keys per tile (MMA M)
 constexpr int kBlkBytes = kTile * 128; // 16 KB: 128 keys x 64 dims
 constexpr int kQBlkBytes = kH * 128;   // 8 KB: 64 heads x 64 dims
 constexpr int kWorkerWarps = 16;                  // gather + softmax warps
@@ -88,6 +86,7 @@ constexpr int kIssuers = 2;                        // MMA-issuing warps
 constexpr int kMaxRegs = 96;                       // 19 warps: 5 share one 16K-register sub-partition
 constexpr int kThreads = 32 * (1 + kIssuers) + kWorkers;  // warp 0 Q loader, warps 1-2 MMA, warps 3.. workers
 constexpr int kHG = kH / (kWorkerWarps / 4);       // 16 heads per worker warp
+static_assert(kHG == 16, "warp_transpose_reduce16 takes a head group of 16");
 constexpr int kGroupThreads = 4 * 32;              // the four warps sharing a head group
 constexpr int kSegs = 4;               // PV releases the stage by 128-dim latent chunk (the rope block with the last)
 static_assert(kWorkerWarps == 16 && kTile == 128, "a worker warp copies four rows of each 64-key half");
@@ -119,21 +118,13 @@ static_assert(TM_O + 4 * 64 <= 512, "tensor memory columns");
 constexpr uint32_t IDESC_QK = idesc_bf16_f32(128, 64, false, false);
 constexpr uint32_t IDESC_PV = idesc_bf16_f32(128, 64, true, true);
 
-struct AttnParams {
+struct AttnParams : AttnShape {
     const __nv_bfloat16* kv;   // [B][Nmax][576]
-    const int32_t* idx;        // [rows][top_k]
-    const int32_t* kv_len;     // [B] or nullptr (then every row may use Nmax keys)
     void* out;                 // final: [rows][64][512], float32 or bf16 (out_f32)
     int out_f32;               // 1: float32 output; 0: bf16 (round to nearest even)
     float* lse;                // final: [rows][64] or nullptr
     float* part_o;             // partial: [rows][nsplit][64][512]
     float* part_lse;           // partial: [rows][nsplit][64]
-    int rows;                  // queries (prefill) or sequences (decode)
-    int prefill;               // 1: all rows read batch 0 of kv; 0: row r reads batch r
-    int Nmax;
-    int top_k;
-    int nsplit, split_len;     // slots per item = split_len (multiple of 128)
-    int n_items;               // rows * nsplit
     float scale_log2;          // scale * log2(e)
     int32_t* status;           // device error word
     PageTable pages;           // paged cache (pages.table == nullptr: dense rows)
@@ -144,95 +135,6 @@ struct AttnParams {
 __device__ __forceinline__ bool worker_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
     return mbar_wait(bar, parity, abort, status);
 }
-
-struct Item {
-    int row, split, batch, slot0, slot_end, bound;
-};
-
-__device__ __forceinline__ Item decode_item(const AttnParams& p, int item) {
-    Item it;
-    it.row = item / p.nsplit;
-    it.split = item % p.nsplit;
-    it.batch = p.prefill ? 0 : it.row;
-    it.slot0 = it.split * p.split_len;
-    it.slot_end = min(p.top_k, it.slot0 + p.split_len);
-    it.bound = p.kv_len ? min(__ldg(p.kv_len + it.batch), p.Nmax) : p.Nmax;
-    return it;
-}
-
-__device__ __forceinline__ int nth_item(const AttnParams& p, int s) {
-    int base = s * (int)gridDim.x;
-    if (base >= p.n_items) return -1;
-    int k = (s & 1) ? ((int)gridDim.x - 1 - (int)blockIdx.x) : (int)blockIdx.x;
-    int item = base + k;
-    return item < p.n_items ? item : -2;
-}
-
-// Number of 128-slot tiles up to the last non-negative index of the item's
-// slot range (warp-collective; every lane gets the same answer).  A full
-// selection ends with a valid index, so the last 32 slots are looked at first;
-// otherwise (a query with fewer causal keys than top_k: a valid prefix, then
-// -1) the range is scanned backwards 512 slots a round, 16 independent loads a
-// lane, so that a short item costs a few L2 round trips rather than one per 32
-// slots.
-__device__ __forceinline__ int item_tiles(const AttnParams& p, const Item& I, uint32_t lane) {
-    const int32_t* ir = p.idx + (int64_t)I.row * p.top_k;
-    int hi = I.slot_end - 32;   // slots [hi, slot_end) first
-    {
-        const int s = hi + (int)lane;
-        const bool v = (s >= I.slot0) && (s < I.slot_end) && (__ldg(ir + s) >= 0);
-        const uint32_t m = __ballot_sync(0xffffffffu, v);
-        if (m) return (hi + 31 - __clz(m) - I.slot0) / kTile + 1;
-    }
-    for (; hi > I.slot0; hi -= 512) {   // slots [max(slot0, hi - 512), hi)
-        const int lo = hi - 512;
-        int last = -1;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const int s = lo + 32 * k + (int)lane;
-            if (s >= I.slot0 && s < hi && __ldg(ir + s) >= 0) last = s;
-        }
-        last = __reduce_max_sync(0xffffffffu, last);
-        if (last >= 0) return (last - I.slot0) / kTile + 1;
-    }
-    return 0;
-}
-
-// Transposing butterfly over a warp: on entry every lane holds 16 values (one
-// per head of the warp's head group); on exit lanes 2i and 2i+1 hold the
-// warp-wide reduction for head i of the group.
-template <bool MAX>
-__device__ __forceinline__ float warp_transpose_reduce16(const float (&x)[16], uint32_t lane) {
-    float a[8];
-    {
-        const bool up = lane & 16;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float mine = up ? x[8 + k] : x[k];
-            const float other = up ? x[k] : x[8 + k];
-            const float recv = __shfl_xor_sync(0xffffffffu, other, 16);
-            a[k] = MAX ? fmaxf(mine, recv) : mine + recv;
-        }
-    }
-#pragma unroll
-    for (int step = 0; step < 3; ++step) {
-        const int half = 4 >> step;   // 4, 2, 1 values kept
-        const int off = 8 >> step;    // shuffle distance 8, 4, 2
-        const bool up = lane & off;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (k < half) {
-                const float mine = up ? a[half + k] : a[k];
-                const float other = up ? a[k] : a[half + k];
-                const float recv = __shfl_xor_sync(0xffffffffu, other, off);
-                a[k] = MAX ? fmaxf(mine, recv) : mine + recv;
-            }
-        }
-    }
-    const float o = __shfl_xor_sync(0xffffffffu, a[0], 1);
-    return MAX ? fmaxf(a[0], o) : a[0] + o;
-}
-
 
 template <bool PARTIAL, bool PAGED>
 __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
@@ -810,6 +712,8 @@ dsa_status_t launch_kernel(const void* q, int q_rows, const AttnParams& prm, cud
 // share of the merge).  The split count with the least such cost wins, the smaller on a tie
 // (fewer partials to merge).  Rounding the split count up from SMs / B instead left a second,
 // mostly idle round at many batch sizes (B = 16: 160 items on 152 SMs).
+}  // namespace
+
 int decode_splits(int B, int top_k) {
     const int tiles = ceil_div(top_k, kTile);
     const int sms = device_sm_count();
@@ -827,6 +731,16 @@ int decode_splits(int B, int top_k) {
     }
     return best;
 }
+
+dsa_status_t launch_decode_combine(const float* part_o, const float* part_lse, int B, int nsplit, void* out, int out_f32,
+                                   float* lse, cudaStream_t stream) {
+    if (launch_pdl(mla_decode_combine_kernel, dim3(B * kH), dim3(128), 0, stream, part_o, part_lse, nsplit, out, out_f32,
+                   lse) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+namespace {
 
 // Decode: prefetch the rows of an item's next tile into L2 when the caches the launch gathers from
 // are large against L2 (see launch_attn_prefill) and an item has at least 8 tiles.  One persistent
@@ -897,10 +811,7 @@ dsa_status_t launch_attn_decode(const void* q, const void* kv, const int32_t* kv
     p.l2_prefetch = want_l2_prefetch_decode((size_t)B * Nmax * kRowBytes, p.split_len);
     dsa_status_t st = p.pages.table ? launch_kernel<true, true>(q, B, p, stream) : launch_kernel<true, false>(q, B, p, stream);
     if (st != DSA_OK) return st;
-    if (launch_pdl(mla_decode_combine_kernel, dim3(B * kH), dim3(128), 0, stream, (const float*)p.part_o,
-                   (const float*)p.part_lse, p.nsplit, out, out_f32, lse) != cudaSuccess)
-        return DSA_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    return launch_decode_combine(p.part_o, p.part_lse, B, p.nsplit, out, out_f32, lse, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -964,10 +875,7 @@ dsa_status_t launch_attn_decode_noalloc(const void* q, const void* kv, const int
     p.l2_prefetch = want_l2_prefetch_decode((size_t)B * Nmax * kRowBytes, p.split_len);
     st = launch_kernel<true, false>(q, B, p, stream);
     if (st != DSA_OK) return st;
-    if (launch_pdl(mla_decode_combine_kernel, dim3(B * kH), dim3(128), 0, stream, (const float*)p.part_o,
-                   (const float*)p.part_lse, p.nsplit, out, out_f32, lse) != cudaSuccess)
-        return DSA_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+    return launch_decode_combine(p.part_o, p.part_lse, B, p.nsplit, out, out_f32, lse, stream);
 }
 
 }  // namespace dsa

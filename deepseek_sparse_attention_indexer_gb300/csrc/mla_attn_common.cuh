@@ -1,0 +1,117 @@
+// mla_attn_common.cuh -- what the two attention kernels (bf16 rows, 8-bit rows)
+// share: the split of a launch into items of one query's selected keys, their
+// assignment to persistent CTAs, and the transposing warp reduction.
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "dsa_internal.h"
+#include "dsa_ptx.cuh"
+
+namespace dsa {
+
+constexpr int kH = DSA_HEADS;          // 64
+constexpr int kDv = DSA_V_DIM;         // 512
+constexpr int kTile = 128;             // keys per tile (MMA M)
+
+// The queries, their selections and the split into items.
+struct AttnShape {
+    const int32_t* idx;        // [rows][top_k]
+    const int32_t* kv_len;     // [B] or nullptr (then every row may use Nmax keys)
+    int rows;                  // queries (prefill) or sequences (decode)
+    int prefill;               // 1: all rows read batch 0 of kv; 0: row r reads batch r
+    int Nmax;
+    int top_k;
+    int nsplit, split_len;     // slots per item = split_len (multiple of 128)
+    int n_items;               // rows * nsplit
+};
+
+struct Item {
+    int row, split, batch, slot0, slot_end, bound;
+};
+
+__device__ __forceinline__ Item decode_item(const AttnShape& p, int item) {
+    Item it;
+    it.row = item / p.nsplit;
+    it.split = item % p.nsplit;
+    it.batch = p.prefill ? 0 : it.row;
+    it.slot0 = it.split * p.split_len;
+    it.slot_end = min(p.top_k, it.slot0 + p.split_len);
+    it.bound = p.kv_len ? min(__ldg(p.kv_len + it.batch), p.Nmax) : p.Nmax;
+    return it;
+}
+
+__device__ __forceinline__ int nth_item(const AttnShape& p, int s) {
+    int base = s * (int)gridDim.x;
+    if (base >= p.n_items) return -1;
+    int k = (s & 1) ? ((int)gridDim.x - 1 - (int)blockIdx.x) : (int)blockIdx.x;
+    int item = base + k;
+    return item < p.n_items ? item : -2;
+}
+
+// Number of 128-slot tiles up to the last non-negative index of the item's
+// slot range (warp-collective; every lane gets the same answer).  A full
+// selection ends with a valid index, so the last 32 slots are looked at first;
+// otherwise (a query with fewer causal keys than top_k: a valid prefix, then
+// -1) the range is scanned backwards 512 slots a round, 16 independent loads a
+// lane, so that a short item costs a few L2 round trips rather than one per 32
+// slots.
+__device__ __forceinline__ int item_tiles(const AttnShape& p, const Item& I, uint32_t lane) {
+    const int32_t* ir = p.idx + (int64_t)I.row * p.top_k;
+    int hi = I.slot_end - 32;   // slots [hi, slot_end) first
+    {
+        const int s = hi + (int)lane;
+        const bool v = (s >= I.slot0) && (s < I.slot_end) && (__ldg(ir + s) >= 0);
+        const uint32_t m = __ballot_sync(0xffffffffu, v);
+        if (m) return (hi + 31 - __clz(m) - I.slot0) / kTile + 1;
+    }
+    for (; hi > I.slot0; hi -= 512) {   // slots [max(slot0, hi - 512), hi)
+        const int lo = hi - 512;
+        int last = -1;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const int s = lo + 32 * k + (int)lane;
+            if (s >= I.slot0 && s < hi && __ldg(ir + s) >= 0) last = s;
+        }
+        last = __reduce_max_sync(0xffffffffu, last);
+        if (last >= 0) return (last - I.slot0) / kTile + 1;
+    }
+    return 0;
+}
+
+// Transposing butterfly over a warp: on entry every lane holds 16 values (one
+// per head of the warp's head group); on exit lanes 2i and 2i+1 hold the
+// warp-wide reduction for head i of the group.
+template <bool MAX>
+__device__ __forceinline__ float warp_transpose_reduce16(const float (&x)[16], uint32_t lane) {
+    float a[8];
+    {
+        const bool up = lane & 16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float mine = up ? x[8 + k] : x[k];
+            const float other = up ? x[k] : x[8 + k];
+            const float recv = __shfl_xor_sync(0xffffffffu, other, 16);
+            a[k] = MAX ? fmaxf(mine, recv) : mine + recv;
+        }
+    }
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {
+        const int half = 4 >> step;   // 4, 2, 1 values kept
+        const int off = 8 >> step;    // shuffle distance 8, 4, 2
+        const bool up = lane & off;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k < half) {
+                const float mine = up ? a[half + k] : a[k];
+                const float other = up ? a[k] : a[half + k];
+                const float recv = __shfl_xor_sync(0xffffffffu, other, off);
+                a[k] = MAX ? fmaxf(mine, recv) : mine + recv;
+            }
+        }
+    }
+    const float o = __shfl_xor_sync(0xffffffffu, a[0], 1);
+    return MAX ? fmaxf(a[0], o) : a[0] + o;
+}
+
+}  // namespace dsa
