@@ -112,6 +112,26 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, v
     }
 }
 
+// The same contract with the limit in SM clocks: reading the global timer once per wait, as the two
+// above do, can outlast the wait itself.  SPIN polls with test_wait, else the thread may be suspended.
+constexpr long long kWaitLimitClocks = 4000000000ll;  // about 2 s
+template <bool SPIN>
+__device__ __forceinline__ bool mbar_wait_clk(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+    if (SPIN ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (SPIN ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if ((it & 63u) == 0) {
+            if (*abort) return false;
+            if (clock64() - t0 > kWaitLimitClocks) {
+                *abort = 1;
+                raise_dev_error(status, DEV_ERR_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
 // ---------------------------------------------------------------- grid dependencies
 // Wait until the previous kernel on the stream has completed and its memory is
 // visible (returns at once when the launch had no programmatic dependency).
@@ -358,6 +378,17 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn, b
 __host__ __device__ constexpr uint32_t idesc_e4m3_scaled_f32(int M, int N, bool a_mn, bool b_mn) {
     return ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
            (static_cast<uint32_t>(M >> 7) << 27);
+}
+
+// Register budget of the calling warpgroup (all four warps; inc waits until the CTA's own released
+// registers suffice).
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ uint32_t lane_id() {

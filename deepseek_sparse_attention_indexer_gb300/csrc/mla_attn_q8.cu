@@ -45,39 +45,49 @@ namespace {
 
 constexpr int kBlk = 128 * 128;                    // 16 KB: 128 rows of 128 bytes
 constexpr int kChunks = kQ8Latent / 128;           // 4 latent chunks of 128 dims a tile
-constexpr int kRing = 7;                           // chunk slots
-constexpr int kWorkerWarps = 16;
-constexpr int kWorkers = kWorkerWarps * 32;
+constexpr int kStages = 2;                         // tiles in shared memory
+constexpr int kRopeHalf = 128 * 64;                // 8 KB: 128 rows of 32 rope dims
 constexpr int kPvIssuers = 2;
-constexpr int kFirstWorker = 1 + kPvIssuers;       // warp 0 QK, warps 1-2 PV, warps 3.. workers
-constexpr int kThreads = 32 * kFirstWorker + kWorkers;
-constexpr int kMaxRegs = 96;                       // 19 warps: 5 share one 16K-register sub-partition
+constexpr int kGatherWarps = 8;                    // rows and query
+constexpr int kWorkerWarps = 16;                   // softmax and output
+constexpr int kWorkers = kWorkerWarps * 32;
+// warp 0 QK, warps 1-2 PV, warp 3 none; warps 4-11 gather; warps 12-27 workers.  The register split is by
+// warpgroups of four warps out of what the launch holds: 896 threads of 72 registers.
+constexpr int kFirstGather = 4;
+constexpr int kFirstWorker = kFirstGather + kGatherWarps;
+constexpr int kThreads = 32 * (kFirstWorker + kWorkerWarps);
+constexpr int kLaunchRegs = 72, kIssueRegs = 56, kGatherRegs = 64, kWorkerRegs = 80;
+static_assert(kThreads * kLaunchRegs >=
+                  32 * (kFirstGather * kIssueRegs + kGatherWarps * kGatherRegs + kWorkerWarps * kWorkerRegs),
+              "registers of the CTA");
+constexpr int kRowsPerWarp = kTile / kGatherWarps; // 16 rows of a tile, 8 query heads a gather warp
 constexpr int kHG = kH / (kWorkerWarps / 4);       // 16 heads a worker warp
 constexpr int kGroupThreads = 4 * 32;              // the four warps sharing a head group
-static_assert(kHG == 16 && kWorkerWarps == 16, "a worker warp: 16 heads, 8 rows of a tile, 4 query heads");
+constexpr uint32_t kGatherBar = 7;                 // named barriers: 1, 2 workers, 3-6 head groups, 7 gather
+static_assert(kHG == 16 && kWorkerWarps == 16, "warp_transpose_reduce16 takes a head group of 16");
 
 constexpr float kFirstTop = 5.5f;                  // log2 of the first tile's largest P'
 constexpr float kMostTop = 8.75f;                  // log2 of the largest P' (430 <= 448)
 constexpr float kNoRef = 3.0e38f;                  // -m before the reference is set (finite: see mla_attn.cu)
 
-// smem layout (1024-aligned base)
+// smem layout
 constexpr int OFF_QHL = 0;                         // 4 chunks x (64 hi rows, 64 lo rows) x 128 B
-constexpr int OFF_QR = OFF_QHL + kChunks * kBlk;   // 64 heads x 64 bf16
-constexpr int OFF_LAT = OFF_QR + kH * 128;         // ring of latent chunks
-constexpr int OFF_ROPE = OFF_LAT + kRing * kBlk;   // 128 keys x 64 bf16
-constexpr int OFF_P = OFF_ROPE + kBlk;             // 128 keys x (64 hi | 64 lo)
-constexpr int OFF_SC = OFF_P + kBlk;               // float [2][128]: scales of the tile's rows, 0 = no key
-constexpr int OFF_QS = OFF_SC + 2 * kTile * 4;     // float [2][64]: scale * log2(e) * 2^k of the query's heads
-constexpr int OFF_RED = OFF_QS + 2 * kH * 4;       // float [4][64]
+constexpr int OFF_QR = OFF_QHL + kChunks * kBlk;   // rope dims of 64 heads: two halves of 64 rows x 64 B
+constexpr int OFF_LAT = OFF_QR + kH * 128;         // 2 tiles x 4 latent chunks
+constexpr int OFF_ROPE = OFF_LAT + kStages * kChunks * kBlk;   // half of a tile's rope dims
+constexpr int OFF_P = OFF_ROPE + kRopeHalf;        // 128 keys x (64 hi | 64 lo)
+constexpr int OFF_SC = OFF_P + kBlk;               // float [128]: scales of the tile's rows, 0 = no key
+constexpr int OFF_QS = OFF_SC + kTile * 4;         // float [3][64]: scale * log2(e) * 2^k of a query's heads
+constexpr int OFF_RED = OFF_QS + 3 * kH * 4;       // float [4][64]
 constexpr int OFF_MNEG = OFF_RED + 4 * kH * 4;     // float [64]: minus the references
-constexpr int OFF_ALPHA = OFF_MNEG + kH * 4;       // float [64]
-constexpr int OFF_INVL = OFF_ALPHA + kH * 4;       // float [64]
-constexpr int OFF_BAR = OFF_INVL + kH * 4;
-// barriers: full[7], free[7], rope_full, s_full, s_free, p_full, q_full
-constexpr int kBars = 2 * kRing + 5;
+constexpr int OFF_ALPHA = OFF_MNEG + kH * 4;       // float [64]: rescale factors; at an item's end 1 / l
+constexpr int OFF_BAR = OFF_ALPHA + kH * 4;
+// barriers: full[8], free[8], rope_full, rope_free, s_full, s_free, p_full, q_full
+constexpr int kSlots = kStages * kChunks;
+constexpr int kBars = 2 * kSlots + 6;
 constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
-constexpr int kSmemBytes = OFF_ABORT + 4 + 1024;
+constexpr int kSmemBytes = OFF_ABORT + 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
 constexpr uint32_t kTmemCols = 512;
@@ -87,6 +97,10 @@ constexpr uint32_t TM_O = 192;                     // O^T chunk c at TM_O + 64 c
 constexpr uint32_t TM_ONE = 448;                   // scale bytes 2^0
 constexpr uint32_t TM_LO = 464;                    // scale bytes 2^-4
 
+// Operands: 128-byte swizzle, 8-row groups 1 KB apart.  The descriptors' high words are the same; the
+// low words (address, leading offset) are sums that stay below the address field's end (see sdesc).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescHiRope = (512u >> 4) | (1u << 14) | (4u << 29);   // rope halves: 64-byte rows and swizzle
 constexpr uint32_t IDESC_QK = idesc_e4m3_f32(128, 128, false, false);
 constexpr uint32_t IDESC_ROPE = idesc_bf16_f32(128, 64, false, false);
 constexpr uint32_t IDESC_PV = idesc_e4m3_scaled_f32(128, 64, true, true);
@@ -130,24 +144,48 @@ __device__ __forceinline__ uint32_t split_e4m3x2(float x, float y) {
 __device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
+// Transposes over groups of G lanes.  Lane j of a group holds N words (N / G to each lane of the group, in
+// order); afterwards word i * (N / G) + k is word j * (N / G) + k of the group's lane i.
+template <int N, int G>
+__device__ __forceinline__ void transpose_words(uint32_t (&v)[N], uint32_t lane) {
+    constexpr int K = N / G;
+#pragma unroll
+    for (int s = G / 2; s; s >>= 1) {        // swap the off-diagonal halves of every 2s x 2s block
+        const bool up = lane & s;
+#pragma unroll
+        for (int b = 0; b < G; ++b) {
+            if (b & s) continue;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                uint32_t &lo = v[b * K + k], &hi = v[(b + s) * K + k];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
+                if (up) lo = got; else hi = got;
+            }
+        }
+    }
+}
+
 template <bool PARTIAL>
-__global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
-    mla_attn_q8_kernel(const AttnQ8Params p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+__global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const AttnQ8Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {   // the operands' swizzle counts from 1 KB boundaries; there is no room to round up
+        if (threadIdx.x == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
+        return;
+    }
     float* sc_s = reinterpret_cast<float*>(smem + OFF_SC);
     float* qs_s = reinterpret_cast<float*>(smem + OFF_QS);
     float* red = reinterpret_cast<float*>(smem + OFF_RED);
     float* m_neg = reinterpret_cast<float*>(smem + OFF_MNEG);
     float* alpha_s = reinterpret_cast<float*>(smem + OFF_ALPHA);
-    float* invl_s = reinterpret_cast<float*>(smem + OFF_INVL);
+    float* invl_s = alpha_s;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-    uint64_t* freed = full + kRing;
-    uint64_t* rope_full = freed + kRing;
-    uint64_t* s_full = rope_full + 1;
-    uint64_t* s_free = rope_full + 2;
-    uint64_t* p_full = rope_full + 3;
-    uint64_t* q_full = rope_full + 4;
+    uint64_t* freed = full + kSlots;
+    uint64_t* rope_full = freed + kSlots;
+    uint64_t* rope_free = rope_full + 1;
+    uint64_t* s_full = rope_full + 2;
+    uint64_t* s_free = rope_full + 3;
+    uint64_t* p_full = rope_full + 4;
+    uint64_t* q_full = rope_full + 5;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
 
@@ -155,15 +193,16 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
     const uint32_t lane = lane_id();
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRing; ++i) {
-            mbar_init(&full[i], kWorkers);      // one cp.async arrival per worker thread
-            mbar_init(&freed[i], 1);            // the commit of the PV issuer that consumed the chunk
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&full[i], kGatherWarps * 32);   // one cp.async arrival per gather thread
+            mbar_init(&freed[i], 1);                  // the commit of the PV issuer that consumed the chunk
         }
-        mbar_init(rope_full, kWorkers);
-        mbar_init(s_full, 1);
+        mbar_init(rope_full, kGatherWarps * 32);
+        mbar_init(rope_free, 1);
+        mbar_init(s_full, 2);                   // the QK issuer: its commit, and that it has seen the rows' scales
         mbar_init(s_free, kWorkerWarps);
         mbar_init(p_full, kWorkerWarps);
-        mbar_init(q_full, kWorkerWarps);
+        mbar_init(q_full, kGatherWarps);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -191,7 +230,8 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
     tc_fence_after();
     griddep_wait();                 // inputs and outputs may belong to the previous kernel until here
 
-    // Chunk n = 4 g + c of the CTA's g-th tile lies in slot n % 7; its slot's barriers are in use n / 7.
+    // Chunk c of the CTA's g-th tile lies in slot 4 (g % 2) + c; the slot's barriers are in their use g / 2.
+    if (warp < kFirstGather) setmaxnreg_dec<kIssueRegs>();
     if (warp == 0) {
         // ------------------------------------------------------------ QK issuer
         int gt = 0, qi = 0;
@@ -204,34 +244,35 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
             const int T = item_tiles(p, I, lane);
             if (T == 0) continue;
             if (lane == 0) {
-                const uint64_t lat = sdesc_sw128(smem_u32(smem + OFF_LAT), 16, 1024);
-                const uint64_t qhl = sdesc_sw128(smem_u32(smem + OFF_QHL), 16, 1024);
-                const uint64_t rope = sdesc_sw128(smem_u32(smem + OFF_ROPE), 16, 1024);
-                const uint64_t qr = sdesc_sw128(smem_u32(smem + OFF_QR), 16, 1024);
-                ok = mbar_wait_spin(q_full, qi & 1, abort_flag, p.status);
+                const uint32_t base = (smem_u32(smem) >> 4) | ((16u >> 4) << 16);   // leading offset: one atom wide
+                ok = mbar_wait_clk<true>(q_full, qi & 1, abort_flag, p.status);
                 for (int t = 0; ok && t < T; ++t, ++gt) {
                     // the workers have read the previous tile's S^T
-                    if (!(ok = mbar_wait_spin(s_free, (gt & 1) ^ 1, abort_flag, p.status))) break;
+                    if (!(ok = mbar_wait_clk<true>(s_free, (gt & 1) ^ 1, abort_flag, p.status))) break;
                     tc_fence_after();
+                    const uint32_t lat = base + (OFF_LAT >> 4) + (gt & 1) * (kChunks * kBlk >> 4);
+                    // first half of the rope dims; the second half takes its place while the chunks run
 #pragma unroll
-                    for (int j = 0; j < 5; ++j) {   // chunks 0, 1, 2, the rope block, chunk 3 (its copy comes last)
-                        if (j == 3) {
-                            if (!(ok = mbar_wait_spin(rope_full, gt & 1, abort_flag, p.status))) break;
+                    for (int j = 0; j < 2 + kChunks; ++j) {
+                        if (j == 0 || j == 1 + kChunks) {
+                            const int half = j ? 1 : 0;
+                            if (!(ok = mbar_wait_clk<true>(rope_full, half, abort_flag, p.status))) break;
+                            if (half) mbar_arrive(s_full);
                             fence_proxy_async_smem();
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16_ss_lo(tmem_base + TM_R, (uint32_t)rope + 2 * kk, (uint32_t)(rope >> 32),
-                                               (uint32_t)qr + 2 * kk, (uint32_t)(qr >> 32), IDESC_ROPE, kk ? 1u : 0u);
+                            for (int kk = 0; kk < 2; ++kk)
+                                mma_bf16_ss_lo(tmem_base + TM_R, base + (OFF_ROPE >> 4) + 2 * kk, kDescHiRope,
+                                               base + ((OFF_QR + half * kH * 64) >> 4) + 2 * kk, kDescHiRope, IDESC_ROPE,
+                                               (half | kk) ? 1u : 0u);
+                            if (!half) mma_commit(rope_free);
                         } else {
-                            const int c = j < 3 ? j : 3;
-                            const uint32_t n = 4u * (uint32_t)gt + (uint32_t)c, slot = n % kRing;
-                            if (!(ok = mbar_wait_spin(&full[slot], (n / kRing) & 1, abort_flag, p.status))) break;
+                            const int c = j - 1;
+                            if (!(ok = mbar_wait_clk<true>(&full[4 * (gt & 1) + c], (gt >> 1) & 1, abort_flag, p.status))) break;
                             fence_proxy_async_smem();
-                            const uint32_t a = (uint32_t)lat + slot * (kBlk >> 4);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)   // 32 dims a step
-                                mma_e4m3_ss_lo(tmem_base + TM_S, a + 2 * kk, (uint32_t)(lat >> 32),
-                                               (uint32_t)qhl + c * (kBlk >> 4) + 2 * kk, (uint32_t)(qhl >> 32), IDESC_QK,
+                                mma_e4m3_ss_lo(tmem_base + TM_S, lat + c * (kBlk >> 4) + 2 * kk, kDescHi,
+                                               base + (OFF_QHL >> 4) + c * (kBlk >> 4) + 2 * kk, kDescHi, IDESC_QK,
                                                (c | kk) ? 1u : 0u);
                         }
                     }
@@ -255,24 +296,22 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
             if (lane == 0) {
                 // A = V^T MN-major: 128 dims a row, 8-key groups 1 KB apart; B = P^T MN-major, hi at byte 0 of a
                 // row, lo at byte 64
-                const uint64_t lat = sdesc_sw128(smem_u32(smem + OFF_LAT), kBlk, 1024);
-                const uint64_t pt = sdesc_sw128(smem_u32(smem + OFF_P), kBlk, 1024);
+                const uint32_t base = (smem_u32(smem) >> 4) | ((uint32_t)(kBlk >> 4) << 16);
                 for (int t = 0; ok && t < T; ++t, ++gt) {
-                    if (!(ok = mbar_wait_spin(p_full, gt & 1, abort_flag, p.status))) break;
+                    if (!(ok = mbar_wait_clk<true>(p_full, gt & 1, abort_flag, p.status))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int c = iss + 2 * j;
-                        const uint32_t slot = (4u * (uint32_t)gt + (uint32_t)c) % kRing;
-                        const uint32_t a = (uint32_t)lat + slot * (kBlk >> 4);
+                        const uint32_t slot = 4u * (uint32_t)(gt & 1) + (uint32_t)c;
+                        const uint32_t a = base + (OFF_LAT >> 4) + slot * (kBlk >> 4);
                         const uint32_t d = tmem_base + TM_O + 64 * (uint32_t)c;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {     // 32 keys (four 8-key groups, 4 KB) a step
-                            mma_e4m3_scaled_ss_lo(d, a + kk * (4096 >> 4), (uint32_t)(lat >> 32),
-                                                  (uint32_t)pt + kk * (4096 >> 4), (uint32_t)(pt >> 32), IDESC_PV,
+                            const uint32_t b = base + (OFF_P >> 4) + kk * (4096 >> 4);
+                            mma_e4m3_scaled_ss_lo(d, a + kk * (4096 >> 4), kDescHi, b, kDescHi, IDESC_PV,
                                                   tmem_base + TM_ONE, tmem_base + TM_ONE, (t | kk) ? 1u : 0u);
-                            mma_e4m3_scaled_ss_lo(d, a + kk * (4096 >> 4), (uint32_t)(lat >> 32),
-                                                  (uint32_t)pt + kk * (4096 >> 4) + (64 >> 4), (uint32_t)(pt >> 32), IDESC_PV,
+                            mma_e4m3_scaled_ss_lo(d, a + kk * (4096 >> 4), kDescHi, b + (64 >> 4), kDescHi, IDESC_PV,
                                                   tmem_base + TM_ONE, tmem_base + TM_LO, 1u);
                         }
                         mma_commit(&freed[slot]);
@@ -281,114 +320,111 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
             }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
-    } else {
-        // ------------------------------------------------------------ workers
-        const int ww = warp - kFirstWorker;       // 0..15
-        const int quad = warp & 3;                // TMEM lane quadrant this warp may access
-        const int hg = ww >> 2;                   // head group: heads h0 .. h0 + 15
-        const int h0 = hg * kHG;
-        const uint32_t group_bar = 3 + (uint32_t)hg;
-        const int tid = ww * 32 + (int)lane;      // 0..511
-        const int key = quad * 32 + (int)lane;    // TMEM lane == key row of the tile == dim row of O^T
-        const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+    } else if (warp >= kFirstGather && warp < kFirstWorker) {
+        // ------------------------------------------------------------ gather
+        setmaxnreg_dec<kGatherRegs>();
+        const int gw = warp - kFirstGather;       // 0..7: rows 16 gw .. 16 gw + 15 of a tile, query heads 8 gw ..
         const uint32_t smem_base = smem_u32(smem);
+        // One thread polls, a named barrier releases the eight warps.  (A thread suspended in try_wait was seen
+        // to resume 800 to 3400 cycles after the phase had completed; threads that all poll take the issue slots
+        // of the softmax.)  The answer is the same in every warp: all leave together when a wait gives up.
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-            return mbar_wait(bar, parity, abort_flag, p.status);
+            bool ok = true;
+            if (threadIdx.x == 32 * kFirstGather) ok = mbar_wait_clk<true>(bar, parity, abort_flag, p.status);
+            return named_bar_and(kGatherBar, kGatherWarps * 32, ok);
         };
-        auto chunk_free = [&](uint32_t n) -> bool {   // PV has consumed chunk n
-            return wait(&freed[n % kRing], (n / kRing) & 1);
-        };
-        auto pv_done = [&](int g) -> bool { return chunk_free(4u * g + 2) && chunk_free(4u * g + 3); };
-
-        // ---- gather.  The warp copies rows 64 h + 4 ww + i (h < 2, i < 4) of every tile; lanes 0..7 carry
-        // row 4 h + i of them through three stages: the selected key (fetch), its cache row (resolve: a page
-        // lookup when paged), the copies.  Each stage runs one tile ahead of the next, so that its loads
-        // are in flight during a softmax.
-        int f_s = 0, f_t = 0, f_T = 0;            // fetch cursor: next tile to fetch
-        Item fI{};
-        bool f_open = true;
-        auto fetch = [&](int& j, int& batch, int& bound) -> bool {   // false: no more tiles
-            while (f_open && f_t >= f_T) {
+        // Lanes 0..15 carry their row through three stages: the selected key (fetch), its cache row (resolve: a
+        // page lookup when paged), the copies.  Each stage runs one tile ahead of the next, so that its loads
+        // are in flight during the copies of the tile before.
+        int f_s = 0, f_T = 0;                     // next item of the CTA; tiles of the current one still to fetch
+        const int32_t* f_idx = p.idx;             // this lane's next slot, and how many slots are left from it on
+        int f_left = 0, f_batch = 0, f_bound = 0;
+        int f_key = -1, f_first = -1;             // the fetched tile's key; its query when it is an item's first tile
+        auto fetch = [&]() -> bool {
+            f_first = -1;
+            while (f_T == 0) {
                 const int it = nth_item(p, f_s++);
-                if (it == -1) {
-                    f_open = false;
-                } else if (it >= 0) {
-                    fI = decode_item(p, it);
-                    f_T = item_tiles(p, fI, lane);
-                    f_t = 0;
-                }
+                if (it == -1) return false;
+                if (it < 0) continue;
+                const Item I = decode_item(p, it);
+                f_T = item_tiles(p, I, lane);
+                f_idx = p.idx + (int64_t)I.row * p.top_k + I.slot0 + kRowsPerWarp * gw + (int)lane;
+                f_left = lane < kRowsPerWarp ? I.slot_end - I.slot0 - kRowsPerWarp * gw - (int)lane : 0;
+                f_batch = I.batch;
+                f_bound = I.bound;
+                f_first = I.row;
+                if (lane == 0)                    // the warp's heads of the query, into L2
+                    l2_prefetch_bulk(p.q + ((int64_t)I.row * kH + kH / kGatherWarps * gw) * DSA_QK_DIM,
+                                     kH / kGatherWarps * DSA_QK_DIM * 2);
             }
-            if (!f_open) return false;
-            const int slot = fI.slot0 + f_t * kTile + 64 * (int)(lane >> 2) + 4 * ww + (int)(lane & 3);
-            j = (lane < 8 && slot < fI.slot_end) ? __ldg(p.idx + (int64_t)fI.row * p.top_k + slot) : -1;
-            batch = fI.batch;
-            bound = fI.bound;
-            ++f_t;
+            f_key = f_left > 0 ? __ldg(f_idx) : -1;
+            f_idx += kTile;
+            f_left -= kTile;
+            --f_T;
             return true;
         };
-        // cache row of key j; -1: no key, -2: a page outside the pool (a row of zeros)
-        auto resolve = [&](int j, int batch, int bound) -> int {
+        // cache row of the fetched key; -1: no key, -2: a page outside the pool (a row of zeros)
+        auto resolve = [&]() -> int {
+            const int j = f_key;
             if (j < 0) return -1;
-            if (j >= bound) {
+            if (j >= f_bound) {
                 raise_dev_error(p.status, DEV_ERR_BOUNDS);
                 return -1;
             }
             if (p.pages.table) {
-                const int row = (int)paged_row(p.pages, batch, j);
+                const int row = (int)paged_row(p.pages, f_batch, j);
                 if (row < 0) raise_dev_error(p.status, DEV_ERR_BOUNDS);
                 return row < 0 ? -2 : row;
             }
-            return (int)((int64_t)batch * p.Nmax + j);
+            return (int)((int64_t)f_batch * p.Nmax + j);
         };
-        const int ci = (int)(lane >> 3);          // the warp's row i of a half this lane copies for
-        const int cc = (int)(lane & 7);           // 16-byte piece of the 128-byte block
-        uint32_t dst_h[2];
+        // One 128-byte block (blk 0..3 latent, 4 rope) of the warp's 16 rows: a warp instruction copies a block of
+        // four different rows, 8 lanes a row.
+        const int ci = (int)(lane >> 3), cc = (int)(lane & 7);
+        const uint32_t dst0 = smem_base + (uint32_t)((kRowsPerWarp * gw + ci) * 128);
+        auto copy_chunk = [&](int row, int g, int c) -> bool {      // chunk c of the CTA's g-th tile
+            const uint32_t slot = 4u * (uint32_t)(g & 1) + (uint32_t)c;
+            if (!wait(&freed[slot], ((g >> 1) & 1) ^ 1)) return false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = 64 * h + 4 * ww + ci;
-            dst_h[h] = (uint32_t)(r * 128 + ((cc ^ (r & 7)) << 4));
-        }
-        // one 128-byte block (blk 0..3 latent, 4 rope) of the warp's 8 rows, row8 held by lanes 0..7
-        auto copy_block = [&](int row8, int blk, uint32_t dst) {
+            for (int i = 0; i < kRowsPerWarp / 4; ++i) {
+                const int r = __shfl_sync(0xffffffffu, row, 4 * i + ci);
+                cp_async_16(dst0 + OFF_LAT + slot * kBlk + i * 512 + ((cc ^ (4 * (i & 1) + ci)) << 4),
+                            p.cache + (r < 0 ? 0 : (int64_t)r * kQ8Row + c * 128 + cc * 16), r < 0 ? 0u : 16u);
+            }
+            cp_async_arrive_noinc(&full[slot]);
+            return true;
+        };
+        // half of the rope dims: 64-byte rows, 4 lanes a row, 8 rows a warp instruction
+        auto copy_rope = [&](int row, int half) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = __shfl_sync(0xffffffffu, row8, 4 * h + ci);
-                cp_async_16(dst + dst_h[h], p.cache + (r < 0 ? 0 : (int64_t)r * kQ8Row + blk * 128 + cc * 16),
-                            r < 0 ? 0u : 16u);
+            for (int i = 0; i < kRowsPerWarp / 8; ++i) {
+                const int tr = 8 * i + (int)(lane >> 2);
+                const int r = __shfl_sync(0xffffffffu, row, tr);
+                const int pc = (int)(lane & 3);
+                cp_async_16(smem_base + OFF_ROPE + (kRowsPerWarp * gw + tr) * 64 + ((pc ^ ((tr >> 1) & 3)) << 4),
+                            p.cache + (r < 0 ? 0 : (int64_t)r * kQ8Row + kQ8Latent + half * 64 + pc * 16), r < 0 ? 0u : 16u);
             }
         };
-        auto copy_chunk = [&](int row8, int g, int c) -> bool {      // chunk c of the CTA's g-th tile
-            const uint32_t n = 4u * (uint32_t)g + (uint32_t)c, slot = n % kRing;
-            const bool ok = __all_sync(0xffffffffu, wait(&freed[slot], ((n / kRing) & 1) ^ 1));
-            if (ok) copy_block(row8, c, smem_base + OFF_LAT + slot * kBlk);
-            if (ok) cp_async_arrive_noinc(&full[slot]);
-            return ok;
+        // Query head h: lane l holds dims 8l.. and 256 + 8l.., and rope dims 2l, 2l + 1.
+        struct Head {
+            uint4 w[2];
+            uint32_t pe;
         };
-        auto copy_rope = [&](int row8, int g) {   // the rope block and the scales: QK of tile g - 1 is complete
-            copy_block(row8, kChunks, smem_base + OFF_ROPE);
-            if (lane < 8) {
-                const int r = 64 * (int)(lane >> 2) + 4 * ww + (int)(lane & 3);
-                cp_async_4(smem_base + OFF_SC + ((g & 1) * kTile + r) * 4,
-                           row8 >= 0 ? p.cache_scale + row8 : &g_unit_scale, row8 == -1 ? 0u : 4u);
-            }
-            cp_async_arrive_noinc(rope_full);
-        };
-
-        // ---- query: the warp converts heads 4 ww .. 4 ww + 3.  Lane l holds dims 8l.. and 256 + 8l.. of a head.
-        auto q_head = [&](int row, int qpar, int i) {
-            const int h = 4 * ww + i;
+        auto load_head = [&](int row, int h) -> Head {
             const __nv_bfloat16* src = p.q + ((int64_t)row * kH + h) * DSA_QK_DIM;
-            uint4 raw[2];
-            raw[0] = ldg_nc_v4(src + 8 * lane);
-            raw[1] = ldg_nc_v4(src + 256 + 8 * lane);
-            const uint32_t pe = __ldg(reinterpret_cast<const uint32_t*>(src + kQ8Latent) + lane);
-            const uint32_t w[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+            Head q;
+            q.w[0] = ldg_nc_v4(src + 8 * lane);
+            q.w[1] = ldg_nc_v4(src + 256 + 8 * lane);
+            q.pe = __ldg(reinterpret_cast<const uint32_t*>(src + kQ8Latent) + lane);
+            return q;
+        };
+        auto convert_head = [&](const Head& q, int qbuf, int h) {
+            const uint32_t w[8] = {q.w[0].x, q.w[0].y, q.w[0].z, q.w[0].w, q.w[1].x, q.w[1].y, q.w[1].z, q.w[1].w};
             float amax = 0.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const int e = e4m3_scale_exponent(amax);
+            // magnitudes compare as their bit patterns do
+            const int e = e4m3_scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
             const float inv = exp2_int(-e);
             const uint32_t swz = (uint32_t)((((lane & 15) >> 1) ^ (h & 7)) << 4) + (lane & 1) * 8;
 #pragma unroll
@@ -400,13 +436,79 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
                 *reinterpret_cast<uint2*>(d) = make_uint2(lows(s[0], s[1]), lows(s[2], s[3]));
                 *reinterpret_cast<uint2*>(d + 64 * 128) = make_uint2(highs(s[0], s[1]), highs(s[2], s[3]));
             }
-            *reinterpret_cast<uint32_t*>(smem + OFF_QR + h * 128 + (((lane >> 2) ^ (h & 7)) << 4) + (lane & 3) * 4) = pe;
-            if (lane == 0) qs_s[qpar * kH + h] = p.scale_log2 * exp2_int(e);
+            *reinterpret_cast<uint32_t*>(smem + OFF_QR + (lane >> 4) * (kH * 64) + h * 64 +
+                                         ((((lane & 15) >> 2) ^ ((h >> 1) & 3)) << 4) + (lane & 3) * 4) = q.pe;
+            if (lane == 0) qs_s[qbuf * kH + h] = p.scale_log2 * exp2_int(e);
         };
-        auto q_ready = [&]() {
-            fence_proxy_async_smem();
+
+        bool has0 = fetch(), has1;                // tile being copied; tile fetched
+        int row0 = has0 ? resolve() : -1, first0 = f_first;
+        has1 = has0 && fetch();
+        int qbuf = 0;
+        for (int g = 0; has0; ++g) {
+            const int row1 = has1 ? resolve() : -1, first1 = f_first;
+            bool ok = true;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) ok = ok && copy_chunk(row0, g, c);
+            // QK of the previous tile is complete: the rope block, and after an item's last tile the query, are free
+            if (ok && g > 0) ok = wait(s_full, (g - 1) & 1);
+            if (!ok) break;
+            copy_rope(row0, 0);
+            cp_async_arrive_noinc(rope_full);
+            if (first0 >= 0) {
+                constexpr int kHeads = kH / kGatherWarps;
+                Head q = load_head(first0, kHeads * gw);
+#pragma unroll 1
+                for (int i = 0; i < kHeads; ++i) {
+                    const Head next = load_head(first0, kHeads * gw + min(i + 1, kHeads - 1));
+                    convert_head(q, qbuf, kHeads * gw + i);
+                    q = next;
+                }
+                qbuf = qbuf == 2 ? 0 : qbuf + 1;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_full);
+            }
+            // the first half is consumed: QK of this tile has begun, so the workers have read the scales before
+            if (!wait(rope_free, g & 1)) break;
+            copy_rope(row0, 1);
+            if (lane < kRowsPerWarp)
+                cp_async_4(smem_base + OFF_SC + (kRowsPerWarp * gw + lane) * 4,
+                           row0 >= 0 ? p.cache_scale + row0 : &g_unit_scale, row0 == -1 ? 0u : 4u);
+            cp_async_arrive_noinc(rope_full);
+            row0 = row1;
+            has0 = has1;
+            first0 = first1;
+            has1 = has1 && fetch();
+        }
+        cp_async_wait_all();
+    } else if (warp >= kFirstWorker) {
+        // ------------------------------------------------------------ workers
+        setmaxnreg_inc<kWorkerRegs>();
+        const int ww = warp - kFirstWorker;       // 0..15
+        const int quad = warp & 3;                // TMEM lane quadrant this warp may access
+        const int hg = ww >> 2;                   // head group: heads h0 .. h0 + 15
+        const int h0 = hg * kHG;
+        const uint32_t group_bar = 3 + (uint32_t)hg;
+        const int tid = ww * 32 + (int)lane;      // 0..511
+        const int key = quad * 32 + (int)lane;    // TMEM lane == key row of the tile == dim row of O^T
+        const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+        // Spinning waits, as in the gather: of one thread for all workers (the answer is common), or of one lane for
+        // its warp.
+        auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+            bool ok = true;
+            if (tid == 0) ok = mbar_wait_clk<true>(bar, parity, abort_flag, p.status);
+            return named_bar_and(1, kWorkers, ok);
+        };
+        auto pv_done = [&](int g) -> bool {           // both PV issuers' last chunk of tile g is consumed
+            bool ok = true;
+            if (lane == 0) {
+                const uint32_t par = (g >> 1) & 1;
+                ok = mbar_wait_clk<true>(&freed[4 * (g & 1) + 2], par, abort_flag, p.status) &&
+                     mbar_wait_clk<true>(&freed[4 * (g & 1) + 3], par, abort_flag, p.status);
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
+            return ok;
         };
 
         // ---- items.  One without a selected key gets zeros and lse = -inf here.
@@ -441,41 +543,14 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
             }
         };
 
-        // ---- prologue: tile 0 whole, chunks 0-2 of tile 1, the query of the first item.  `gok` is this thread's
-        // wait status: a wait that gives up does not change the control flow inside an item (all workers keep
-        // meeting the same named barriers); the consensus barrier at the item's end takes all out together.
+        // `gok` is the thread's wait status: a wait that gives up does not change the control flow inside an item
+        // (all workers keep meeting the same named barriers); the consensus barrier at the item's end takes all
+        // out together.
         bool gok = true;
-        int fj, fb, fl;                           // fetched: key, batch, bound of the tile three ahead
-        int rowA, rowR = -1;                      // rows of the next tile to copy whole, of the one after it
-        bool hasA, hasR, hasF;
-        hasA = fetch(fj, fb, fl);
-        {
-            int j1, b1, l1;
-            hasR = fetch(j1, b1, l1);
-            rowA = hasA ? resolve(fj, fb, fl) : -1;
-            if (hasA) {
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) gok = copy_chunk(rowA, 0, c) && gok;
-                copy_rope(rowA, 0);
-            }
-            rowA = hasR ? resolve(j1, b1, l1) : -1;
-            hasA = hasR;
-            if (hasA)
-#pragma unroll
-                for (int c = 0; c < 3; ++c) gok = copy_chunk(rowA, 1, c) && gok;
-        }
-        hasR = fetch(fj, fb, fl);
-        rowR = hasR ? resolve(fj, fb, fl) : -1;
-        hasF = fetch(fj, fb, fl);
         bool more = next_item();
-        if (more) {
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) q_head(nI.row, 0, i);
-            q_ready();
-        }
         bool failed = false;
         int gt = 0;                               // tiles done by this CTA
-        int qpar = 0;                             // parity of the item's query scales
+        int qbuf = 0;                             // the item's query scales
         while (more && !failed) {
             const Item I = nI;
             const int T = nT;
@@ -487,12 +562,10 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
             for (int i = 0; i < kHG / 2; ++i) l2[i] = make_float2(0.f, 0.f);
             named_bar_sync(1, kWorkers);
             for (int t = 0; t < T; ++t, ++gt) {
-                gok = gok && wait(s_full, gt & 1);
-                gok = gok && wait(rope_full, gt & 1);   // complete (QK needed it): makes the scales visible here
+                gok = wait_all(s_full, gt & 1) && gok;
                 tc_fence_after();
-                if (hasA && __all_sync(0xffffffffu, gok)) copy_rope(rowA, gt + 1);
                 float2 t2[kHG / 2];               // log2(e) s + log2(c): the exponents before the reference
-                const float c = sc_s[(gt & 1) * kTile + key];
+                const float c = sc_s[key];
                 {
                     uint32_t hi[kHG], lo[kHG], ro[kHG];
                     tmem_ld16(tmem_base + lane_addr + TM_S + h0, hi);
@@ -511,7 +584,7 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
                         const float2 a = make_float2(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]));
                         const float2 b = make_float2(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]));
                         const float2 r = make_float2(__uint_as_float(ro[2 * i]), __uint_as_float(ro[2 * i + 1]));
-                        const float2 qs = reinterpret_cast<const float2*>(qs_s + qpar * kH + h0)[i];
+                        const float2 qs = reinterpret_cast<const float2*>(qs_s + qbuf * kH + h0)[i];
                         t2[i] = __ffma2_rn(__ffma2_rn(b, sixteenth, a), __fmul2_rn(qs, c2), __ffma2_rn(r, sl2, lc2));
                     }
                 }
@@ -600,26 +673,8 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
-                // copies of chunk 3 of the next tile and chunks 0-2 of the one after it, as PV frees their slots;
-                // after an item's last tile its QK is complete: the next query is converted between them
-                const bool conv = more && t == T - 1;
-#pragma unroll
-                for (int k = 0; k < kChunks; ++k) {
-                    if (conv) q_head(nI.row, qpar ^ 1, k);
-                    if (k == 0) {
-                        if (hasA) gok = copy_chunk(rowA, gt + 1, 3) && gok;
-                    } else if (hasR) {
-                        gok = copy_chunk(rowR, gt + 2, k - 1) && gok;
-                    }
-                }
-                if (conv) q_ready();
-                rowA = rowR;
-                hasA = hasR;
-                rowR = hasF ? resolve(fj, fb, fl) : -1;
-                hasR = hasF;
-                if (hasF) hasF = fetch(fj, fb, fl);
             }
-            qpar ^= 1;
+            qbuf = qbuf == 2 ? 0 : qbuf + 1;
             // ---------------- final: l = sum of partial row sums; out = O^T / l
             {
                 float l_part[kHG];
@@ -643,32 +698,39 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
                 store_lse(I, tid, (l > 0.f) ? (log2f(l) - m_neg[tid]) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l));
             }
             named_bar_sync(1, kWorkers);
+            // A lane holds one dim of 16 heads; the lanes of a group exchange them so that each stores 16
+            // contiguous bytes of a head (with a store of one element a lane an item's output took 5 us).
 #pragma unroll 1
             for (int ch = 0; ch < kChunks; ++ch) {
                 uint32_t v[kHG];
                 tmem_ld16(tmem_base + lane_addr + TM_O + 64 * ch + h0, v);
                 tmem_ld_wait();
-                float o[kHG];
 #pragma unroll
-                for (int h = 0; h < kHG; ++h) o[h] = __uint_as_float(v[h]) * invl_s[h0 + h];
-                const int dim = ch * 128 + key;
-                if (PARTIAL) {
-                    float* dst = p.part_o + (((int64_t)I.row * p.nsplit + I.split) * kH + h0) * kDv + dim;
+                for (int h = 0; h < kHG; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * invl_s[h0 + h]);
+                const int dim0 = ch * 128 + quad * 32;
+                if (PARTIAL || p.out_f32) {       // groups of 4 lanes: lane j gets heads 4j.. of the group's 4 dims
+                    float* base = PARTIAL ? p.part_o + (((int64_t)I.row * p.nsplit + I.split) * kH + h0) * kDv
+                                          : static_cast<float*>(p.out) + ((int64_t)I.row * kH + h0) * kDv;
+                    transpose_words<16, 4>(v, lane);
+                    float* dst = base + (int)(lane & 3) * 4 * kDv + dim0 + (int)(lane & ~3u);
 #pragma unroll
-                    for (int h = 0; h < kHG; ++h) dst[h * kDv] = o[h];
-                } else if (p.out_f32) {
-                    float* dst = static_cast<float*>(p.out) + ((int64_t)I.row * kH + h0) * kDv + dim;
+                    for (int h = 0; h < 4; ++h)
+                        *reinterpret_cast<uint4*>(dst + h * kDv) = make_uint4(v[h], v[4 + h], v[8 + h], v[12 + h]);
+                } else {                          // groups of 8 lanes: lane j gets heads 2j, 2j + 1 of the group's 8 dims
+                    uint32_t w[8];
 #pragma unroll
-                    for (int h = 0; h < kHG; ++h) dst[h * kDv] = o[h];
-                } else {
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)I.row * kH + h0) * kDv + dim;
-#pragma unroll
-                    for (int h = 0; h < kHG; ++h) dst[h * kDv] = __float2bfloat16_rn(o[h]);
+                    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    transpose_words<8, 8>(w, lane);
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
+                                         ((int64_t)I.row * kH + h0 + (int)(lane & 7) * 2) * kDv + dim0 + (int)(lane & ~7u);
+                    *reinterpret_cast<uint4*>(dst) =
+                        make_uint4(lows(w[0], w[1]), lows(w[2], w[3]), lows(w[4], w[5]), lows(w[6], w[7]));
+                    *reinterpret_cast<uint4*>(dst + kDv) =
+                        make_uint4(highs(w[0], w[1]), highs(w[2], w[3]), highs(w[4], w[5]), highs(w[6], w[7]));
                 }
             }
             tc_fence_before();
         }
-        cp_async_wait_all();
     }
 
     tc_fence_before();
