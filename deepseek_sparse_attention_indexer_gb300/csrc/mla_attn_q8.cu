@@ -48,22 +48,25 @@ constexpr int kChunks = kQ8Latent / 128;           // 4 latent chunks of 128 dim
 constexpr int kStages = 2;                         // tiles in shared memory
 constexpr int kRopeHalf = 128 * 64;                // 8 KB: 128 rows of 32 rope dims
 constexpr int kPvIssuers = 2;
-constexpr int kGatherWarps = 8;                    // rows and query
+constexpr int kGatherWarps = 4;                    // latent rows, half of the query
+constexpr int kRopeWarps = 4;                      // rope rows, scales, the other half of the query
 constexpr int kWorkerWarps = 16;                   // softmax and output
 constexpr int kWorkers = kWorkerWarps * 32;
-// warp 0 QK, warps 1-2 PV, warp 3 none; warps 4-11 gather; warps 12-27 workers.  The register split is by
+// warp 0 QK, warps 1-2 PV, warp 3 none; warps 4-7 latent rows, 8-11 rope rows; warps 12-27 workers.  The register split is by
 // warpgroups of four warps out of what the launch holds: 896 threads of 72 registers.
 constexpr int kFirstGather = 4;
-constexpr int kFirstWorker = kFirstGather + kGatherWarps;
+constexpr int kFirstRope = kFirstGather + kGatherWarps;
+constexpr int kFirstWorker = kFirstRope + kRopeWarps;
 constexpr int kThreads = 32 * (kFirstWorker + kWorkerWarps);
 constexpr int kLaunchRegs = 72, kIssueRegs = 56, kGatherRegs = 64, kWorkerRegs = 80;
 static_assert(kThreads * kLaunchRegs >=
-                  32 * (kFirstGather * kIssueRegs + kGatherWarps * kGatherRegs + kWorkerWarps * kWorkerRegs),
+                  32 * (kFirstGather * kIssueRegs + (kGatherWarps + kRopeWarps) * kGatherRegs + kWorkerWarps * kWorkerRegs),
               "registers of the CTA");
-constexpr int kRowsPerWarp = kTile / kGatherWarps; // 16 rows of a tile, 8 query heads a gather warp
+constexpr int kQHeads = kH / (kGatherWarps + kRopeWarps);   // query heads a gather or rope warp converts
+static_assert(kGatherWarps == 4 && kRopeWarps == 4, "a warp of either kind has 32 rows of a tile, one a lane");
 constexpr int kHG = kH / (kWorkerWarps / 4);       // 16 heads a worker warp
 constexpr int kGroupThreads = 4 * 32;              // the four warps sharing a head group
-constexpr uint32_t kGatherBar = 7;                 // named barriers: 1, 2 workers, 3-6 head groups, 7 gather
+constexpr uint32_t kGatherBar = 7;                 // named barriers: 1, 2 workers, 3-6 head groups, 7 gather, 8 rope
 static_assert(kHG == 16 && kWorkerWarps == 16, "warp_transpose_reduce16 takes a head group of 16");
 
 constexpr float kFirstTop = 5.5f;                  // log2 of the first tile's largest P'
@@ -82,9 +85,9 @@ constexpr int OFF_RED = OFF_QS + 3 * kH * 4;       // float [4][64]
 constexpr int OFF_MNEG = OFF_RED + 4 * kH * 4;     // float [64]: minus the references
 constexpr int OFF_ALPHA = OFF_MNEG + kH * 4;       // float [64]: rescale factors; at an item's end 1 / l
 constexpr int OFF_BAR = OFF_ALPHA + kH * 4;
-// barriers: full[8], free[8], rope_full, rope_free, s_full, s_free, p_full, q_full
+// barriers: full[8], free[4], rope_full, rope_free, s_full, s_free, p_full, q_raw, q_full
 constexpr int kSlots = kStages * kChunks;
-constexpr int kBars = 2 * kSlots + 6;
+constexpr int kBars = kSlots + 2 * kStages + 7;
 constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
 constexpr int kSmemBytes = OFF_ABORT + 4;
@@ -144,29 +147,54 @@ __device__ __forceinline__ uint32_t split_e4m3x2(float x, float y) {
 __device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
-// Transposes over groups of G lanes.  Lane j of a group holds N words (N / G to each lane of the group, in
-// order); afterwards word i * (N / G) + k is word j * (N / G) + k of the group's lane i.
-template <int N, int G>
-__device__ __forceinline__ void transpose_words(uint32_t (&v)[N], uint32_t lane) {
-    constexpr int K = N / G;
-#pragma unroll
-    for (int s = G / 2; s; s >>= 1) {        // swap the off-diagonal halves of every 2s x 2s block
-        const bool up = lane & s;
-#pragma unroll
-        for (int b = 0; b < G; ++b) {
-            if (b & s) continue;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
-                uint32_t &lo = v[b * K + k], &hi = v[(b + s) * K + k];
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, s);
-                if (up) lo = got; else hi = got;
-            }
+// The rows of this CTA's tiles, tile after tile, one a lane (row `base` of a tile), in two steps so that the
+// loads of one are in flight while the caller works: fetch() loads the selected key of the next tile,
+// resolve() turns it into a cache row (a page lookup when paged).
+struct RowStream {
+    int s = 0, tiles = 0;               // next item of the CTA; tiles of the current one still to fetch
+    const int32_t* at = nullptr;        // this lane's slot of the next tile, and the slots from it to the item's end
+    int left = 0, batch = 0, bound = 0;
+    int key = -1;
+    int first = -1;                     // the item's query when the fetched tile is its first, else -1
+
+    __device__ __forceinline__ bool fetch(const AttnQ8Params& p, uint32_t lane, int base) {
+        first = -1;
+        while (tiles == 0) {
+            const int it = nth_item(p, s++);
+            if (it == -1) return false;
+            if (it < 0) continue;
+            const Item I = decode_item(p, it);
+            tiles = item_tiles(p, I, lane);
+            at = p.idx + (int64_t)I.row * p.top_k + I.slot0 + base;
+            left = I.slot_end - I.slot0 - base;
+            batch = I.batch;
+            bound = I.bound;
+            first = I.row;
         }
+        key = left > 0 ? __ldg(at) : -1;
+        at += kTile;
+        left -= kTile;
+        --tiles;
+        return true;
     }
-}
+    // cache row of the fetched key; -1: no key, -2: a page outside the pool (a row of zeros)
+    __device__ __forceinline__ int resolve(const AttnQ8Params& p) const {
+        if (key < 0) return -1;
+        if (key >= bound) {
+            raise_dev_error(p.status, DEV_ERR_BOUNDS);
+            return -1;
+        }
+        if (!p.pages.table) return (int)((int64_t)batch * p.Nmax + key);
+        const int row = (int)paged_row(p.pages, batch, key);
+        if (row >= 0) return row;
+        raise_dev_error(p.status, DEV_ERR_BOUNDS);
+        return -2;
+    }
+};
 
 template <bool PARTIAL>
-__global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const AttnQ8Params p) {
+__global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_pe,
+                       const AttnQ8Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {   // the operands' swizzle counts from 1 KB boundaries; there is no room to round up
         if (threadIdx.x == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
@@ -180,12 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const AttnQ8Pa
     float* invl_s = alpha_s;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint64_t* freed = full + kSlots;
-    uint64_t* rope_full = freed + kSlots;
+    uint64_t* rope_full = freed + 2 * kStages;
     uint64_t* rope_free = rope_full + 1;
     uint64_t* s_full = rope_full + 2;
     uint64_t* s_free = rope_full + 3;
     uint64_t* p_full = rope_full + 4;
-    uint64_t* q_full = rope_full + 5;
+    uint64_t* q_raw = rope_full + 5;
+    uint64_t* q_full = rope_full + 6;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
 
@@ -195,14 +224,15 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const AttnQ8Pa
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&full[i], kGatherWarps * 32);   // one cp.async arrival per gather thread
-            mbar_init(&freed[i], 1);                  // the commit of the PV issuer that consumed the chunk
         }
-        mbar_init(rope_full, kGatherWarps * 32);
+        for (int i = 0; i < 2 * kStages; ++i) mbar_init(&freed[i], kPvIssuers);   // both issuers' commits of a chunk
+        mbar_init(rope_full, kRopeWarps * 32);
         mbar_init(rope_free, 1);
         mbar_init(s_full, 2);                   // the QK issuer: its commit, and that it has seen the rows' scales
         mbar_init(s_free, kWorkerWarps);
         mbar_init(p_full, kWorkerWarps);
-        mbar_init(q_full, kGatherWarps);
+        mbar_init(q_raw, 1);
+        mbar_init(q_full, kGatherWarps + kRopeWarps);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -230,7 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const AttnQ8Pa
     tc_fence_after();
     griddep_wait();                 // inputs and outputs may belong to the previous kernel until here
 
-    // Chunk c of the CTA's g-th tile lies in slot 4 (g % 2) + c; the slot's barriers are in their use g / 2.
+    // Chunk c of the CTA's g-th tile lies in slot 4 (g % 2) + c; the slots' barriers are in their use g / 2.  PV frees
+    // them by pairs: chunks 0 and 1 (one of each issuer), then 2 and 3.
     if (warp < kFirstGather) setmaxnreg_dec<kIssueRegs>();
     if (warp == 0) {
         // ------------------------------------------------------------ QK issuer
@@ -314,172 +345,150 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const AttnQ8Pa
                             mma_e4m3_scaled_ss_lo(d, a + kk * (4096 >> 4), kDescHi, b + (64 >> 4), kDescHi, IDESC_PV,
                                                   tmem_base + TM_ONE, tmem_base + TM_LO, 1u);
                         }
-                        mma_commit(&freed[slot]);
+                        mma_commit(&freed[2 * (gt & 1) + j]);
                     }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
     } else if (warp >= kFirstGather && warp < kFirstWorker) {
-        // ------------------------------------------------------------ gather
+        // ------------------------------------------------------------ gather: latent rows, rope rows, queries
         setmaxnreg_dec<kGatherRegs>();
-        const int gw = warp - kFirstGather;       // 0..7: rows 16 gw .. 16 gw + 15 of a tile, query heads 8 gw ..
+        const bool is_rope = warp >= kFirstRope;
+        const int gw = (warp - kFirstGather) & 3; // rows 32 gw .. 32 gw + 31 of a tile
+        const int qh0 = kQHeads * (warp - kFirstGather);
         const uint32_t smem_base = smem_u32(smem);
-        // One thread polls, a named barrier releases the eight warps.  (A thread suspended in try_wait was seen
+        // One thread polls, a named barrier releases the four warps.  (A thread suspended in try_wait was seen
         // to resume 800 to 3400 cycles after the phase had completed; threads that all poll take the issue slots
         // of the softmax.)  The answer is the same in every warp: all leave together when a wait gives up.
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
             bool ok = true;
-            if (threadIdx.x == 32 * kFirstGather) ok = mbar_wait_clk<true>(bar, parity, abort_flag, p.status);
-            return named_bar_and(kGatherBar, kGatherWarps * 32, ok);
+            if (gw == 0 && lane == 0) ok = mbar_wait_clk<true>(bar, parity, abort_flag, p.status);
+            return named_bar_and(kGatherBar + (is_rope ? 1 : 0), 128, ok);
         };
-        // Lanes 0..15 carry their row through three stages: the selected key (fetch), its cache row (resolve: a
-        // page lookup when paged), the copies.  Each stage runs one tile ahead of the next, so that its loads
-        // are in flight during the copies of the tile before.
-        int f_s = 0, f_T = 0;                     // next item of the CTA; tiles of the current one still to fetch
-        const int32_t* f_idx = p.idx;             // this lane's next slot, and how many slots are left from it on
-        int f_left = 0, f_batch = 0, f_bound = 0;
-        int f_key = -1, f_first = -1;             // the fetched tile's key; its query when it is an item's first tile
-        auto fetch = [&]() -> bool {
-            f_first = -1;
-            while (f_T == 0) {
-                const int it = nth_item(p, f_s++);
-                if (it == -1) return false;
-                if (it < 0) continue;
-                const Item I = decode_item(p, it);
-                f_T = item_tiles(p, I, lane);
-                f_idx = p.idx + (int64_t)I.row * p.top_k + I.slot0 + kRowsPerWarp * gw + (int)lane;
-                f_left = lane < kRowsPerWarp ? I.slot_end - I.slot0 - kRowsPerWarp * gw - (int)lane : 0;
-                f_batch = I.batch;
-                f_bound = I.bound;
-                f_first = I.row;
-                if (lane == 0)                    // the warp's heads of the query, into L2
-                    l2_prefetch_bulk(p.q + ((int64_t)I.row * kH + kH / kGatherWarps * gw) * DSA_QK_DIM,
-                                     kH / kGatherWarps * DSA_QK_DIM * 2);
-            }
-            f_key = f_left > 0 ? __ldg(f_idx) : -1;
-            f_idx += kTile;
-            f_left -= kTile;
-            --f_T;
-            return true;
-        };
-        // cache row of the fetched key; -1: no key, -2: a page outside the pool (a row of zeros)
-        auto resolve = [&]() -> int {
-            const int j = f_key;
-            if (j < 0) return -1;
-            if (j >= f_bound) {
-                raise_dev_error(p.status, DEV_ERR_BOUNDS);
-                return -1;
-            }
-            if (p.pages.table) {
-                const int row = (int)paged_row(p.pages, f_batch, j);
-                if (row < 0) raise_dev_error(p.status, DEV_ERR_BOUNDS);
-                return row < 0 ? -2 : row;
-            }
-            return (int)((int64_t)f_batch * p.Nmax + j);
-        };
-        // One 128-byte block (blk 0..3 latent, 4 rope) of the warp's 16 rows: a warp instruction copies a block of
-        // four different rows, 8 lanes a row.
-        const int ci = (int)(lane >> 3), cc = (int)(lane & 7);
-        const uint32_t dst0 = smem_base + (uint32_t)((kRowsPerWarp * gw + ci) * 128);
-        auto copy_chunk = [&](int row, int g, int c) -> bool {      // chunk c of the CTA's g-th tile
-            const uint32_t slot = 4u * (uint32_t)(g & 1) + (uint32_t)c;
-            if (!wait(&freed[slot], ((g >> 1) & 1) ^ 1)) return false;
-#pragma unroll
-            for (int i = 0; i < kRowsPerWarp / 4; ++i) {
-                const int r = __shfl_sync(0xffffffffu, row, 4 * i + ci);
-                cp_async_16(dst0 + OFF_LAT + slot * kBlk + i * 512 + ((cc ^ (4 * (i & 1) + ci)) << 4),
-                            p.cache + (r < 0 ? 0 : (int64_t)r * kQ8Row + c * 128 + cc * 16), r < 0 ? 0u : 16u);
-            }
-            cp_async_arrive_noinc(&full[slot]);
-            return true;
-        };
-        // half of the rope dims: 64-byte rows, 4 lanes a row, 8 rows a warp instruction
-        auto copy_rope = [&](int row, int half) {
-#pragma unroll
-            for (int i = 0; i < kRowsPerWarp / 8; ++i) {
-                const int tr = 8 * i + (int)(lane >> 2);
-                const int r = __shfl_sync(0xffffffffu, row, tr);
-                const int pc = (int)(lane & 3);
-                cp_async_16(smem_base + OFF_ROPE + (kRowsPerWarp * gw + tr) * 64 + ((pc ^ ((tr >> 1) & 3)) << 4),
-                            p.cache + (r < 0 ? 0 : (int64_t)r * kQ8Row + kQ8Latent + half * 64 + pc * 16), r < 0 ? 0u : 16u);
-            }
-        };
-        // Query head h: lane l holds dims 8l.. and 256 + 8l.., and rope dims 2l, 2l + 1.
-        struct Head {
-            uint4 w[2];
-            uint32_t pe;
-        };
-        auto load_head = [&](int row, int h) -> Head {
-            const __nv_bfloat16* src = p.q + ((int64_t)row * kH + h) * DSA_QK_DIM;
-            Head q;
-            q.w[0] = ldg_nc_v4(src + 8 * lane);
-            q.w[1] = ldg_nc_v4(src + 256 + 8 * lane);
-            q.pe = __ldg(reinterpret_cast<const uint32_t*>(src + kQ8Latent) + lane);
-            return q;
-        };
-        auto convert_head = [&](const Head& q, int qbuf, int h) {
-            const uint32_t w[8] = {q.w[0].x, q.w[0].y, q.w[0].z, q.w[0].w, q.w[1].x, q.w[1].y, q.w[1].z, q.w[1].w};
+        // Query head h from its bf16 dims to its e4m3 parts, in place: lane l holds dims 16 l .. 16 l + 15.
+        auto convert_head = [&](int qbuf, int h) {
+            const int j = (int)(lane >> 2), pc = 2 * (int)(lane & 3);
+            const uint8_t* raw = smem + OFF_QHL + (j & 3) * kBlk + ((j >> 2) * kH + h) * 128;
+            const uint4 a = *reinterpret_cast<const uint4*>(raw + ((pc ^ (h & 7)) << 4));
+            const uint4 b = *reinterpret_cast<const uint4*>(raw + (((pc + 1) ^ (h & 7)) << 4));
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             float amax = 0.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
-            // magnitudes compare as their bit patterns do
+            // magnitudes compare as their bit patterns do; every lane has read its dims when this returns
             const int e = e4m3_scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
             const float inv = exp2_int(-e);
-            const uint32_t swz = (uint32_t)((((lane & 15) >> 1) ^ (h & 7)) << 4) + (lane & 1) * 8;
+            uint32_t s[8];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t s[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s[k] = split_e4m3x2(bf16_lo(w[4 * b + k]) * inv, bf16_hi(w[4 * b + k]) * inv);
-                uint8_t* d = smem + OFF_QHL + (2 * b + (int)(lane >> 4)) * kBlk + h * 128 + swz;
-                *reinterpret_cast<uint2*>(d) = make_uint2(lows(s[0], s[1]), lows(s[2], s[3]));
-                *reinterpret_cast<uint2*>(d + 64 * 128) = make_uint2(highs(s[0], s[1]), highs(s[2], s[3]));
-            }
-            *reinterpret_cast<uint32_t*>(smem + OFF_QR + (lane >> 4) * (kH * 64) + h * 64 +
-                                         ((((lane & 15) >> 2) ^ ((h >> 1) & 3)) << 4) + (lane & 3) * 4) = q.pe;
+            for (int k = 0; k < 8; ++k) s[k] = split_e4m3x2(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
+            uint8_t* d = smem + OFF_QHL + (int)(lane >> 3) * kBlk + h * 128 + (((int)(lane & 7) ^ (h & 7)) << 4);
+            __syncwarp();
+            *reinterpret_cast<uint4*>(d) = make_uint4(lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7]));
+            *reinterpret_cast<uint4*>(d + kH * 128) =
+                make_uint4(highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7]));
             if (lane == 0) qs_s[qbuf * kH + h] = p.scale_log2 * exp2_int(e);
         };
+        int qi = 0, qbuf = 0;
+        auto convert = [&]() -> bool {            // the warp's heads of the item's query, once it has landed
+            if (!wait(q_raw, qi & 1)) return false;
+#pragma unroll 2
+            for (int i = 0; i < kQHeads; ++i) convert_head(qbuf, qh0 + i);
+            ++qi;
+            qbuf = qbuf == 2 ? 0 : qbuf + 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            return true;
+        };
 
-        bool has0 = fetch(), has1;                // tile being copied; tile fetched
-        int row0 = has0 ? resolve() : -1, first0 = f_first;
-        has1 = has0 && fetch();
-        int qbuf = 0;
-        for (int g = 0; has0; ++g) {
-            const int row1 = has1 ? resolve() : -1, first1 = f_first;
-            bool ok = true;
+        RowStream rs;
+        const int base = 32 * gw + (int)lane;
+        bool has = rs.fetch(p, lane, base);
+        if (!is_rope) {
+            // A warp instruction copies a 128-byte block of four different rows, 8 lanes a row: this lane's rows are
+            // 32 gw + 4 i + l / 8.
+            const int ci = (int)(lane >> 3), cc = (int)(lane & 7);
+            const uint32_t dst0 = smem_base + OFF_LAT + (uint32_t)((32 * gw + ci) * 128);
+            const uint32_t sw0 = (uint32_t)((cc ^ ci) << 4), sw1 = (uint32_t)((cc ^ (4 + ci)) << 4);
+            for (int g = 0; has; ++g) {
+                const int row = rs.resolve(p), first = rs.first;
+                const uint8_t* src[8];
+                uint32_t valid = 0;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) ok = ok && copy_chunk(row0, g, c);
-            // QK of the previous tile is complete: the rope block, and after an item's last tile the query, are free
-            if (ok && g > 0) ok = wait(s_full, (g - 1) & 1);
-            if (!ok) break;
-            copy_rope(row0, 0);
-            cp_async_arrive_noinc(rope_full);
-            if (first0 >= 0) {
-                constexpr int kHeads = kH / kGatherWarps;
-                Head q = load_head(first0, kHeads * gw);
-#pragma unroll 1
-                for (int i = 0; i < kHeads; ++i) {
-                    const Head next = load_head(first0, kHeads * gw + min(i + 1, kHeads - 1));
-                    convert_head(q, qbuf, kHeads * gw + i);
-                    q = next;
+                for (int i = 0; i < 8; ++i) {
+                    const int r = __shfl_sync(0xffffffffu, row, 4 * i + ci);
+                    src[i] = p.cache + (r < 0 ? 0 : (int64_t)r * kQ8Row + cc * 16);
+                    valid |= (r < 0 ? 0u : 16u) << i;            // bit 4 + i
                 }
-                qbuf = qbuf == 2 ? 0 : qbuf + 1;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(q_full);
+                has = rs.fetch(p, lane, base);
+                const uint32_t dst = dst0 + (g & 1) * (kChunks * kBlk);
+                bool ok = true;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    ok = wait(&freed[2 * (g & 1) + half], ((g >> 1) & 1) ^ 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int c = 2 * half; c < 2 * half + 2; ++c) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            cp_async_16(dst + c * kBlk + i * 512 + ((i & 1) ? sw1 : sw0), src[i] + c * 128, (valid >> i) & 16u);
+                        cp_async_arrive_noinc(&full[4 * (g & 1) + c]);
+                    }
+                }
+                if (!ok) break;
+                if (first >= 0 && !convert()) break;
             }
-            // the first half is consumed: QK of this tile has begun, so the workers have read the scales before
-            if (!wait(rope_free, g & 1)) break;
-            copy_rope(row0, 1);
-            if (lane < kRowsPerWarp)
-                cp_async_4(smem_base + OFF_SC + (kRowsPerWarp * gw + lane) * 4,
-                           row0 >= 0 ? p.cache_scale + row0 : &g_unit_scale, row0 == -1 ? 0u : 4u);
-            cp_async_arrive_noinc(rope_full);
-            row0 = row1;
-            has0 = has1;
-            first0 = first1;
-            has1 = has1 && fetch();
+        } else {
+            // half of the rope dims: 64-byte rows, 4 lanes a row, this lane's rows are 32 gw + 8 i + l / 4
+            const int ci = (int)(lane >> 2), pc = (int)(lane & 3);
+            const uint32_t dst = smem_base + OFF_ROPE + (uint32_t)((32 * gw + ci) * 64 + ((pc ^ ((ci >> 1) & 3)) << 4));
+            for (int g = 0; has; ++g) {
+                const int row = rs.resolve(p), first = rs.first;
+                const uint8_t* src[4];
+                uint32_t valid = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = __shfl_sync(0xffffffffu, row, 8 * i + ci);
+                    src[i] = p.cache + (r < 0 ? 0 : (int64_t)r * kQ8Row + kQ8Latent + pc * 16);
+                    valid |= (r < 0 ? 0u : 16u) << i;
+                }
+                const float* sc = row >= 0 ? p.cache_scale + row : &g_unit_scale;
+                has = rs.fetch(p, lane, base);
+                if (has && rs.first >= 0 && gw == 0 && lane == 0)   // the next query, into L2
+                    l2_prefetch_bulk(p.q + (int64_t)rs.first * (kH * DSA_QK_DIM), kH * DSA_QK_DIM * 2);
+                // QK of the previous tile is complete: the rope block, and after an item's last tile the query, are free
+                if (g > 0 && !wait(s_full, (g - 1) & 1)) break;
+                if (first >= 0 && gw == 0 && lane == 0) {
+                    // the query as it is, into the place of its e4m3 parts: dims 64 j.. of the heads go where the rows
+                    // of chunk j % 4 will be, hi rows for j < 4, lo rows for the others
+                    mbar_arrive_expect_tx(q_raw, kH * DSA_QK_DIM * 2);
+#pragma unroll 1
+                    for (int j = 0; j < 8; ++j)
+                        tma_load_2d(smem + OFF_QHL + (j & 3) * kBlk + (j >> 2) * (kH * 128), &tmap_q, q_raw, 64 * j, first * kH);
+                    for (int j = 0; j < 2; ++j)
+                        tma_load_2d(smem + OFF_QR + j * (kH * 64), &tmap_pe, q_raw, kQ8Latent + 32 * j, first * kH);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (half) {
+                        if (first >= 0 && !convert()) {
+                            has = false;
+                            break;
+                        }
+                        // the first half is consumed: QK of this tile has begun, so the workers have read the scales before
+                        if (!wait(rope_free, g & 1)) {
+                            has = false;
+                            break;
+                        }
+                        cp_async_4(smem_base + OFF_SC + base * 4, sc, row == -1 ? 0u : 4u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cp_async_16(dst + i * 512, src[i] + half * 64, (valid >> i) & 16u);
+                    cp_async_arrive_noinc(rope_full);
+                }
+            }
         }
         cp_async_wait_all();
     } else if (warp >= kFirstWorker) {
@@ -500,13 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const AttnQ8Pa
             if (tid == 0) ok = mbar_wait_clk<true>(bar, parity, abort_flag, p.status);
             return named_bar_and(1, kWorkers, ok);
         };
-        auto pv_done = [&](int g) -> bool {           // both PV issuers' last chunk of tile g is consumed
+        auto pv_done = [&](int g) -> bool {           // PV has consumed tile g
             bool ok = true;
-            if (lane == 0) {
-                const uint32_t par = (g >> 1) & 1;
-                ok = mbar_wait_clk<true>(&freed[4 * (g & 1) + 2], par, abort_flag, p.status) &&
-                     mbar_wait_clk<true>(&freed[4 * (g & 1) + 3], par, abort_flag, p.status);
-            }
+            if (lane == 0)
+                ok = mbar_wait_clk<true>(&freed[2 * (g & 1) + 1], (g >> 1) & 1, abort_flag, p.status);
             __syncwarp();
             return ok;
         };
@@ -698,35 +704,64 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const AttnQ8Pa
                 store_lse(I, tid, (l > 0.f) ? (log2f(l) - m_neg[tid]) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l));
             }
             named_bar_sync(1, kWorkers);
-            // A lane holds one dim of 16 heads; the lanes of a group exchange them so that each stores 16
-            // contiguous bytes of a head (with a store of one element a lane an item's output took 5 us).
+            // P^T is consumed: each warp takes 1 KB of its block to turn its 32 dims x 16 heads so that a store
+            // writes 16 contiguous bytes of a head a lane.
+            uint8_t* stage = smem + OFF_P + ww * 1024;
+            const bool f32 = PARTIAL || p.out_f32;
+            float* out32 = PARTIAL ? p.part_o + (((int64_t)I.row * p.nsplit + I.split) * kH + h0) * kDv
+                                   : static_cast<float*>(p.out) + ((int64_t)I.row * kH + h0) * kDv;
+            __nv_bfloat16* out16 = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)I.row * kH + h0) * kDv;
 #pragma unroll 1
             for (int ch = 0; ch < kChunks; ++ch) {
-                uint32_t v[kHG];
-                tmem_ld16(tmem_base + lane_addr + TM_O + 64 * ch + h0, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int h = 0; h < kHG; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * invl_s[h0 + h]);
                 const int dim0 = ch * 128 + quad * 32;
-                if (PARTIAL || p.out_f32) {       // groups of 4 lanes: lane j gets heads 4j.. of the group's 4 dims
-                    float* base = PARTIAL ? p.part_o + (((int64_t)I.row * p.nsplit + I.split) * kH + h0) * kDv
-                                          : static_cast<float*>(p.out) + ((int64_t)I.row * kH + h0) * kDv;
-                    transpose_words<16, 4>(v, lane);
-                    float* dst = base + (int)(lane & 3) * 4 * kDv + dim0 + (int)(lane & ~3u);
+                if (f32) {                        // a lane a dim, 8 heads at a time: rows of 32 dims
+                    uint32_t v[kHG];
+                    tmem_ld16(tmem_base + lane_addr + TM_O + 64 * ch + h0, v);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 4; ++h)
-                        *reinterpret_cast<uint4*>(dst + h * kDv) = make_uint4(v[h], v[4 + h], v[8 + h], v[12 + h]);
-                } else {                          // groups of 8 lanes: lane j gets heads 2j, 2j + 1 of the group's 8 dims
-                    uint32_t w[8];
+                    for (int half = 0; half < 2; ++half) {
+                        __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                    transpose_words<8, 8>(w, lane);
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                                         ((int64_t)I.row * kH + h0 + (int)(lane & 7) * 2) * kDv + dim0 + (int)(lane & ~7u);
-                    *reinterpret_cast<uint4*>(dst) =
-                        make_uint4(lows(w[0], w[1]), lows(w[2], w[3]), lows(w[4], w[5]), lows(w[6], w[7]));
-                    *reinterpret_cast<uint4*>(dst + kDv) =
-                        make_uint4(highs(w[0], w[1]), highs(w[2], w[3]), highs(w[4], w[5]), highs(w[6], w[7]));
+                        for (int h = 0; h < 8; ++h)
+                            reinterpret_cast<float*>(stage)[h * 32 + lane] =
+                                __uint_as_float(v[8 * half + h]) * invl_s[h0 + 8 * half + h];
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int h = 4 * i + (int)(lane >> 3);
+                            *reinterpret_cast<float4*>(out32 + (8 * half + h) * kDv + dim0 + (int)(lane & 7) * 4) =
+                                reinterpret_cast<const float4*>(stage)[h * 8 + (lane & 7)];
+                        }
+                    }
+                } else {                          // 8 x 8 blocks (dims x heads) stored transposed: rows of 32 dims
+                    uint32_t v[2][8];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)   // 16 dims: a lane has dims l / 4 and l / 4 + 8, heads 2 (l % 4), + 1
+                        tmem_ld_16x256b_x2(tmem_base + lane_addr + (16u * half << 16) + TM_O + 64 * ch + h0, v[half]);
+                    tmem_ld_wait();
+                    __syncwarp();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t w[4];            // blocks: dims 0-7 / 8-15 of heads 0-7, then of heads 8-15
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const float2 il = reinterpret_cast<const float2*>(invl_s + h0 + 8 * b)[lane & 3];
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                w[2 * b + r] = pack_bf16x2(__uint_as_float(v[half][4 * b + 2 * r]) * il.x,
+                                                           __uint_as_float(v[half][4 * b + 2 * r + 1]) * il.y);
+                        }
+                        // row of block m that this lane addresses: head 8 (m / 2) + l % 8, dims 16 half + 8 (m % 2)
+                        const int m = (int)(lane >> 3), h = 8 * (m >> 1) + (int)(lane & 7), pc = 2 * half + (m & 1);
+                        stmatrix_x4_trans(smem_u32(stage) + h * 64 + ((pc ^ ((h >> 1) & 3)) << 4), w);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int h = 8 * i + (int)(lane >> 2), pc = (int)(lane & 3);
+                        *reinterpret_cast<uint4*>(out16 + h * kDv + dim0 + pc * 8) =
+                            *reinterpret_cast<const uint4*>(stage + h * 64 + ((pc ^ ((h >> 1) & 3)) << 4));
+                    }
                 }
             }
             tc_fence_before();
@@ -746,8 +781,13 @@ dsa_status_t launch(const AttnQ8Params& p, cudaStream_t stream) {
     auto kern = mla_attn_q8_kernel<PARTIAL>;
     dsa_status_t st = ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmemBytes);
     if (st != DSA_OK) return st;
+    CUtensorMap tq, tpe;
+    if ((st = make_tmap_bf16_2d(&tq, p.q, DSA_QK_DIM, (uint64_t)p.rows * kH, DSA_QK_DIM * 2, 64, kH)) != DSA_OK) return st;
+    if ((st = make_tmap_bf16_2d_sw64(&tpe, p.q, DSA_QK_DIM, (uint64_t)p.rows * kH, DSA_QK_DIM * 2, 32, kH)) != DSA_OK)
+        return st;
     const int sms = device_sm_count();
-    if (launch_pdl(kern, dim3(p.n_items < sms ? p.n_items : sms), dim3(kThreads), kSmemBytes, stream, p) != cudaSuccess)
+    if (launch_pdl(kern, dim3(p.n_items < sms ? p.n_items : sms), dim3(kThreads), kSmemBytes, stream, tq, tpe, p) !=
+        cudaSuccess)
         return DSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
