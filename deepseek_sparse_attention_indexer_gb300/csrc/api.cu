@@ -125,11 +125,6 @@ dsa_status_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t cols
     return make_tmap_impl(map, base, cols, rows, row_bytes, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-dsa_status_t make_tmap_bf16_2d_sw64(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
-                                    uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows) {
-    return make_tmap_impl(map, base, cols, rows, row_bytes, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
 }  // namespace dsa
 
 using namespace dsa;
@@ -368,7 +363,7 @@ dsa_status_t mla_sparse_attn_prefill_q8(const void* q, const void* cache, const 
     (void)ws_bytes;
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
-    if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
     return launch_attn_q8_prefill(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32, lse,
                                   PageTable{}, static_cast<cudaStream_t>(stream));
@@ -386,7 +381,7 @@ dsa_status_t mla_sparse_attn_prefill_q8_paged(const void* q, const void* cache, 
     PageTable pt;
     const int stride = page_size > 0 ? (int)(((long long)N + page_size - 1) / page_size) : 0;
     if ((st = make_page_table(block_table, stride, page_size, num_pages, N, &pt)) != DSA_OK) return st;
-    if (!aligned16(q) || !aligned16(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
     return launch_attn_q8_prefill(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32, lse,
                                   pt, static_cast<cudaStream_t>(stream));
@@ -400,7 +395,7 @@ dsa_status_t mla_sparse_attn_decode_q8(const void* q, const void* cache, const f
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, B, Nmax, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
     if ((long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if (ws_bytes < attn_decode_workspace(B, top_k)) return DSA_ERR_WORKSPACE_TOO_SMALL;
     if ((st = check_device()) != DSA_OK) return st;
     return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
@@ -419,7 +414,7 @@ dsa_status_t mla_sparse_attn_decode_q8_paged(const void* q, const void* cache, c
     PageTable pt;
     if ((st = make_page_table(block_table, bt_stride, page_size, num_pages, Nmax, &pt)) != DSA_OK) return st;
     if ((long long)B * bt_stride > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if (ws_bytes < attn_decode_workspace(B, top_k)) return DSA_ERR_WORKSPACE_TOO_SMALL;
     if ((st = check_device()) != DSA_OK) return st;
     return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
@@ -434,7 +429,7 @@ dsa_status_t mla_cache_write_q8(const void* kv_a, int64_t kv_a_stride, const flo
     if (R < 1 || max_pos < 1 || cache_rows < 1 || kv_a_stride < DSA_QK_DIM || !eps_ok(eps)) return DSA_ERR_INVALID_ARG;
     if (interleave != 0 && interleave != 1) return DSA_ERR_INVALID_ARG;
     if (cache_rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(kv_a) || !aligned16(norm_w) || !aligned16(cos_sin) || !aligned16(cache) || kv_a_stride % 8)
+    if (!aligned16(kv_a) || !aligned16(norm_w) || !aligned16(cos_sin) || !aligned32(cache) || kv_a_stride % 8)
         return DSA_ERR_MISALIGNED;
     dsa_status_t st = check_device();
     if (st != DSA_OK) return st;
@@ -447,7 +442,7 @@ dsa_status_t mla_cache_read_q8(const void* cache, const float* cache_scale, int6
     if (!cache || !cache_scale || !slots || !out) return DSA_ERR_INVALID_ARG;
     if (R < 1 || cache_rows < 1) return DSA_ERR_INVALID_ARG;
     if (cache_rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if (!aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
     dsa_status_t st = check_device();
     if (st != DSA_OK) return st;
     return launch_cache_read_q8(cache, cache_scale, (int)cache_rows, slots, R, out, static_cast<cudaStream_t>(stream));
@@ -462,7 +457,7 @@ dsa_status_t mla_cache_read_q8_paged(const void* cache, const float* cache_scale
     dsa_status_t st = make_page_table(block_table, bt_stride, page_size, num_pages, Nmax, &pt);
     if (st != DSA_OK) return st;
     if ((long long)B * bt_stride > 0x7FFFFFFFLL || (long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
-    if (!aligned16(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if (!aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
     return launch_cache_read_q8_paged(cache, cache_scale, kv_len, B, Nmax, out, pt, static_cast<cudaStream_t>(stream));
 }

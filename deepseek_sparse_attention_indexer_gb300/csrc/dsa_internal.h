@@ -24,9 +24,6 @@ dsa_status_t ensure_smem_attr(const void* func, int bytes);
 // box = box_cols x box_rows, 128-byte swizzle, zero fill out of bounds.
 dsa_status_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
                                uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows);
-// The same with the 64-byte swizzle (boxes of 32 columns).
-dsa_status_t make_tmap_bf16_2d_sw64(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows,
-                                    uint64_t row_bytes, uint32_t box_cols, uint32_t box_rows);
 
 // Launch with programmatic dependent launch allowed: the launch is prepared
 // while the previous kernel on the stream runs and the kernel starts as that
@@ -52,6 +49,7 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 // Page table of a paged key cache: logical key j of sequence b is pool row
 // table[b * stride + (j >> shift)] * 2^shift + (j & (2^shift - 1)).  A null

@@ -46,13 +46,13 @@ namespace {
 constexpr int kBlk = 128 * 128;                    // 16 KB: 128 rows of 128 bytes
 constexpr int kChunks = kQ8Latent / 128;           // 4 latent chunks of 128 dims a tile
 constexpr int kStages = 2;                         // tiles in shared memory
-constexpr int kRopeHalf = 128 * 64;                // 8 KB: 128 rows of 32 rope dims
 constexpr int kPvIssuers = 2;
 constexpr int kGatherWarps = 4;                    // latent rows, half of the query
+constexpr int kQueryWarp = 1 + kPvIssuers;
 constexpr int kRopeWarps = 4;                      // rope rows, scales, the other half of the query
 constexpr int kWorkerWarps = 16;                   // softmax and output
 constexpr int kWorkers = kWorkerWarps * 32;
-// warp 0 QK, warps 1-2 PV, warp 3 none; warps 4-7 latent rows, 8-11 rope rows; warps 12-27 workers.  The register split is by
+// warp 0 QK, warps 1-2 PV, warp 3 the query's TMA; warps 4-7 latent rows, 8-11 rope rows; warps 12-27 workers.  The register split is by
 // warpgroups of four warps out of what the launch holds: 896 threads of 72 registers.
 constexpr int kFirstGather = 4;
 constexpr int kFirstRope = kFirstGather + kGatherWarps;
@@ -75,17 +75,17 @@ constexpr float kNoRef = 3.0e38f;                  // -m before the reference is
 
 // smem layout
 constexpr int OFF_QHL = 0;                         // 4 chunks x (64 hi rows, 64 lo rows) x 128 B
-constexpr int OFF_QR = OFF_QHL + kChunks * kBlk;   // rope dims of 64 heads: two halves of 64 rows x 64 B
+constexpr int OFF_QR = OFF_QHL + kChunks * kBlk;   // rope dims of 64 heads: 64 rows x 128 B
 constexpr int OFF_LAT = OFF_QR + kH * 128;         // 2 tiles x 4 latent chunks
-constexpr int OFF_ROPE = OFF_LAT + kStages * kChunks * kBlk;   // half of a tile's rope dims
-constexpr int OFF_P = OFF_ROPE + kRopeHalf;        // 128 keys x (64 hi | 64 lo)
-constexpr int OFF_SC = OFF_P + kBlk;               // float [128]: scales of the tile's rows, 0 = no key
-constexpr int OFF_QS = OFF_SC + kTile * 4;         // float [3][64]: scale * log2(e) * 2^k of a query's heads
+constexpr int OFF_P = OFF_LAT + kStages * kChunks * kBlk;   // 128 keys x (64 hi | 64 lo)
+constexpr int OFF_SC = OFF_P + kBlk;               // float [2][128]: scales of a tile's rows, 0 = no key
+constexpr int OFF_QS = OFF_SC + 2 * kTile * 4;       // float [3][64]: scale * log2(e) * 2^k of a query's heads
 constexpr int OFF_RED = OFF_QS + 3 * kH * 4;       // float [4][64]
 constexpr int OFF_MNEG = OFF_RED + 4 * kH * 4;     // float [64]: minus the references
-constexpr int OFF_ALPHA = OFF_MNEG + kH * 4;       // float [64]: rescale factors; at an item's end 1 / l
-constexpr int OFF_BAR = OFF_ALPHA + kH * 4;
-// barriers: full[8], free[4], rope_full, rope_free, s_full, s_free, p_full, q_raw, q_full
+constexpr int OFF_ALPHA = OFF_MNEG + kH * 4;       // float [64]: rescale factors
+constexpr int OFF_INVL = OFF_ALPHA + kH * 4;       // float [64]
+constexpr int OFF_BAR = OFF_INVL + kH * 4;
+// barriers: full[8], free[4], rope_full, s_full, s_free, p_full, q_free, q_raw, q_full
 constexpr int kSlots = kStages * kChunks;
 constexpr int kBars = kSlots + 2 * kStages + 7;
 constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
@@ -99,16 +99,15 @@ constexpr uint32_t TM_R = 128;                     // the rope product, 64 colum
 constexpr uint32_t TM_O = 192;                     // O^T chunk c at TM_O + 64 c
 constexpr uint32_t TM_ONE = 448;                   // scale bytes 2^0
 constexpr uint32_t TM_LO = 464;                    // scale bytes 2^-4
+constexpr uint32_t TM_K = 480;                     // the tile's rope rows, 32 columns of two bf16
+static_assert(TM_K + kQ8Rope / 2 <= kTmemCols, "tensor memory columns");
 
 // Operands: 128-byte swizzle, 8-row groups 1 KB apart.  The descriptors' high words are the same; the
 // low words (address, leading offset) are sums that stay below the address field's end (see sdesc).
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-constexpr uint32_t kDescHiRope = (512u >> 4) | (1u << 14) | (4u << 29);   // rope halves: 64-byte rows and swizzle
 constexpr uint32_t IDESC_QK = idesc_e4m3_f32(128, 128, false, false);
 constexpr uint32_t IDESC_ROPE = idesc_bf16_f32(128, 64, false, false);
 constexpr uint32_t IDESC_PV = idesc_e4m3_scaled_f32(128, 64, true, true);
-
-__device__ float g_unit_scale = 1.f;               // scale of a row whose page lies outside the pool (zeros)
 
 struct AttnQ8Params : AttnShape {
     const __nv_bfloat16* q;    // [rows][64][576]
@@ -193,8 +192,7 @@ struct RowStream {
 };
 
 template <bool PARTIAL>
-__global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_pe,
-                       const AttnQ8Params p) {
+__global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const AttnQ8Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {   // the operands' swizzle counts from 1 KB boundaries; there is no room to round up
         if (threadIdx.x == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
@@ -205,14 +203,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
     float* red = reinterpret_cast<float*>(smem + OFF_RED);
     float* m_neg = reinterpret_cast<float*>(smem + OFF_MNEG);
     float* alpha_s = reinterpret_cast<float*>(smem + OFF_ALPHA);
-    float* invl_s = alpha_s;
+    float* invl_s = reinterpret_cast<float*>(smem + OFF_INVL);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint64_t* freed = full + kSlots;
     uint64_t* rope_full = freed + 2 * kStages;
-    uint64_t* rope_free = rope_full + 1;
-    uint64_t* s_full = rope_full + 2;
-    uint64_t* s_free = rope_full + 3;
-    uint64_t* p_full = rope_full + 4;
+    uint64_t* s_full = rope_full + 1;
+    uint64_t* s_free = rope_full + 2;
+    uint64_t* p_full = rope_full + 3;
+    uint64_t* q_free = rope_full + 4;
     uint64_t* q_raw = rope_full + 5;
     uint64_t* q_full = rope_full + 6;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
@@ -226,11 +224,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             mbar_init(&full[i], kGatherWarps * 32);   // one cp.async arrival per gather thread
         }
         for (int i = 0; i < 2 * kStages; ++i) mbar_init(&freed[i], kPvIssuers);   // both issuers' commits of a chunk
-        mbar_init(rope_full, kRopeWarps * 32);
-        mbar_init(rope_free, 1);
+        mbar_init(rope_full, kRopeWarps);
         mbar_init(s_full, 2);                   // the QK issuer: its commit, and that it has seen the rows' scales
         mbar_init(s_free, kWorkerWarps);
         mbar_init(p_full, kWorkerWarps);
+        mbar_init(q_free, 1);
         mbar_init(q_raw, 1);
         mbar_init(q_full, kGatherWarps + kRopeWarps);
         *abort_flag = 0;
@@ -282,32 +280,26 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     if (!(ok = mbar_wait_clk<true>(s_free, (gt & 1) ^ 1, abort_flag, p.status))) break;
                     tc_fence_after();
                     const uint32_t lat = base + (OFF_LAT >> 4) + (gt & 1) * (kChunks * kBlk >> 4);
-                    // first half of the rope dims; the second half takes its place while the chunks run
 #pragma unroll
-                    for (int j = 0; j < 2 + kChunks; ++j) {
-                        if (j == 0 || j == 1 + kChunks) {
-                            const int half = j ? 1 : 0;
-                            if (!(ok = mbar_wait_clk<true>(rope_full, half, abort_flag, p.status))) break;
-                            if (half) mbar_arrive(s_full);
-                            fence_proxy_async_smem();
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (!(ok = mbar_wait_clk<true>(&full[4 * (gt & 1) + c], (gt >> 1) & 1, abort_flag, p.status))) break;
+                        fence_proxy_async_smem();
 #pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)
-                                mma_bf16_ss_lo(tmem_base + TM_R, base + (OFF_ROPE >> 4) + 2 * kk, kDescHiRope,
-                                               base + ((OFF_QR + half * kH * 64) >> 4) + 2 * kk, kDescHiRope, IDESC_ROPE,
-                                               (half | kk) ? 1u : 0u);
-                            if (!half) mma_commit(rope_free);
-                        } else {
-                            const int c = j - 1;
-                            if (!(ok = mbar_wait_clk<true>(&full[4 * (gt & 1) + c], (gt >> 1) & 1, abort_flag, p.status))) break;
-                            fence_proxy_async_smem();
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)   // 32 dims a step
-                                mma_e4m3_ss_lo(tmem_base + TM_S, lat + c * (kBlk >> 4) + 2 * kk, kDescHi,
-                                               base + (OFF_QHL >> 4) + c * (kBlk >> 4) + 2 * kk, kDescHi, IDESC_QK,
-                                               (c | kk) ? 1u : 0u);
-                        }
+                        for (int kk = 0; kk < 4; ++kk)   // 32 dims a step
+                            mma_e4m3_ss_lo(tmem_base + TM_S, lat + c * (kBlk >> 4) + 2 * kk, kDescHi,
+                                           base + (OFF_QHL >> 4) + c * (kBlk >> 4) + 2 * kk, kDescHi, IDESC_QK,
+                                           (c | kk) ? 1u : 0u);
                     }
-                    if (ok) mma_commit(s_full);
+                    if (!ok) break;
+                    if (!(ok = mbar_wait_clk<true>(rope_full, gt & 1, abort_flag, p.status))) break;
+                    mbar_arrive(s_full);
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)       // 16 dims a step, the keys from tensor memory
+                        mma_bf16_ts_lo(tmem_base + TM_R, tmem_base + TM_K + 8 * kk, base + (OFF_QR >> 4) + 2 * kk, kDescHi,
+                                       IDESC_ROPE, kk ? 1u : 0u);
+                    mma_commit(s_full);
+                    if (t == T - 1) mma_commit(q_free);
                 }
                 ++qi;
             }
@@ -348,6 +340,32 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                         mma_commit(&freed[2 * (gt & 1) + j]);
                     }
                 }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+    } else if (warp == kQueryWarp) {
+        // ------------------------------------------------------------ queries (TMA)
+        int qi = 0;
+        bool ok = true;
+        for (int s = 0; ok; ++s) {
+            const int item = nth_item(p, s);
+            if (item == -1) break;
+            if (item < 0) continue;
+            const Item I = decode_item(p, item);
+            if (item_tiles(p, I, lane) == 0) continue;
+            if (lane == 0) {
+                if (qi > 0) l2_prefetch_bulk(p.q + (int64_t)I.row * (kH * DSA_QK_DIM), kH * DSA_QK_DIM * 2);
+                ok = mbar_wait_clk<true>(q_free, (qi & 1) ^ 1, abort_flag, p.status);
+                if (ok) {
+                    // the query as it is, into the place of its e4m3 parts: dims 64 j.. of the heads go where the rows
+                    // of chunk j % 4 will be, hi rows for j < 4, lo rows for the others
+                    mbar_arrive_expect_tx(q_raw, kH * DSA_QK_DIM * 2);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        tma_load_2d(smem + OFF_QHL + (j & 3) * kBlk + (j >> 2) * (kH * 128), &tmap_q, q_raw, 64 * j, I.row * kH);
+                    tma_load_2d(smem + OFF_QR, &tmap_q, q_raw, kQ8Latent, I.row * kH);
+                }
+                ++qi;
             }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
@@ -440,54 +458,32 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 if (first >= 0 && !convert()) break;
             }
         } else {
-            // half of the rope dims: 64-byte rows, 4 lanes a row, this lane's rows are 32 gw + 8 i + l / 4
-            const int ci = (int)(lane >> 2), pc = (int)(lane & 3);
-            const uint32_t dst = smem_base + OFF_ROPE + (uint32_t)((32 * gw + ci) * 64 + ((pc ^ ((ci >> 1) & 3)) << 4));
+            // A lane carries one key's 64 rope dims (128 bytes) through registers into its lane of tensor memory: the
+            // loads run a tile ahead, and only the store waits for QK of the tile before.
+            const uint32_t tm_k = tmem_base + TM_K + (static_cast<uint32_t>(32 * gw) << 16);
             for (int g = 0; has; ++g) {
                 const int row = rs.resolve(p), first = rs.first;
-                const uint8_t* src[4];
-                uint32_t valid = 0;
+                uint32_t k[32];
+                float sc = row == -1 ? 0.f : 1.f;        // a page outside the pool: a row of zeros with scale 1
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = __shfl_sync(0xffffffffu, row, 8 * i + ci);
-                    src[i] = p.cache + (r < 0 ? 0 : (int64_t)r * kQ8Row + kQ8Latent + pc * 16);
-                    valid |= (r < 0 ? 0u : 16u) << i;
+                for (int i = 0; i < 32; ++i) k[i] = 0;
+                if (row >= 0) {
+                    const uint8_t* src = p.cache + (int64_t)row * kQ8Row + kQ8Latent;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ldg_nc_v8(src + 32 * i, k + 8 * i);
+                    sc = __ldg(p.cache_scale + row);
                 }
-                const float* sc = row >= 0 ? p.cache_scale + row : &g_unit_scale;
                 has = rs.fetch(p, lane, base);
-                if (has && rs.first >= 0 && gw == 0 && lane == 0)   // the next query, into L2
-                    l2_prefetch_bulk(p.q + (int64_t)rs.first * (kH * DSA_QK_DIM), kH * DSA_QK_DIM * 2);
-                // QK of the previous tile is complete: the rope block, and after an item's last tile the query, are free
-                if (g > 0 && !wait(s_full, (g - 1) & 1)) break;
-                if (first >= 0 && gw == 0 && lane == 0) {
-                    // the query as it is, into the place of its e4m3 parts: dims 64 j.. of the heads go where the rows
-                    // of chunk j % 4 will be, hi rows for j < 4, lo rows for the others
-                    mbar_arrive_expect_tx(q_raw, kH * DSA_QK_DIM * 2);
-#pragma unroll 1
-                    for (int j = 0; j < 8; ++j)
-                        tma_load_2d(smem + OFF_QHL + (j & 3) * kBlk + (j >> 2) * (kH * 128), &tmap_q, q_raw, 64 * j, first * kH);
-                    for (int j = 0; j < 2; ++j)
-                        tma_load_2d(smem + OFF_QR + j * (kH * 64), &tmap_pe, q_raw, kQ8Latent + 32 * j, first * kH);
-                }
+                if (g > 0 && !wait(s_full, (g - 1) & 1)) break;   // QK of the tile before is complete
+                tc_fence_after();
                 __syncwarp();
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    if (half) {
-                        if (first >= 0 && !convert()) {
-                            has = false;
-                            break;
-                        }
-                        // the first half is consumed: QK of this tile has begun, so the workers have read the scales before
-                        if (!wait(rope_free, g & 1)) {
-                            has = false;
-                            break;
-                        }
-                        cp_async_4(smem_base + OFF_SC + base * 4, sc, row == -1 ? 0u : 4u);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) cp_async_16(dst + i * 512, src[i] + half * 64, (valid >> i) & 16u);
-                    cp_async_arrive_noinc(rope_full);
-                }
+                tmem_st32(tm_k, k);
+                sc_s[(g & 1) * kTile + base] = sc;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(rope_full);
+                if (first >= 0 && !convert()) break;
             }
         }
         cp_async_wait_all();
@@ -571,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 gok = wait_all(s_full, gt & 1) && gok;
                 tc_fence_after();
                 float2 t2[kHG / 2];               // log2(e) s + log2(c): the exponents before the reference
-                const float c = sc_s[key];
+                const float c = sc_s[(gt & 1) * kTile + key];
                 {
                     uint32_t hi[kHG], lo[kHG], ro[kHG];
                     tmem_ld16(tmem_base + lane_addr + TM_S + h0, hi);
@@ -781,12 +777,10 @@ dsa_status_t launch(const AttnQ8Params& p, cudaStream_t stream) {
     auto kern = mla_attn_q8_kernel<PARTIAL>;
     dsa_status_t st = ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmemBytes);
     if (st != DSA_OK) return st;
-    CUtensorMap tq, tpe;
+    CUtensorMap tq;
     if ((st = make_tmap_bf16_2d(&tq, p.q, DSA_QK_DIM, (uint64_t)p.rows * kH, DSA_QK_DIM * 2, 64, kH)) != DSA_OK) return st;
-    if ((st = make_tmap_bf16_2d_sw64(&tpe, p.q, DSA_QK_DIM, (uint64_t)p.rows * kH, DSA_QK_DIM * 2, 32, kH)) != DSA_OK)
-        return st;
     const int sms = device_sm_count();
-    if (launch_pdl(kern, dim3(p.n_items < sms ? p.n_items : sms), dim3(kThreads), kSmemBytes, stream, tq, tpe, p) !=
+    if (launch_pdl(kern, dim3(p.n_items < sms ? p.n_items : sms), dim3(kThreads), kSmemBytes, stream, tq, p) !=
         cudaSuccess)
         return DSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;

@@ -277,7 +277,7 @@ dsa_status_t mla_sparse_attn_prefill_paged(const void *q, const void *kv_pool,
  * value.  As written by mla_cache_write_q8 the scale is a power of two, which
  * makes every stored value exactly a bf16 number; readers take any positive
  * finite scale in [2^-64, 2^64].  The rope dims stay bf16: they carry the
- * position.  Rows are addressed as in the bf16 cache (dense [B, Nmax] rows or
+ * position.  `cache` is 32-byte aligned (so is every row then).  Rows are addressed as in the bf16 cache (dense [B, Nmax] rows or
  * pages of a pool; rows * 640 may pass 2^32).  No counterpart on the pages,
  * whose caches hold bf16 or float32 rows.
  */
@@ -308,8 +308,8 @@ dsa_status_t mla_sparse_attn_prefill_paged(const void *q, const void *kv_pool,
  * value leaves that token's row unspecified, and no other row.
  * Errors (host): DSA_ERR_INVALID_ARG for a null pointer, R < 1, max_pos < 1, cache_rows < 1,
  * kv_a_stride < 576, eps not finite or < 0, interleave not 0 or 1; DSA_ERR_UNSUPPORTED_SHAPE for
- * cache_rows > 2^31 - 1; DSA_ERR_MISALIGNED for kv_a, norm_w, cos_sin or cache not 16-byte aligned or
- * kv_a_stride not a multiple of 8.
+ * cache_rows > 2^31 - 1; DSA_ERR_MISALIGNED for kv_a, norm_w or cos_sin not 16-byte aligned, cache not
+ * 32-byte aligned or kv_a_stride not a multiple of 8.
  */
 dsa_status_t mla_cache_write_q8(const void *kv_a, int64_t kv_a_stride, const float *norm_w, float eps,
                                 const float *cos_sin, int max_pos, int interleave, const int32_t *pos,

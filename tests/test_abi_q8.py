@@ -37,7 +37,7 @@ def test_write_refusals(lib):
         + [{"R": 0}, {"R": -1}, {"max_pos": 0}, {"cache_rows": 0}, {"kv_a_stride": 568}, {"eps": -1e-6},
            {"eps": math.inf}, {"eps": math.nan}, {"interleave": 2}, {"interleave": -1}],
         SHAPE: [{"cache_rows": 1 << 31}],
-        ALIGN: [{"kv_a": P + 2}, {"norm_w": P + 4}, {"cos_sin": P + 8}, {"cache": P + 8}, {"kv_a_stride": 580}],
+        ALIGN: [{"kv_a": P + 2}, {"norm_w": P + 4}, {"cos_sin": P + 8}, {"cache": P + 16}, {"kv_a_stride": 580}],
     })
 
 
@@ -46,7 +46,7 @@ def test_read_refusals(lib):
     refusals(lib.mla_cache_read_q8, names, (P, P, 1024, P, 8, P, None), {
         INVALID: [{n: None} for n in ("cache", "cache_scale", "slots", "out")] + [{"R": 0}, {"cache_rows": 0}],
         SHAPE: [{"cache_rows": 1 << 31}],
-        ALIGN: [{"cache": P + 8}, {"out": P + 2}],
+        ALIGN: [{"cache": P + 16}, {"out": P + 2}],
     })
     names = ("cache", "cache_scale", "kv_len", "block_table", "bt_stride", "page_size", "num_pages", "B", "Nmax", "out",
              "stream")
@@ -55,7 +55,7 @@ def test_read_refusals(lib):
         + [{"B": 0}, {"Nmax": 0}, {"Nmax": 257}, {"bt_stride": 0}, {"num_pages": 0}],
         SHAPE: [{"page_size": 8}, {"page_size": 48}, {"page_size": 1 << 17}, {"num_pages": 1 << 25},
                 {"B": 1 << 24, "Nmax": 256}, {"B": 1 << 30}],
-        ALIGN: [{"cache": P + 8}, {"out": P + 2}],
+        ALIGN: [{"cache": P + 16}, {"out": P + 2}],
     })
 
 
@@ -64,7 +64,7 @@ ATTN_BAD = {
     + [{"rows": 0}, {"N": 0}, {"scale": 0.0}, {"scale": -1.0}, {"scale": math.nan}, {"scale": math.inf},
        {"out_dtype": 2}, {"out_dtype": -1}],
     SHAPE: [{"top_k": 0}, {"top_k": 2049}, {"rows": 1 << 26}],
-    ALIGN: [{"q": P + 2}, {"cache": P + 8}, {"out": P + 4}],
+    ALIGN: [{"q": P + 2}, {"cache": P + 16}, {"out": P + 4}],
 }
 
 
