@@ -112,24 +112,19 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, v
     }
 }
 
-// The same contract with the limit in SM clocks: reading the global timer once per wait, as the two
-// above do, can outlast the wait itself.  SPIN polls with test_wait, else the thread may be suspended.
-constexpr long long kWaitLimitClocks = 4000000000ll;  // about 2 s
-template <bool SPIN>
-__device__ __forceinline__ bool mbar_wait_clk(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
-    if (SPIN ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (uint32_t it = 1;; ++it) {
-        if (SPIN ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*abort) return false;
-            if (clock64() - t0 > kWaitLimitClocks) {
-                *abort = 1;
-                raise_dev_error(status, DEV_ERR_TIMEOUT);
-                return false;
-            }
+// mbar_wait_spin with the limit as a count of polls (each takes 30 cycles or more, so about 1 s at least):
+// no timer is read, whose first reading can outlast the wait itself, and few registers are held.
+constexpr uint32_t kWaitLimitPolls = 1u << 26;
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+    uint32_t it = 0;
+    while (!mbar_test_wait(bar, parity)) {
+        if ((++it & 255u) == 0 && (*abort || it >= kWaitLimitPolls)) {
+            if (it >= kWaitLimitPolls) raise_dev_error(status, DEV_ERR_TIMEOUT);
+            *abort = 1;
+            return false;
         }
     }
+    return true;
 }
 
 // ---------------------------------------------------------------- grid dependencies
@@ -157,6 +152,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
                  "r"(smem_u32(src)), "r"(c0), "r"(c1)
                  : "memory");
 }
+// Untiled copy global -> shared (both 16-byte aligned, bytes a multiple of 16).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Wait until the committed bulk stores have read their shared-memory source.
 __device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
@@ -167,6 +169,9 @@ __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wa
 // 16-byte copy global -> shared; src_bytes = 0 writes 16 zero bytes.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // Bring [src, src + bytes) into L2 (bytes a multiple of 16, src 16-byte aligned); no completion
 // to wait for
@@ -200,6 +205,9 @@ __device__ __forceinline__ void ldg_nc_v8(const void* p, uint32_t* r) {
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+
+// the same for every state space
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

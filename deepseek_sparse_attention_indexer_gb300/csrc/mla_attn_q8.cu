@@ -69,21 +69,20 @@ constexpr int kGroupThreads = 4 * 32;              // the four warps sharing a h
 constexpr uint32_t kGatherBar = 7;                 // named barriers: 1, 2 workers, 3-6 head groups, 7 gather, 8 rope
 static_assert(kHG == 16 && kWorkerWarps == 16, "warp_transpose_reduce16 takes a head group of 16");
 
-constexpr float kFirstTop = 5.5f;                  // log2 of the first tile's largest P'
+constexpr float kFirstTop = 4.5f;                  // log2 of the first tile's largest P'
 constexpr float kMostTop = 8.75f;                  // log2 of the largest P' (430 <= 448)
-constexpr float kNoRef = 3.0e38f;                  // -m before the reference is set (finite: see mla_attn.cu)
 
 // smem layout
 constexpr int OFF_QHL = 0;                         // 4 chunks x (64 hi rows, 64 lo rows) x 128 B
 constexpr int OFF_QR = OFF_QHL + kChunks * kBlk;   // rope dims of 64 heads: 64 rows x 128 B
 constexpr int OFF_LAT = OFF_QR + kH * 128;         // 2 tiles x 4 latent chunks
 constexpr int OFF_P = OFF_LAT + kStages * kChunks * kBlk;   // 128 keys x (64 hi | 64 lo)
-constexpr int OFF_SC = OFF_P + kBlk;               // float [2][128]: scales of a tile's rows, 0 = no key
-constexpr int OFF_QS = OFF_SC + 2 * kTile * 4;       // float [3][64]: scale * log2(e) * 2^k of a query's heads
-constexpr int OFF_RED = OFF_QS + 3 * kH * 4;       // float [4][64]
+constexpr int OFF_SC = OFF_P + kBlk;               // float4 [2][128]: c, log2 c, 1 / c of a tile's rows; 0, -inf, 0: no key
+constexpr int OFF_QS = OFF_SC + 2 * kTile * 16;       // float [4][64]: scale * log2(e) * 2^k of a query's heads
+constexpr int OFF_RED = OFF_QS + 4 * kH * 4;       // float [4][64]
 constexpr int OFF_MNEG = OFF_RED + 4 * kH * 4;     // float [64]: minus the references
-constexpr int OFF_ALPHA = OFF_MNEG + kH * 4;       // float [64]: rescale factors
-constexpr int OFF_INVL = OFF_ALPHA + kH * 4;       // float [64]
+constexpr int OFF_DELTA = OFF_MNEG + kH * 4;       // float [64]: how far a reference has just risen
+constexpr int OFF_INVL = OFF_DELTA + kH * 4;       // float [64]
 constexpr int OFF_BAR = OFF_INVL + kH * 4;
 // barriers: full[8], free[4], rope_full, s_full, s_free, p_full, q_free, q_raw, q_full
 constexpr int kSlots = kStages * kChunks;
@@ -109,6 +108,8 @@ constexpr uint32_t IDESC_QK = idesc_e4m3_f32(128, 128, false, false);
 constexpr uint32_t IDESC_ROPE = idesc_bf16_f32(128, 64, false, false);
 constexpr uint32_t IDESC_PV = idesc_e4m3_scaled_f32(128, 64, true, true);
 
+__device__ __align__(16) uint8_t g_no_row[kQ8Latent];   // zeros, the latent dims of a slot without a row
+
 struct AttnQ8Params : AttnShape {
     const __nv_bfloat16* q;    // [rows][64][576]
     const uint8_t* cache;      // 640-byte rows
@@ -121,6 +122,7 @@ struct AttnQ8Params : AttnShape {
     float scale_log2;          // scale * log2(e)
     int32_t* status;           // device error word
     PageTable pages;           // paged cache (pages.table == nullptr: dense rows)
+    int l2_prefetch;           // 1: rows go into L2 a tile before their copy
 };
 
 // log2 on the special-function unit; exact for the powers of two that the cache holds.
@@ -154,10 +156,10 @@ struct RowStream {
     const int32_t* at = nullptr;        // this lane's slot of the next tile, and the slots from it to the item's end
     int left = 0, batch = 0, bound = 0;
     int key = -1;
-    int first = -1;                     // the item's query when the fetched tile is its first, else -1
+    bool first = false;                 // the fetched tile is its item's first
 
     __device__ __forceinline__ bool fetch(const AttnQ8Params& p, uint32_t lane, int base) {
-        first = -1;
+        first = false;
         while (tiles == 0) {
             const int it = nth_item(p, s++);
             if (it == -1) return false;
@@ -168,7 +170,7 @@ struct RowStream {
             left = I.slot_end - I.slot0 - base;
             batch = I.batch;
             bound = I.bound;
-            first = I.row;
+            first = true;
         }
         key = left > 0 ? __ldg(at) : -1;
         at += kTile;
@@ -192,17 +194,36 @@ struct RowStream {
 };
 
 template <bool PARTIAL>
+__device__ __forceinline__ void store_lse(const AttnQ8Params& p, const Item& I, int h, float v) {
+    if (PARTIAL)
+        p.part_lse[((int64_t)I.row * p.nsplit + I.split) * kH + h] = v;
+    else if (p.lse)
+        p.lse[(int64_t)I.row * kH + h] = v;
+}
+
+// An item without a selected key: zeros and lse = -inf, by all workers.
+template <bool PARTIAL>
+__device__ __noinline__ void zero_item(const AttnQ8Params& p, const Item& I, int tid) {
+    if (tid < kH) store_lse<PARTIAL>(p, I, tid, -INFINITY);
+    const int n = kH * kDv * (PARTIAL || p.out_f32 ? 4 : 2) / 16;
+    uint4* d = PARTIAL ? reinterpret_cast<uint4*>(p.part_o) + ((int64_t)I.row * p.nsplit + I.split) * n
+                       : static_cast<uint4*>(p.out) + (int64_t)I.row * n;
+#pragma unroll 1
+    for (int i = tid; i < n; i += kWorkers) d[i] = make_uint4(0, 0, 0, 0);
+}
+
+template <bool PARTIAL>
 __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const AttnQ8Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {   // the operands' swizzle counts from 1 KB boundaries; there is no room to round up
         if (threadIdx.x == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
         return;
     }
-    float* sc_s = reinterpret_cast<float*>(smem + OFF_SC);
+    float4* sc_s = reinterpret_cast<float4*>(smem + OFF_SC);
     float* qs_s = reinterpret_cast<float*>(smem + OFF_QS);
     float* red = reinterpret_cast<float*>(smem + OFF_RED);
     float* m_neg = reinterpret_cast<float*>(smem + OFF_MNEG);
-    float* alpha_s = reinterpret_cast<float*>(smem + OFF_ALPHA);
+    float* delta_s = reinterpret_cast<float*>(smem + OFF_DELTA);
     float* invl_s = reinterpret_cast<float*>(smem + OFF_INVL);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
     uint64_t* freed = full + kSlots;
@@ -274,16 +295,32 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             if (T == 0) continue;
             if (lane == 0) {
                 const uint32_t base = (smem_u32(smem) >> 4) | ((16u >> 4) << 16);   // leading offset: one atom wide
-                ok = mbar_wait_clk<true>(q_full, qi & 1, abort_flag, p.status);
+                ok = mbar_poll(q_full, qi & 1, abort_flag, p.status);
                 for (int t = 0; ok && t < T; ++t, ++gt) {
-                    // the workers have read the previous tile's S^T
-                    if (!(ok = mbar_wait_clk<true>(s_free, (gt & 1) ^ 1, abort_flag, p.status))) break;
-                    tc_fence_after();
+                    // A poll between MMAs waits until the tensor core has taken those before it (about 300 cycles), so
+                    // what can be known before the first MMA is looked at before: the rope rows, chunks 0 and 1, and
+                    // whether chunks 2 and 3 have come; last, that the workers have read the previous tile's S^T.
+                    uint64_t* ch = full + 4 * (gt & 1);
+                    const uint32_t par = (gt >> 1) & 1;
                     const uint32_t lat = base + (OFF_LAT >> 4) + (gt & 1) * (kChunks * kBlk >> 4);
+                    ok = mbar_poll(rope_full, gt & 1, abort_flag, p.status) && mbar_poll(ch, par, abort_flag, p.status) &&
+                         mbar_poll(ch + 1, par, abort_flag, p.status);
+                    if (!ok) break;
+                    mbar_arrive(s_full);
+                    const bool all = mbar_test_wait(ch + 2, par) && mbar_test_wait(ch + 3, par);
+                    fence_proxy_async_smem();
+                    if (!(ok = mbar_poll(s_free, (gt & 1) ^ 1, abort_flag, p.status))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)       // 16 dims a step, the keys from tensor memory
+                        mma_bf16_ts_lo(tmem_base + TM_R, tmem_base + TM_K + 8 * kk, base + (OFF_QR >> 4) + 2 * kk, kDescHi,
+                                       IDESC_ROPE, kk ? 1u : 0u);
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c) {
-                        if (!(ok = mbar_wait_clk<true>(&full[4 * (gt & 1) + c], (gt >> 1) & 1, abort_flag, p.status))) break;
-                        fence_proxy_async_smem();
+                        if (c == 2 && !all) {
+                            ok = mbar_poll(ch + 2, par, abort_flag, p.status) && mbar_poll(ch + 3, par, abort_flag, p.status);
+                            fence_proxy_async_smem();
+                        }
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)   // 32 dims a step
                             mma_e4m3_ss_lo(tmem_base + TM_S, lat + c * (kBlk >> 4) + 2 * kk, kDescHi,
@@ -291,13 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                                            (c | kk) ? 1u : 0u);
                     }
                     if (!ok) break;
-                    if (!(ok = mbar_wait_clk<true>(rope_full, gt & 1, abort_flag, p.status))) break;
-                    mbar_arrive(s_full);
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)       // 16 dims a step, the keys from tensor memory
-                        mma_bf16_ts_lo(tmem_base + TM_R, tmem_base + TM_K + 8 * kk, base + (OFF_QR >> 4) + 2 * kk, kDescHi,
-                                       IDESC_ROPE, kk ? 1u : 0u);
                     mma_commit(s_full);
                     if (t == T - 1) mma_commit(q_free);
                 }
@@ -321,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 // row, lo at byte 64
                 const uint32_t base = (smem_u32(smem) >> 4) | ((uint32_t)(kBlk >> 4) << 16);
                 for (int t = 0; ok && t < T; ++t, ++gt) {
-                    if (!(ok = mbar_wait_clk<true>(p_full, gt & 1, abort_flag, p.status))) break;
+                    if (!(ok = mbar_poll(p_full, gt & 1, abort_flag, p.status))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -355,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             if (item_tiles(p, I, lane) == 0) continue;
             if (lane == 0) {
                 if (qi > 0) l2_prefetch_bulk(p.q + (int64_t)I.row * (kH * DSA_QK_DIM), kH * DSA_QK_DIM * 2);
-                ok = mbar_wait_clk<true>(q_free, (qi & 1) ^ 1, abort_flag, p.status);
+                // QK of the item before is complete: its query's place is free
+                ok = mbar_poll(q_free, (qi & 1) ^ 1, abort_flag, p.status);
                 if (ok) {
                     // the query as it is, into the place of its e4m3 parts: dims 64 j.. of the heads go where the rows
                     // of chunk j % 4 will be, hi rows for j < 4, lo rows for the others
@@ -376,12 +407,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         const int gw = (warp - kFirstGather) & 3; // rows 32 gw .. 32 gw + 31 of a tile
         const int qh0 = kQHeads * (warp - kFirstGather);
         const uint32_t smem_base = smem_u32(smem);
-        // One thread polls, a named barrier releases the four warps.  (A thread suspended in try_wait was seen
+        // One thread polls (the roles' pollers on different schedulers), a named barrier releases the four warps.  (A thread suspended in try_wait was seen
         // to resume 800 to 3400 cycles after the phase had completed; threads that all poll take the issue slots
         // of the softmax.)  The answer is the same in every warp: all leave together when a wait gives up.
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
             bool ok = true;
-            if (gw == 0 && lane == 0) ok = mbar_wait_clk<true>(bar, parity, abort_flag, p.status);
+            if (gw == (is_rope ? 2 : 1) && lane == 0) ok = mbar_poll(bar, parity, abort_flag, p.status);
             return named_bar_and(kGatherBar + (is_rope ? 1 : 0), 128, ok);
         };
         // Query head h from its bf16 dims to its e4m3 parts, in place: lane l holds dims 16 l .. 16 l + 15.
@@ -413,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
 #pragma unroll 2
             for (int i = 0; i < kQHeads; ++i) convert_head(qbuf, qh0 + i);
             ++qi;
-            qbuf = qbuf == 2 ? 0 : qbuf + 1;
+            qbuf = (qbuf + 1) & 3;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
@@ -422,49 +453,26 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
 
         RowStream rs;
         const int base = 32 * gw + (int)lane;
+        // `has`: there is a tile to copy, `row` its row; `more`: one is fetched behind it
         bool has = rs.fetch(p, lane, base);
-        if (!is_rope) {
-            // A warp instruction copies a 128-byte block of four different rows, 8 lanes a row: this lane's rows are
-            // 32 gw + 4 i + l / 8.
-            const int ci = (int)(lane >> 3), cc = (int)(lane & 7);
-            const uint32_t dst0 = smem_base + OFF_LAT + (uint32_t)((32 * gw + ci) * 128);
-            const uint32_t sw0 = (uint32_t)((cc ^ ci) << 4), sw1 = (uint32_t)((cc ^ (4 + ci)) << 4);
-            for (int g = 0; has; ++g) {
-                const int row = rs.resolve(p), first = rs.first;
-                const uint8_t* src[8];
-                uint32_t valid = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = __shfl_sync(0xffffffffu, row, 4 * i + ci);
-                    src[i] = p.cache + (r < 0 ? 0 : (int64_t)r * kQ8Row + cc * 16);
-                    valid |= (r < 0 ? 0u : 16u) << i;            // bit 4 + i
-                }
-                has = rs.fetch(p, lane, base);
-                const uint32_t dst = dst0 + (g & 1) * (kChunks * kBlk);
-                bool ok = true;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    ok = wait(&freed[2 * (g & 1) + half], ((g >> 1) & 1) ^ 1);
-                    if (!ok) break;
-#pragma unroll
-                    for (int c = 2 * half; c < 2 * half + 2; ++c) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            cp_async_16(dst + c * kBlk + i * 512 + ((i & 1) ? sw1 : sw0), src[i] + c * 128, (valid >> i) & 16u);
-                        cp_async_arrive_noinc(&full[4 * (g & 1) + c]);
-                    }
-                }
-                if (!ok) break;
-                if (first >= 0 && !convert()) break;
-            }
-        } else {
-            // A lane carries one key's 64 rope dims (128 bytes) through registers into its lane of tensor memory: the
-            // loads run a tile ahead, and only the store waits for QK of the tile before.
-            const uint32_t tm_k = tmem_base + TM_K + (static_cast<uint32_t>(32 * gw) << 16);
-            for (int g = 0; has; ++g) {
-                const int row = rs.resolve(p), first = rs.first;
+        int row = has ? rs.resolve(p) : -1;
+        bool first = rs.first, more = has && rs.fetch(p, lane, base);
+        // latent rows: a warp instruction copies a 128-byte block of four different rows, 8 lanes a row; this lane's
+        // rows are 32 gw + 4 i + l / 8
+        const int ci = (int)(lane >> 3), cc = (int)(lane & 7);
+        const uint32_t dst0 = smem_base + OFF_LAT + (uint32_t)((32 * gw + ci) * 128);
+        const uint32_t sw0 = (uint32_t)((cc ^ ci) << 4), sw1 = (uint32_t)((cc ^ (4 + ci)) << 4);
+        for (int g = 0; has; ++g) {
+            const int row1 = more ? rs.resolve(p) : -1;
+            const bool first1 = rs.first, has1 = more;
+            // a row of a large cache into L2 a tile before it is copied (by the time of the copy HBM has answered)
+            if (p.l2_prefetch && !is_rope && row1 >= 0) l2_prefetch_bulk(p.cache + (int64_t)row1 * kQ8Row, kQ8Row);
+            more = more && rs.fetch(p, lane, base);
+            if (is_rope) {
+                // A lane carries one key's 64 rope dims (128 bytes) through registers into its lane of tensor memory:
+                // the loads run ahead, and only the store waits for QK of the tile before.
                 uint32_t k[32];
-                float sc = row == -1 ? 0.f : 1.f;        // a page outside the pool: a row of zeros with scale 1
+                float sc = 1.f;                   // a page outside the pool: a row of zeros with scale 1
 #pragma unroll
                 for (int i = 0; i < 32; ++i) k[i] = 0;
                 if (row >= 0) {
@@ -473,18 +481,44 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     for (int i = 0; i < 4; ++i) ldg_nc_v8(src + 32 * i, k + 8 * i);
                     sc = __ldg(p.cache_scale + row);
                 }
-                has = rs.fetch(p, lane, base);
                 if (g > 0 && !wait(s_full, (g - 1) & 1)) break;   // QK of the tile before is complete
                 tc_fence_after();
                 __syncwarp();
-                tmem_st32(tm_k, k);
-                sc_s[(g & 1) * kTile + base] = sc;
+                tmem_st32(tmem_base + TM_K + (static_cast<uint32_t>(32 * gw) << 16), k);
+                sc_s[(g & 1) * kTile + base] =
+                    row == -1 ? make_float4(0.f, -INFINITY, 0.f, 0.f) : make_float4(sc, lg2_approx(sc), 1.f / sc, 0.f);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(rope_full);
-                if (first >= 0 && !convert()) break;
+            } else {
+                const uint8_t* mine = row < 0 ? g_no_row : p.cache + (int64_t)row * kQ8Row;
+                const uint8_t* src[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    src[i] = reinterpret_cast<const uint8_t*>(__shfl_sync(
+                                 0xffffffffu, reinterpret_cast<unsigned long long>(mine), 4 * i + ci)) + cc * 16;
+                const uint32_t dst = dst0 + (g & 1) * (kChunks * kBlk);
+                bool ok = true;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    ok = ok && wait(&freed[2 * (g & 1) + half], ((g >> 1) & 1) ^ 1);
+                    if (ok) {
+#pragma unroll
+                        for (int c = 2 * half; c < 2 * half + 2; ++c) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                cp_async_16(dst + c * kBlk + i * 512 + ((i & 1) ? sw1 : sw0), src[i] + c * 128);
+                            cp_async_arrive_noinc(&full[4 * (g & 1) + c]);
+                        }
+                    }
+                }
+                if (!ok) break;
             }
+            if (first && !convert()) break;
+            row = row1;
+            first = first1;
+            has = has1;
         }
         cp_async_wait_all();
     } else if (warp >= kFirstWorker) {
@@ -502,46 +536,24 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         // its warp.
         auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
             bool ok = true;
-            if (tid == 0) ok = mbar_wait_clk<true>(bar, parity, abort_flag, p.status);
+            if (tid == 3 * 32) ok = mbar_poll(bar, parity, abort_flag, p.status);
             return named_bar_and(1, kWorkers, ok);
         };
-        auto pv_done = [&](int g) -> bool {           // PV has consumed tile g
-            bool ok = true;
-            if (lane == 0)
-                ok = mbar_wait_clk<true>(&freed[2 * (g & 1) + 1], (g >> 1) & 1, abort_flag, p.status);
-            __syncwarp();
-            return ok;
+        auto pv_done = [&](int g) -> bool {           // PV has consumed tile g (most often it has: every lane looks)
+            return mbar_poll(&freed[2 * (g & 1) + 1], (g >> 1) & 1, abort_flag, p.status);
         };
 
         // ---- items.  One without a selected key gets zeros and lse = -inf here.
-        int n_s = 0;
-        Item nI{};
-        int nT = 0;
-        auto store_lse = [&](const Item& I, int h, float v) {
-            if (PARTIAL)
-                p.part_lse[((int64_t)I.row * p.nsplit + I.split) * kH + h] = v;
-            else if (p.lse)
-                p.lse[(int64_t)I.row * kH + h] = v;
-        };
+        int n_s = 0, n_item = 0, nT = 0;
         auto next_item = [&]() -> bool {
             for (;;) {
-                const int it = nth_item(p, n_s++);
-                if (it == -1) return false;
-                if (it < 0) continue;
-                nI = decode_item(p, it);
+                n_item = nth_item(p, n_s++);
+                if (n_item == -1) return false;
+                if (n_item < 0) continue;
+                const Item nI = decode_item(p, n_item);
                 nT = item_tiles(p, nI, lane);
                 if (nT > 0) return true;
-                if (tid < kH) store_lse(nI, tid, -INFINITY);
-                if (PARTIAL) {
-                    float* d = p.part_o + ((int64_t)nI.row * p.nsplit + nI.split) * (kH * kDv);
-                    for (int i = tid; i < kH * kDv; i += kWorkers) d[i] = 0.f;
-                } else if (p.out_f32) {
-                    float* d = static_cast<float*>(p.out) + (int64_t)nI.row * (kH * kDv);
-                    for (int i = tid; i < kH * kDv; i += kWorkers) d[i] = 0.f;
-                } else {
-                    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.out) + (int64_t)nI.row * (kH * kDv);
-                    for (int i = tid; i < kH * kDv; i += kWorkers) d[i] = __float2bfloat16_rn(0.f);
-                }
+                zero_item<PARTIAL>(p, nI, tid);
             }
         };
 
@@ -554,11 +566,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         int gt = 0;                               // tiles done by this CTA
         int qbuf = 0;                             // the item's query scales
         while (more && !failed) {
-            const Item I = nI;
-            const int T = nT;
-            more = next_item();
+            const int item = n_item, T = nT;
             named_bar_sync(1, kWorkers);          // the previous item's readers of m_neg / invl are done
-            if (tid < kH) m_neg[tid] = kNoRef;
+            if (tid < kH) m_neg[tid] = 0.f;
+            bool unset = true;
             float2 l2[kHG / 2];                   // row sums of heads (h0 + 2i, h0 + 2i + 1)
 #pragma unroll
             for (int i = 0; i < kHG / 2; ++i) l2[i] = make_float2(0.f, 0.f);
@@ -566,8 +577,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             for (int t = 0; t < T; ++t, ++gt) {
                 gok = wait_all(s_full, gt & 1) && gok;
                 tc_fence_after();
-                float2 t2[kHG / 2];               // log2(e) s + log2(c): the exponents before the reference
-                const float c = sc_s[(gt & 1) * kTile + key];
+                // the exponents e = log2(e) s + log2(c) - m of this key's 16 weights
+                float2 e2[kHG / 2];
+                const float4 sc = sc_s[(gt & 1) * kTile + key];
                 {
                     uint32_t hi[kHG], lo[kHG], ro[kHG];
                     tmem_ld16(tmem_base + lane_addr + TM_S + h0, hi);
@@ -577,8 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_free);
-                    const float lc = c > 0.f ? lg2_approx(c) : -INFINITY;   // no key: weight 0
-                    const float2 lc2 = make_float2(lc, lc), c2 = make_float2(c, c);
+                    const float2 lc2 = make_float2(sc.y, sc.y), c2 = make_float2(sc.x, sc.x);
                     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
                     const float2 sixteenth = make_float2(0.0625f, 0.0625f);
 #pragma unroll
@@ -587,70 +598,69 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                         const float2 b = make_float2(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]));
                         const float2 r = make_float2(__uint_as_float(ro[2 * i]), __uint_as_float(ro[2 * i + 1]));
                         const float2 qs = reinterpret_cast<const float2*>(qs_s + qbuf * kH + h0)[i];
-                        t2[i] = __ffma2_rn(__ffma2_rn(b, sixteenth, a), __fmul2_rn(qs, c2), __ffma2_rn(r, sl2, lc2));
+                        const float2 mn = reinterpret_cast<const float2*>(m_neg + h0)[i];
+                        e2[i] = __ffma2_rn(__ffma2_rn(b, sixteenth, a), __fmul2_rn(qs, c2),
+                                           __ffma2_rn(r, sl2, __fadd2_rn(lc2, mn)));
                     }
                 }
-                float2 e2[kHG / 2];
-                auto shift = [&]() {
-#pragma unroll
-                    for (int h4 = 0; h4 < kHG / 4; ++h4) {
-                        const float4 n4 = reinterpret_cast<const float4*>(m_neg + h0)[h4];
-                        e2[2 * h4] = __fadd2_rn(t2[2 * h4], make_float2(n4.x, n4.y));
-                        e2[2 * h4 + 1] = __fadd2_rn(t2[2 * h4 + 1], make_float2(n4.z, n4.w));
-                    }
-                };
-                shift();
-                // The vote on moving a reference, and the rare move, involve the group's four warps only.
-                bool viol = false;
-#pragma unroll
-                for (int i = 0; i < kHG / 2; ++i) viol |= (e2[i].x > kMostTop) || (e2[i].y > kMostTop);
+                // The vote on moving a reference, and the rare move, involve the group's four warps only.  While no key
+                // has been seen (`unset`, the same in the whole group: a padding slot is one for every head) the
+                // reference is 0 and there is nothing to vote on.
                 bool any_upd = false;
-                if (named_bar_or(group_bar, kGroupThreads, viol)) {
+                bool move = unset;
+                if (!unset) {
+                    float top = e2[0].x;
+#pragma unroll
+                    for (int i = 0; i < kHG / 2; ++i) top = fmaxf(fmaxf(top, e2[i].x), e2[i].y);
+                    move = named_bar_or(group_bar, kGroupThreads, top > kMostTop);
+                }
+                if (move) {
                     float xm[kHG];
 #pragma unroll
                     for (int i = 0; i < kHG / 2; ++i) {
-                        xm[2 * i] = t2[i].x;
-                        xm[2 * i + 1] = t2[i].y;
+                        xm[2 * i] = e2[i].x;
+                        xm[2 * i + 1] = e2[i].y;
                     }
                     const float r = warp_transpose_reduce16<true>(xm, lane);
                     if ((lane & 1u) == 0) red[quad * kH + h0 + (int)(lane >> 1)] = r;
                     named_bar_sync(group_bar, kGroupThreads);
-                    bool upd = false;
+                    bool seen = false;
                     if (ww == 4 * hg && lane < kHG) {   // one lane per head of the group
                         const int h = h0 + (int)lane;
-                        const float mt = fmaxf(fmaxf(red[h], red[kH + h]), fmaxf(red[2 * kH + h], red[3 * kH + h])) - kFirstTop;
-                        const bool unset = (m_neg[h] == kNoRef);
-                        const float mo = -m_neg[h];
-                        float a = 1.f;
-                        if (mt > -INFINITY && (unset || mt > mo + (kMostTop - kFirstTop))) {
-                            a = unset ? 0.f : ex2_approx(mo - mt);
-                            m_neg[h] = -mt;
-                            upd = !unset;
-                        }
-                        alpha_s[h] = a;
+                        const float top = fmaxf(fmaxf(red[h], red[kH + h]), fmaxf(red[2 * kH + h], red[3 * kH + h]));
+                        float d = 0.f;                  // how far the reference rises
+                        if (top > (unset ? -INFINITY : kMostTop)) d = top - kFirstTop;
+                        m_neg[h] -= d;
+                        delta_s[h] = d;
+                        seen = top > -INFINITY;
                     }
-                    any_upd = named_bar_or(group_bar, kGroupThreads, upd);
-                    shift();
-                    if (any_upd) {
+                    // any key at all: the references are set; from then on a move scales the sums
+                    seen = named_bar_or(group_bar, kGroupThreads, seen);
+                    any_upd = !unset;
+                    unset = unset && !seen;
+                    float al[kHG];
 #pragma unroll
-                        for (int h4 = 0; h4 < kHG / 4; ++h4) {
-                            const float4 a4 = reinterpret_cast<const float4*>(alpha_s + h0)[h4];
-                            l2[2 * h4] = __fmul2_rn(l2[2 * h4], make_float2(a4.x, a4.y));
-                            l2[2 * h4 + 1] = __fmul2_rn(l2[2 * h4 + 1], make_float2(a4.z, a4.w));
-                        }
+                    for (int i = 0; i < kHG / 2; ++i) {
+                        const float2 d = reinterpret_cast<const float2*>(delta_s + h0)[i];
+                        e2[i].x -= d.x;
+                        e2[i].y -= d.y;
+                        al[2 * i] = ex2_approx(-d.x);
+                        al[2 * i + 1] = ex2_approx(-d.y);
                     }
+                    if (any_upd)
+#pragma unroll
+                        for (int i = 0; i < kHG / 2; ++i) l2[i] = __fmul2_rn(l2[i], make_float2(al[2 * i], al[2 * i + 1]));
                 }
                 // P' and its two e4m3 parts; the row sum takes the float32 weight with the row's scale divided out
-                const float ic = c > 0.f ? __frcp_rn(c) : 0.f;
                 uint32_t w[kHG / 2];
 #pragma unroll
                 for (int i = 0; i < kHG / 2; ++i) {
                     const float2 pr = make_float2(ex2_approx(e2[i].x), ex2_approx(e2[i].y));
-                    l2[i] = __ffma2_rn(pr, make_float2(ic, ic), l2[i]);
+                    l2[i] = __ffma2_rn(pr, make_float2(sc.z, sc.z), l2[i]);
                     w[i] = split_e4m3x2(pr.x, pr.y);
                 }
                 if (gt > 0) gok = gok && pv_done(gt - 1);   // P^T and O^T are free
-                if (any_upd && t > 0) {
+                if (any_upd) {                    // t > 0: some key came before
                     tc_fence_after();
 #pragma unroll 1
                     for (int ch = 0; ch < kChunks; ++ch) {
@@ -659,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                         tmem_ld16(a, v);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < kHG; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * alpha_s[h0 + k]);
+                        for (int k = 0; k < kHG; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * ex2_approx(-delta_s[h0 + k]));
                         tmem_st16(a, v);
                     }
                     tmem_st_wait();
@@ -675,8 +685,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full);
+                if (t == 0) more = next_item();   // its loads beside PV
             }
-            qbuf = qbuf == 2 ? 0 : qbuf + 1;
+            qbuf = (qbuf + 1) & 3;
             // ---------------- final: l = sum of partial row sums; out = O^T / l
             {
                 float l_part[kHG];
@@ -693,11 +704,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 break;
             }
             tc_fence_after();
+            const Item I = decode_item(p, item);
             if (tid < kH) {
                 const float l = red[tid] + red[kH + tid] + red[2 * kH + tid] + red[3 * kH + tid];
                 // l = 0: every selected key was outside the cache
                 invl_s[tid] = (l > 0.f) ? 1.f / l : (l == 0.f ? 0.f : l);
-                store_lse(I, tid, (l > 0.f) ? (log2f(l) - m_neg[tid]) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l));
+                store_lse<PARTIAL>(p, I, tid, (l > 0.f) ? (log2f(l) - m_neg[tid]) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l));
             }
             named_bar_sync(1, kWorkers);
             // P^T is consumed: each warp takes 1 KB of its block to turn its 32 dims x 16 heads so that a store
@@ -799,6 +811,7 @@ AttnQ8Params base_params(const void* q, const void* cache, const float* cache_sc
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = device_status_ptr();
     p.pages = pages;
+    p.l2_prefetch = device_l2_bytes() > 0 ? 1 : 0;
     return p;
 }
 
