@@ -9,6 +9,7 @@ instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -310,43 +311,47 @@ Q8_ROW = 640        # bytes of a cache row: 512 e4m3 latent dims | 64 bf16 rope 
 NORMS = {"rms": 0, "layer": 1}
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
+# The checks below are a few attribute reads a tensor: a decode step calls these functions once a layer and
+# token, and a call that takes longer on the host than on the device bounds the step.
+_BITS16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
+_F32 = frozenset((torch.float32,))
+_I32 = frozenset((torch.int32,))
+_U8 = frozenset((torch.uint8,))
+_attn_workspace_bytes = functools.lru_cache(maxsize=1024)(attn_workspace_size)   # a function of two integers
 
 
-def _here(device: torch.device, *tensors: Optional[torch.Tensor]):
-    """The kernels launch on the current device, so every tensor has to live there."""
-    _need(device.index == torch.cuda.current_device(), "the tensors are not on the current CUDA device")
-    for t in tensors:
-        _need(t is None or t.device == device, "the tensors are not all on one CUDA device")
+def _current_device() -> int:
+    return torch.cuda.current_device()
 
 
-def _rows_ptr(t: torch.Tensor, width: int, what: str) -> int:
-    """Pointer of a 16-bit tensor whose rows (one a token, `width` elements) may be strided: a slice
-    of a wider projection's output."""
-    _need(t.is_cuda and _is16(t), f"{what}: a bf16 CUDA tensor is expected")
-    row = t[0]
-    _need(row.numel() == width and row.is_contiguous(), f"{what}: rows of {width} contiguous elements are expected")
-    return t.data_ptr()
+def _bad(what: str):
+    raise ValueError(what)
 
 
-def _ints(t: torch.Tensor, n: int, what: str):
-    _need(t.dtype == torch.int32 and t.numel() == n, f"{what}: int32 of {n} elements is expected")
+def _p(t: torch.Tensor, dev: int, dtypes, n: int, what: str) -> int:
+    """Device pointer of a contiguous tensor of n elements on the current device, where the kernels launch."""
+    if t.dtype in dtypes and t.numel() == n and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what}: expected a contiguous tensor of {n} elements of {'/'.join(map(str, sorted(dtypes, key=str)))} "
+                     f"on the current CUDA device, got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-def _cache_q8(cache: torch.Tensor, cache_scale: torch.Tensor) -> int:
-    """Checks an 8-bit cache (uint8 [..., 640] and float32 [...]) and returns its rows."""
-    _need(cache.dtype == torch.uint8 and cache.shape[-1] == Q8_ROW, "the cache is uint8 with rows of 640 bytes")
-    rows = cache.numel() // Q8_ROW
-    _need(cache_scale.dtype == torch.float32 and cache_scale.numel() == rows, "cache_scale is float32, one a row")
-    return rows
+def _opt(t: Optional[torch.Tensor], dev: int, dtypes, n: int, what: str) -> Optional[int]:
+    return None if t is None else _p(t, dev, dtypes, n, what)
 
 
-def _torch_stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream()
-    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+def _rows(t: torch.Tensor, dev: int, inner, what: str):
+    """(pointer, row stride in elements) of a 16-bit tensor whose rows, one a token, are contiguous but may lie
+    apart: a slice of a wider projection's output.  inner: the strides inside a row."""
+    s = t.stride()
+    if t.dtype in _BITS16 and s[1:] == inner and t.get_device() == dev:
+        return t.data_ptr(), s[0]
+    raise ValueError(f"{what}: expected 16-bit rows of strides {inner} on the current CUDA device, got {tuple(t.shape)} "
+                     f"{t.dtype} of strides {s} on {t.device}")
+
+
+def _stream_on(dev: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _new(shape, dtype, device, stream) -> torch.Tensor:
@@ -354,13 +359,21 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
     overlaps the call."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(_torch_stream(stream)):
+    with torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _cos_sin(t: torch.Tensor) -> int:
-    _need(t.dtype == torch.float32 and t.dim() == 2 and t.shape[1] == 64, "cos_sin is float32 [max_pos, 64]")
-    return t.shape[0]
+def _q8_rows(cache: torch.Tensor) -> int:
+    """Rows of an 8-bit cache (uint8, last dim 640)."""
+    if cache.shape[-1] != Q8_ROW:
+        _bad("the cache is uint8 with rows of 640 bytes")
+    return cache.numel() // Q8_ROW
+
+
+def _max_pos(cos_sin: torch.Tensor) -> int:
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
+        _bad("cos_sin is float32 [max_pos, 64]")
+    return cos_sin.shape[0]
 
 
 def mla_cache_write_q8(kv_a: torch.Tensor, norm_w: torch.Tensor, eps: float, cos_sin: torch.Tensor, pos: torch.Tensor,
@@ -371,32 +384,41 @@ def mla_cache_write_q8(kv_a: torch.Tensor, norm_w: torch.Tensor, eps: float, cos
     kv_a [R, 576] bf16 (rows may be strided), norm_w [512] f32, cos_sin [max_pos, 64] f32 (32 cosines |
     32 sines a position), pos and slots [R] int32 (a negative slot skips the token; slots differ), cache
     uint8 [..., 640], cache_scale f32 [...]."""
-    R = kv_a.shape[0]
-    p = _rows_ptr(kv_a, 576, "kv_a") if R else None
-    rows = _cache_q8(cache, cache_scale)
-    _need(norm_w.dtype == torch.float32 and norm_w.numel() == 512, "norm_w is float32 [512]")
-    _ints(pos, R, "pos")
-    _ints(slots, R, "slots")
-    _here(cache.device, kv_a, norm_w, cos_sin, pos, slots, cache_scale)
-    rc = load().mla_cache_write_q8(p, kv_a.stride(0) if R > 1 else 576, _ptr(norm_w), eps, _ptr(cos_sin),
-                                   _cos_sin(cos_sin), 1 if interleave else 0, _ptr(pos), _ptr(slots), R, _ptr(cache),
-                                   _ptr(cache_scale), rows, _stream(stream))
-    _check("mla_cache_write_q8", rc)
+    dev = _current_device()
+    R, width = kv_a.shape
+    if width != 576:
+        _bad("kv_a is [R, 576]")
+    p, ld = _rows(kv_a, dev, (1,), "kv_a")
+    rows, n_pos = _q8_rows(cache), _max_pos(cos_sin)
+    rc = (_lib or load()).mla_cache_write_q8(
+        p, ld if R > 1 else 576, _p(norm_w, dev, _F32, 512, "norm_w"), eps, _p(cos_sin, dev, _F32, n_pos * 64, "cos_sin"), n_pos,
+        1 if interleave else 0, _p(pos, dev, _I32, R, "pos"), _p(slots, dev, _I32, R, "slots"), R,
+        _p(cache, dev, _U8, rows * Q8_ROW, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"), rows,
+        _stream_on(dev, stream))
+    if rc:
+        raise DsaError("mla_cache_write_q8", rc)
 
 
 def mla_cache_read_q8(cache: torch.Tensor, cache_scale: torch.Tensor, slots: torch.Tensor,
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out [R, 576] bf16: the rows `slots` [R] int32 of the 8-bit cache (zeros for a negative slot)."""
-    R = slots.numel()
-    rows = _cache_q8(cache, cache_scale)
-    _ints(slots, R, "slots")
+    dev = _current_device()
+    R, rows = slots.numel(), _q8_rows(cache)
     if out is None:
         out = _new((R, 576), torch.bfloat16, cache.device, stream)
-    _need(_is16(out) and out.numel() == R * 576, "out is bf16 [R, 576]")
-    _here(cache.device, cache_scale, slots, out)
-    rc = load().mla_cache_read_q8(_ptr(cache), _ptr(cache_scale), rows, _ptr(slots), R, _ptr(out), _stream(stream))
-    _check("mla_cache_read_q8", rc)
+    rc = (_lib or load()).mla_cache_read_q8(
+        _p(cache, dev, _U8, rows * Q8_ROW, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"), rows,
+        _p(slots, dev, _I32, R, "slots"), R, _p(out, dev, _BITS16, R * 576, "out"), _stream_on(dev, stream))
+    if rc:
+        raise DsaError("mla_cache_read_q8", rc)
     return out
+
+
+def _table(block_table: torch.Tensor, B: int) -> int:
+    """Pages a sequence of a [B, pages] table."""
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        _bad("block_table is int32 [B, pages]")
+    return block_table.shape[1]
 
 
 def mla_cache_read_q8_paged(cache: torch.Tensor, cache_scale: torch.Tensor, kv_len: torch.Tensor,
@@ -404,44 +426,49 @@ def mla_cache_read_q8_paged(cache: torch.Tensor, cache_scale: torch.Tensor, kv_l
                             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out [B, Nmax, 576] bf16: the kv_len[b] rows of each sequence of a paged 8-bit cache; later rows
     of a given `out` stay as they are (a new one has zeros there)."""
-    B = kv_len.numel()
-    rows = _cache_q8(cache, cache_scale)
-    _ints(kv_len, B, "kv_len")
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B,
-          "block_table is int32 [B, pages]")
+    dev = _current_device()
+    B, rows = kv_len.numel(), _q8_rows(cache)
+    stride = _table(block_table, B)
     if out is None:
-        with torch.cuda.stream(_torch_stream(stream)):
-            out = torch.zeros((B, Nmax, 576), dtype=torch.bfloat16, device=cache.device)
-    _need(_is16(out) and out.numel() == B * Nmax * 576, "out is bf16 [B, Nmax, 576]")
-    _here(cache.device, cache_scale, kv_len, block_table, out)
-    rc = load().mla_cache_read_q8_paged(_ptr(cache), _ptr(cache_scale), _ptr(kv_len), _ptr(block_table),
-                                        block_table.shape[1], page_size, rows // page_size if page_size > 0 else 0, B,
-                                        Nmax, _ptr(out), _stream(stream))
-    _check("mla_cache_read_q8_paged", rc)
+        out = _new((B, Nmax, 576), torch.bfloat16, cache.device, stream)
+        with torch.cuda.stream(torch.cuda.ExternalStream(_stream_on(dev, stream))):
+            out.zero_()
+    rc = (_lib or load()).mla_cache_read_q8_paged(
+        _p(cache, dev, _U8, rows * Q8_ROW, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"),
+        _p(kv_len, dev, _I32, B, "kv_len"), _p(block_table, dev, _I32, B * stride, "block_table"), stride, page_size,
+        rows // page_size if page_size > 0 else 0, B, Nmax, _p(out, dev, _BITS16, B * Nmax * 576, "out"),
+        _stream_on(dev, stream))
+    if rc:
+        raise DsaError("mla_cache_read_q8_paged", rc)
     return out
 
 
-def _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream):
-    """Checks and output buffers the 8-bit attention calls share: (rows, top_k, out, lse, cache rows)."""
-    _need(q.dim() == 3 and q.shape[1] == 64 and q.shape[2] == 576 and _is16(q), "q is bf16 [rows, 64, 576]")
-    rows, top_k = q.shape[0], idx.shape[-1]
-    _ints(idx, rows * top_k, "idx")
-    n = _cache_q8(cache, cache_scale)
+def _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream):
+    """Checks and output buffers the 8-bit attention calls share: the device, the sizes, the tensors to return
+    and the pointers of q, cache, cache_scale, idx, out, lse."""
+    dev = _current_device()
+    rows, heads, width = q.shape
+    if heads != 64 or width != 576:
+        _bad("q is bf16 [rows, 64, 576]")
+    top_k, n = idx.shape[-1], _q8_rows(cache)
     if out is None:
-        _need(out_dtype in (torch.float32, torch.bfloat16), f"attention output must be float32 or bf16, got {out_dtype}")
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            _bad(f"attention output must be float32 or bf16, got {out_dtype}")
         out = _new((rows, 64, 512), out_dtype, q.device, stream)
-    _need(out.numel() == rows * 64 * 512, "out is [rows, 64, 512]")
     if lse is None and want_lse:
         lse = _new((rows, 64), torch.float32, q.device, stream)
-    _need(lse is None or (lse.dtype == torch.float32 and lse.numel() == rows * 64), "lse is float32 [rows, 64]")
-    _here(q.device, cache, cache_scale, idx, out, lse)
-    return rows, top_k, out, lse, n
+    f32 = out.dtype is torch.float32
+    return (dev, rows, top_k, n, out, lse, DSA_OUT_F32 if f32 else DSA_OUT_BF16, _p(q, dev, _BITS16, rows * 36864, "q"),
+            _p(cache, dev, _U8, n * Q8_ROW, "cache"), _p(cache_scale, dev, _F32, n, "cache_scale"),
+            _p(idx, dev, _I32, rows * top_k, "idx"), _p(out, dev, _F32 if f32 else _BITS16, rows * 32768, "out"),
+            _opt(lse, dev, _F32, rows * 64, "lse"))
 
 
-def _decode_workspace(workspace, B, top_k, device, stream):
+def _decode_workspace(workspace, B, top_k, dev, device, stream):
     if workspace is None:
-        return _new((attn_workspace_size(B, top_k),), torch.uint8, device, stream)
-    _need(workspace.device == device, "the workspace is on another device")
+        return _new((_attn_workspace_bytes(B, top_k),), torch.uint8, device, stream)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        _bad("the workspace is contiguous on the current CUDA device")
     return workspace
 
 
@@ -449,10 +476,12 @@ def mla_sparse_attn_prefill_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale
                                scale: float, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                                want_lse: bool = False, stream=None, out_dtype=torch.float32):
     """mla_sparse_attn_prefill over an 8-bit cache: cache uint8 [N, 640], cache_scale f32 [N]."""
-    L, top_k, out, lse, N = _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream)
-    rc = load().mla_sparse_attn_prefill_q8(_ptr(q), _ptr(cache), _ptr(cache_scale), _ptr(idx), L, N, top_k, scale,
-                                           _ptr(out), _out_dtype(out), _ptr(lse), None, 0, _stream(stream))
-    _check("mla_sparse_attn_prefill_q8", rc)
+    dev, L, top_k, N, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
+                                                                      out_dtype, stream)
+    rc = (_lib or load()).mla_sparse_attn_prefill_q8(pq, pc, ps, pi, L, N, top_k, scale, po, od, pl, None, 0,
+                                                     _stream_on(dev, stream))
+    if rc:
+        raise DsaError("mla_sparse_attn_prefill_q8", rc)
     return (out, lse) if want_lse else out
 
 
@@ -461,14 +490,16 @@ def mla_sparse_attn_prefill_q8_paged(q: torch.Tensor, cache: torch.Tensor, cache
                                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                                      want_lse: bool = False, stream=None, out_dtype=torch.float32):
     """mla_sparse_attn_prefill_paged over an 8-bit pool: cache uint8 [num_pages * page_size, 640]."""
-    L, top_k, out, lse, n = _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream)
-    _need(block_table.dtype == torch.int32, "block_table is int32")
-    _need(page_size < 1 or block_table.numel() >= -(-N // page_size), "block_table holds ceil(N / page_size) pages")
-    _here(q.device, block_table)
-    rc = load().mla_sparse_attn_prefill_q8_paged(_ptr(q), _ptr(cache), _ptr(cache_scale), _ptr(block_table), page_size,
-                                                 n // page_size if page_size > 0 else 0, _ptr(idx), L, N, top_k, scale,
-                                                 _ptr(out), _out_dtype(out), _ptr(lse), None, 0, _stream(stream))
-    _check("mla_sparse_attn_prefill_q8_paged", rc)
+    dev, L, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
+                                                                      out_dtype, stream)
+    pages = block_table.numel()
+    if page_size > 0 and pages < -(-N // page_size):
+        _bad("block_table holds ceil(N / page_size) pages")
+    rc = (_lib or load()).mla_sparse_attn_prefill_q8_paged(
+        pq, pc, ps, _p(block_table, dev, _I32, pages, "block_table"), page_size, n // page_size if page_size > 0 else 0, pi,
+        L, N, top_k, scale, po, od, pl, None, 0, _stream_on(dev, stream))
+    if rc:
+        raise DsaError("mla_sparse_attn_prefill_q8_paged", rc)
     return (out, lse) if want_lse else out
 
 
@@ -477,15 +508,16 @@ def mla_sparse_attn_decode_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale:
                               lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                               want_lse: bool = False, stream=None, out_dtype=torch.float32):
     """mla_sparse_attn_decode over an 8-bit cache: cache uint8 [B, Nmax, 640], cache_scale f32 [B, Nmax]."""
-    B, top_k, out, lse, n = _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream)
-    _need(cache.dim() == 3 and cache.shape[0] == B, "the cache is uint8 [B, Nmax, 640]")
-    _ints(kv_len, B, "kv_len")
-    workspace = _decode_workspace(workspace, B, top_k, q.device, stream)
-    _here(q.device, kv_len)
-    rc = load().mla_sparse_attn_decode_q8(_ptr(q), _ptr(cache), _ptr(cache_scale), _ptr(kv_len), _ptr(idx), B,
-                                          cache.shape[1], top_k, scale, _ptr(out), _out_dtype(out), _ptr(lse),
-                                          _ptr(workspace), workspace.nbytes, _stream(stream))
-    _check("mla_sparse_attn_decode_q8", rc)
+    dev, B, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
+                                                                      out_dtype, stream)
+    if cache.dim() != 3 or cache.shape[0] != B:
+        _bad("the cache is uint8 [B, Nmax, 640]")
+    workspace = _decode_workspace(workspace, B, top_k, dev, q.device, stream)
+    rc = (_lib or load()).mla_sparse_attn_decode_q8(
+        pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), pi, B, cache.shape[1], top_k, scale, po, od, pl,
+        workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream))
+    if rc:
+        raise DsaError("mla_sparse_attn_decode_q8", rc)
     return (out, lse) if want_lse else out
 
 
@@ -495,18 +527,16 @@ def mla_sparse_attn_decode_q8_paged(q: torch.Tensor, cache: torch.Tensor, cache_
                                     lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                                     want_lse: bool = False, stream=None, out_dtype=torch.float32):
     """mla_sparse_attn_decode_paged over an 8-bit pool: cache uint8 [num_pages * page_size, 640]."""
-    B, top_k, out, lse, n = _attn_q8_args(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream)
-    _ints(kv_len, B, "kv_len")
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B,
-          "block_table is int32 [B, pages]")
-    workspace = _decode_workspace(workspace, B, top_k, q.device, stream)
-    _here(q.device, kv_len, block_table)
-    rc = load().mla_sparse_attn_decode_q8_paged(_ptr(q), _ptr(cache), _ptr(cache_scale), _ptr(kv_len),
-                                                _ptr(block_table), block_table.shape[1], page_size,
-                                                n // page_size if page_size > 0 else 0, _ptr(idx), B, Nmax, top_k,
-                                                scale, _ptr(out), _out_dtype(out), _ptr(lse), _ptr(workspace),
-                                                workspace.nbytes, _stream(stream))
-    _check("mla_sparse_attn_decode_q8_paged", rc)
+    dev, B, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
+                                                                      out_dtype, stream)
+    stride = _table(block_table, B)
+    workspace = _decode_workspace(workspace, B, top_k, dev, q.device, stream)
+    rc = (_lib or load()).mla_sparse_attn_decode_q8_paged(
+        pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), _p(block_table, dev, _I32, B * stride, "block_table"), stride,
+        page_size, n // page_size if page_size > 0 else 0, pi, B, Nmax, top_k, scale, po, od, pl, workspace.data_ptr(),
+        workspace.nbytes, _stream_on(dev, stream))
+    if rc:
+        raise DsaError("mla_sparse_attn_decode_q8_paged", rc)
     return (out, lse) if want_lse else out
 
 
@@ -520,24 +550,26 @@ def indexer_norm_rope(q: torch.Tensor, k: torch.Tensor, k_w: Optional[torch.Tens
     q [R, 32, 128] and k [R, 128] bf16 (rows may be strided), weights and biases f32 [128] or None (not
     normalised / nothing added), cos_sin [max_pos, 64] f32, pos and slots [R] int32 (a negative slot
     writes no key; slots differ), k_cache bf16 [..., 128], norm "rms" or "layer"."""
-    R = q.shape[0]
-    _need(k.shape[0] == R, "q and k hold one row a token")
-    qp, kp = (_rows_ptr(q, 4096, "q"), _rows_ptr(k, 128, "k")) if R else (None, None)
-    _need(norm in NORMS, f"norm is one of {sorted(NORMS)}")
-    for w in (q_w, q_b, k_w, k_b):
-        _need(w is None or (w.dtype == torch.float32 and w.numel() == 128), "weights and biases are float32 [128]")
-    _need(_is16(k_cache) and k_cache.shape[-1] == 128, "k_cache is bf16 with rows of 128")
-    _ints(pos, R, "pos")
-    _ints(slots, R, "slots")
+    dev = _current_device()
+    R, heads, width = q.shape
+    if heads != 32 or width != 128 or k.shape != (R, 128) or k_cache.shape[-1] != 128:
+        _bad("q is [R, 32, 128], k [R, 128], k_cache [..., 128]")
+    kind = NORMS.get(norm, -1)
+    if kind < 0:
+        _bad(f"norm is one of {sorted(NORMS)}")
+    qp, q_ld = _rows(q, dev, (128, 1), "q")
+    kp, k_ld = _rows(k, dev, (1,), "k")
+    n_pos, rows = _max_pos(cos_sin), k_cache.numel() // 128
     if q_out is None:
         q_out = _new((R, 32, 128), torch.bfloat16, q.device, stream)
-    _need(_is16(q_out) and q_out.numel() == R * 4096, "q_out is bf16 [R, 32, 128]")
-    _here(q.device, k, q_w, q_b, k_w, k_b, cos_sin, pos, slots, k_cache, q_out)
-    rc = load().dsa_indexer_norm_rope(qp, q.stride(0) if R > 1 else 4096, kp, k.stride(0) if R > 1 else 128,
-                                      NORMS[norm], _ptr(q_w), _ptr(q_b), _ptr(k_w), _ptr(k_b), eps, _ptr(cos_sin),
-                                      _cos_sin(cos_sin), 1 if interleave else 0, _ptr(pos), _ptr(slots), R,
-                                      _ptr(q_out), _ptr(k_cache), k_cache.numel() // 128, _stream(stream))
-    _check("dsa_indexer_norm_rope", rc)
+    rc = (_lib or load()).dsa_indexer_norm_rope(
+        qp, q_ld if R > 1 else 4096, kp, k_ld if R > 1 else 128, kind, _opt(q_w, dev, _F32, 128, "q_w"),
+        _opt(q_b, dev, _F32, 128, "q_b"), _opt(k_w, dev, _F32, 128, "k_w"), _opt(k_b, dev, _F32, 128, "k_b"), eps,
+        _p(cos_sin, dev, _F32, n_pos * 64, "cos_sin"), n_pos, 1 if interleave else 0, _p(pos, dev, _I32, R, "pos"),
+        _p(slots, dev, _I32, R, "slots"), R, _p(q_out, dev, _BITS16, R * 4096, "q_out"),
+        _p(k_cache, dev, _BITS16, rows * 128, "k_cache"), rows, _stream_on(dev, stream))
+    if rc:
+        raise DsaError("dsa_indexer_norm_rope", rc)
     return q_out
 
 
