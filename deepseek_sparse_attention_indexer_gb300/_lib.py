@@ -51,6 +51,7 @@ SIGNATURES = {
     "mla_cache_write_q8": (ctypes.c_int32, [_P, _I64, _P, _F, _P, _I, _I, _P, _P, _I, _P, _P, _I64, _P]),
     "mla_cache_read_q8": (ctypes.c_int32, [_P, _P, _I64, _P, _I, _P, _P]),
     "mla_cache_read_q8_paged": (ctypes.c_int32, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    "mla_sparse_attn_q8_workspace_size": (_SZ, [_I, _I]),
     "mla_sparse_attn_prefill_q8": (ctypes.c_int32, [_P, _P, _P, _P, _I, _I, _I, _F, _P, _I, _P, _P, _SZ, _P]),
     "mla_sparse_attn_prefill_q8_paged": (ctypes.c_int32, [_P, _P, _P, _P, _I, _I, _P, _I, _I, _I, _F, _P, _I, _P, _P,
                                                           _SZ, _P]),
@@ -317,7 +318,12 @@ _BITS16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))
 _F32 = frozenset((torch.float32,))
 _I32 = frozenset((torch.int32,))
 _U8 = frozenset((torch.uint8,))
-_attn_workspace_bytes = functools.lru_cache(maxsize=1024)(attn_workspace_size)   # a function of two integers
+
+
+@functools.lru_cache(maxsize=4096)
+def _q8_workspace_bytes(dev: int, B: int, top_k: int) -> int:
+    """The library's answer for a device and two sizes."""
+    return int(load().mla_sparse_attn_q8_workspace_size(B, top_k))
 
 
 def _current_device() -> int:
@@ -464,12 +470,32 @@ def _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream):
             _opt(lse, dev, _F32, rows * 64, "lse"))
 
 
+def attn_q8_workspace_size(B: int, top_k: int) -> int:
+    """Bytes a decode call over an 8-bit cache takes on the current device (0 for many sequences)."""
+    return _q8_workspace_bytes(_current_device(), B, top_k)
+
+
+# Decode workspaces by (device, stream): calls on one stream run in order, so they may share one.  Not used while
+# a graph is being captured (its buffers live in the graph's own pool, one for each call) nor for a given stream.
+_workspaces = {}
+
+
 def _decode_workspace(workspace, B, top_k, dev, device, stream):
+    """(tensor to keep until the call, pointer, bytes)."""
     if workspace is None:
-        return _new((_attn_workspace_bytes(B, top_k),), torch.uint8, device, stream)
-    if workspace.get_device() != dev or not workspace.is_contiguous():
+        need = _q8_workspace_bytes(dev, B, top_k)
+        if need == 0:
+            return None, None, 0
+        if stream is None and not torch.cuda.is_current_stream_capturing():
+            key = (dev, torch._C._cuda_getCurrentRawStream(dev))
+            workspace = _workspaces.get(key)
+            if workspace is None or workspace.nbytes < need:
+                workspace = _workspaces[key] = torch.empty((need,), dtype=torch.uint8, device=device)
+        else:
+            workspace = _new((need,), torch.uint8, device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         _bad("the workspace is contiguous on the current CUDA device")
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def mla_sparse_attn_prefill_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor, idx: torch.Tensor,
@@ -512,10 +538,10 @@ def mla_sparse_attn_decode_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale:
                                                                       out_dtype, stream)
     if cache.dim() != 3 or cache.shape[0] != B:
         _bad("the cache is uint8 [B, Nmax, 640]")
-    workspace = _decode_workspace(workspace, B, top_k, dev, q.device, stream)
+    workspace, pw, n_ws = _decode_workspace(workspace, B, top_k, dev, q.device, stream)
     rc = (_lib or load()).mla_sparse_attn_decode_q8(
         pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), pi, B, cache.shape[1], top_k, scale, po, od, pl,
-        workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream))
+        pw, n_ws, _stream_on(dev, stream))
     if rc:
         raise DsaError("mla_sparse_attn_decode_q8", rc)
     return (out, lse) if want_lse else out
@@ -530,11 +556,10 @@ def mla_sparse_attn_decode_q8_paged(q: torch.Tensor, cache: torch.Tensor, cache_
     dev, B, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
                                                                       out_dtype, stream)
     stride = _table(block_table, B)
-    workspace = _decode_workspace(workspace, B, top_k, dev, q.device, stream)
+    workspace, pw, n_ws = _decode_workspace(workspace, B, top_k, dev, q.device, stream)
     rc = (_lib or load()).mla_sparse_attn_decode_q8_paged(
         pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), _p(block_table, dev, _I32, B * stride, "block_table"), stride,
-        page_size, n // page_size if page_size > 0 else 0, pi, B, Nmax, top_k, scale, po, od, pl, workspace.data_ptr(),
-        workspace.nbytes, _stream_on(dev, stream))
+        page_size, n // page_size if page_size > 0 else 0, pi, B, Nmax, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))
     if rc:
         raise DsaError("mla_sparse_attn_decode_q8_paged", rc)
     return (out, lse) if want_lse else out

@@ -356,6 +356,18 @@ dsa_status_t check_attn_q8(const void* q, const void* cache, const float* cache_
 bool eps_ok(float eps) { return eps >= 0.f && eps < 3.0e38f; }
 }  // namespace
 
+size_t mla_sparse_attn_q8_workspace_size(int B, int top_k) {
+    if (B < 1 || top_k < 1 || top_k > DSA_MAX_TOPK || check_device() != DSA_OK) return 0;
+    return attn_q8_decode_workspace(B, top_k);
+}
+
+namespace {
+dsa_status_t check_workspace(const void* workspace, size_t have, size_t need) {
+    if (need > 0 && !workspace) return DSA_ERR_INVALID_ARG;
+    return have < need ? DSA_ERR_WORKSPACE_TOO_SMALL : DSA_OK;
+}
+}  // namespace
+
 dsa_status_t mla_sparse_attn_prefill_q8(const void* q, const void* cache, const float* cache_scale,
                                         const int32_t* idx, int L, int N, int top_k, float scale, void* out,
                                         int out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
@@ -391,13 +403,13 @@ dsa_status_t mla_sparse_attn_decode_q8(const void* q, const void* cache, const f
                                        const int32_t* kv_len, const int32_t* idx, int B, int Nmax, int top_k,
                                        float scale, void* out, int out_dtype, float* lse, void* workspace,
                                        size_t ws_bytes, void* stream) {
-    if (!kv_len || !workspace) return DSA_ERR_INVALID_ARG;
+    if (!kv_len) return DSA_ERR_INVALID_ARG;
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, B, Nmax, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
     if ((long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
-    if (ws_bytes < attn_decode_workspace(B, top_k)) return DSA_ERR_WORKSPACE_TOO_SMALL;
     if ((st = check_device()) != DSA_OK) return st;
+    if ((st = check_workspace(workspace, ws_bytes, attn_q8_decode_workspace(B, top_k))) != DSA_OK) return st;
     return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
                                  out_dtype == DSA_OUT_F32, lse, workspace, PageTable{},
                                  static_cast<cudaStream_t>(stream));
@@ -408,15 +420,15 @@ dsa_status_t mla_sparse_attn_decode_q8_paged(const void* q, const void* cache, c
                                              int page_size, int num_pages, const int32_t* idx, int B, int Nmax,
                                              int top_k, float scale, void* out, int out_dtype, float* lse,
                                              void* workspace, size_t ws_bytes, void* stream) {
-    if (!kv_len || !workspace) return DSA_ERR_INVALID_ARG;
+    if (!kv_len) return DSA_ERR_INVALID_ARG;
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, B, Nmax, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
     PageTable pt;
     if ((st = make_page_table(block_table, bt_stride, page_size, num_pages, Nmax, &pt)) != DSA_OK) return st;
     if ((long long)B * bt_stride > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
-    if (ws_bytes < attn_decode_workspace(B, top_k)) return DSA_ERR_WORKSPACE_TOO_SMALL;
     if ((st = check_device()) != DSA_OK) return st;
+    if ((st = check_workspace(workspace, ws_bytes, attn_q8_decode_workspace(B, top_k))) != DSA_OK) return st;
     return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
                                  out_dtype == DSA_OUT_F32, lse, workspace, pt, static_cast<cudaStream_t>(stream));
 }

@@ -73,10 +73,6 @@ dsa_status_t launch_attn_prefill(const void* q, const void* kv, const int32_t* i
                                  float scale, void* out, int out_f32, float* lse, const PageTable& pages,
                                  cudaStream_t stream);
 size_t attn_decode_workspace(int B, int top_k);
-// Splits of a sequence's selected keys over CTAs, and the merge of their partial (output, lse) pairs.
-int decode_splits(int B, int top_k);
-dsa_status_t launch_decode_combine(const float* part_o, const float* part_lse, int B, int nsplit, void* out, int out_f32,
-                                   float* lse, cudaStream_t stream);
 dsa_status_t launch_attn_decode_noalloc(const void* q, const void* kv, const int32_t* kv_len, const int32_t* idx,
                                         int B, int Nmax, int top_k, float scale, void* out, int out_f32,
                                         float* lse, cudaStream_t stream);
@@ -94,6 +90,10 @@ dsa_status_t launch_cache_read_q8_paged(const void* cache, const float* cache_sc
 dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, const int32_t* idx,
                                     int L, int N, int top_k, float scale, void* out, int out_f32, float* lse,
                                     const PageTable& pages, cudaStream_t stream);
+size_t attn_q8_decode_workspace(int B, int top_k);
+// Merge of nsplit partial (normalised output, lse) pairs a sequence.
+dsa_status_t launch_decode_combine(const float* part_o, const float* part_lse, int B, int nsplit, void* out, int out_f32,
+                                   float* lse, cudaStream_t stream);
 dsa_status_t launch_attn_q8_decode(const void* q, const void* cache, const float* cache_scale, const int32_t* kv_len,
                                    const int32_t* idx, int B, int Nmax, int top_k, float scale, void* out,
                                    int out_f32, float* lse, void* workspace, const PageTable& pages,

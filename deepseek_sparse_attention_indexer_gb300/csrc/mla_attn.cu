@@ -712,8 +712,6 @@ dsa_status_t launch_kernel(const void* q, int q_rows, const AttnParams& prm, cud
 // share of the merge).  The split count with the least such cost wins, the smaller on a tie
 // (fewer partials to merge).  Rounding the split count up from SMs / B instead left a second,
 // mostly idle round at many batch sizes (B = 16: 160 items on 152 SMs).
-}  // namespace
-
 int decode_splits(int B, int top_k) {
     const int tiles = ceil_div(top_k, kTile);
     const int sms = device_sm_count();
@@ -731,6 +729,8 @@ int decode_splits(int B, int top_k) {
     }
     return best;
 }
+
+}  // namespace
 
 dsa_status_t launch_decode_combine(const float* part_o, const float* part_lse, int B, int nsplit, void* out, int out_f32,
                                    float* lse, cudaStream_t stream) {

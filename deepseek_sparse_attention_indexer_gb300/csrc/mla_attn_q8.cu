@@ -19,21 +19,30 @@
 //     the bf16 kernel's probabilities have.  The row's scale is folded in before the split:
 //     P' = 2^(t - m) with t = log2(e) s + log2(c), so that e4m3's range (2^-9 .. 448, and 2^-13 with
 //     lo) is spent on the weights that the value sum sees; the row sum divides it out again.
-//   * The reference m of a head is set from the query's first tile so that its largest P' is 2^5.5,
+//   * The reference m of a head is set from the query's first tile so that its largest P' is 2^4.5,
 //     and moved when a later one would pass 2^8.75 (e4m3 ends at 448): a higher start would leave
 //     less room and rescale O^T more often, a lower one would lose the small weights sooner (a
-//     weight keeps 8 bits down to 2^-11.5 of the largest at worst, 2^-14.8 at best).
-//   * Shared memory holds 7 latent chunks (128 keys x 128 dims, 16 KB) as a ring, one rope block and
-//     one P^T block beside the 72 KB query: tile t + 1 is gathered, and its QK issued, while tile t is
-//     in its softmax and PV.  Chunk 3 of tile t + 1 takes the place of chunk 0 of tile t.
-//   * Roles (19 warps): warp 0 issues QK, warps 1 and 2 PV (chunks 0, 2 and 1, 3), 16 worker warps
-//     gather (cp.async), convert the query, do the softmax and write the output.  Two PV issuers: one
-//     thread reaches an N = 64 scaled MMA every ~80 cycles, two one every ~52, which is the rate of the
-//     operands' shared-memory reads (6 KB at 128 B a cycle); one N = 128 issuer reaches its 64.
-//   * Decode splits a sequence's selected keys over CTAs and writes partial (normalised output, lse)
-//     pairs; the bf16 path's merge kernel joins them.
+//     weight keeps 8 bits down to 2^-10.5 of the largest at worst, 2^-14.8 at best).
+//   * Shared memory holds two tiles' latent rows (64 KB each), the 72 KB query and one P^T block.  The rope
+//     rows go through registers into tensor memory, as the A operand of their MMA: shared memory is what the
+//     kernel runs short of, and the operand reads of a tile's other MMAs alone take it 2750 cycles.
+//   * Roles (28 warps, registers moved to the workers by setmaxnreg): warp 0 issues QK, warps 1 and 2 PV
+//     (chunks 0, 2 and 1, 3), warp 3 the query's TMA; 4 warps gather latent rows (cp.async), 4 the rope rows and
+//     scales, 16 worker warps do the softmax and write the output; the query, read as bf16, is split in place
+//     by the eight gathering warps when its predecessor's last QK has read the old one.  Two PV issuers: one
+//     thread reaches an N = 64 scaled MMA every 80 cycles, two one every 52; one N = 128 issuer reaches its 64.
+//     Spinning waits are one thread's a role: a poll of an mbarrier takes from the MMAs' shared memory.
+//   * Decode of few sequences splits a sequence's selected keys over CTAs (one item a CTA) and writes partial
+//     (normalised output, lse) pairs, which the bf16 path's merge kernel joins; other calls run whole queries
+//     on persistent CTAs.  Merging inside a thread-block cluster was slower: reading the other CTAs' parts from
+//     distributed shared memory took 13 thousand cycles, storing them there 20 thousand, and a cluster barrier
+//     with the parts in global memory made a call of 8 sequences 18.2 us, against 14.9 with the merge kernel.
+//   * Measured: 4096 queries of 2048 keys 1.26 ms (0.47 of the bf16 matrix peak for the 1088 products a key and
+//     head; about 5000 cycles a tile of 128 keys, whose operand reads, copies and softmax traffic take shared
+//     memory some 3400), decode of 256 sequences 106 us, of 8 14.9 us, of one 13.3 us.
 #include <cuda.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "dsa_q8.cuh"
@@ -52,8 +61,8 @@ constexpr int kQueryWarp = 1 + kPvIssuers;
 constexpr int kRopeWarps = 4;                      // rope rows, scales, the other half of the query
 constexpr int kWorkerWarps = 16;                   // softmax and output
 constexpr int kWorkers = kWorkerWarps * 32;
-// warp 0 QK, warps 1-2 PV, warp 3 the query's TMA; warps 4-7 latent rows, 8-11 rope rows; warps 12-27 workers.  The register split is by
-// warpgroups of four warps out of what the launch holds: 896 threads of 72 registers.
+// warp 0 QK, warps 1-2 PV, warp 3 the query's TMA; warps 4-7 latent rows, 8-11 rope rows; 12-27 workers.
+// The register split is by warpgroups of four warps out of what the launch holds: 896 threads of 72 registers.
 constexpr int kFirstGather = 4;
 constexpr int kFirstRope = kFirstGather + kGatherWarps;
 constexpr int kFirstWorker = kFirstRope + kRopeWarps;
@@ -117,8 +126,8 @@ struct AttnQ8Params : AttnShape {
     void* out;                 // final: [rows][64][512], float32 or bf16 (out_f32)
     int out_f32;
     float* lse;                // final: [rows][64] or nullptr
-    float* part_o;             // partial: [rows][nsplit][64][512]
-    float* part_lse;           // partial: [rows][nsplit][64]
+    float* part_o;             // split: [rows][nsplit][64][512] normalised partial outputs
+    float* part_lse;           // split: [rows][nsplit][64]
     float scale_log2;          // scale * log2(e)
     int32_t* status;           // device error word
     PageTable pages;           // paged cache (pages.table == nullptr: dense rows)
@@ -165,14 +174,15 @@ struct RowStream {
             if (it == -1) return false;
             if (it < 0) continue;
             const Item I = decode_item(p, it);
-            tiles = item_tiles(p, I, lane);
             at = p.idx + (int64_t)I.row * p.top_k + I.slot0 + base;
             left = I.slot_end - I.slot0 - base;
             batch = I.batch;
             bound = I.bound;
             first = true;
+            key = left > 0 ? __ldg(at) : -1;    // beside the loads of item_tiles
+            tiles = item_tiles(p, I, lane);
         }
-        key = left > 0 ? __ldg(at) : -1;
+        if (!first) key = left > 0 ? __ldg(at) : -1;
         at += kTile;
         left -= kTile;
         --tiles;
@@ -193,26 +203,52 @@ struct RowStream {
     }
 };
 
-template <bool PARTIAL>
+// Query head h from its bf16 dims to its e4m3 parts, in place, by a warp: lane l holds dims 16 l .. 16 l + 15.
+__device__ __forceinline__ void convert_head(uint8_t* smem, int qbuf, int h, float scale_log2, uint32_t lane) {
+    const int j = (int)(lane >> 2), pc = 2 * (int)(lane & 3);
+    const uint8_t* raw = smem + OFF_QHL + (j & 3) * kBlk + ((j >> 2) * kH + h) * 128;
+    const uint4 a = *reinterpret_cast<const uint4*>(raw + ((pc ^ (h & 7)) << 4));
+    const uint4 b = *reinterpret_cast<const uint4*>(raw + (((pc + 1) ^ (h & 7)) << 4));
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+    // magnitudes compare as their bit patterns do; every lane has read its dims when this returns
+    const int e = e4m3_scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
+    const float inv = exp2_int(-e);
+    uint32_t s[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] = split_e4m3x2(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
+    uint8_t* d = smem + OFF_QHL + (int)(lane >> 3) * kBlk + h * 128 + (((int)(lane & 7) ^ (h & 7)) << 4);
+    __syncwarp();
+    *reinterpret_cast<uint4*>(d) = make_uint4(lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7]));
+    *reinterpret_cast<uint4*>(d + kH * 128) =
+        make_uint4(highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7]));
+    if (lane == 0) reinterpret_cast<float*>(smem + OFF_QS)[qbuf * kH + h] = scale_log2 * exp2_int(e);
+}
+
+template <bool SPLIT>
 __device__ __forceinline__ void store_lse(const AttnQ8Params& p, const Item& I, int h, float v) {
-    if (PARTIAL)
+    if (SPLIT)
         p.part_lse[((int64_t)I.row * p.nsplit + I.split) * kH + h] = v;
     else if (p.lse)
         p.lse[(int64_t)I.row * kH + h] = v;
 }
 
 // An item without a selected key: zeros and lse = -inf, by all workers.
-template <bool PARTIAL>
-__device__ __noinline__ void zero_item(const AttnQ8Params& p, const Item& I, int tid) {
-    if (tid < kH) store_lse<PARTIAL>(p, I, tid, -INFINITY);
-    const int n = kH * kDv * (PARTIAL || p.out_f32 ? 4 : 2) / 16;
-    uint4* d = PARTIAL ? reinterpret_cast<uint4*>(p.part_o) + ((int64_t)I.row * p.nsplit + I.split) * n
-                       : static_cast<uint4*>(p.out) + (int64_t)I.row * n;
+template <bool SPLIT>
+__device__ __noinline__ void zero_item(const AttnQ8Params& p, int row, int split, int tid) {
+    const Item I{row, split, 0, 0, 0, 0};
+    if (tid < kH) store_lse<SPLIT>(p, I, tid, -INFINITY);
+    const int n = kH * kDv * (SPLIT || p.out_f32 ? 4 : 2) / 16;
+    uint4* d = SPLIT ? reinterpret_cast<uint4*>(p.part_o) + ((int64_t)row * p.nsplit + split) * n
+                     : static_cast<uint4*>(p.out) + (int64_t)row * n;
 #pragma unroll 1
     for (int i = tid; i < n; i += kWorkers) d[i] = make_uint4(0, 0, 0, 0);
 }
 
-template <bool PARTIAL>
+// SPLIT: one item a CTA, a part of a query, into the partial results; else persistent CTAs, whole queries.
+template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const AttnQ8Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {   // the operands' swizzle counts from 1 KB boundaries; there is no room to round up
@@ -251,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         mbar_init(p_full, kWorkerWarps);
         mbar_init(q_free, 1);
         mbar_init(q_raw, 1);
-        mbar_init(q_full, kGatherWarps + kRopeWarps);
+        mbar_init(q_full, SPLIT ? kWorkerWarps : kGatherWarps + kRopeWarps);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -415,34 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             if (gw == (is_rope ? 2 : 1) && lane == 0) ok = mbar_poll(bar, parity, abort_flag, p.status);
             return named_bar_and(kGatherBar + (is_rope ? 1 : 0), 128, ok);
         };
-        // Query head h from its bf16 dims to its e4m3 parts, in place: lane l holds dims 16 l .. 16 l + 15.
-        auto convert_head = [&](int qbuf, int h) {
-            const int j = (int)(lane >> 2), pc = 2 * (int)(lane & 3);
-            const uint8_t* raw = smem + OFF_QHL + (j & 3) * kBlk + ((j >> 2) * kH + h) * 128;
-            const uint4 a = *reinterpret_cast<const uint4*>(raw + ((pc ^ (h & 7)) << 4));
-            const uint4 b = *reinterpret_cast<const uint4*>(raw + (((pc + 1) ^ (h & 7)) << 4));
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            float amax = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
-            // magnitudes compare as their bit patterns do; every lane has read its dims when this returns
-            const int e = e4m3_scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
-            const float inv = exp2_int(-e);
-            uint32_t s[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) s[k] = split_e4m3x2(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
-            uint8_t* d = smem + OFF_QHL + (int)(lane >> 3) * kBlk + h * 128 + (((int)(lane & 7) ^ (h & 7)) << 4);
-            __syncwarp();
-            *reinterpret_cast<uint4*>(d) = make_uint4(lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7]));
-            *reinterpret_cast<uint4*>(d + kH * 128) =
-                make_uint4(highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7]));
-            if (lane == 0) qs_s[qbuf * kH + h] = p.scale_log2 * exp2_int(e);
-        };
         int qi = 0, qbuf = 0;
         auto convert = [&]() -> bool {            // the warp's heads of the item's query, once it has landed
             if (!wait(q_raw, qi & 1)) return false;
 #pragma unroll 2
-            for (int i = 0; i < kQHeads; ++i) convert_head(qbuf, qh0 + i);
+            for (int i = 0; i < kQHeads; ++i) convert_head(smem, qbuf, qh0 + i, p.scale_log2, lane);
             ++qi;
             qbuf = (qbuf + 1) & 3;
             fence_proxy_async_smem();
@@ -515,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 }
                 if (!ok) break;
             }
-            if (first && !convert()) break;
+            if (!SPLIT && first && !convert()) break;   // split: the workers, idle so far, convert the only query
             row = row1;
             first = first1;
             has = has1;
@@ -553,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 const Item nI = decode_item(p, n_item);
                 nT = item_tiles(p, nI, lane);
                 if (nT > 0) return true;
-                zero_item<PARTIAL>(p, nI, tid);
+                zero_item<SPLIT>(p, nI.row, nI.split, tid);
             }
         };
 
@@ -563,6 +576,15 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         bool gok = true;
         bool more = next_item();
         bool failed = false;
+        if (SPLIT && more) {
+            gok = wait_all(q_raw, 0);
+#pragma unroll 1
+            for (int i = 0; i < kH / kWorkerWarps; ++i)
+                convert_head(smem, 0, kH / kWorkerWarps * ww + i, p.scale_log2, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
         int gt = 0;                               // tiles done by this CTA
         int qbuf = 0;                             // the item's query scales
         while (more && !failed) {
@@ -709,20 +731,32 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 const float l = red[tid] + red[kH + tid] + red[2 * kH + tid] + red[3 * kH + tid];
                 // l = 0: every selected key was outside the cache
                 invl_s[tid] = (l > 0.f) ? 1.f / l : (l == 0.f ? 0.f : l);
-                store_lse<PARTIAL>(p, I, tid, (l > 0.f) ? (log2f(l) - m_neg[tid]) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l));
+                store_lse<SPLIT>(p, I, tid,
+                                 (l > 0.f) ? (log2f(l) - m_neg[tid]) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l));
             }
             named_bar_sync(1, kWorkers);
+            if (SPLIT) {                          // the CTA's part, float32: a store of a warp is 128 bytes of a head
+                float* part = p.part_o + (((int64_t)I.row * p.nsplit + I.split) * kH + h0) * kDv + key;
+#pragma unroll 2
+                for (int ch = 0; ch < kChunks; ++ch) {
+                    uint32_t v[kHG];
+                    tmem_ld16(tmem_base + lane_addr + TM_O + 64 * ch + h0, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int h = 0; h < kHG; ++h) __stcg(part + h * kDv + ch * 128, __uint_as_float(v[h]) * invl_s[h0 + h]);
+                }
+                tc_fence_before();
+                continue;
+            }
             // P^T is consumed: each warp takes 1 KB of its block to turn its 32 dims x 16 heads so that a store
             // writes 16 contiguous bytes of a head a lane.
             uint8_t* stage = smem + OFF_P + ww * 1024;
-            const bool f32 = PARTIAL || p.out_f32;
-            float* out32 = PARTIAL ? p.part_o + (((int64_t)I.row * p.nsplit + I.split) * kH + h0) * kDv
-                                   : static_cast<float*>(p.out) + ((int64_t)I.row * kH + h0) * kDv;
+            float* out32 = static_cast<float*>(p.out) + ((int64_t)I.row * kH + h0) * kDv;
             __nv_bfloat16* out16 = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)I.row * kH + h0) * kDv;
 #pragma unroll 1
             for (int ch = 0; ch < kChunks; ++ch) {
                 const int dim0 = ch * 128 + quad * 32;
-                if (f32) {                        // a lane a dim, 8 heads at a time: rows of 32 dims
+                if (p.out_f32) {                  // a lane a dim, 8 heads at a time: rows of 32 dims
                     uint32_t v[kHG];
                     tmem_ld16(tmem_base + lane_addr + TM_O + 64 * ch + h0, v);
                     tmem_ld_wait();
@@ -784,18 +818,43 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
     }
 }
 
-template <bool PARTIAL>
+// Shared-memory limit of a kernel, raised once a device.
+template <bool SPLIT>
+dsa_status_t prepare_kernel() {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> done[kMaxDevices];
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DSA_ERR_CUDA;
+    if (done[dev].load(std::memory_order_acquire)) return DSA_OK;
+    const dsa_status_t st = ensure_smem_attr(reinterpret_cast<const void*>(mla_attn_q8_kernel<SPLIT>), kSmemBytes);
+    if (st == DSA_OK) done[dev].store(true, std::memory_order_release);
+    return st;
+}
+
+template <bool SPLIT>
 dsa_status_t launch(const AttnQ8Params& p, cudaStream_t stream) {
-    auto kern = mla_attn_q8_kernel<PARTIAL>;
-    dsa_status_t st = ensure_smem_attr(reinterpret_cast<const void*>(kern), kSmemBytes);
+    dsa_status_t st = prepare_kernel<SPLIT>();
     if (st != DSA_OK) return st;
     CUtensorMap tq;
     if ((st = make_tmap_bf16_2d(&tq, p.q, DSA_QK_DIM, (uint64_t)p.rows * kH, DSA_QK_DIM * 2, 64, kH)) != DSA_OK) return st;
     const int sms = device_sm_count();
-    if (launch_pdl(kern, dim3(p.n_items < sms ? p.n_items : sms), dim3(kThreads), kSmemBytes, stream, tq, p) !=
-        cudaSuccess)
+    if (launch_pdl(mla_attn_q8_kernel<SPLIT>, dim3(p.n_items < sms ? p.n_items : sms), dim3(kThreads), kSmemBytes, stream,
+                   tq, p) != cudaSuccess)
         return DSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+// Splits of a sequence, at most one item a CTA (SM) in all: a launch takes about as long as an item's tiles
+// and, split, the merge (about two tiles' time); 1, whole sequences, when that is no more.
+void split_tiles(int B, int top_k, int* splits, int* each) {
+    const int tiles = ceil_div(top_k, kTile), most = device_sm_count() / B;
+    *splits = 1;
+    *each = tiles;
+    if (most < 2 || tiles < 2) return;
+    const int n = ceil_div(tiles, most < tiles ? most : tiles);   // tiles an item
+    if (n + 2 > tiles) return;
+    *each = n;
+    *splits = ceil_div(tiles, n);
 }
 
 AttnQ8Params base_params(const void* q, const void* cache, const float* cache_scale, const int32_t* idx, int rows,
@@ -831,18 +890,29 @@ dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const floa
     return launch<false>(p, stream);
 }
 
+size_t attn_q8_decode_workspace(int B, int top_k) {
+    int splits, each;
+    split_tiles(B, top_k, &splits, &each);
+    return splits == 1 ? 0 : (size_t)B * splits * kH * (kDv + 1) * sizeof(float);
+}
+
 dsa_status_t launch_attn_q8_decode(const void* q, const void* cache, const float* cache_scale, const int32_t* kv_len,
                                    const int32_t* idx, int B, int Nmax, int top_k, float scale, void* out,
                                    int out_f32, float* lse, void* workspace, const PageTable& pages,
                                    cudaStream_t stream) {
     AttnQ8Params p = base_params(q, cache, cache_scale, idx, B, Nmax, top_k, scale, pages);
+    int each;
+    split_tiles(B, top_k, &p.nsplit, &each);
     p.kv_len = kv_len;
-    p.split_len = ceil_div(ceil_div(top_k, kTile), decode_splits(B, top_k)) * kTile;
-    p.nsplit = ceil_div(top_k, p.split_len);
+    p.split_len = each * kTile;
     p.n_items = B * p.nsplit;
+    p.out = out;
+    p.out_f32 = out_f32;
+    p.lse = lse;
+    if (p.nsplit == 1) return launch<false>(p, stream);
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = p.part_o + (size_t)B * p.nsplit * kH * kDv;
-    dsa_status_t st = launch<true>(p, stream);
+    const dsa_status_t st = launch<true>(p, stream);
     if (st != DSA_OK) return st;
     return launch_decode_combine(p.part_o, p.part_lse, B, p.nsplit, out, out_f32, lse, stream);
 }

@@ -5,7 +5,7 @@ import math
 import pytest
 
 P = 4096          # a 16-byte aligned non-null address, never dereferenced
-INVALID, SHAPE, ALIGN, SMALL = 1, 2, 3, 4
+INVALID, SHAPE, ALIGN = 1, 2, 3
 
 
 @pytest.fixture(scope="module")
@@ -81,21 +81,22 @@ def test_prefill_refusals(lib):
 
 
 def test_decode_refusals(lib):
-    ws = lib.mla_sparse_attn_workspace_size(4, 1, 64, 1)
-    more = {INVALID: [{"kv_len": None}, {"ws": None}], SMALL: [{"bytes": ws - 1}, {"bytes": 0}], ALIGN: [{"ws": P + 8}]}
     names = ("q", "cache", "cache_scale", "kv_len", "idx", "rows", "N", "top_k", "scale", "out", "out_dtype", "lse", "ws",
              "bytes", "stream")
-    good = (P, P, P, P, P, 4, 256, 64, 0.0625, P, 0, None, P, ws, None)
+    good = (P, P, P, P, P, 4, 256, 64, 0.0625, P, 0, None, P, 1 << 24, None)
+    more = {INVALID: [{"kv_len": None}], ALIGN: [{"ws": P + 8}]}
     refusals(lib.mla_sparse_attn_decode_q8, names, good, ATTN_BAD)
     refusals(lib.mla_sparse_attn_decode_q8, names, good, more)
     refusals(lib.mla_sparse_attn_decode_q8, names, good, {SHAPE: [{"rows": 1 << 20, "N": 1 << 12}]})
     names = ("q", "cache", "cache_scale", "kv_len", "table", "stride", "page", "pages", "idx", "rows", "N", "top_k",
              "scale", "out", "out_dtype", "lse", "ws", "bytes", "stream")
-    good = (P, P, P, P, P, 4, 64, 8, P, 4, 256, 64, 0.0625, P, 0, None, P, ws, None)
+    good = (P, P, P, P, P, 4, 64, 8, P, 4, 256, 64, 0.0625, P, 0, None, P, 1 << 24, None)
     refusals(lib.mla_sparse_attn_decode_q8_paged, names, good, ATTN_BAD)
     refusals(lib.mla_sparse_attn_decode_q8_paged, names, good, more)
     refusals(lib.mla_sparse_attn_decode_q8_paged, names, good,
              {INVALID: [{"table": None}, {"stride": 0}, {"N": 257}, {"pages": 0}], SHAPE: [{"page": 100}]})
+    for B, top_k in ((0, 64), (-1, 64), (4, 0), (4, 2049)):
+        assert lib.mla_sparse_attn_q8_workspace_size(B, top_k) == 0
 
 
 def test_norm_rope_refusals(lib):
