@@ -4,16 +4,22 @@
 // section 5: indexer_rope_interleave).
 //   y = (x - [mean]) * rsqrt(mean((x - [mean])^2) + eps) * w + b,
 //   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin) for the 32 pairs of dims 0..63
-// 16.9 KB a token in and out, a few operations an element.
+// 16.9 KB a token in and out, a few operations an element.  4096 tokens with both norms (69 MB) take 13.3 us, 5.2 TB/s,
+// eight 16-byte loads of a lane in flight: with four 14.0, with two 16.3, with one 24; CTAs of 64 threads, so that
+// a token's end leaves few lanes waiting (256 threads: 14.5 against 14.0, four loads).  8 tokens take 2.1 us, 1.7
+// with two loads: less than the time the host needs to issue the call, so one form serves both.
 #include "dsa_q8.cuh"
 
 namespace dsa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kHeadsPerToken = DSA_INDEXER_HEADS + 1;   // 32 query heads, then the key
+constexpr int kThreads = 64;
+constexpr int kHalves = kThreads / 16;                // half warps a CTA
+constexpr int kHeads = DSA_INDEXER_HEADS;             // query heads of a token, beside its one key
 constexpr int kD = DSA_INDEXER_DIM;
+constexpr int kN = 8;                                 // query heads a half warp
+static_assert(kHeads % kN == 0, "a half warp's heads are of one token");
 
 struct NormRopeParams {
     const __nv_bfloat16 *q, *k;
@@ -23,9 +29,10 @@ struct NormRopeParams {
     const float* cos_sin;
     int max_pos;
     const int32_t *pos, *slots;
-    int units;              // R * 33
+    int R;
     __nv_bfloat16 *q_out, *k_cache;
     int cache_rows;
+    int q_blocks;           // CTAs of queries; those behind them turn keys
     int32_t* status;
 };
 
@@ -36,22 +43,110 @@ __device__ __forceinline__ float half_sum(float x) {
     return x;
 }
 
-__device__ __forceinline__ void load8(const float* w, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+// Half a lane's dims of a head: 4, at `at` and at `at + gap`.
+__device__ __forceinline__ void load8(const float* at, int gap, float2 (&v)[4]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(at)), b = __ldg(reinterpret_cast<const float4*>(at + gap));
+    v[0] = make_float2(a.x, a.y); v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y); v[3] = make_float2(b.z, b.w);
 }
 
-// Half a warp a head: lane l of it holds dims 8l..8l+7 (16 bytes).  Lanes 0..7 hold the turned dims.
-// Every lane of a warp takes part in the shuffles; a half warp without work stores nothing.
+// N heads of one token by half a warp; every lane of the warp takes part in the shuffles, a half warp without
+// work stores nothing.  Lanes 0..7 hold the turned dims, both dims of a pair on one lane: interleaved, lane l has
+// dims 8l..8l+7 (16 bytes); split in halves, lane l < 8 has dims 4l..4l+3 and 32 more (8 bytes each), lane l >= 8
+// dims 8l..8l+7.  The pairs of lane l are 4l..4l+3 either way.  Arithmetic in pairs of floats: the instructions'
+// issue bounds the kernel beside HBM.
+template <bool LAYER, bool INTERLEAVE, int N>
+__device__ __forceinline__ void turn_heads(const __nv_bfloat16* src, __nv_bfloat16* dst, const float* nw, const float* nb,
+                                           const float* cs, float eps, int l, bool live) {
+    const int at = !INTERLEAVE && l < 8 ? 4 * l : 8 * l;        // the lane's first 4 dims
+    const int gap = !INTERLEAVE && l < 8 ? 32 : 4;              // and how much further its last 4 lie
+    uint2 raw[N][2];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        if (INTERLEAVE) {
+            const uint4 v = live ? *reinterpret_cast<const uint4*>(src + n * kD + at) : make_uint4(0, 0, 0, 0);
+            raw[n][0] = make_uint2(v.x, v.y);
+            raw[n][1] = make_uint2(v.z, v.w);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                raw[n][j] = live ? *reinterpret_cast<const uint2*>(src + n * kD + at + j * gap) : make_uint2(0, 0);
+        }
+    }
+    float c[4], s[4];
+    if (l < 8) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(cs) + l);
+        const float4 b = __ldg(reinterpret_cast<const float4*>(cs + 32) + l);
+        c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
+        s[0] = b.x; s[1] = b.y; s[2] = b.z; s[3] = b.w;
+    }
+    float2 w[4], wb[4];
+    if (nw) load8(nw + at, gap, w);
+    if (nb) load8(nb + at, gap, wb);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const uint32_t words[4] = {raw[n][0].x, raw[n][0].y, raw[n][1].x, raw[n][1].y};
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = make_float2(bf16_lo(words[i]), bf16_hi(words[i]));
+        if (nw) {
+            if (LAYER) {
+                const float2 sum = __fadd2_rn(__fadd2_rn(x[0], x[1]), __fadd2_rn(x[2], x[3]));
+                const float mean = half_sum(sum.x + sum.y) * (1.f / kD);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = __fadd2_rn(x[i], make_float2(-mean, -mean));
+            }
+            float2 ss = __fmul2_rn(x[0], x[0]);
+#pragma unroll
+            for (int i = 1; i < 4; ++i) ss = __ffma2_rn(x[i], x[i], ss);
+            const float rstd = rsqrtf(half_sum(ss.x + ss.y) * (1.f / kD) + eps);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = __fmul2_rn(x[i], make_float2(rstd, rstd));
+                x[i] = nb ? __ffma2_rn(x[i], w[i], wb[i]) : __fmul2_rn(x[i], w[i]);
+            }
+        }
+        if (l < 8) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = x[i].x;
+                v[2 * i + 1] = x[i].y;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float &va = v[INTERLEAVE ? 2 * i : i], &vb = v[INTERLEAVE ? 2 * i + 1 : i + 4];
+                const float a = va, b = vb;
+                va = a * c[i] - b * s[i];
+                vb = b * c[i] + a * s[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = make_float2(v[2 * i], v[2 * i + 1]);
+        }
+        if (live) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(x[i].x, x[i].y);
+            if (INTERLEAVE) {
+                *reinterpret_cast<uint4*>(dst + n * kD + at) = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                *reinterpret_cast<uint2*>(dst + n * kD + at) = make_uint2(o[0], o[1]);
+                *reinterpret_cast<uint2*>(dst + n * kD + at + gap) = make_uint2(o[2], o[3]);
+            }
+        }
+    }
+}
+
+// Query CTAs: a half warp has kN heads of a token, whose loads are in flight together and share weights
+// and angles.  Key CTAs: a half warp a token.
 template <bool LAYER, bool INTERLEAVE>
 __global__ void __launch_bounds__(kThreads) indexer_norm_rope_kernel(const NormRopeParams p) {
     griddep_wait();
-    const int unit = blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
     const int l = threadIdx.x & 15;
-    const int token = unit / kHeadsPerToken, h = unit % kHeadsPerToken;
-    const bool is_k = h == DSA_INDEXER_HEADS;
-    bool live = unit < p.units;
+    const bool is_k = (int)blockIdx.x >= p.q_blocks;
+    const int unit = (is_k ? (int)blockIdx.x - p.q_blocks : (int)blockIdx.x) * kHalves + (threadIdx.x >> 4);
+    const int token = is_k ? unit : unit / (kHeads / kN);
+    bool live = token < p.R;
     int pos = 0, slot = 0;
     if (live) {
         pos = __ldg(p.pos + token);
@@ -62,74 +157,15 @@ __global__ void __launch_bounds__(kThreads) indexer_norm_rope_kernel(const NormR
         }
         live = live && slot >= 0;
     }
-    float x[8];
-    {
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live)
-            raw = *reinterpret_cast<const uint4*>((is_k ? p.k + (int64_t)token * p.k_stride
-                                                        : p.q + (int64_t)token * p.q_stride + h * kD) + 8 * l);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = bf16_lo(w[i]);
-            x[2 * i + 1] = bf16_hi(w[i]);
-        }
-    }
-    const float* nw = is_k ? p.k_w : p.q_w;
-    const float* nb = is_k ? p.k_b : p.q_b;
-    float mean = 0.f;
-    if (LAYER) {
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += x[i];
-        mean = half_sum(s) * (1.f / kD);
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i] - mean, x[i] - mean, ss);
-    const float rstd = rsqrtf(half_sum(ss) * (1.f / kD) + p.eps);
-    if (nw) {
-        float w[8];
-        load8(nw + 8 * l, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (x[i] - mean) * rstd * w[i];
-        if (nb) {
-            load8(nb + 8 * l, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] += w[i];
-        }
-    }
     const float* cs = p.cos_sin + (int64_t)(live ? pos : 0) * 64;
-    if (INTERLEAVE) {          // lane l < 8 holds pairs 4l..4l+3
-        if (l < 8) {
-            const float4 c = __ldg(reinterpret_cast<const float4*>(cs) + l);
-            const float4 s = __ldg(reinterpret_cast<const float4*>(cs + 32) + l);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = a * cc[i] - b * sn[i];
-                x[2 * i + 1] = b * cc[i] + a * sn[i];
-            }
-        }
-    } else {                   // dims 8l..8l+7 of lane l < 4 pair with those of lane l + 4
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __shfl_xor_sync(0xffffffffu, x[i], 4);
-        if (l < 8) {
-            float c[8], s[8];
-            load8(cs + 8 * (l & 3), c);
-            load8(cs + 32 + 8 * (l & 3), s);
-            const float sign = l < 4 ? -1.f : 1.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + sign * (y[i] * s[i]);
-        }
+    if (is_k) {
+        turn_heads<LAYER, INTERLEAVE, 1>(p.k + (int64_t)token * p.k_stride, p.k_cache + (int64_t)slot * kD, p.k_w, p.k_b,
+                                         cs, p.eps, l, live);
+    } else {
+        const int h = unit % (kHeads / kN) * kN;
+        turn_heads<LAYER, INTERLEAVE, kN>(p.q + (int64_t)token * p.q_stride + h * kD,
+                                          p.q_out + ((int64_t)token * kHeads + h) * kD, p.q_w, p.q_b, cs, p.eps, l, live);
     }
-    if (!live) return;
-    __nv_bfloat16* dst = is_k ? p.k_cache + (int64_t)slot * kD
-                              : p.q_out + (int64_t)token * (DSA_INDEXER_HEADS * kD) + h * kD;
-    *reinterpret_cast<uint4*>(dst + 8 * l) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                        pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
 }  // namespace
@@ -139,15 +175,15 @@ dsa_status_t launch_indexer_norm_rope(const void* q, int64_t q_stride, const voi
                                       float eps, const float* cos_sin, int max_pos, int interleave,
                                       const int32_t* pos, const int32_t* slots, int R, void* q_out, void* k_cache,
                                       int cache_rows, cudaStream_t stream) {
+    const int q_blocks = ceil_div(R * (kHeads / kN), kHalves);
     const NormRopeParams p{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), q_stride,
-                           k_stride, q_w, q_b, k_w, k_b, eps, cos_sin, max_pos, pos, slots, R * kHeadsPerToken,
+                           k_stride, q_w, q_b, k_w, k_b, eps, cos_sin, max_pos, pos, slots, R,
                            static_cast<__nv_bfloat16*>(q_out), static_cast<__nv_bfloat16*>(k_cache), cache_rows,
-                           device_status_ptr()};
+                           q_blocks, device_status_ptr()};
     auto kern = norm == DSA_NORM_LAYER
                     ? (interleave ? indexer_norm_rope_kernel<true, true> : indexer_norm_rope_kernel<true, false>)
                     : (interleave ? indexer_norm_rope_kernel<false, true> : indexer_norm_rope_kernel<false, false>);
-    const int grid = ceil_div(p.units, kThreads / 16);
-    if (launch_pdl(kern, dim3(grid), dim3(kThreads), 0, stream, p) != cudaSuccess) return DSA_ERR_CUDA;
+    if (launch_pdl(kern, dim3(q_blocks + ceil_div(R, kHalves)), dim3(kThreads), 0, stream, p) != cudaSuccess) return DSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

@@ -844,15 +844,17 @@ dsa_status_t launch(const AttnQ8Params& p, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
-// Splits of a sequence, at most one item a CTA (SM) in all: a launch takes about as long as an item's tiles
-// and, split, the merge (about two tiles' time); 1, whole sequences, when that is no more.
+// Splits of a sequence, at most one item a CTA (SM) in all; 1, whole sequences, when that is no slower.  A launch
+// takes an item's tiles (2.5 us each) and, split, the merge, whose time grows with the sequences: 1 tile's for a
+// few, 3 tiles' for 70.  Whole / split, us: 4 sequences of 2 tiles 15.5 / 12.9; 40 of 3 tiles 18.4 / 17.0; 70 of
+// 4 tiles 21.1 / 22.2, of 5 23.5 / 25.1, of 6 26.0 / 25.3, of 16 54.1 / 41.8.
 void split_tiles(int B, int top_k, int* splits, int* each) {
     const int tiles = ceil_div(top_k, kTile), most = device_sm_count() / B;
     *splits = 1;
     *each = tiles;
     if (most < 2 || tiles < 2) return;
     const int n = ceil_div(tiles, most < tiles ? most : tiles);   // tiles an item
-    if (n + 2 > tiles) return;
+    if (n + 1 + B / 32 > tiles) return;
     *each = n;
     *splits = ceil_div(tiles, n);
 }
