@@ -37,9 +37,10 @@
 //     on persistent CTAs.  Merging inside a thread-block cluster was slower: reading the other CTAs' parts from
 //     distributed shared memory took 13 thousand cycles, storing them there 20 thousand, and a cluster barrier
 //     with the parts in global memory made a call of 8 sequences 18.2 us, against 14.9 with the merge kernel.
-//   * Measured: 4096 queries of 2048 keys 1.26 ms (0.47 of the bf16 matrix peak for the 1088 products a key and
+//   * Measured: 4096 queries of 2048 keys 1.15 ms (0.52 of the bf16 matrix peak for the 1088 products a key and
 //     head; about 5000 cycles a tile of 128 keys, whose operand reads, copies and softmax traffic take shared
-//     memory some 3400), decode of 256 sequences 106 us, of 8 14.9 us, of one 13.3 us.
+//     memory some 3400; without the vote and the softmax's reads of shared memory 1.08, with half of PV or of QK
+//     1.07), decode of 256 sequences 104 us, of 8 14.4 us, of one 12.7 us.
 #include <cuda.h>
 
 #include <atomic>
@@ -131,7 +132,7 @@ struct AttnQ8Params : AttnShape {
     float scale_log2;          // scale * log2(e)
     int32_t* status;           // device error word
     PageTable pages;           // paged cache (pages.table == nullptr: dense rows)
-    int l2_prefetch;           // 1: rows go into L2 a tile before their copy
+    int l2_prefetch;           // 1: rows go into L2 a tile before their copy (want_l2_prefetch)
 };
 
 // log2 on the special-function unit; exact for the powers of two that the cache holds.
@@ -141,21 +142,27 @@ __device__ __forceinline__ float lg2_approx(float x) {
     return y;
 }
 
-// Two values as hi + lo / 16 in e4m3 (|x| <= 448): hi in the low 16 bits of the result, lo in the
-// high ones.  The half-precision step between keeps 11 bits, the difference x - hi is exact.
-__device__ __forceinline__ uint32_t split_e4m3x2(float x, float y) {
-    uint32_t h, back, r;
-    uint16_t hi, lo;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(hi) : "r"(h));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(back));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(r), "r"(0x4c004c00u));   // 16
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(lo) : "r"(r));
-    return (uint32_t)hi | ((uint32_t)lo << 16);
+// Four values as hi + lo / 16 in e4m3 (|x| <= 448): the four hi bytes, the four lo bytes.  The half-precision step
+// between keeps 11 bits, the difference x - hi is exact.
+__device__ __forceinline__ void split_e4m3x4(float x, float y, float z, float w, uint32_t& hi, uint32_t& lo) {
+    asm("{\n\t.reg .b32 a, b, p, q;\n\t.reg .b16 s, t;\n\t"
+        "cvt.rn.f16x2.f32 a, %3, %2;\n\t"
+        "cvt.rn.f16x2.f32 b, %5, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 s, a;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 t, b;\n\t"
+        "mov.b32 %0, {s, t};\n\t"
+        "cvt.rn.f16x2.e4m3x2 p, s;\n\t"
+        "cvt.rn.f16x2.e4m3x2 q, t;\n\t"
+        "sub.rn.f16x2 a, a, p;\n\t"
+        "sub.rn.f16x2 b, b, q;\n\t"
+        "mul.rn.f16x2 a, a, %6;\n\t"
+        "mul.rn.f16x2 b, b, %6;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 s, a;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 t, b;\n\t"
+        "mov.b32 %1, {s, t};\n\t}\n"
+        : "=&r"(hi), "=&r"(lo)
+        : "f"(x), "f"(y), "f"(z), "f"(w), "r"(0x4c004c00u));   // 16, twice
 }
-__device__ __forceinline__ uint32_t lows(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
-__device__ __forceinline__ uint32_t highs(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
 // The rows of this CTA's tiles, tile after tile, one a lane (row `base` of a tile), in two steps so that the
 // loads of one are in flight while the caller works: fetch() loads the selected key of the next tile,
@@ -216,14 +223,15 @@ __device__ __forceinline__ void convert_head(uint8_t* smem, int qbuf, int h, flo
     // magnitudes compare as their bit patterns do; every lane has read its dims when this returns
     const int e = e4m3_scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
     const float inv = exp2_int(-e);
-    uint32_t s[8];
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] = split_e4m3x2(bf16_lo(w[k]) * inv, bf16_hi(w[k]) * inv);
+    for (int k = 0; k < 4; ++k)
+        split_e4m3x4(bf16_lo(w[2 * k]) * inv, bf16_hi(w[2 * k]) * inv, bf16_lo(w[2 * k + 1]) * inv,
+                     bf16_hi(w[2 * k + 1]) * inv, hi[k], lo[k]);
     uint8_t* d = smem + OFF_QHL + (int)(lane >> 3) * kBlk + h * 128 + (((int)(lane & 7) ^ (h & 7)) << 4);
     __syncwarp();
-    *reinterpret_cast<uint4*>(d) = make_uint4(lows(s[0], s[1]), lows(s[2], s[3]), lows(s[4], s[5]), lows(s[6], s[7]));
-    *reinterpret_cast<uint4*>(d + kH * 128) =
-        make_uint4(highs(s[0], s[1]), highs(s[2], s[3]), highs(s[4], s[5]), highs(s[6], s[7]));
+    *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(d + kH * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     if (lane == 0) reinterpret_cast<float*>(smem + OFF_QS)[qbuf * kH + h] = scale_log2 * exp2_int(e);
 }
 
@@ -329,47 +337,67 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             const Item I = decode_item(p, item);
             const int T = item_tiles(p, I, lane);
             if (T == 0) continue;
-            if (lane == 0) {
-                const uint32_t base = (smem_u32(smem) >> 4) | ((16u >> 4) << 16);   // leading offset: one atom wide
-                ok = mbar_poll(q_full, qi & 1, abort_flag, p.status);
-                for (int t = 0; ok && t < T; ++t, ++gt) {
-                    // A poll between MMAs waits until the tensor core has taken those before it (about 300 cycles), so
-                    // what can be known before the first MMA is looked at before: the rope rows, chunks 0 and 1, and
-                    // whether chunks 2 and 3 have come; last, that the workers have read the previous tile's S^T.
-                    uint64_t* ch = full + 4 * (gt & 1);
-                    const uint32_t par = (gt >> 1) & 1;
-                    const uint32_t lat = base + (OFF_LAT >> 4) + (gt & 1) * (kChunks * kBlk >> 4);
-                    ok = mbar_poll(rope_full, gt & 1, abort_flag, p.status) && mbar_poll(ch, par, abort_flag, p.status) &&
-                         mbar_poll(ch + 1, par, abort_flag, p.status);
-                    if (!ok) break;
-                    mbar_arrive(s_full);
-                    const bool all = mbar_test_wait(ch + 2, par) && mbar_test_wait(ch + 3, par);
-                    fence_proxy_async_smem();
-                    if (!(ok = mbar_poll(s_free, (gt & 1) ^ 1, abort_flag, p.status))) break;
-                    tc_fence_after();
+            const uint32_t base = (smem_u32(smem) >> 4) | ((16u >> 4) << 16);   // leading offset: one atom wide
+            for (int t = 0; ok && t < T; ++t, ++gt) {
+                // A poll between MMAs waits until the tensor core has taken those before it (about 300 cycles), and each
+                // of several in a row takes its own time: a lane a barrier, the warp looks at all of them at once.
+                // Lanes 0-3: the rope rows, chunks 0 and 1, that the workers have read the previous tile's S^T; lane 4:
+                // the query; 5, 6: chunks 2 and 3, whose coming may be waited for between the MMAs.
+                uint64_t* ch = full + 4 * (gt & 1);
+                const uint32_t par = (gt >> 1) & 1;
+                uint64_t* mine = lane == 0 ? rope_full : lane == 3 ? s_free : lane == 4 ? q_full
+                                 : lane < 3 ? ch + lane - 1 : lane < 7 ? ch + lane - 3 : ch;
+                const uint32_t mpar = lane == 0 ? gt & 1 : lane == 3 ? (gt & 1) ^ 1 : lane == 4 ? qi & 1 : par;
+                // all of the barriers `need` names: what has come of the seven, 0 when the wait gives up
+                auto poll = [&](uint32_t need) -> uint32_t {
+                    for (uint32_t it = 1;; ++it) {
+                        const uint32_t got = __ballot_sync(0xffffffffu, lane < 7 && mbar_test_wait(mine, mpar));
+                        if ((got & need) == need) return got;
+                        if ((it & 255u) == 0 && (*abort_flag || it >= kWaitLimitPolls)) {
+                            if (it >= kWaitLimitPolls && lane == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
+                            *abort_flag = 1;
+                        }
+                        if (__any_sync(0xffffffffu, (it & 255u) == 0 && *abort_flag)) return 0;
+                    }
+                };
+                const uint32_t got = poll(0x1f);
+                ok = got != 0;
+                if (!ok) break;
+                const uint32_t lat = base + (OFF_LAT >> 4) + (gt & 1) * (kChunks * kBlk >> 4);
+                auto chunk = [&](int c) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)       // 32 dims a step
+                        mma_e4m3_ss_lo(tmem_base + TM_S, lat + c * (kBlk >> 4) + 2 * kk, kDescHi,
+                                       base + (OFF_QHL >> 4) + c * (kBlk >> 4) + 2 * kk, kDescHi, IDESC_QK, (c | kk) ? 1u : 0u);
+                };
+                fence_proxy_async_smem();   // of every lane that saw a barrier, before the lane that issues
+                __syncwarp();
+                tc_fence_after();
+                if (lane == 0) {
+                    chunk(0);
+                    chunk(1);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)       // 16 dims a step, the keys from tensor memory
                         mma_bf16_ts_lo(tmem_base + TM_R, tmem_base + TM_K + 8 * kk, base + (OFF_QR >> 4) + 2 * kk, kDescHi,
                                        IDESC_ROPE, kk ? 1u : 0u);
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        if (c == 2 && !all) {
-                            ok = mbar_poll(ch + 2, par, abort_flag, p.status) && mbar_poll(ch + 3, par, abort_flag, p.status);
-                            fence_proxy_async_smem();
-                        }
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)   // 32 dims a step
-                            mma_e4m3_ss_lo(tmem_base + TM_S, lat + c * (kBlk >> 4) + 2 * kk, kDescHi,
-                                           base + (OFF_QHL >> 4) + c * (kBlk >> 4) + 2 * kk, kDescHi, IDESC_QK,
-                                           (c | kk) ? 1u : 0u);
-                    }
+                }
+                __syncwarp();
+                if ((got & 0x60) != 0x60) {
+                    ok = poll(0x60) != 0;
                     if (!ok) break;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    chunk(2);
+                    chunk(3);
+                    mbar_arrive(s_full);
                     mma_commit(s_full);
                     if (t == T - 1) mma_commit(q_free);
                 }
-                ++qi;
+                __syncwarp();
             }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            ++qi;
         }
     } else if (warp <= kPvIssuers) {
         // ------------------------------------------------------------ PV issuers
@@ -619,8 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                         const float2 a = make_float2(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]));
                         const float2 b = make_float2(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]));
                         const float2 r = make_float2(__uint_as_float(ro[2 * i]), __uint_as_float(ro[2 * i + 1]));
-                        const float2 qs = reinterpret_cast<const float2*>(qs_s + qbuf * kH + h0)[i];
-                        const float2 mn = reinterpret_cast<const float2*>(m_neg + h0)[i];
+                        const float4 q4 = reinterpret_cast<const float4*>(qs_s + qbuf * kH + h0)[i / 2];
+                        const float4 m4 = reinterpret_cast<const float4*>(m_neg + h0)[i / 2];
+                        const float2 qs = (i & 1) ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
+                        const float2 mn = (i & 1) ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y);
                         e2[i] = __ffma2_rn(__ffma2_rn(b, sixteenth, a), __fmul2_rn(qs, c2),
                                            __ffma2_rn(r, sl2, __fadd2_rn(lc2, mn)));
                     }
@@ -673,15 +703,19 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
 #pragma unroll
                         for (int i = 0; i < kHG / 2; ++i) l2[i] = __fmul2_rn(l2[i], make_float2(al[2 * i], al[2 * i + 1]));
                 }
+                // looked at before the exponentials, so that the poll's time does not follow theirs
+                const bool early = gt == 0 || mbar_test_wait(&freed[2 * ((gt - 1) & 1) + 1], ((gt - 1) >> 1) & 1);
                 // P' and its two e4m3 parts; the row sum takes the float32 weight with the row's scale divided out
-                uint32_t w[kHG / 2];
+                uint32_t whi[kHG / 4], wlo[kHG / 4];
 #pragma unroll
-                for (int i = 0; i < kHG / 2; ++i) {
-                    const float2 pr = make_float2(ex2_approx(e2[i].x), ex2_approx(e2[i].y));
-                    l2[i] = __ffma2_rn(pr, make_float2(sc.z, sc.z), l2[i]);
-                    w[i] = split_e4m3x2(pr.x, pr.y);
+                for (int i = 0; i < kHG / 4; ++i) {
+                    const float2 p0 = make_float2(ex2_approx(e2[2 * i].x), ex2_approx(e2[2 * i].y));
+                    const float2 p1 = make_float2(ex2_approx(e2[2 * i + 1].x), ex2_approx(e2[2 * i + 1].y));
+                    l2[2 * i] = __ffma2_rn(p0, make_float2(sc.z, sc.z), l2[2 * i]);
+                    l2[2 * i + 1] = __ffma2_rn(p1, make_float2(sc.z, sc.z), l2[2 * i + 1]);
+                    split_e4m3x4(p0.x, p0.y, p1.x, p1.y, whi[i], wlo[i]);
                 }
-                if (gt > 0) gok = gok && pv_done(gt - 1);   // P^T and O^T are free
+                if (!early) gok = gok && pv_done(gt - 1);   // P^T and O^T are free
                 if (any_upd) {                    // t > 0: some key came before
                     tc_fence_after();
 #pragma unroll 1
@@ -699,10 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 }
                 {   // P^T row `key`: 16 heads hi at 16-byte piece hg of the swizzled row, lo at piece 4 + hg
                     uint8_t* d = smem + OFF_P + key * 128;
-                    *reinterpret_cast<uint4*>(d + ((hg ^ (key & 7)) << 4)) =
-                        make_uint4(lows(w[0], w[1]), lows(w[2], w[3]), lows(w[4], w[5]), lows(w[6], w[7]));
-                    *reinterpret_cast<uint4*>(d + (((4 + hg) ^ (key & 7)) << 4)) =
-                        make_uint4(highs(w[0], w[1]), highs(w[2], w[3]), highs(w[4], w[5]), highs(w[6], w[7]));
+                    *reinterpret_cast<uint4*>(d + ((hg ^ (key & 7)) << 4)) = make_uint4(whi[0], whi[1], whi[2], whi[3]);
+                    *reinterpret_cast<uint4*>(d + (((4 + hg) ^ (key & 7)) << 4)) = make_uint4(wlo[0], wlo[1], wlo[2], wlo[3]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -859,6 +891,14 @@ void split_tiles(int B, int top_k, int* splits, int* each) {
     *splits = ceil_div(tiles, n);
 }
 
+// Rows go into L2 a tile before their copy when the keys of the call are more than half of L2 and an item has 8
+// tiles or more to run ahead in; a prefetch of rows that L2 holds, or of few tiles, only takes from the copies.
+// Without / with, us: 1216 queries at 16k keys (10 MB) 349 / 355, at 131k (84 MB) 379 / 375, at 1M 412 / 397;
+// decode of 152 sequences of 8k 63.3 / 62.8, of 304 of 32k 122.4 / 120.0, of 32 of 131k (4 tiles an item) 29.7 / 30.4.
+int want_l2_prefetch(int64_t keys, int split_len) {
+    return split_len >= 8 * kTile && (size_t)keys * kQ8Row > device_l2_bytes() / 2 ? 1 : 0;
+}
+
 AttnQ8Params base_params(const void* q, const void* cache, const float* cache_scale, const int32_t* idx, int rows,
                          int Nmax, int top_k, float scale, const PageTable& pages) {
     AttnQ8Params p{};
@@ -872,7 +912,6 @@ AttnQ8Params base_params(const void* q, const void* cache, const float* cache_sc
     p.scale_log2 = scale * 1.4426950408889634f;
     p.status = device_status_ptr();
     p.pages = pages;
-    p.l2_prefetch = device_l2_bytes() > 0 ? 1 : 0;
     return p;
 }
 
@@ -886,6 +925,7 @@ dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const floa
     p.nsplit = 1;
     p.split_len = ceil_div(top_k, kTile) * kTile;
     p.n_items = L;
+    p.l2_prefetch = want_l2_prefetch(N, p.split_len);
     p.out = out;
     p.out_f32 = out_f32;
     p.lse = lse;
@@ -908,6 +948,7 @@ dsa_status_t launch_attn_q8_decode(const void* q, const void* cache, const float
     p.kv_len = kv_len;
     p.split_len = each * kTile;
     p.n_items = B * p.nsplit;
+    p.l2_prefetch = want_l2_prefetch((int64_t)B * Nmax, p.split_len);
     p.out = out;
     p.out_f32 = out_f32;
     p.lse = lse;
