@@ -475,9 +475,15 @@ def attn_q8_workspace_size(B: int, top_k: int) -> int:
     return _q8_workspace_bytes(_current_device(), B, top_k)
 
 
-# Decode workspaces by (device, stream): calls on one stream run in order, so they may share one.  Not used while
-# a graph is being captured (its buffers live in the graph's own pool, one for each call) nor for a given stream.
-_workspaces = {}
+# Decode workspaces by (device, stream), a set for each thread: calls that one thread makes on one stream run in
+# order, so they may share one; a call is two kernels, and another thread's may come between them.  Not used while a
+# graph is being captured (its buffers live in the graph's own pool, one for each call) nor for a given stream.
+class _Workspaces(threading.local):
+    def __init__(self):
+        self.by_stream = {}
+
+
+_workspaces = _Workspaces()
 
 
 def _decode_workspace(workspace, B, top_k, dev, device, stream):
@@ -488,9 +494,10 @@ def _decode_workspace(workspace, B, top_k, dev, device, stream):
             return None, None, 0
         if stream is None and not torch.cuda.is_current_stream_capturing():
             key = (dev, torch._C._cuda_getCurrentRawStream(dev))
-            workspace = _workspaces.get(key)
+            by_stream = _workspaces.by_stream
+            workspace = by_stream.get(key)
             if workspace is None or workspace.nbytes < need:
-                workspace = _workspaces[key] = torch.empty((need,), dtype=torch.uint8, device=device)
+                workspace = by_stream[key] = torch.empty((need,), dtype=torch.uint8, device=device)
         else:
             workspace = _new((need,), torch.uint8, device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():

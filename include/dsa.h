@@ -277,9 +277,10 @@ dsa_status_t mla_sparse_attn_prefill_paged(const void *q, const void *kv_pool,
  * value.  As written by mla_cache_write_q8 the scale is a power of two, which
  * makes every stored value exactly a bf16 number; readers take any positive
  * finite scale in [2^-64, 2^64].  The rope dims stay bf16: they carry the
- * position.  `cache` is 32-byte aligned (so is every row then).  Rows are addressed as in the bf16 cache (dense [B, Nmax] rows or
- * pages of a pool; rows * 640 may pass 2^32).  No counterpart on the pages,
- * whose caches hold bf16 or float32 rows.
+ * position.  `cache` is 32-byte aligned (so is every row then).  Rows are
+ * addressed as in the bf16 cache (dense [B, Nmax] rows or pages of a pool;
+ * rows * 640 may pass 2^32).  No counterpart on the pages, whose caches hold
+ * bf16 or float32 rows.
  */
 
 /*
@@ -351,7 +352,11 @@ dsa_status_t mla_cache_read_q8_paged(const void *cache, const float *cache_scale
  * numbers a value (exact for bf16 down to 2^-14 of a head's largest value), and
  * so do the probabilities, whose relative error is at most 2^-8 as in the bf16
  * calls; a probability (times its row's scale) below 2^-10.5 of the head's
- * largest is held to 2^-18.5 of that.
+ * largest is held to 2^-18.5 of that.  Latent dims of a query must be finite
+ * and at most 448 * 2^64 in magnitude (larger ones, infinities among them, are
+ * cut near there); a NaN makes its head's output NaN.
+ * Two calls at once need a workspace each, also on one stream when two threads
+ * issue them: a split call is two kernels.
  */
 size_t mla_sparse_attn_q8_workspace_size(int B, int top_k);
 dsa_status_t mla_sparse_attn_prefill_q8(const void *q, const void *cache, const float *cache_scale,

@@ -21,6 +21,7 @@ Tolerances, from the arithmetic:
   output, by a factor e^(2 d): (e^(2 d) - 1) A more.
 """
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -640,6 +641,38 @@ def test_decode_workspace(dsa):
             with pytest.raises(dsa.DsaError) as e:
                 dsa.mla_sparse_attn_decode_q8(q, cache, scale, kv_len, idx, SCALE, workspace=guard[:need - 16])
             assert e.value.code == 4
+
+
+def test_threads_on_one_stream(dsa):
+    """Decode calls of two threads on the same stream, which may enqueue their kernels in any order: the bits of
+    calls made alone, and no workspace of one in the hands of the other."""
+    g = gen(22)
+    B, N, K = 4, 900, 700
+    cache, scale = make_cache(g, B * N)
+    cache, scale = cache.view(B, N, 640), scale.view(B, N)
+    kv_len = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    qs = [randn(g, B, 64, 576).bfloat16() for _ in range(2)]
+    ids = [choose(g, [N] * B, N, K) for _ in range(2)]
+    want = [dsa.mla_sparse_attn_decode_q8(q, cache, scale, kv_len, i, SCALE) for q, i in zip(qs, ids)]
+    torch.cuda.synchronize()
+    got, held, start = [[], []], [None, None], threading.Barrier(2)
+
+    def work(n):
+        start.wait()
+        for _ in range(100):
+            got[n].append(dsa.mla_sparse_attn_decode_q8(qs[n], cache, scale, kv_len, ids[n], SCALE))
+        held[n] = {w.data_ptr() for w in dsa._workspaces.by_stream.values()}
+        start.wait()
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert held[0] and held[1] and not held[0] & held[1]
+    for n in range(2):
+        assert len(got[n]) == 100 and all(torch.equal(o, want[n]) for o in got[n])
 
 
 def test_wrapper_refusals(dsa):
