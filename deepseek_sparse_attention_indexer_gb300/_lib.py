@@ -321,9 +321,9 @@ _U8 = frozenset((torch.uint8,))
 
 
 @functools.lru_cache(maxsize=4096)
-def _q8_workspace_bytes(dev: int, B: int, top_k: int) -> int:
+def _q8_workspace_bytes(dev: int, rows: int, top_k: int) -> int:
     """The library's answer for a device and two sizes."""
-    return int(load().mla_sparse_attn_q8_workspace_size(B, top_k))
+    return int(load().mla_sparse_attn_q8_workspace_size(rows, top_k))
 
 
 def _current_device() -> int:
@@ -470,13 +470,13 @@ def _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream):
             _opt(lse, dev, _F32, rows * 64, "lse"))
 
 
-def attn_q8_workspace_size(B: int, top_k: int) -> int:
-    """Bytes a decode call over an 8-bit cache takes on the current device (0 for many sequences)."""
-    return _q8_workspace_bytes(_current_device(), B, top_k)
+def attn_q8_workspace_size(rows: int, top_k: int) -> int:
+    """Bytes an attention call of so many queries over an 8-bit cache takes on the current device (0: none)."""
+    return _q8_workspace_bytes(_current_device(), rows, top_k)
 
 
-# Decode workspaces by (device, stream), a set for each thread: calls that one thread makes on one stream run in
-# order, so they may share one; a call is two kernels, and another thread's may come between them.  Not used while a
+# Workspaces of the attention by (device, stream), a set for each thread: calls that one thread makes on one stream run in
+# order, so they may share one; a call is several kernels, and another thread's may come between them.  Not used while a
 # graph is being captured (its buffers live in the graph's own pool, one for each call) nor for a given stream.
 class _Workspaces(threading.local):
     def __init__(self):
@@ -486,10 +486,10 @@ class _Workspaces(threading.local):
 _workspaces = _Workspaces()
 
 
-def _decode_workspace(workspace, B, top_k, dev, device, stream):
+def _q8_workspace(workspace, rows, top_k, dev, device, stream):
     """(tensor to keep until the call, pointer, bytes)."""
     if workspace is None:
-        need = _q8_workspace_bytes(dev, B, top_k)
+        need = _q8_workspace_bytes(dev, rows, top_k)
         if need == 0:
             return None, None, 0
         if stream is None and not torch.cuda.is_current_stream_capturing():
@@ -507,11 +507,13 @@ def _decode_workspace(workspace, B, top_k, dev, device, stream):
 
 def mla_sparse_attn_prefill_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor, idx: torch.Tensor,
                                scale: float, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                               want_lse: bool = False, stream=None, out_dtype=torch.float32):
+                               want_lse: bool = False, stream=None, out_dtype=torch.float32,
+                               workspace: Optional[torch.Tensor] = None):
     """mla_sparse_attn_prefill over an 8-bit cache: cache uint8 [N, 640], cache_scale f32 [N]."""
     dev, L, top_k, N, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
                                                                       out_dtype, stream)
-    rc = (_lib or load()).mla_sparse_attn_prefill_q8(pq, pc, ps, pi, L, N, top_k, scale, po, od, pl, None, 0,
+    workspace, pw, n_ws = _q8_workspace(workspace, L, top_k, dev, q.device, stream)
+    rc = (_lib or load()).mla_sparse_attn_prefill_q8(pq, pc, ps, pi, L, N, top_k, scale, po, od, pl, pw, n_ws,
                                                      _stream_on(dev, stream))
     if rc:
         raise DsaError("mla_sparse_attn_prefill_q8", rc)
@@ -521,16 +523,18 @@ def mla_sparse_attn_prefill_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale
 def mla_sparse_attn_prefill_q8_paged(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor,
                                      block_table: torch.Tensor, page_size: int, idx: torch.Tensor, scale: float, N: int,
                                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                                     want_lse: bool = False, stream=None, out_dtype=torch.float32):
+                                     want_lse: bool = False, stream=None, out_dtype=torch.float32,
+                                     workspace: Optional[torch.Tensor] = None):
     """mla_sparse_attn_prefill_paged over an 8-bit pool: cache uint8 [num_pages * page_size, 640]."""
     dev, L, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
                                                                       out_dtype, stream)
     pages = block_table.numel()
     if page_size > 0 and pages < -(-N // page_size):
         _bad("block_table holds ceil(N / page_size) pages")
+    workspace, pw, n_ws = _q8_workspace(workspace, L, top_k, dev, q.device, stream)
     rc = (_lib or load()).mla_sparse_attn_prefill_q8_paged(
         pq, pc, ps, _p(block_table, dev, _I32, pages, "block_table"), page_size, n // page_size if page_size > 0 else 0, pi,
-        L, N, top_k, scale, po, od, pl, None, 0, _stream_on(dev, stream))
+        L, N, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))
     if rc:
         raise DsaError("mla_sparse_attn_prefill_q8_paged", rc)
     return (out, lse) if want_lse else out
@@ -545,7 +549,7 @@ def mla_sparse_attn_decode_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale:
                                                                       out_dtype, stream)
     if cache.dim() != 3 or cache.shape[0] != B:
         _bad("the cache is uint8 [B, Nmax, 640]")
-    workspace, pw, n_ws = _decode_workspace(workspace, B, top_k, dev, q.device, stream)
+    workspace, pw, n_ws = _q8_workspace(workspace, B, top_k, dev, q.device, stream)
     rc = (_lib or load()).mla_sparse_attn_decode_q8(
         pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), pi, B, cache.shape[1], top_k, scale, po, od, pl,
         pw, n_ws, _stream_on(dev, stream))
@@ -563,7 +567,7 @@ def mla_sparse_attn_decode_q8_paged(q: torch.Tensor, cache: torch.Tensor, cache_
     dev, B, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
                                                                       out_dtype, stream)
     stride = _table(block_table, B)
-    workspace, pw, n_ws = _decode_workspace(workspace, B, top_k, dev, q.device, stream)
+    workspace, pw, n_ws = _q8_workspace(workspace, B, top_k, dev, q.device, stream)
     rc = (_lib or load()).mla_sparse_attn_decode_q8_paged(
         pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), _p(block_table, dev, _I32, B * stride, "block_table"), stride,
         page_size, n // page_size if page_size > 0 else 0, pi, B, Nmax, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))

@@ -358,7 +358,7 @@ bool eps_ok(float eps) { return eps >= 0.f && eps < 3.0e38f; }
 
 size_t mla_sparse_attn_q8_workspace_size(int B, int top_k) {
     if (B < 1 || top_k < 1 || top_k > DSA_MAX_TOPK || check_device() != DSA_OK) return 0;
-    return attn_q8_decode_workspace(B, top_k);
+    return attn_q8_workspace(B, top_k);
 }
 
 namespace {
@@ -371,14 +371,13 @@ dsa_status_t check_workspace(const void* workspace, size_t have, size_t need) {
 dsa_status_t mla_sparse_attn_prefill_q8(const void* q, const void* cache, const float* cache_scale,
                                         const int32_t* idx, int L, int N, int top_k, float scale, void* out,
                                         int out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
-    (void)workspace;
-    (void)ws_bytes;
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
-    if (!aligned16(q) || !aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
+    if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(L, top_k))) != DSA_OK) return st;
     return launch_attn_q8_prefill(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32, lse,
-                                  PageTable{}, static_cast<cudaStream_t>(stream));
+                                  workspace, PageTable{}, static_cast<cudaStream_t>(stream));
 }
 
 dsa_status_t mla_sparse_attn_prefill_q8_paged(const void* q, const void* cache, const float* cache_scale,
@@ -386,17 +385,16 @@ dsa_status_t mla_sparse_attn_prefill_q8_paged(const void* q, const void* cache, 
                                               const int32_t* idx, int L, int N, int top_k, float scale, void* out,
                                               int out_dtype, float* lse, void* workspace, size_t ws_bytes,
                                               void* stream) {
-    (void)workspace;
-    (void)ws_bytes;
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
     PageTable pt;
     const int stride = page_size > 0 ? (int)(((long long)N + page_size - 1) / page_size) : 0;
     if ((st = make_page_table(block_table, stride, page_size, num_pages, N, &pt)) != DSA_OK) return st;
-    if (!aligned16(q) || !aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
+    if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(L, top_k))) != DSA_OK) return st;
     return launch_attn_q8_prefill(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32, lse,
-                                  pt, static_cast<cudaStream_t>(stream));
+                                  workspace, pt, static_cast<cudaStream_t>(stream));
 }
 
 dsa_status_t mla_sparse_attn_decode_q8(const void* q, const void* cache, const float* cache_scale,
@@ -409,7 +407,7 @@ dsa_status_t mla_sparse_attn_decode_q8(const void* q, const void* cache, const f
     if ((long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
-    if ((st = check_workspace(workspace, ws_bytes, attn_q8_decode_workspace(B, top_k))) != DSA_OK) return st;
+    if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(B, top_k))) != DSA_OK) return st;
     return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
                                  out_dtype == DSA_OUT_F32, lse, workspace, PageTable{},
                                  static_cast<cudaStream_t>(stream));
@@ -428,7 +426,7 @@ dsa_status_t mla_sparse_attn_decode_q8_paged(const void* q, const void* cache, c
     if ((long long)B * bt_stride > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
-    if ((st = check_workspace(workspace, ws_bytes, attn_q8_decode_workspace(B, top_k))) != DSA_OK) return st;
+    if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(B, top_k))) != DSA_OK) return st;
     return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
                                  out_dtype == DSA_OUT_F32, lse, workspace, pt, static_cast<cudaStream_t>(stream));
 }

@@ -89,8 +89,8 @@ dsa_status_t launch_cache_read_q8_paged(const void* cache, const float* cache_sc
                                         int Nmax, void* out, const PageTable& pages, cudaStream_t stream);
 dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, const int32_t* idx,
                                     int L, int N, int top_k, float scale, void* out, int out_f32, float* lse,
-                                    const PageTable& pages, cudaStream_t stream);
-size_t attn_q8_decode_workspace(int B, int top_k);
+                                    void* workspace, const PageTable& pages, cudaStream_t stream);
+size_t attn_q8_workspace(int rows, int top_k);
 // Merge of nsplit partial (normalised output, lse) pairs a sequence.
 dsa_status_t launch_decode_combine(const float* part_o, const float* part_lse, int B, int nsplit, void* out, int out_f32,
                                    float* lse, cudaStream_t stream);

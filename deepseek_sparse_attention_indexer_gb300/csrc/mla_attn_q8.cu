@@ -32,9 +32,9 @@
 //     by the eight gathering warps when its predecessor's last QK has read the old one.  Two PV issuers: one
 //     thread reaches an N = 64 scaled MMA every 80 cycles, two one every 52; one N = 128 issuer reaches its 64.
 //     Spinning waits are one thread's a role: a poll of an mbarrier takes from the MMAs' shared memory.
-//   * Decode of few sequences splits a sequence's selected keys over CTAs (one item a CTA) and writes partial
-//     (normalised output, lse) pairs, which the bf16 path's merge kernel joins; other calls run whole queries
-//     on persistent CTAs.  Merging inside a thread-block cluster was slower: reading the other CTAs' parts from
+//   * Queries run whole on persistent CTAs; those behind the last full round of the SMs (all, for few) have
+//     their selected keys cut into parts, one a CTA, which write partial (normalised output, lse) pairs for the
+//     bf16 path's merge kernel.  Merging inside a thread-block cluster was slower: reading the other CTAs' parts from
 //     distributed shared memory took 13 thousand cycles, storing them there 20 thousand, and a cluster barrier
 //     with the parts in global memory made a call of 8 sequences 18.2 us, against 14.9 with the merge kernel.
 //   * Measured: 4096 queries of 2048 keys 1.15 ms (0.52 of the bf16 matrix peak for the 1088 products a key and
@@ -876,19 +876,26 @@ dsa_status_t launch(const AttnQ8Params& p, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
-// Splits of a sequence, at most one item a CTA (SM) in all; 1, whole sequences, when that is no slower.  A launch
-// takes an item's tiles (2.5 us each) and, split, the merge, whose time grows with the sequences: 1 tile's for a
-// few, 3 tiles' for 70.  Whole / split, us: 4 sequences of 2 tiles 15.5 / 12.9; 40 of 3 tiles 18.4 / 17.0; 70 of
-// 4 tiles 21.1 / 22.2, of 5 23.5 / 25.1, of 6 26.0 / 25.3, of 16 54.1 / 41.8.
-void split_tiles(int B, int top_k, int* splits, int* each) {
-    const int tiles = ceil_div(top_k, kTile), most = device_sm_count() / B;
-    *splits = 1;
-    *each = tiles;
-    if (most < 2 || tiles < 2) return;
-    const int n = ceil_div(tiles, most < tiles ? most : tiles);   // tiles an item
-    if (n + 1 + B / 32 > tiles) return;
-    *each = n;
-    *splits = ceil_div(tiles, n);
+// How a launch's queries are cut: `whole` of them run whole on persistent CTAs, the `cut` others in `splits` parts
+// of `each` tiles, one part a CTA (SM), into the workspace, and are merged.
+struct Cut {
+    int whole, cut, splits, each;
+};
+
+// The queries behind the last full round of the SMs are cut when that is no slower: they would take an item's
+// tiles (2.6 us each) with most SMs idle, and take, cut, a part's tiles and the merge, whose time grows with the
+// queries (1 tile's for a few, 3 tiles' for 70), and behind whole queries a second launch (2 tiles').  Whole / cut,
+// us: 1 query of 16 tiles 45.7 / 12.6; 4 of 2 tiles 15.5 / 12.9; 40 of 3 18.4 / 17.0; 70 of 4 21.1 / 22.2, of 5
+// 23.5 / 25.1, of 6 26.0 / 25.3; behind a full round, 1 of 16 tiles 87.8 / 60.3, 76 of 16 89.1 / 84.9, 8 of 3 tiles
+// 30.0 / 30.8, of 4 33.8 / 33.0, 38 of 4 34.1 / 38.9, 68 of 8 52.5 / 55.9.
+Cut cut_rows(int rows, int top_k) {
+    const int sms = device_sm_count(), tiles = ceil_div(top_k, kTile);
+    if (sms < 1) return Cut{rows, 0, 1, tiles};
+    const int rest = rows % sms, most = rest > 0 ? sms / rest : 1;
+    if (most < 2 || tiles < 2) return Cut{rows, 0, 1, tiles};
+    const int n = ceil_div(tiles, most < tiles ? most : tiles);   // tiles a part
+    if (n + 1 + rest / 32 + (rows > rest ? 2 : 0) > tiles) return Cut{rows, 0, 1, tiles};
+    return Cut{rows - rest, rest, ceil_div(tiles, n), n};
 }
 
 // Rows go into L2 a tile before their copy when the keys of the call are more than half of L2 and an item has 8
@@ -899,65 +906,90 @@ int want_l2_prefetch(int64_t keys, int split_len) {
     return split_len >= 8 * kTile && (size_t)keys * kQ8Row > device_l2_bytes() / 2 ? 1 : 0;
 }
 
-AttnQ8Params base_params(const void* q, const void* cache, const float* cache_scale, const int32_t* idx, int rows,
-                         int Nmax, int top_k, float scale, const PageTable& pages) {
+AttnQ8Params base_params(const void* q, const void* cache, const float* cache_scale, const int32_t* idx, int Nmax,
+                         int top_k, float scale, void* out, int out_f32, float* lse, const PageTable& pages) {
     AttnQ8Params p{};
     p.idx = idx;
-    p.rows = rows;
     p.Nmax = Nmax;
     p.top_k = top_k;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.cache = static_cast<const uint8_t*>(cache);
     p.cache_scale = cache_scale;
     p.scale_log2 = scale * 1.4426950408889634f;
+    p.out = out;
+    p.out_f32 = out_f32;
+    p.lse = lse;
     p.status = device_status_ptr();
     p.pages = pages;
     return p;
 }
 
+// The queries from `first` on.
+AttnQ8Params from_row(AttnQ8Params p, int first) {
+    p.q += (int64_t)first * kH * DSA_QK_DIM;
+    p.idx += (int64_t)first * p.top_k;
+    p.out = static_cast<char*>(p.out) + (int64_t)first * kH * kDv * (p.out_f32 ? 4 : 2);
+    if (p.lse) p.lse += (int64_t)first * kH;
+    if (p.kv_len) p.kv_len += first;
+    if (!p.prefill) {               // a sequence each: their rows, or their lines of the page table
+        if (p.pages.table)
+            p.pages.table += (int64_t)first * p.pages.stride;
+        else {
+            p.cache += (int64_t)first * p.Nmax * kQ8Row;
+            p.cache_scale += (int64_t)first * p.Nmax;
+        }
+    }
+    return p;
+}
+
+dsa_status_t launch_rows(AttnQ8Params p, int rows, void* workspace, cudaStream_t stream) {
+    const Cut c = cut_rows(rows, p.top_k);
+    const int64_t keys = (p.prefill ? 1 : (int64_t)rows) * p.Nmax;
+    dsa_status_t st = DSA_OK;
+    if (c.whole > 0) {
+        p.rows = p.n_items = c.whole;
+        p.nsplit = 1;
+        p.split_len = ceil_div(p.top_k, kTile) * kTile;
+        p.l2_prefetch = want_l2_prefetch(keys, p.split_len);
+        if ((st = launch<false>(p, stream)) != DSA_OK) return st;
+    }
+    if (c.cut > 0) {
+        AttnQ8Params r = from_row(p, c.whole);
+        r.rows = c.cut;
+        r.nsplit = c.splits;
+        r.split_len = c.each * kTile;
+        r.n_items = c.cut * c.splits;
+        r.l2_prefetch = want_l2_prefetch(keys, r.split_len);
+        r.part_o = static_cast<float*>(workspace);
+        r.part_lse = r.part_o + (size_t)r.n_items * kH * kDv;
+        if ((st = launch<true>(r, stream)) != DSA_OK) return st;
+        st = launch_decode_combine(r.part_o, r.part_lse, r.rows, r.nsplit, r.out, r.out_f32, r.lse, stream);
+    }
+    return st;
+}
+
 }  // namespace
+
+size_t attn_q8_workspace(int rows, int top_k) {
+    const Cut c = cut_rows(rows, top_k);
+    return (size_t)c.cut * c.splits * kH * (kDv + 1) * sizeof(float);
+}
 
 dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, const int32_t* idx,
                                     int L, int N, int top_k, float scale, void* out, int out_f32, float* lse,
-                                    const PageTable& pages, cudaStream_t stream) {
-    AttnQ8Params p = base_params(q, cache, cache_scale, idx, L, N, top_k, scale, pages);
+                                    void* workspace, const PageTable& pages, cudaStream_t stream) {
+    AttnQ8Params p = base_params(q, cache, cache_scale, idx, N, top_k, scale, out, out_f32, lse, pages);
     p.prefill = 1;
-    p.nsplit = 1;
-    p.split_len = ceil_div(top_k, kTile) * kTile;
-    p.n_items = L;
-    p.l2_prefetch = want_l2_prefetch(N, p.split_len);
-    p.out = out;
-    p.out_f32 = out_f32;
-    p.lse = lse;
-    return launch<false>(p, stream);
-}
-
-size_t attn_q8_decode_workspace(int B, int top_k) {
-    int splits, each;
-    split_tiles(B, top_k, &splits, &each);
-    return splits == 1 ? 0 : (size_t)B * splits * kH * (kDv + 1) * sizeof(float);
+    return launch_rows(p, L, workspace, stream);
 }
 
 dsa_status_t launch_attn_q8_decode(const void* q, const void* cache, const float* cache_scale, const int32_t* kv_len,
                                    const int32_t* idx, int B, int Nmax, int top_k, float scale, void* out,
                                    int out_f32, float* lse, void* workspace, const PageTable& pages,
                                    cudaStream_t stream) {
-    AttnQ8Params p = base_params(q, cache, cache_scale, idx, B, Nmax, top_k, scale, pages);
-    int each;
-    split_tiles(B, top_k, &p.nsplit, &each);
+    AttnQ8Params p = base_params(q, cache, cache_scale, idx, Nmax, top_k, scale, out, out_f32, lse, pages);
     p.kv_len = kv_len;
-    p.split_len = each * kTile;
-    p.n_items = B * p.nsplit;
-    p.l2_prefetch = want_l2_prefetch((int64_t)B * Nmax, p.split_len);
-    p.out = out;
-    p.out_f32 = out_f32;
-    p.lse = lse;
-    if (p.nsplit == 1) return launch<false>(p, stream);
-    p.part_o = static_cast<float*>(workspace);
-    p.part_lse = p.part_o + (size_t)B * p.nsplit * kH * kDv;
-    const dsa_status_t st = launch<true>(p, stream);
-    if (st != DSA_OK) return st;
-    return launch_decode_combine(p.part_o, p.part_lse, B, p.nsplit, out, out_f32, lse, stream);
+    return launch_rows(p, B, workspace, stream);
 }
 
 }  // namespace dsa

@@ -342,11 +342,11 @@ dsa_status_t mla_cache_read_q8_paged(const void *cache, const float *cache_scale
  * e4m3.  Arguments, checks and results are those of the bf16 call of the same
  * name, with `cache` (640-byte rows) and `cache_scale` in place of kv.  The
  * cache may hold up to 2^31 - 1 rows.
- * Workspace: none for prefill (pass NULL, 0).  A decode call for few sequences
- * splits their keys over CTAs and merges the partial results; it takes a
+ * Workspace: the queries (or sequences) behind the last full round of the SMs
+ * are cut into parts of their keys, one a CTA, and merged; the call then takes a
  * 16-byte aligned device buffer of at least
- * mla_sparse_attn_q8_workspace_size(B, top_k) bytes, contents of no matter.  For
- * more sequences that size is 0 and NULL will do.  It depends on the current
+ * mla_sparse_attn_q8_workspace_size(rows, top_k) bytes, rows = L or B, contents of
+ * no matter.  Where that size is 0, NULL will do.  It depends on the current
  * device (0 where the library does not run) and is the same in every call.
  * Precision: products and sums are float32.  The query enters as two e4m3
  * numbers a value (exact for bf16 down to 2^-14 of a head's largest value), and
@@ -358,7 +358,7 @@ dsa_status_t mla_cache_read_q8_paged(const void *cache, const float *cache_scale
  * Two calls at once need a workspace each, also on one stream when two threads
  * issue them: a split call is two kernels.
  */
-size_t mla_sparse_attn_q8_workspace_size(int B, int top_k);
+size_t mla_sparse_attn_q8_workspace_size(int rows, int top_k);
 dsa_status_t mla_sparse_attn_prefill_q8(const void *q, const void *cache, const float *cache_scale,
                                         const int32_t *idx, int L, int N, int top_k, float scale,
                                         void *out, int out_dtype, float *lse, void *workspace,

@@ -449,6 +449,13 @@ def one_row(dsa, q, cache, scale, idx, sm=SCALE, large=False):
     ref = attention64(q, lambda s: kv[idx[s].clamp(min=0).long()], idx >= 0, sm)
     out, lse = dsa.mla_sparse_attn_prefill_q8(q, cache, scale, idx, sm, want_lse=True)
     close(out, lse, ref, normal=False, S=S)
+    # as many rows as SMs: whole queries, tile after tile, where the few rows above are cut into parts
+    R = idx.shape[0]
+    many = torch.arange(torch.cuda.get_device_properties(0).multi_processor_count, device="cuda") % R
+    assert dsa.attn_q8_workspace_size(len(many), idx.shape[1]) == 0
+    out2, lse2 = dsa.mla_sparse_attn_prefill_q8(q[many].contiguous(), cache, scale, idx[many].contiguous(), sm, want_lse=True)
+    close(out2[:R], lse2[:R], ref, normal=False, S=S)
+    assert torch.equal(out2, out2[:R][many]) and torch.equal(lse2, lse2[:R][many])
     return out, lse, ref
 
 
@@ -641,6 +648,15 @@ def test_decode_workspace(dsa):
             with pytest.raises(dsa.DsaError) as e:
                 dsa.mla_sparse_attn_decode_q8(q, cache, scale, kv_len, idx, SCALE, workspace=guard[:need - 16])
             assert e.value.code == 4
+
+
+@pytest.mark.parametrize("more,K,page", [(1, 2048, 0), (8, 640, 16), (30, 1000, 0)])
+def test_rows_behind_the_last_round(dsa, more, K, page):
+    """A few queries more than a round of the SMs takes: those are cut and merged, the others run whole."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert dsa.attn_q8_workspace_size(sms + more, K) > 0 and dsa.attn_q8_workspace_size(sms, K) == 0
+    test_prefill(dsa, sms + more, K + 77, K, page)
+    test_decode(dsa, sms + more, K + 5, K, page)
 
 
 def test_threads_on_one_stream(dsa):
