@@ -31,7 +31,7 @@
 //     scales, 16 worker warps do the softmax and write the output; the query, read as bf16, is split in place
 //     by the eight gathering warps when its predecessor's last QK has read the old one.  Two PV issuers: one
 //     thread reaches an N = 64 scaled MMA every 80 cycles, two one every 52; one N = 128 issuer reaches its 64.
-//     Spinning waits are one thread's a role: a poll of an mbarrier takes from the MMAs' shared memory.
+//     Spinning waits are one thread's a role (with a poller in each gathering warp 1.18 ms became 1.40).
 //   * Queries run whole on persistent CTAs; those behind the last full round of the SMs (all, for few) have
 //     their selected keys cut into parts, one a CTA, which write partial (normalised output, lse) pairs for the
 //     bf16 path's merge kernel.  Merging inside a thread-block cluster was slower: reading the other CTAs' parts from
@@ -39,8 +39,8 @@
 //     with the parts in global memory made a call of 8 sequences 18.2 us, against 14.9 with the merge kernel.
 //   * Measured: 4096 queries of 2048 keys 1.15 ms (0.52 of the bf16 matrix peak for the 1088 products a key and
 //     head; about 5000 cycles a tile of 128 keys, whose operand reads, copies and softmax traffic take shared
-//     memory some 3400; without the vote and the softmax's reads of shared memory 1.08, with half of PV or of QK
-//     1.07), decode of 256 sequences 104 us, of 8 14.4 us, of one 12.7 us.
+//     memory some 3400; leaving out the vote and the softmax's reads of shared memory took 1.18 to 1.11, half of PV
+//     or of QK 1.25 to 1.15), decode of 256 sequences 104 us, of 8 14.4 us, of one 12.7 us.
 #include <cuda.h>
 
 #include <atomic>
@@ -127,13 +127,28 @@ struct AttnQ8Params : AttnShape {
     void* out;                 // final: [rows][64][512], float32 or bf16 (out_f32)
     int out_f32;
     float* lse;                // final: [rows][64] or nullptr
-    float* part_o;             // split: [rows][nsplit][64][512] normalised partial outputs
-    float* part_lse;           // split: [rows][nsplit][64]
+    int whole;                 // queries that are one item each; the others have nsplit each (parts)
+    float* part_o;             // [parts][64][512] normalised partial outputs
+    float* part_lse;           // [parts][64]
     float scale_log2;          // scale * log2(e)
     int32_t* status;           // device error word
     PageTable pages;           // paged cache (pages.table == nullptr: dense rows)
     int l2_prefetch;           // 1: rows go into L2 a tile before their copy (want_l2_prefetch)
 };
+
+// Items: the whole queries, then the parts of the others; Item::split is the part's number, -1 for a whole query.
+__device__ __forceinline__ Item item_at(const AttnQ8Params& p, int item) {
+    Item it{item, -1, 0, 0, p.top_k, 0};
+    if (item >= p.whole) {
+        it.split = item - p.whole;
+        it.row = p.whole + it.split / p.nsplit;
+        it.slot0 = it.split % p.nsplit * p.split_len;
+        it.slot_end = min(p.top_k, it.slot0 + p.split_len);
+    }
+    it.batch = p.prefill ? 0 : it.row;
+    it.bound = p.kv_len ? min(__ldg(p.kv_len + it.batch), p.Nmax) : p.Nmax;
+    return it;
+}
 
 // log2 on the special-function unit; exact for the powers of two that the cache holds.
 __device__ __forceinline__ float lg2_approx(float x) {
@@ -180,7 +195,7 @@ struct RowStream {
             const int it = nth_item(p, s++);
             if (it == -1) return false;
             if (it < 0) continue;
-            const Item I = decode_item(p, it);
+            const Item I = item_at(p, it);
             at = p.idx + (int64_t)I.row * p.top_k + I.slot0 + base;
             left = I.slot_end - I.slot0 - base;
             batch = I.batch;
@@ -235,27 +250,24 @@ __device__ __forceinline__ void convert_head(uint8_t* smem, int qbuf, int h, flo
     if (lane == 0) reinterpret_cast<float*>(smem + OFF_QS)[qbuf * kH + h] = scale_log2 * exp2_int(e);
 }
 
-template <bool SPLIT>
-__device__ __forceinline__ void store_lse(const AttnQ8Params& p, const Item& I, int h, float v) {
-    if (SPLIT)
-        p.part_lse[((int64_t)I.row * p.nsplit + I.split) * kH + h] = v;
+__device__ __forceinline__ void store_lse(const AttnQ8Params& p, int row, int split, int h, float v) {
+    if (split >= 0)
+        p.part_lse[(int64_t)split * kH + h] = v;
     else if (p.lse)
-        p.lse[(int64_t)I.row * kH + h] = v;
+        p.lse[(int64_t)row * kH + h] = v;
 }
 
 // An item without a selected key: zeros and lse = -inf, by all workers.
-template <bool SPLIT>
 __device__ __noinline__ void zero_item(const AttnQ8Params& p, int row, int split, int tid) {
-    const Item I{row, split, 0, 0, 0, 0};
-    if (tid < kH) store_lse<SPLIT>(p, I, tid, -INFINITY);
-    const int n = kH * kDv * (SPLIT || p.out_f32 ? 4 : 2) / 16;
-    uint4* d = SPLIT ? reinterpret_cast<uint4*>(p.part_o) + ((int64_t)row * p.nsplit + split) * n
-                     : static_cast<uint4*>(p.out) + (int64_t)row * n;
+    if (tid < kH) store_lse(p, row, split, tid, -INFINITY);
+    const int n = kH * kDv * (split >= 0 || p.out_f32 ? 4 : 2) / 16;
+    uint4* d = split >= 0 ? reinterpret_cast<uint4*>(p.part_o) + (int64_t)split * n
+                          : static_cast<uint4*>(p.out) + (int64_t)row * n;
 #pragma unroll 1
     for (int i = tid; i < n; i += kWorkers) d[i] = make_uint4(0, 0, 0, 0);
 }
 
-// SPLIT: one item a CTA, a part of a query, into the partial results; else persistent CTAs, whole queries.
+// SPLIT: one item a CTA, a part of a query; else persistent CTAs, whole queries and then parts.
 template <bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const AttnQ8Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -334,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             const int item = nth_item(p, s);
             if (item == -1) break;
             if (item < 0) continue;
-            const Item I = decode_item(p, item);
+            const Item I = item_at(p, item);
             const int T = item_tiles(p, I, lane);
             if (T == 0) continue;
             const uint32_t base = (smem_u32(smem) >> 4) | ((16u >> 4) << 16);   // leading offset: one atom wide
@@ -408,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             const int item = nth_item(p, s);
             if (item == -1) break;
             if (item < 0) continue;
-            const Item I = decode_item(p, item);
+            const Item I = item_at(p, item);
             const int T = item_tiles(p, I, lane);
             if (lane == 0) {
                 // A = V^T MN-major: 128 dims a row, 8-key groups 1 KB apart; B = P^T MN-major, hi at byte 0 of a
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             const int item = nth_item(p, s);
             if (item == -1) break;
             if (item < 0) continue;
-            const Item I = decode_item(p, item);
+            const Item I = item_at(p, item);
             if (item_tiles(p, I, lane) == 0) continue;
             if (lane == 0) {
                 if (qi > 0) l2_prefetch_bulk(p.q + (int64_t)I.row * (kH * DSA_QK_DIM), kH * DSA_QK_DIM * 2);
@@ -471,9 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         const int gw = (warp - kFirstGather) & 3; // rows 32 gw .. 32 gw + 31 of a tile
         const int qh0 = kQHeads * (warp - kFirstGather);
         const uint32_t smem_base = smem_u32(smem);
-        // One thread polls (the roles' pollers on different schedulers), a named barrier releases the four warps.  (A thread suspended in try_wait was seen
-        // to resume 800 to 3400 cycles after the phase had completed; threads that all poll take the issue slots
-        // of the softmax.)  The answer is the same in every warp: all leave together when a wait gives up.
+        // One thread polls (the roles' pollers on different schedulers), a named barrier releases the four warps.  (A
+        // thread suspended in try_wait was seen to resume 800 to 3400 cycles after the phase had completed; warps that
+        // poll for themselves copy out of step.)  The answer is the same in every warp: all leave together when a wait gives up.
         auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
             bool ok = true;
             if (gw == (is_rope ? 2 : 1) && lane == 0) ok = mbar_poll(bar, parity, abort_flag, p.status);
@@ -591,10 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 n_item = nth_item(p, n_s++);
                 if (n_item == -1) return false;
                 if (n_item < 0) continue;
-                const Item nI = decode_item(p, n_item);
+                const Item nI = item_at(p, n_item);
                 nT = item_tiles(p, nI, lane);
                 if (nT > 0) return true;
-                zero_item<SPLIT>(p, nI.row, nI.split, tid);
+                zero_item(p, nI.row, nI.split, tid);
             }
         };
 
@@ -758,17 +770,17 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 break;
             }
             tc_fence_after();
-            const Item I = decode_item(p, item);
+            const Item I = item_at(p, item);
             if (tid < kH) {
                 const float l = red[tid] + red[kH + tid] + red[2 * kH + tid] + red[3 * kH + tid];
                 // l = 0: every selected key was outside the cache
                 invl_s[tid] = (l > 0.f) ? 1.f / l : (l == 0.f ? 0.f : l);
-                store_lse<SPLIT>(p, I, tid,
-                                 (l > 0.f) ? (log2f(l) - m_neg[tid]) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l));
+                store_lse(p, I.row, I.split, tid,
+                          (l > 0.f) ? (log2f(l) - m_neg[tid]) * 0.6931471805599453f : (l == 0.f ? -INFINITY : l));
             }
             named_bar_sync(1, kWorkers);
             if (SPLIT) {                          // the CTA's part, float32: a store of a warp is 128 bytes of a head
-                float* part = p.part_o + (((int64_t)I.row * p.nsplit + I.split) * kH + h0) * kDv + key;
+                float* part = p.part_o + ((int64_t)I.split * kH + h0) * kDv + key;
 #pragma unroll 2
                 for (int ch = 0; ch < kChunks; ++ch) {
                     uint32_t v[kHG];
@@ -783,12 +795,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             // P^T is consumed: each warp takes 1 KB of its block to turn its 32 dims x 16 heads so that a store
             // writes 16 contiguous bytes of a head a lane.
             uint8_t* stage = smem + OFF_P + ww * 1024;
-            float* out32 = static_cast<float*>(p.out) + ((int64_t)I.row * kH + h0) * kDv;
+            const bool f32 = p.out_f32 || I.split >= 0;
+            float* out32 = (I.split >= 0 ? p.part_o + (int64_t)I.split * kH * kDv
+                                         : static_cast<float*>(p.out) + (int64_t)I.row * kH * kDv) + h0 * kDv;
             __nv_bfloat16* out16 = static_cast<__nv_bfloat16*>(p.out) + ((int64_t)I.row * kH + h0) * kDv;
 #pragma unroll 1
             for (int ch = 0; ch < kChunks; ++ch) {
                 const int dim0 = ch * 128 + quad * 32;
-                if (p.out_f32) {                  // a lane a dim, 8 heads at a time: rows of 32 dims
+                if (f32) {                        // a lane a dim, 8 heads at a time: rows of 32 dims
                     uint32_t v[kHG];
                     tmem_ld16(tmem_base + lane_addr + TM_O + 64 * ch + h0, v);
                     tmem_ld_wait();
@@ -876,25 +890,25 @@ dsa_status_t launch(const AttnQ8Params& p, cudaStream_t stream) {
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
-// How a launch's queries are cut: `whole` of them run whole on persistent CTAs, the `cut` others in `splits` parts
-// of `each` tiles, one part a CTA (SM), into the workspace, and are merged.
+// How a launch's queries are cut: `whole` of them run whole, the `cut` others in `splits` parts of `each` tiles,
+// at most one part a CTA (SM), into the workspace, and are merged.
 struct Cut {
     int whole, cut, splits, each;
 };
 
 // The queries behind the last full round of the SMs are cut when that is no slower: they would take an item's
 // tiles (2.6 us each) with most SMs idle, and take, cut, a part's tiles and the merge, whose time grows with the
-// queries (1 tile's for a few, 3 tiles' for 70), and behind whole queries a second launch (2 tiles').  Whole / cut,
-// us: 1 query of 16 tiles 45.7 / 12.6; 4 of 2 tiles 15.5 / 12.9; 40 of 3 18.4 / 17.0; 70 of 4 21.1 / 22.2, of 5
-// 23.5 / 25.1, of 6 26.0 / 25.3; behind a full round, 1 of 16 tiles 87.8 / 60.3, 76 of 16 89.1 / 84.9, 8 of 3 tiles
-// 30.0 / 30.8, of 4 33.8 / 33.0, 38 of 4 34.1 / 38.9, 68 of 8 52.5 / 55.9.
+// queries (1 tile's for a few, 3 tiles' for 70; one more behind whole queries, whose CTAs lose the overlap with a
+// next one).  Whole / cut, us: 1 query of 16 tiles 45.7 / 12.7; 4 of 2 tiles 15.5 / 12.9; 40 of 3 18.4 / 17.0; 70
+// of 4 21.1 / 22.2, of 5 23.5 / 25.1, of 6 26.0 / 25.3; behind a full round, 1 of 16 tiles 87.8 / 56.4, 76 of 16
+// 89.1 / 80.4, 8 of 3 tiles 30.0 / 27.1, 38 of 4 34.1 / 33.3, 68 of 6 43.9 / 45.2, of 8 52.5 / 51.7.
 Cut cut_rows(int rows, int top_k) {
     const int sms = device_sm_count(), tiles = ceil_div(top_k, kTile);
     if (sms < 1) return Cut{rows, 0, 1, tiles};
     const int rest = rows % sms, most = rest > 0 ? sms / rest : 1;
     if (most < 2 || tiles < 2) return Cut{rows, 0, 1, tiles};
     const int n = ceil_div(tiles, most < tiles ? most : tiles);   // tiles a part
-    if (n + 1 + rest / 32 + (rows > rest ? 2 : 0) > tiles) return Cut{rows, 0, 1, tiles};
+    if (n + 1 + rest / 32 + (rows > rest ? 1 : 0) > tiles) return Cut{rows, 0, 1, tiles};
     return Cut{rows - rest, rest, ceil_div(tiles, n), n};
 }
 
@@ -924,48 +938,21 @@ AttnQ8Params base_params(const void* q, const void* cache, const float* cache_sc
     return p;
 }
 
-// The queries from `first` on.
-AttnQ8Params from_row(AttnQ8Params p, int first) {
-    p.q += (int64_t)first * kH * DSA_QK_DIM;
-    p.idx += (int64_t)first * p.top_k;
-    p.out = static_cast<char*>(p.out) + (int64_t)first * kH * kDv * (p.out_f32 ? 4 : 2);
-    if (p.lse) p.lse += (int64_t)first * kH;
-    if (p.kv_len) p.kv_len += first;
-    if (!p.prefill) {               // a sequence each: their rows, or their lines of the page table
-        if (p.pages.table)
-            p.pages.table += (int64_t)first * p.pages.stride;
-        else {
-            p.cache += (int64_t)first * p.Nmax * kQ8Row;
-            p.cache_scale += (int64_t)first * p.Nmax;
-        }
-    }
-    return p;
-}
-
 dsa_status_t launch_rows(AttnQ8Params p, int rows, void* workspace, cudaStream_t stream) {
     const Cut c = cut_rows(rows, p.top_k);
-    const int64_t keys = (p.prefill ? 1 : (int64_t)rows) * p.Nmax;
-    dsa_status_t st = DSA_OK;
-    if (c.whole > 0) {
-        p.rows = p.n_items = c.whole;
-        p.nsplit = 1;
-        p.split_len = ceil_div(p.top_k, kTile) * kTile;
-        p.l2_prefetch = want_l2_prefetch(keys, p.split_len);
-        if ((st = launch<false>(p, stream)) != DSA_OK) return st;
-    }
-    if (c.cut > 0) {
-        AttnQ8Params r = from_row(p, c.whole);
-        r.rows = c.cut;
-        r.nsplit = c.splits;
-        r.split_len = c.each * kTile;
-        r.n_items = c.cut * c.splits;
-        r.l2_prefetch = want_l2_prefetch(keys, r.split_len);
-        r.part_o = static_cast<float*>(workspace);
-        r.part_lse = r.part_o + (size_t)r.n_items * kH * kDv;
-        if ((st = launch<true>(r, stream)) != DSA_OK) return st;
-        st = launch_decode_combine(r.part_o, r.part_lse, r.rows, r.nsplit, r.out, r.out_f32, r.lse, stream);
-    }
-    return st;
+    p.rows = rows;
+    p.whole = c.whole;
+    p.nsplit = c.splits;
+    p.split_len = c.each * kTile;
+    p.n_items = c.whole + c.cut * c.splits;
+    p.l2_prefetch = want_l2_prefetch((p.prefill ? 1 : (int64_t)rows) * p.Nmax, c.whole > 0 ? p.top_k : p.split_len);
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = p.part_o + (size_t)c.cut * c.splits * kH * kDv;
+    const dsa_status_t st = c.whole > 0 ? launch<false>(p, stream) : launch<true>(p, stream);
+    if (st != DSA_OK || c.cut == 0) return st;
+    void* out = static_cast<char*>(p.out) + (int64_t)c.whole * kH * kDv * (p.out_f32 ? 4 : 2);
+    float* lse = p.lse ? p.lse + (int64_t)c.whole * kH : nullptr;
+    return launch_decode_combine(p.part_o, p.part_lse, c.cut, c.splits, out, p.out_f32, lse, stream);
 }
 
 }  // namespace
