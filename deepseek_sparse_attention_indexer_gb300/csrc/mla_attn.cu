@@ -73,6 +73,52 @@ namespace dsa {
 
 namespace {
 
+__device__ __forceinline__ Item decode_item(const AttnShape& p, int item) {
+    Item it;
+    it.row = item / p.nsplit;
+    it.split = item % p.nsplit;
+    it.batch = p.prefill ? 0 : it.row;
+    it.slot0 = it.split * p.split_len;
+    it.slot_end = min(p.top_k, it.slot0 + p.split_len);
+    it.bound = p.kv_len ? min(__ldg(p.kv_len + it.batch), p.Nmax) : p.Nmax;
+    return it;
+}
+
+// Transposing butterfly over a warp: on entry every lane holds 16 values (one
+// per head of the warp's head group); on exit lanes 2i and 2i+1 hold the
+// warp-wide reduction for head i of the group.
+template <bool MAX>
+__device__ __forceinline__ float warp_transpose_reduce16(const float (&x)[16], uint32_t lane) {
+    float a[8];
+    {
+        const bool up = lane & 16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float mine = up ? x[8 + k] : x[k];
+            const float other = up ? x[k] : x[8 + k];
+            const float recv = __shfl_xor_sync(0xffffffffu, other, 16);
+            a[k] = MAX ? fmaxf(mine, recv) : mine + recv;
+        }
+    }
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {
+        const int half = 4 >> step;   // 4, 2, 1 values kept
+        const int off = 8 >> step;    // shuffle distance 8, 4, 2
+        const bool up = lane & off;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k < half) {
+                const float mine = up ? a[half + k] : a[k];
+                const float other = up ? a[k] : a[half + k];
+                const float recv = __shfl_xor_sync(0xffffffffu, other, off);
+                a[k] = MAX ? fmaxf(mine, recv) : mine + recv;
+            }
+        }
+    }
+    const float o = __shfl_xor_sync(0xffffffffu, a[0], 1);
+    return MAX ? fmaxf(a[0], o) : a[0] + o;
+}
+
 constexpr int kD = DSA_QK_DIM;         // 576
 constexpr int kRowBytes = kD * 2;      // 1152
 constexpr int kBlkBytes = kTile * 128; // 16 KB: 128 keys x 64 dims

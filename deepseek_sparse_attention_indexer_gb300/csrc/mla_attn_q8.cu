@@ -37,10 +37,10 @@
 //     bf16 path's merge kernel.  Merging inside a thread-block cluster was slower: reading the other CTAs' parts from
 //     distributed shared memory took 13 thousand cycles, storing them there 20 thousand, and a cluster barrier
 //     with the parts in global memory made a call of 8 sequences 18.2 us, against 14.9 with the merge kernel.
-//   * Measured: 4096 queries of 2048 keys 1.15 ms (0.52 of the bf16 matrix peak for the 1088 products a key and
-//     head; about 5000 cycles a tile of 128 keys, whose operand reads, copies and softmax traffic take shared
-//     memory some 3400; leaving out the vote and the softmax's reads of shared memory took 1.18 to 1.11, half of PV
-//     or of QK 1.25 to 1.15), decode of 256 sequences 104 us, of 8 14.4 us, of one 12.7 us.
+//   * Measured: 4096 queries of 2048 keys 1.14 ms (0.52 of the bf16 matrix peak for the 1088 products a key and
+//     head), decode of 256 sequences 103 us, of 8 14.4 us, of one 12.7 us.  About 5000 cycles a tile of 128 keys:
+//     the loop copy, QK, softmax, PV of a stage is 10 thousand, and two stages fit.  Leaving out the vote and the
+//     softmax's reads of shared memory took 1.18 to 1.11 ms, half of PV or of QK 1.25 to 1.15.
 #include <cuda.h>
 
 #include <atomic>
@@ -77,7 +77,7 @@ static_assert(kGatherWarps == 4 && kRopeWarps == 4, "a warp of either kind has 3
 constexpr int kHG = kH / (kWorkerWarps / 4);       // 16 heads a worker warp
 constexpr int kGroupThreads = 4 * 32;              // the four warps sharing a head group
 constexpr uint32_t kGatherBar = 7;                 // named barriers: 1, 2 workers, 3-6 head groups, 7 gather, 8 rope
-static_assert(kHG == 16 && kWorkerWarps == 16, "warp_transpose_reduce16 takes a head group of 16");
+static_assert(kHG == 16 && kWorkerWarps == 16, "a warp's loads of S^T take a head group of 16");
 
 constexpr float kFirstTop = 4.5f;                  // log2 of the first tile's largest P'
 constexpr float kMostTop = 8.75f;                  // log2 of the largest P' (430 <= 448)
@@ -135,6 +135,12 @@ struct AttnQ8Params : AttnShape {
     PageTable pages;           // paged cache (pages.table == nullptr: dense rows)
     int l2_prefetch;           // 1: rows go into L2 a tile before their copy (want_l2_prefetch)
 };
+
+// P^T, and so O^T, hold a group's 16 heads in another order than S^T: position p is head head_at(p).  A thread that
+// holds heads 2 a, 2 a + 1, 8 + 2 a, 9 + 2 a of S^T (a = lane % 4) writes them as four neighbouring bytes.  Four
+// heads of four keys a thread, in place of 16 heads of one key: the heads' scales and references stay in registers
+// (prefill of 4096 queries 1148 -> 1140 us, of 333 112.7 -> 110.7).
+__device__ __forceinline__ constexpr int head_at(int p) { return 8 * ((p >> 1) & 1) + 2 * (p >> 2) + (p & 1); }
 
 // Items: the whole queries, then the parts of the others; Item::split is the part's number, -1 for a whole query.
 __device__ __forceinline__ Item item_at(const AttnQ8Params& p, int item) {
@@ -632,40 +638,55 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             named_bar_sync(1, kWorkers);          // the previous item's readers of m_neg / invl are done
             if (tid < kH) m_neg[tid] = 0.f;
             bool unset = true;
-            float2 l2[kHG / 2];                   // row sums of heads (h0 + 2i, h0 + 2i + 1)
+            // of the thread's heads h0 + 8 b + 2 (l % 4), + 1: row sums, scales, minus the references
+            float2 l2[2], qs2[2], mn2[2];
 #pragma unroll
-            for (int i = 0; i < kHG / 2; ++i) l2[i] = make_float2(0.f, 0.f);
+            for (int b = 0; b < 2; ++b) l2[b] = qs2[b] = mn2[b] = make_float2(0.f, 0.f);
             named_bar_sync(1, kWorkers);
             for (int t = 0; t < T; ++t, ++gt) {
                 gok = wait_all(s_full, gt & 1) && gok;
                 tc_fence_after();
-                // the exponents e = log2(e) s + log2(c) - m of this key's 16 weights
+                if (t == 0)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        qs2[b] = reinterpret_cast<const float2*>(qs_s + qbuf * kH + h0)[4 * b + (lane & 3)];
+                // The exponents e = log2(e) s + log2(c) - m of the thread's 16 weights: keys 16 f + 8 r + l / 4 of the warp's
+                // 32 (their scales sc[2 f + r]) with the heads above: e2[4 f + 2 b + r].
+                const float4* my_sc = sc_s + (gt & 1) * kTile + quad * 32 + (int)(lane >> 2);
                 float2 e2[kHG / 2];
-                const float4 sc = sc_s[(gt & 1) * kTile + key];
                 {
-                    uint32_t hi[kHG], lo[kHG], ro[kHG];
-                    tmem_ld16(tmem_base + lane_addr + TM_S + h0, hi);
-                    tmem_ld16(tmem_base + lane_addr + TM_S + 64 + h0, lo);
-                    tmem_ld16(tmem_base + lane_addr + TM_R + h0, ro);
+                    float2 sc[4];                 // c and log2 c
+                    uint32_t hi[2][8], lo[2][8], ro[2][8];
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const uint32_t at = tmem_base + lane_addr + (16u * f << 16) + h0;
+                        tmem_ld_16x256b_x2(at + TM_S, hi[f]);
+                        tmem_ld_16x256b_x2(at + TM_S + 64, lo[f]);
+                        tmem_ld_16x256b_x2(at + TM_R, ro[f]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[k] = *reinterpret_cast<const float2*>(my_sc + 8 * k);
                     tmem_ld_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_free);
-                    const float2 lc2 = make_float2(sc.y, sc.y), c2 = make_float2(sc.x, sc.x);
                     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
                     const float2 sixteenth = make_float2(0.0625f, 0.0625f);
 #pragma unroll
-                    for (int i = 0; i < kHG / 2; ++i) {
-                        const float2 a = make_float2(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1]));
-                        const float2 b = make_float2(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1]));
-                        const float2 r = make_float2(__uint_as_float(ro[2 * i]), __uint_as_float(ro[2 * i + 1]));
-                        const float4 q4 = reinterpret_cast<const float4*>(qs_s + qbuf * kH + h0)[i / 2];
-                        const float4 m4 = reinterpret_cast<const float4*>(m_neg + h0)[i / 2];
-                        const float2 qs = (i & 1) ? make_float2(q4.z, q4.w) : make_float2(q4.x, q4.y);
-                        const float2 mn = (i & 1) ? make_float2(m4.z, m4.w) : make_float2(m4.x, m4.y);
-                        e2[i] = __ffma2_rn(__ffma2_rn(b, sixteenth, a), __fmul2_rn(qs, c2),
-                                           __ffma2_rn(r, sl2, __fadd2_rn(lc2, mn)));
-                    }
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const int i = 4 * b + 2 * r;
+                                const float2 s = sc[2 * f + r];
+                                const float2 x = make_float2(__uint_as_float(hi[f][i]), __uint_as_float(hi[f][i + 1]));
+                                const float2 y = make_float2(__uint_as_float(lo[f][i]), __uint_as_float(lo[f][i + 1]));
+                                const float2 z = make_float2(__uint_as_float(ro[f][i]), __uint_as_float(ro[f][i + 1]));
+                                e2[4 * f + 2 * b + r] =
+                                    __ffma2_rn(__ffma2_rn(y, sixteenth, x), __fmul2_rn(qs2[b], make_float2(s.x, s.x)),
+                                               __ffma2_rn(z, sl2, __fadd2_rn(make_float2(s.y, s.y), mn2[b])));
+                            }
                 }
                 // The vote on moving a reference, and the rare move, involve the group's four warps only.  While no key
                 // has been seen (`unset`, the same in the whole group: a padding slot is one for every head) the
@@ -679,14 +700,21 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     move = named_bar_or(group_bar, kGroupThreads, top > kMostTop);
                 }
                 if (move) {
-                    float xm[kHG];
 #pragma unroll
-                    for (int i = 0; i < kHG / 2; ++i) {
-                        xm[2 * i] = e2[i].x;
-                        xm[2 * i + 1] = e2[i].y;
+                    for (int b = 0; b < 2; ++b) {
+                        float2 x = e2[2 * b];
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) {
+                            const float2 y = e2[4 * (k >> 1) + 2 * b + (k & 1)];
+                            x = make_float2(fmaxf(x.x, y.x), fmaxf(x.y, y.y));
+                        }
+#pragma unroll
+                        for (int o = 4; o < 32; o *= 2) {
+                            x.x = fmaxf(x.x, __shfl_xor_sync(0xffffffffu, x.x, o));
+                            x.y = fmaxf(x.y, __shfl_xor_sync(0xffffffffu, x.y, o));
+                        }
+                        if (lane < 4) reinterpret_cast<float2*>(red + quad * kH + h0)[4 * b + lane] = x;
                     }
-                    const float r = warp_transpose_reduce16<true>(xm, lane);
-                    if ((lane & 1u) == 0) red[quad * kH + h0 + (int)(lane >> 1)] = r;
                     named_bar_sync(group_bar, kGroupThreads);
                     bool seen = false;
                     if (ww == 4 * hg && lane < kHG) {   // one lane per head of the group
@@ -702,30 +730,32 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     seen = named_bar_or(group_bar, kGroupThreads, seen);
                     any_upd = !unset;
                     unset = unset && !seen;
-                    float al[kHG];
 #pragma unroll
-                    for (int i = 0; i < kHG / 2; ++i) {
-                        const float2 d = reinterpret_cast<const float2*>(delta_s + h0)[i];
-                        e2[i].x -= d.x;
-                        e2[i].y -= d.y;
-                        al[2 * i] = ex2_approx(-d.x);
-                        al[2 * i + 1] = ex2_approx(-d.y);
+                    for (int b = 0; b < 2; ++b) {
+                        const float2 d = reinterpret_cast<const float2*>(delta_s + h0)[4 * b + (lane & 3)];
+                        mn2[b] = make_float2(mn2[b].x - d.x, mn2[b].y - d.y);
+                        if (any_upd) l2[b] = __fmul2_rn(l2[b], make_float2(ex2_approx(-d.x), ex2_approx(-d.y)));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float2& e = e2[4 * (k >> 1) + 2 * b + (k & 1)];
+                            e = make_float2(e.x - d.x, e.y - d.y);
+                        }
                     }
-                    if (any_upd)
-#pragma unroll
-                        for (int i = 0; i < kHG / 2; ++i) l2[i] = __fmul2_rn(l2[i], make_float2(al[2 * i], al[2 * i + 1]));
                 }
                 // looked at before the exponentials, so that the poll's time does not follow theirs
                 const bool early = gt == 0 || mbar_test_wait(&freed[2 * ((gt - 1) & 1) + 1], ((gt - 1) >> 1) & 1);
                 // P' and its two e4m3 parts; the row sum takes the float32 weight with the row's scale divided out
-                uint32_t whi[kHG / 4], wlo[kHG / 4];
+                uint32_t whi[4], wlo[4];          // four heads of each of the thread's keys
 #pragma unroll
-                for (int i = 0; i < kHG / 4; ++i) {
-                    const float2 p0 = make_float2(ex2_approx(e2[2 * i].x), ex2_approx(e2[2 * i].y));
-                    const float2 p1 = make_float2(ex2_approx(e2[2 * i + 1].x), ex2_approx(e2[2 * i + 1].y));
-                    l2[2 * i] = __ffma2_rn(p0, make_float2(sc.z, sc.z), l2[2 * i]);
-                    l2[2 * i + 1] = __ffma2_rn(p1, make_float2(sc.z, sc.z), l2[2 * i + 1]);
-                    split_e4m3x4(p0.x, p0.y, p1.x, p1.y, whi[i], wlo[i]);
+                for (int k = 0; k < 4; ++k) {
+                    const float2 x0 = e2[4 * (k >> 1) + (k & 1)], x1 = e2[4 * (k >> 1) + 2 + (k & 1)];
+                    const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
+                    const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
+                    const float c1 = my_sc[8 * k].z;
+                    const float2 ic = make_float2(c1, c1);
+                    l2[0] = __ffma2_rn(p0, ic, l2[0]);
+                    l2[1] = __ffma2_rn(p1, ic, l2[1]);
+                    split_e4m3x4(p0.x, p0.y, p1.x, p1.y, whi[k], wlo[k]);
                 }
                 if (!early) gok = gok && pv_done(gt - 1);   // P^T and O^T are free
                 if (any_upd) {                    // t > 0: some key came before
@@ -737,16 +767,16 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                         tmem_ld16(a, v);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < kHG; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * ex2_approx(-delta_s[h0 + k]));
+                        for (int k = 0; k < kHG; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * ex2_approx(-delta_s[h0 + head_at(k)]));
                         tmem_st16(a, v);
                     }
                     tmem_st_wait();
                     tc_fence_before();
                 }
                 {   // P^T row `key`: 16 heads hi at 16-byte piece hg of the swizzled row, lo at piece 4 + hg
-                    uint8_t* d = smem + OFF_P + key * 128;
-                    *reinterpret_cast<uint4*>(d + ((hg ^ (key & 7)) << 4)) = make_uint4(whi[0], whi[1], whi[2], whi[3]);
-                    *reinterpret_cast<uint4*>(d + (((4 + hg) ^ (key & 7)) << 4)) = make_uint4(wlo[0], wlo[1], wlo[2], wlo[3]);
+                    const uint32_t d = smem_u32(smem + OFF_P + key * 128);
+                    stmatrix_x4(d + ((hg ^ (key & 7)) << 4), whi);
+                    stmatrix_x4(d + (((4 + hg) ^ (key & 7)) << 4), wlo);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -755,15 +785,14 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             }
             qbuf = (qbuf + 1) & 3;
             // ---------------- final: l = sum of partial row sums; out = O^T / l
-            {
-                float l_part[kHG];
 #pragma unroll
-                for (int i = 0; i < kHG / 2; ++i) {
-                    l_part[2 * i] = l2[i].x;
-                    l_part[2 * i + 1] = l2[i].y;
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int o = 4; o < 32; o *= 2) {
+                    l2[b].x += __shfl_xor_sync(0xffffffffu, l2[b].x, o);
+                    l2[b].y += __shfl_xor_sync(0xffffffffu, l2[b].y, o);
                 }
-                const float r = warp_transpose_reduce16<false>(l_part, lane);
-                if ((lane & 1u) == 0) red[quad * kH + h0 + (int)(lane >> 1)] = r;
+                if (lane < 4) reinterpret_cast<float2*>(red + quad * kH + h0)[4 * b + lane] = l2[b];
             }
             if (!named_bar_and(2, kWorkers, gok && pv_done(gt - 1))) {
                 failed = true;
@@ -787,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     tmem_ld16(tmem_base + lane_addr + TM_O + 64 * ch + h0, v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < kHG; ++h) __stcg(part + h * kDv + ch * 128, __uint_as_float(v[h]) * invl_s[h0 + h]);
+                    for (int h = 0; h < kHG; ++h) __stcg(part + head_at(h) * kDv + ch * 128, __uint_as_float(v[h]) * invl_s[h0 + head_at(h)]);
                 }
                 tc_fence_before();
                 continue;
@@ -812,12 +841,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
 #pragma unroll
                         for (int h = 0; h < 8; ++h)
                             reinterpret_cast<float*>(stage)[h * 32 + lane] =
-                                __uint_as_float(v[8 * half + h]) * invl_s[h0 + 8 * half + h];
+                                __uint_as_float(v[8 * half + h]) * invl_s[h0 + head_at(8 * half + h)];
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const int h = 4 * i + (int)(lane >> 3);
-                            *reinterpret_cast<float4*>(out32 + (8 * half + h) * kDv + dim0 + (int)(lane & 7) * 4) =
+                            *reinterpret_cast<float4*>(out32 + head_at(8 * half + h) * kDv + dim0 + (int)(lane & 7) * 4) =
                                 reinterpret_cast<const float4*>(stage)[h * 8 + (lane & 7)];
                         }
                     }
@@ -833,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                         uint32_t w[4];            // blocks: dims 0-7 / 8-15 of heads 0-7, then of heads 8-15
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {
-                            const float2 il = reinterpret_cast<const float2*>(invl_s + h0 + 8 * b)[lane & 3];
+                            const float2 il = *reinterpret_cast<const float2*>(invl_s + h0 + head_at(8 * b + 2 * (int)(lane & 3)));
 #pragma unroll
                             for (int r = 0; r < 2; ++r)
                                 w[2 * b + r] = pack_bf16x2(__uint_as_float(v[half][4 * b + 2 * r]) * il.x,
@@ -847,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int h = 8 * i + (int)(lane >> 2), pc = (int)(lane & 3);
-                        *reinterpret_cast<uint4*>(out16 + h * kDv + dim0 + pc * 8) =
+                        *reinterpret_cast<uint4*>(out16 + head_at(h) * kDv + dim0 + pc * 8) =
                             *reinterpret_cast<const uint4*>(stage + h * 64 + ((pc ^ ((h >> 1) & 3)) << 4));
                     }
                 }
