@@ -87,8 +87,12 @@ constexpr int OFF_QHL = 0;                         // 4 chunks x (64 hi rows, 64
 constexpr int OFF_QR = OFF_QHL + kChunks * kBlk;   // rope dims of 64 heads: 64 rows x 128 B
 constexpr int OFF_LAT = OFF_QR + kH * 128;         // 2 tiles x 4 latent chunks
 constexpr int OFF_P = OFF_LAT + kStages * kChunks * kBlk;   // 128 keys x (64 hi | 64 lo)
-constexpr int OFF_SC = OFF_P + kBlk;               // float4 [2][128]: c, log2 c, 1 / c of a tile's rows; 0, -inf, 0: no key
-constexpr int OFF_QS = OFF_SC + 2 * kTile * 16;       // float [4][64]: scale * log2(e) * 2^k of a query's heads
+// A tile's rows: c, log2 c (0, -inf: no key), of two tiles, and 1 / c (0), of four: the workers read the first
+// before they give S^T free, the second after, while the rows of later tiles come in.  The slot of tile g is
+// next written for tile g + 4, behind QK of g + 3, which waits for every worker's reading of S^T of g + 2.
+constexpr int OFF_SC = OFF_P + kBlk;               // float2 [2][128]
+constexpr int OFF_IC = OFF_SC + 2 * kTile * 8;     // float [4][128]
+constexpr int OFF_QS = OFF_IC + 4 * kTile * 4;       // float [4][64]: scale * log2(e) * 2^k of a query's heads
 constexpr int OFF_RED = OFF_QS + 4 * kH * 4;       // float [4][64]
 constexpr int OFF_MNEG = OFF_RED + 4 * kH * 4;     // float [64]: minus the references
 constexpr int OFF_DELTA = OFF_MNEG + kH * 4;       // float [64]: how far a reference has just risen
@@ -281,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         if (threadIdx.x == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
         return;
     }
-    float4* sc_s = reinterpret_cast<float4*>(smem + OFF_SC);
+    float2* sc_s = reinterpret_cast<float2*>(smem + OFF_SC);
+    float* ic_s = reinterpret_cast<float*>(smem + OFF_IC);
     float* qs_s = reinterpret_cast<float*>(smem + OFF_QS);
     float* red = reinterpret_cast<float*>(smem + OFF_RED);
     float* m_neg = reinterpret_cast<float*>(smem + OFF_MNEG);
@@ -544,8 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 tc_fence_after();
                 __syncwarp();
                 tmem_st32(tmem_base + TM_K + (static_cast<uint32_t>(32 * gw) << 16), k);
-                sc_s[(g & 1) * kTile + base] =
-                    row == -1 ? make_float4(0.f, -INFINITY, 0.f, 0.f) : make_float4(sc, lg2_approx(sc), 1.f / sc, 0.f);
+                sc_s[(g & 1) * kTile + base] = row == -1 ? make_float2(0.f, -INFINITY) : make_float2(sc, lg2_approx(sc));
+                ic_s[(g & 3) * kTile + base] = row == -1 ? 0.f : 1.f / sc;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -652,7 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                         qs2[b] = reinterpret_cast<const float2*>(qs_s + qbuf * kH + h0)[4 * b + (lane & 3)];
                 // The exponents e = log2(e) s + log2(c) - m of the thread's 16 weights: keys 16 f + 8 r + l / 4 of the warp's
                 // 32 (their scales sc[2 f + r]) with the heads above: e2[4 f + 2 b + r].
-                const float4* my_sc = sc_s + (gt & 1) * kTile + quad * 32 + (int)(lane >> 2);
+                const float2* my_sc = sc_s + (gt & 1) * kTile + quad * 32 + (int)(lane >> 2);
+                const float* my_ic = ic_s + (gt & 3) * kTile + quad * 32 + (int)(lane >> 2);
                 float2 e2[kHG / 2];
                 {
                     float2 sc[4];                 // c and log2 c
@@ -665,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                         tmem_ld_16x256b_x2(at + TM_R, ro[f]);
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[k] = *reinterpret_cast<const float2*>(my_sc + 8 * k);
+                    for (int k = 0; k < 4; ++k) sc[k] = my_sc[8 * k];
                     tmem_ld_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     const float2 x0 = e2[4 * (k >> 1) + (k & 1)], x1 = e2[4 * (k >> 1) + 2 + (k & 1)];
                     const float2 p0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
                     const float2 p1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
-                    const float c1 = my_sc[8 * k].z;
+                    const float c1 = my_ic[8 * k];
                     const float2 ic = make_float2(c1, c1);
                     l2[0] = __ffma2_rn(p0, ic, l2[0]);
                     l2[1] = __ffma2_rn(p1, ic, l2[1]);
@@ -775,6 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 }
                 {   // P^T row `key`: 16 heads hi at 16-byte piece hg of the swizzled row, lo at piece 4 + hg
                     const uint32_t d = smem_u32(smem + OFF_P + key * 128);
+                    __syncwarp();
                     stmatrix_x4(d + ((hg ^ (key & 7)) << 4), whi);
                     stmatrix_x4(d + (((4 + hg) ^ (key & 7)) << 4), wlo);
                 }

@@ -657,6 +657,33 @@ def test_rows_behind_the_last_round(dsa, more, K, page):
     assert dsa.attn_q8_workspace_size(sms + more, K) > 0 and dsa.attn_q8_workspace_size(sms, K) == 0
     test_prefill(dsa, sms + more, K + 77, K, page)
     test_decode(dsa, sms + more, K + 5, K, page)
+    g = gen(23)
+    cache, scale = make_cache(g, 64)
+    q, idx = randn(g, sms + more, 64, 576).bfloat16(), torch.zeros(sms + more, K, dtype=torch.int32, device="cuda")
+    small = torch.empty(dsa.attn_q8_workspace_size(sms + more, K) - 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(dsa.DsaError) as e:
+        dsa.mla_sparse_attn_prefill_q8(q, cache, scale, idx, SCALE, workspace=small)
+    assert e.value.code == 4
+
+
+@pytest.mark.parametrize("B,N,K", [(153, 2053, 2048), (152, 1000, 900), (304, 1000, 512), (37, 1003, 700)])
+def test_same_bits_every_time(dsa, B, N, K):
+    """The order of every sum is fixed, so a call's bits are; 60 calls of uneven sequences in a row, whose tiles of
+    several lengths meet the kernel's roles in every relative position, and the first of them right."""
+    g = gen(B + N)
+    lens = [N if b == 0 else (b * 7919) % (N + 1) for b in range(B)]
+    cache, scale = make_cache(g, B * N, exponents=2)
+    cache, scale = cache.view(B, N, 640), scale.view(B, N)
+    idx, q = choose(g, lens, N, K), randn(g, B, 64, 576).bfloat16()
+    kv_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kv = values(cache, scale)
+    ref = attention64(q, lambda s: torch.stack([kv[b][idx[b].clamp(min=0).long()] for b in range(B)[s]]), idx >= 0, SCALE)
+    out, lse = dsa.mla_sparse_attn_decode_q8(q, cache, scale, kv_len, idx, SCALE, want_lse=True)
+    close(out, lse, ref)
+    for _ in range(60):
+        o, l = dsa.mla_sparse_attn_decode_q8(q, cache, scale, kv_len, idx, SCALE, want_lse=True)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    assert dsa.device_status() == 0
 
 
 def test_threads_on_one_stream(dsa):
