@@ -7,7 +7,7 @@
 // Read: out = bf16(e4m3 * scale) | k_pe.
 // Both move about 1.8 KB a token and compute a few operations an element, so HBM bounds them, and the start of a
 // launch the small calls.  A warp a row, every load and store of it one contiguous span.  Writing 4096 rows takes
-// 3.0 us (7.9 MB), 8 rows 2.1 us; reading 65,536 rows 20.8 us (118 MB, 5.7 TB/s), eight uneven contexts of up to
+// 4.7 us (7.9 MB; 3.0 with the norm in float32 alone, see Two), 8 rows 2.5 us, the host 9 us for the call; reading 65,536 rows 20.8 us (118 MB, 5.7 TB/s), eight uneven contexts of up to
 // 4096 rows through their pages 6.0 us.
 #include "dsa_q8.cuh"
 
@@ -17,15 +17,43 @@ namespace {
 
 constexpr int kWarps = 8;   // rows in flight a CTA: one warp a row
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
+}
+
+// The latent dims are computed as unevaluated sums of two floats (Knuth's two-sum, products' errors by fma), about
+// 2^-44 relative: a code is then the nearest of the formula's value, not of a float32 chain's, and does not hang on
+// the order of a sum.  In float32 alone a few codes in a million fall on the other side of a midpoint.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const Two s = two_sum(a.hi, b.hi);
+    return two_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+// 1 / sqrt(x): one Newton step from the unit's value, its residual 1 - x r^2 without cancellation
+__device__ __forceinline__ Two two_rsqrt(Two x) {
+    const float r = rsqrtf(x.hi);
+    const float t = __fmul_rn(r, r), tl = __fmaf_rn(r, r, -t);
+    const float p = __fmul_rn(x.hi, t), pl = __fmaf_rn(x.hi, t, -p);
+    const float e = __fsub_rn(__fsub_rn(__fsub_rn(1.f, p), pl), __fmaf_rn(x.hi, tl, __fmul_rn(x.lo, t)));
+    return {r, __fmul_rn(__fmul_rn(0.5f, r), e)};
+}
+// c * r * w as one float rounded to odd: the float below it in magnitude with its last bit set unless the value is
+// a float, so that rounding it once more to fewer bits, or comparing it, is as rounding or comparing the value
+__device__ __forceinline__ float scaled_to_odd(float c, Two r, float w) {
+    const float a = __fmul_rn(c, r.hi), al = __fmaf_rn(c, r.lo, __fmaf_rn(c, r.hi, -a));
+    const float u = __fmul_rn(a, w), ul = __fmaf_rn(al, w, __fmaf_rn(a, w, -u));
+    const float s = __fadd_rn(u, ul), t = __fsub_rn(ul, __fsub_rn(s, u));
+    uint32_t b = __float_as_uint(s);
+    if (fabsf(t) > 0.f) b = (b - ((__float_as_uint(t) ^ b) >> 31)) | 1u;
+    return fabsf(u) < INFINITY ? __uint_as_float(b) : u;
 }
 
 struct WriteParams {
@@ -47,7 +75,7 @@ struct WriteParams {
 // One warp a row: lane l holds latent dims 8l..8l+7 and 256+8l..256+8l+7 and rope dims 2l, 2l+1,
 // so that every load and store of the warp is one contiguous span.
 template <bool INTERLEAVE>
-__global__ void __launch_bounds__(kWarps * 32) cache_write_q8_kernel(const WriteParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 4) cache_write_q8_kernel(const WriteParams p) {
     griddep_wait();
     const int r = blockIdx.x * kWarps + threadIdx.x / 32;
     const int lane = threadIdx.x & 31;
@@ -76,10 +104,16 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_q8_kernel(const Write
             x[8 * h + 2 * i + 1] = bf16_hi(w[i]);
         }
     }
-    float ss = 0.f;
+    Two ss{0.f, 0.f};                         // a bf16 number's square is a float
 #pragma unroll
-    for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-    const float rstd = rsqrtf(warp_sum(ss) * (1.f / kQ8Latent) + p.eps);
+    for (int i = 0; i < 16; ++i) {
+        const Two s = two_sum(ss.hi, __fmul_rn(x[i], x[i]));
+        ss = {s.hi, __fadd_rn(ss.lo, s.lo)};
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        ss = add(ss, {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
+    const Two rstd = two_rsqrt(add({ss.hi * (1.f / kQ8Latent), ss.lo * (1.f / kQ8Latent)}, {p.eps, 0.f}));
     float amax = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -87,10 +121,10 @@ __global__ void __launch_bounds__(kWarps * 32) cache_write_q8_kernel(const Write
         for (int i = 0; i < 2; ++i) {
             const float4 w = __ldg(reinterpret_cast<const float4*>(p.norm_w + 256 * h + 8 * lane) + i);
             float* y = x + 8 * h + 4 * i;
-            y[0] = y[0] * rstd * w.x;
-            y[1] = y[1] * rstd * w.y;
-            y[2] = y[2] * rstd * w.z;
-            y[3] = y[3] * rstd * w.w;
+            y[0] = scaled_to_odd(y[0], rstd, w.x);
+            y[1] = scaled_to_odd(y[1], rstd, w.y);
+            y[2] = scaled_to_odd(y[2], rstd, w.z);
+            y[3] = scaled_to_odd(y[3], rstd, w.w);
             amax = fmaxf(amax, fmaxf(fmaxf(fabsf(y[0]), fabsf(y[1])), fmaxf(fabsf(y[2]), fabsf(y[3]))));
         }
     const int k = e4m3_scale_exponent(warp_max(amax));

@@ -291,7 +291,7 @@ dsa_status_t mla_sparse_attn_prefill_paged(const void *q, const void *kv_pool,
  * [kv_cmpr 512 | k_pe 64], k_pe rotated, kv_cmpr RMS-normalised); the 8-bit
  * rounding is this library's.
  *
- *   u      = kv_a[r, 0:512] * rsqrt(mean(kv_a[r, 0:512]^2) + eps) * norm_w       (float32)
+ *   u      = kv_a[r, 0:512] * rsqrt(mean(kv_a[r, 0:512]^2) + eps) * norm_w       (to about 2^-44)
  *   k      = the smallest integer with max|u| <= 448 * 2^k, clamped to -64..64; 0 for a row of zeros
  *   latent = e4m3(u * 2^-k), nearest, ties to even, saturating;  cache_scale = 2^k
  *   rope   = bf16 of the 64 rope dims with pair i turned by the angle of pos[r]:

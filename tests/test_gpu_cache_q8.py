@@ -165,6 +165,29 @@ def test_write(dsa, R, ld, interleave):
                   cache[to, 512:].contiguous().view(torch.bfloat16), scale[to])
 
 
+def test_write_codes_are_the_nearest(dsa):
+    """Every code is the e4m3 number nearest the formula's value: the kernel's pairs of floats are off by about 2^-44,
+    the float64 reference by 2^-50, so only a value within 2^-40 of a midpoint could go either way."""
+    g = gen(24)
+    R = 4096
+    kv_a, w = randn(g, R, 576).bfloat16(), torch.exp(0.3 * randn(g, 512))
+    cs = angles(4)
+    zero, slots = torch.zeros(R, dtype=torch.int32, device="cuda"), torch.arange(R, dtype=torch.int32, device="cuda")
+    cache, scale = torch.zeros(R, 640, dtype=torch.uint8, device="cuda"), torch.zeros(R, device="cuda")
+    eps = 2.0 ** -20                                                      # a float32 number
+    dsa.mla_cache_write_q8(kv_a, w, eps, cs, zero, slots, cache, scale)
+    x = kv_a[:, :512].double()
+    u = x / torch.sqrt((x * x).mean(1, keepdim=True) + eps) * w.double()
+    k = torch.exp2(torch.ceil(torch.log2(u.abs().amax(1) / 448.0)))
+    assert torch.equal(scale.double(), k)
+    v = u / k[:, None]
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    near = ((v / step).frac().abs() - 0.5).abs() * step <= 2.0 ** -40 * v.abs()
+    want = torch.round(v / step) * step
+    got = cache[:, :512].contiguous().view(F8).double()
+    assert bool(((got == want) | near).all()) and int(near.sum()) < 10
+
+
 def test_write_extremes(dsa):
     """Tiny, huge and zero rows; weights that reach the scale's clamps and saturate past them."""
     g = gen(5)
