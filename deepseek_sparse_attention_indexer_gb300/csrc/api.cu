@@ -356,9 +356,9 @@ dsa_status_t check_attn_q8(const void* q, const void* cache, const float* cache_
 bool eps_ok(float eps) { return eps >= 0.f && eps < 3.0e38f; }
 }  // namespace
 
-size_t mla_sparse_attn_q8_workspace_size(int B, int top_k) {
-    if (B < 1 || top_k < 1 || top_k > DSA_MAX_TOPK || check_device() != DSA_OK) return 0;
-    return attn_q8_workspace(B, top_k);
+size_t mla_sparse_attn_q8_workspace_size(int rows, int top_k) {
+    if (rows < 1 || top_k < 1 || top_k > DSA_MAX_TOPK || check_device() != DSA_OK) return 0;
+    return attn_q8_workspace(rows, top_k);
 }
 
 namespace {
