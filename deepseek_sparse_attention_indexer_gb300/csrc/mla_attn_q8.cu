@@ -18,7 +18,8 @@
 //     block-scaled MMA (constant scale bytes in TMEM), both into one accumulator: 8 significant bits, as
 //     the bf16 kernel's probabilities have.  The row's scale is folded in before the split:
 //     P' = 2^(t - m) with t = log2(e) s + log2(c), so that e4m3's range (2^-9 .. 448, and 2^-13 with
-//     lo) is spent on the weights that the value sum sees; the row sum divides it out again.
+//     lo) is spent on the weights that the value sum sees; the row sum divides it out again (and takes the
+//     weight without c where c makes P' smaller than float32's numbers).
 //   * The reference m of a head is set from the query's first tile so that its largest P' is 2^4.5,
 //     and moved when a later one would pass 2^8.75 (e4m3 ends at 448): a higher start would leave
 //     less room and rescale O^T more often, a lower one would lose the small weights sooner (a
@@ -81,18 +82,21 @@ static_assert(kHG == 16 && kWorkerWarps == 16, "a warp's loads of S^T take a hea
 
 constexpr float kFirstTop = 4.5f;                  // log2 of the first tile's largest P'
 constexpr float kMostTop = 8.75f;                  // log2 of the largest P' (430 <= 448)
+constexpr float kSmallScale = 0x1p-20f;
+constexpr float kLeastExponent = -126.f;           // ex2_approx gives 0 below
 
 // smem layout
 constexpr int OFF_QHL = 0;                         // 4 chunks x (64 hi rows, 64 lo rows) x 128 B
 constexpr int OFF_QR = OFF_QHL + kChunks * kBlk;   // rope dims of 64 heads: 64 rows x 128 B
 constexpr int OFF_LAT = OFF_QR + kH * 128;         // 2 tiles x 4 latent chunks
 constexpr int OFF_P = OFF_LAT + kStages * kChunks * kBlk;   // 128 keys x (64 hi | 64 lo)
-// A tile's rows: c, log2 c (0, -inf: no key), of two tiles, and 1 / c (0), of four: the workers read the first
-// before they give S^T free, the second after, while the rows of later tiles come in.  The slot of tile g is
+// A tile's rows: c, log2 c (0, -inf: no key), of two tiles, and 1 / c (0) and whether there are small scales, of four:
+// the workers read the first before they give S^T free, the second after, while the rows of later tiles come in.  The slot of tile g is
 // next written for tile g + 4, behind QK of g + 3, which waits for every worker's reading of S^T of g + 2.
 constexpr int OFF_SC = OFF_P + kBlk;               // float2 [2][128]
 constexpr int OFF_IC = OFF_SC + 2 * kTile * 8;     // float [4][128]
-constexpr int OFF_QS = OFF_IC + 4 * kTile * 4;       // float [4][64]: scale * log2(e) * 2^k of a query's heads
+constexpr int OFF_SMALL = OFF_IC + 4 * kTile * 4;    // int [4][4]: one of a quarter of the tile's rows has a small scale
+constexpr int OFF_QS = OFF_SMALL + 4 * 4 * 4;        // float [4][64]: scale * log2(e) * 2^k of a query's heads
 constexpr int OFF_RED = OFF_QS + 4 * kH * 4;       // float [4][64]
 constexpr int OFF_MNEG = OFF_RED + 4 * kH * 4;     // float [64]: minus the references
 constexpr int OFF_DELTA = OFF_MNEG + kH * 4;       // float [64]: how far a reference has just risen
@@ -287,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
     }
     float2* sc_s = reinterpret_cast<float2*>(smem + OFF_SC);
     float* ic_s = reinterpret_cast<float*>(smem + OFF_IC);
+    int* small_s = reinterpret_cast<int*>(smem + OFF_SMALL);
     float* qs_s = reinterpret_cast<float*>(smem + OFF_QS);
     float* red = reinterpret_cast<float*>(smem + OFF_RED);
     float* m_neg = reinterpret_cast<float*>(smem + OFF_MNEG);
@@ -551,6 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 tmem_st32(tmem_base + TM_K + (static_cast<uint32_t>(32 * gw) << 16), k);
                 sc_s[(g & 1) * kTile + base] = row == -1 ? make_float2(0.f, -INFINITY) : make_float2(sc, lg2_approx(sc));
                 ic_s[(g & 3) * kTile + base] = row == -1 ? 0.f : 1.f / sc;
+                const bool small = __any_sync(0xffffffffu, row != -1 && sc < kSmallScale);
+                if (lane == 0) small_s[(g & 3) * 4 + gw] = small;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -740,7 +747,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     for (int b = 0; b < 2; ++b) {
                         const float2 d = reinterpret_cast<const float2*>(delta_s + h0)[4 * b + (lane & 3)];
                         mn2[b] = make_float2(mn2[b].x - d.x, mn2[b].y - d.y);
-                        if (any_upd) l2[b] = __fmul2_rn(l2[b], make_float2(ex2_approx(-d.x), ex2_approx(-d.y)));
+                        if (any_upd) {            // in two steps: a sum of up to 2^84 outlives a rise past 126
+                            const float2 h = make_float2(ex2_approx(-0.5f * d.x), ex2_approx(-0.5f * d.y));
+                            l2[b] = __fmul2_rn(__fmul2_rn(l2[b], h), h);
+                        }
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             float2& e = e2[4 * (k >> 1) + 2 * b + (k & 1)];
@@ -750,6 +760,24 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 }
                 // looked at before the exponentials, so that the poll's time does not follow theirs
                 const bool early = gt == 0 || mbar_test_wait(&freed[2 * ((gt - 1) & 1) + 1], ((gt - 1) >> 1) & 1);
+                // A row of small scale may have its part in the sum though its P' is below float32's numbers: the weight
+                // without the scale, then.  (Without a row below kSmallScale nothing is lost: what P' < 2^-126 adds is
+                // below 2^-106, and the sum at least 2^(4.5 - 64).)
+                if (small_s[(gt & 3) * 4 + quad]) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float c1 = my_ic[8 * k];
+                        if (c1 > 1.f / kSmallScale) {
+                            const float lc1 = lg2_approx(c1);
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                const float2 x = e2[4 * (k >> 1) + 2 * b + (k & 1)];
+                                if (x.x < kLeastExponent) l2[b].x += ex2_approx(x.x + lc1);
+                                if (x.y < kLeastExponent) l2[b].y += ex2_approx(x.y + lc1);
+                            }
+                        }
+                    }
+                }
                 // P' and its two e4m3 parts; the row sum takes the float32 weight with the row's scale divided out
                 uint32_t whi[4], wlo[4];          // four heads of each of the thread's keys
 #pragma unroll
