@@ -82,8 +82,12 @@ static_assert(kHG == 16 && kWorkerWarps == 16, "a warp's loads of S^T take a hea
 
 constexpr float kFirstTop = 4.5f;                  // log2 of the first tile's largest P'
 constexpr float kMostTop = 8.75f;                  // log2 of the largest P' (430 <= 448)
-constexpr float kSmallScale = 0x1p-20f;
 constexpr float kLeastExponent = -126.f;           // ex2_approx gives 0 below
+constexpr float kSmallScale = 0x1p-20f;            // below it the row sum looks at P' < 2^-126
+// A row of zeros is written with scale 1, but any scale stands for the same row: taken is the smallest, so that the
+// row, which adds nothing to the value sum, takes none of e4m3's range from the others.  Only rows of scale 1 or more,
+// few among a normalised latent's (about 2^-6), are looked at: a look at every row's first codes cost 7%.
+constexpr float kZeroRowScale = 0x1p-64f;
 
 // smem layout
 constexpr int OFF_QHL = 0;                         // 4 chunks x (64 hi rows, 64 lo rows) x 128 B
@@ -238,6 +242,16 @@ struct RowStream {
         return -2;
     }
 };
+
+// Whether a row's 512 latent dims are zeros of either sign.
+__device__ __forceinline__ bool latent_is_zero(const uint8_t* row) {
+#pragma unroll 1
+    for (int i = 0; i < kQ8Latent; i += 16) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + i));
+        if (((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0) return false;
+    }
+    return true;
+}
 
 // Query head h from its bf16 dims to its e4m3 parts, in place, by a warp: lane l holds dims 16 l .. 16 l + 15.
 __device__ __forceinline__ void convert_head(uint8_t* smem, int qbuf, int h, float scale_log2, uint32_t lane) {
@@ -541,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 // A lane carries one key's 64 rope dims (128 bytes) through registers into its lane of tensor memory:
                 // the loads run ahead, and only the store waits for QK of the tile before.
                 uint32_t k[32];
-                float sc = 1.f;                   // a page outside the pool: a row of zeros with scale 1
+                float sc = kZeroRowScale;         // of a page outside the pool
 #pragma unroll
                 for (int i = 0; i < 32; ++i) k[i] = 0;
                 if (row >= 0) {
@@ -551,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     sc = __ldg(p.cache_scale + row);
                 }
                 if (g > 0 && !wait(s_full, (g - 1) & 1)) break;   // QK of the tile before is complete
+                if (sc >= 1.f && latent_is_zero(p.cache + (int64_t)row * kQ8Row)) sc = kZeroRowScale;
                 tc_fence_after();
                 __syncwarp();
                 tmem_st32(tmem_base + TM_K + (static_cast<uint32_t>(32 * gw) << 16), k);

@@ -352,7 +352,8 @@ dsa_status_t mla_cache_read_q8_paged(const void *cache, const float *cache_scale
  * numbers a value (exact for bf16 down to 2^-14 of a head's largest value), and
  * so do the probabilities, whose relative error is at most 2^-8 as in the bf16
  * calls; a probability (times its row's scale) below 2^-10.5 of the head's
- * largest is held to 2^-18.5 of that.  Latent dims of a query must be finite
+ * largest is held to 2^-18.5 of that (rows of zeros of scale 1 or more, as
+ * written, do not count here).  Latent dims of a query must be finite
  * and at most 448 * 2^64 in magnitude (larger ones, infinities among them, are
  * cut near there); a NaN makes its head's output NaN.
  * Two calls at once need a workspace each, also on one stream when two threads

@@ -1,5 +1,5 @@
-"""The attention over the 8-bit latent cache at both ends of its scales' range, under the tightest bound its number
-formats allow.
+"""The attention over the 8-bit latent cache at both ends of its scales' range and with rows of zeros, under the
+tightest bound its number formats allow.
 
 Tolerances, from the arithmetic:
 
@@ -19,7 +19,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_cache_q8 import F8, SCALE, gen, make_cache, randn, values  # noqa: E402
+from test_gpu_cache_q8 import F8, SCALE, angles, gen, make_cache, paged, randn, values  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -131,3 +131,47 @@ def test_scores_against_scales(dsa):
     q[3, ::2, 512] = 100.0                                                # scores of -400 .. 400
     S = float((q[:, :, 512:].abs() @ rope.abs().t()).max()) * SCALE
     both_ways(dsa, q.bfloat16(), cache, torch.exp2(k.float()), idx, S=S)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("c", [-6, -11, -27, -60])
+def test_rows_of_zeros_take_no_range(dsa, c):
+    """A row of zeros is written with scale 1; among rows of small scale it adds its part of the sum and nothing else.
+    A row that only begins with zeros is one like the others."""
+    g = gen(34)
+    N = 400
+    cache, scale = make_cache(g, N)
+    scale = torch.full((N,), 2.0 ** c, device="cuda")
+    zero = torch.zeros(1, 576, dtype=torch.bfloat16, device="cuda")
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for at in (3, 130, 399):
+        dsa.mla_cache_write_q8(zero, torch.ones(512, device="cuda"), 1e-6, angles(1), one, one + at, cache, scale)
+        assert float(scale[at]) == 1.0
+    cache[130, :512] = 0x80                                               # zeros of either sign
+    cache[200, :512], cache[200, 1:512:2], scale[200] = 0, 0x80, 1.0
+    cache[5, :480], cache[6, :4], cache[7, 4:512] = 0, 0, 0               # part of the row alone
+    q = (0.5 * randn(g, 2, 64, 576)).bfloat16()
+    idx = torch.arange(N, dtype=torch.int32, device="cuda").repeat(2, 1)
+    idx[1] = idx[1].flip(0)
+    both_ways(dsa, q, cache, scale, idx)
+    only = torch.tensor([[3, 130, 200]], dtype=torch.int32, device="cuda")
+    out, _, _ = both_ways(dsa, q[:1].contiguous(), cache, scale, only)
+    assert bool((out == 0).all())
+
+
+@pytest.mark.gpu
+def test_pages_outside_the_pool_take_no_range(dsa):
+    """Keys of a page outside the pool read as zeros beside rows of small scale."""
+    g = gen(35)
+    N, page = 300, 64
+    cache, _ = make_cache(g, N)
+    scale = torch.full((N,), 2.0 ** -27, device="cuda")
+    q = (0.5 * randn(g, 1, 64, 576)).bfloat16()
+    idx = torch.arange(N, dtype=torch.int32, device="cuda")[None].contiguous()
+    pool, pscale, table, pages = paged(g, cache[None], scale[None], [N], page)
+    table[0, 1] = pages
+    out, lse = dsa.mla_sparse_attn_decode_q8_paged(q, pool, pscale, torch.tensor([N], dtype=torch.int32, device="cuda"), table,
+                                                   page, idx, SCALE, N, want_lse=True)
+    assert dsa.device_status() == 7
+    cache[page:2 * page] = 0
+    close(out, lse, attention64(q, cache, scale, idx))
