@@ -694,7 +694,8 @@ __global__ void __maxnreg__(kMaxRegs)   // kThreads threads, one CTA per SM
     }
 }
 
-// Merge decode partials: out = sum_s exp(lse_s - M) o_s / sum_s exp(lse_s - M).
+// Merge decode partials: out = sum_s exp(lse_s - M) o_s / sum_s exp(lse_s - M).  A partial whose lse is NaN makes
+// both results NaN.
 // A sequence has at most kMaxSplits splits (top_k <= DSA_MAX_TOPK, at least 128
 // slots per split); every thread issues all of its split loads before using any.
 constexpr int kMaxSplits = DSA_MAX_TOPK / kTile;
@@ -718,14 +719,14 @@ __global__ void __launch_bounds__(128) mla_decode_combine_kernel(const float* pa
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int s = 0; s < kMaxSplits; ++s) {
-        const float wgt = (M == -INFINITY || ls[s] == -INFINITY) ? 0.f : expf(ls[s] - M);
+        const float wgt = ls[s] == -INFINITY ? 0.f : expf(ls[s] - M);
         wsum += wgt;
         acc.x += wgt * v[s].x;
         acc.y += wgt * v[s].y;
         acc.z += wgt * v[s].z;
         acc.w += wgt * v[s].w;
     }
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const float inv = wsum > 0.f ? 1.f / wsum : wsum;   // 0: no partial has a key
     const int64_t o = ((int64_t)b * kH + h) * kDv + 4 * threadIdx.x;
     if (out_f32) {
         reinterpret_cast<float4*>(static_cast<float*>(out) + o)[0] =
@@ -737,7 +738,7 @@ __global__ void __launch_bounds__(128) mla_decode_combine_kernel(const float* pa
         dst[2] = __float2bfloat16_rn(acc.z * inv);
         dst[3] = __float2bfloat16_rn(acc.w * inv);
     }
-    if (lse && threadIdx.x == 0) lse[(int64_t)b * kH + h] = wsum > 0.f ? M + logf(wsum) : -INFINITY;
+    if (lse && threadIdx.x == 0) lse[(int64_t)b * kH + h] = wsum > 0.f ? M + logf(wsum) : (wsum == 0.f ? -INFINITY : wsum);
 }
 
 template <bool PARTIAL, bool PAGED>

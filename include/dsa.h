@@ -355,7 +355,7 @@ dsa_status_t mla_cache_read_q8_paged(const void *cache, const float *cache_scale
  * largest is held to 2^-18.5 of that (rows of zeros of scale 1 or more, as
  * written, do not count here).  Latent dims of a query must be finite
  * and at most 448 * 2^64 in magnitude (larger ones, infinities among them, are
- * cut near there); a NaN makes its head's output NaN.
+ * cut near there); a NaN makes its head's output and lse NaN.
  * Two calls at once need a workspace each, also on one stream when two threads
  * issue them: a split call is two kernels.
  */

@@ -1,5 +1,5 @@
-"""The attention over the 8-bit latent cache at both ends of its scales' range and with rows of zeros, under the
-tightest bound its number formats allow.
+"""The attention over the 8-bit latent cache at both ends of its scales' range, with rows of zeros and with queries that
+hold NaN, under the tightest bound its number formats allow.
 
 Tolerances, from the arithmetic:
 
@@ -19,7 +19,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_cache_q8 import F8, SCALE, angles, gen, make_cache, paged, randn, values  # noqa: E402
+from test_gpu_cache_q8 import F8, SCALE, angles, choose, gen, make_cache, paged, randn, values  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -175,3 +175,35 @@ def test_pages_outside_the_pool_take_no_range(dsa):
     assert dsa.device_status() == 7
     cache[page:2 * page] = 0
     close(out, lse, attention64(q, cache, scale, idx))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("where", [0, 100, 511, 512, 575])
+def test_nan_query_heads(dsa, where):
+    """A NaN in a query makes its head's output and lse NaN, the same in a cut query, a whole one and a decode step, and
+    changes no other head."""
+    g = gen(36)
+    N, K = 700, 600
+    cache, scale = make_cache(g, N)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    idx = choose(g, [N] * 2, N, K)
+    q = randn(g, 2, 64, 576).bfloat16()
+    bad = q.clone()
+    heads = torch.tensor([0, 17, 18, 63], device="cuda")
+    bad[1, heads, where] = math.nan
+    rest = torch.ones(2, 64, dtype=torch.bool, device="cuda")
+    rest[1, heads] = False
+    many = torch.arange(sms, device="cuda") % 2
+    for rows in (torch.arange(2, device="cuda"), many):
+        assert (dsa.attn_q8_workspace_size(len(rows), K) > 0) == (len(rows) == 2)
+        i = idx[rows].contiguous()
+        cs = cache[None].expand(len(rows), -1, -1).contiguous(), scale[None].expand(len(rows), -1).contiguous()
+        kv_len = torch.full((len(rows),), N, dtype=torch.int32, device="cuda")
+        for call in (lambda x: dsa.mla_sparse_attn_prefill_q8(x, cache, scale, i, SCALE, want_lse=True),
+                     lambda x: dsa.mla_sparse_attn_decode_q8(x, *cs, kv_len, i, SCALE, want_lse=True)):
+            good, glse = call(q[rows].contiguous())
+            out, lse = call(bad[rows].contiguous())
+            keep = rest[rows]
+            assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], glse[keep])
+            assert bool(out[~keep].isnan().all()) and bool(lse[~keep].isnan().all())
+    assert dsa.device_status() == 0
