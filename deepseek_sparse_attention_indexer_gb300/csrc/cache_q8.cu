@@ -5,10 +5,10 @@
 // RMS-normalised), with the quantisation of this library's cache row:
 //   u = c * rsqrt(mean(c^2) + eps) * w,  2^k >= max|u| / 448,  row = e4m3(u 2^-k) | bf16(turned k_pe)
 // Read: out = bf16(e4m3 * scale) | k_pe.
-// Both move about 1.8 KB a token and compute a few operations an element, so HBM bounds them, and the start of a
-// launch the small calls.  A warp a row, every load and store of it one contiguous span.  Writing 4096 rows takes
-// 4.7 us (7.9 MB; 3.0 with the norm in float32 alone, see Two), 8 rows 2.5 us, the host 9 us for the call; reading 65,536 rows 20.8 us (118 MB, 5.7 TB/s), eight uneven contexts of up to
-// 4096 rows through their pages 6.0 us.
+// Both move about 1.8 KB a token: a warp a row, every load and store of it one contiguous span.  Reading is bound by HBM
+// (65,536 rows 20.8 us: 118 MB, 5.7 TB/s; eight uneven contexts of up to 4096 rows through their pages 6.0 us).  Writing
+// 4096 rows takes 4.7 us (7.9 MB, 1.7 TB/s): a launch's start, one wave of loads and the norm in pairs of floats (see
+// Two; 3.0 us with float32 alone).  8 rows take 2.5 us, the host 9 us for the call.
 #include "dsa_q8.cuh"
 
 namespace dsa {
@@ -56,6 +56,15 @@ __device__ __forceinline__ float scaled_to_odd(float c, Two r, float w) {
     return fabsf(u) < INFINITY ? __uint_as_float(b) : u;
 }
 
+// A row and eps far from 1 are taken at 2^-e and 2^-2e times their size, which leaves the quotient as it is, so that
+// neither a sum of squares nor 1 / sqrt leaves float32's range.  0 where the larger of the row's top and sqrt(eps) lies
+// within 2^-40 .. 2^40: their squares and 2^-80 of them are floats.
+__device__ __forceinline__ int range_exponent(float top, float eps) {
+    const float m = fmaxf(top, sqrtf(eps));
+    if (m >= 0x1p-40f && m <= 0x1p40f) return 0;
+    return max(-126, min(126, (int)(__float_as_uint(m) >> 23) - 127));
+}
+
 struct WriteParams {
     const __nv_bfloat16* kv_a;
     int64_t stride;
@@ -94,7 +103,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) cache_write_q8_kernel(const Wr
     const uint32_t pe = __ldg(reinterpret_cast<const uint32_t*>(src + kQ8Latent) + lane);
     const float* cs = p.cos_sin + (int64_t)pos * kQ8Rope;
 
-    float x[16];
+    float x[16], top = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t w[4] = {raw[h].x, raw[h].y, raw[h].z, raw[h].w};
@@ -102,7 +111,18 @@ __global__ void __launch_bounds__(kWarps * 32, 4) cache_write_q8_kernel(const Wr
         for (int i = 0; i < 4; ++i) {
             x[8 * h + 2 * i] = bf16_lo(w[i]);
             x[8 * h + 2 * i + 1] = bf16_hi(w[i]);
+            top = fmaxf(top, fmaxf(fabsf(x[8 * h + 2 * i]), fabsf(x[8 * h + 2 * i + 1])));
         }
+    }
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));   // magnitudes compare as their bits
+    float eps = p.eps;
+    const int e = range_exponent(top, eps);
+    if (e != 0) {
+        const float f = exp2_int(-e);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] *= f;
+        eps = eps * f * f;
+        if (top == 0.f) eps = 1.f;            // zeros, also over eps = 0
     }
     Two ss{0.f, 0.f};                         // a bf16 number's square is a float
 #pragma unroll
@@ -113,7 +133,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) cache_write_q8_kernel(const Wr
 #pragma unroll
     for (int o = 16; o; o >>= 1)
         ss = add(ss, {__shfl_xor_sync(0xffffffffu, ss.hi, o), __shfl_xor_sync(0xffffffffu, ss.lo, o)});
-    const Two rstd = two_rsqrt(add({ss.hi * (1.f / kQ8Latent), ss.lo * (1.f / kQ8Latent)}, {p.eps, 0.f}));
+    const Two rstd = two_rsqrt(add({ss.hi * (1.f / kQ8Latent), ss.lo * (1.f / kQ8Latent)}, {eps, 0.f}));
     float amax = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h)

@@ -305,8 +305,9 @@ dsa_status_t mla_sparse_attn_prefill_paged(const void *q, const void *kv_pool,
  *            padded batch).  The slots of a call must differ; a slot given twice ends as a mixture.
  *   cache, cache_scale   cache_rows rows; rows no slot names are left as they are
  * A position outside the table or a slot >= cache_rows is recorded as
- * DSA_ERR_DEVICE_BOUNDS and its token skipped.  Inputs must be finite: another
- * value leaves that token's row unspecified, and no other row.
+ * DSA_ERR_DEVICE_BOUNDS and its token skipped.  Inputs must be finite, of any
+ * size (a row of zeros gives zeros, also over eps = 0): another value leaves that
+ * token's row unspecified, and no other row.
  * Errors (host): DSA_ERR_INVALID_ARG for a null pointer, R < 1, max_pos < 1, cache_rows < 1,
  * kv_a_stride < 576, eps not finite or < 0, interleave not 0 or 1; DSA_ERR_UNSUPPORTED_SHAPE for
  * cache_rows > 2^31 - 1; DSA_ERR_MISALIGNED for kv_a, norm_w or cos_sin not 16-byte aligned, cache not

@@ -1,8 +1,10 @@
-"""The attention over the 8-bit latent cache at both ends of its scales' range, with rows of zeros and with queries that
-hold NaN, under the tightest bound its number formats allow.
+"""The ends of what the 8-bit latent cache calls accept: rows of any size, scales at both ends of their range, rows of
+zeros, queries that hold NaN; and the attention under the tightest bound its number formats allow.
 
 Tolerances, from the arithmetic:
 
+* codes and scales of the write: exact, but for values within 2^-40 (relative) of a midpoint or of the scale's border,
+  as the latent dims are computed to about 2^-44.
 * attention, per element: a weight w_t = p_t c_t (probability times the row's scale) enters the value product as
   hi + lo / 16 in e4m3, from a half-precision number: a relative error of at most 2^-9 + 2^-11 < 2^-8 where lo is not
   among e4m3's smallest numbers, and at most half of lo's last step, 2^-10 / 16 = 2^-14, elsewhere, beside a head's
@@ -32,6 +34,50 @@ def dsa():
     _lib.device_status(reset=True)
     yield _lib
     _lib.device_status(reset=True)
+
+
+# ------------------------------------------------------------------------------------------------ write
+
+def check_nearest(kv_a, w, eps, codes, scale):
+    """Codes and scales are the formula's in float64; a row of zeros has codes 0 and scale 1."""
+    x, got = kv_a[:, :512].double(), codes.double()
+    u = torch.nan_to_num(x / torch.sqrt((x * x).mean(1, keepdim=True) + eps)) * w.double()   # 0 / 0: a row of zeros
+    big = u.abs().amax(1)
+    assert bool(((big < 2.0 ** -152) | (big > 2.0 ** -148)).all())
+    zero = big < 2.0 ** -152                                              # below float32's smallest step
+    assert bool((got[zero] == 0).all()) and bool((scale[zero] == 1).all())
+    u, big, got, sc = u[~zero], big[~zero], got[~zero], scale[~zero].double()
+    assert torch.equal(sc, torch.exp2(torch.ceil(torch.log2(big / 448.0)).clamp(-64, 64)))
+    border = torch.log2(big / 448.0)
+    assert bool(((border - border.round()).abs() > 2.0 ** -40).all())     # the data stay clear of it
+    v = (u / sc[:, None]).clamp(-448, 448)
+    step = torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=2.0 ** -6))) - 3)
+    near = ((v / step).frac().abs() - 0.5).abs() * step <= 2.0 ** -40 * v.abs()
+    assert bool(((got == torch.round(v / step) * step) | near).all()) and int(near.sum()) < 10
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-30, 1e-6, 1.0, 1e30, 2.9e38])
+def test_write_rows_of_any_size(dsa, eps):
+    """Rows from bf16's smallest numbers to its largest, alone and next to one outlier, and a row of zeros: squares and
+    1 / sqrt leave float32's range at both ends, the quotient does not."""
+    g = gen(31)
+    eps = float(torch.tensor(eps, dtype=torch.float32))
+    amp = [0.0] + [2.0 ** e for e in (-131, -126, -100, -84, -64, -50, -41, -39, 0, 39, 41, 59, 61, 64, 90, 120, 125)]
+    R = len(amp)
+    kv_a = (randn(g, R, 576).clamp(-3.9, 3.9) * torch.tensor(amp, device="cuda")[:, None]).bfloat16()
+    outlier = torch.randn(3, 576, generator=g, device="cuda").bfloat16()
+    outlier[0, 100], outlier[1, 511], outlier[2] = 3e38, -1e25, outlier[2] * 1e-30
+    outlier[2, 7] = 1e-3
+    kv_a = torch.cat([kv_a, outlier])
+    kv_a[:, 512:] = 1.0
+    R += 3
+    w = torch.exp(0.3 * randn(g, 512))
+    slots, zero = torch.arange(R, dtype=torch.int32, device="cuda"), torch.zeros(R, dtype=torch.int32, device="cuda")
+    cache, scale = torch.full((R, 640), 0x55, dtype=torch.uint8, device="cuda"), torch.full((R,), 7.0, device="cuda")
+    dsa.mla_cache_write_q8(kv_a, w, eps, angles(1), zero, slots, cache, scale)
+    assert dsa.device_status() == 0
+    check_nearest(kv_a, w, eps, cache[:, :512].contiguous().view(F8), scale)
 
 
 # ------------------------------------------------------------------------------------------------ attention
