@@ -253,3 +253,107 @@ def test_nan_query_heads(dsa, where):
             assert torch.equal(out[keep], good[keep]) and torch.equal(lse[keep], glse[keep])
             assert bool(out[~keep].isnan().all()) and bool(lse[~keep].isnan().all())
     assert dsa.device_status() == 0
+
+
+# ------------------------------------------------------------------------------------------------ the bound
+
+def cpu_cache(g, rows, k):
+    cache = torch.empty(rows, 640, dtype=torch.uint8)
+    cache[:, :512] = (torch.randn(rows, 512, generator=g) * 64.0).to(F8).view(torch.uint8)
+    cache[:, 512:] = torch.randn(rows, 64, generator=g).bfloat16().view(torch.uint8)
+    return cache, torch.exp2(k)
+
+
+def far_apart(g):
+    """Scales of 2^-40 .. 2^40, some rows of zeros, logits from the rope dims alone."""
+    cache, scale = cpu_cache(g, 600, torch.randint(-40, 41, (600,), generator=g).float())
+    cache[::7, :512] = 0
+    q = torch.zeros(2, 64, 576)
+    q[:, :, 512:] = torch.randn(2, 64, 64, generator=g)
+    return q.bfloat16(), cache, scale, torch.randperm(600, generator=g)[:1000].int().view(2, 300).sort(1).values
+
+
+def queries_of_every_size(g):
+    """Query heads of 2^-30 .. 2^3, dims of a head 2^20 apart."""
+    cache, scale = cpu_cache(g, 300, torch.full((300,), -6.0))
+    q = torch.randn(2, 64, 576, generator=g) * torch.exp2(torch.linspace(-30, 3, 64))[None, :, None]
+    q[1] = q[1] * torch.exp2(-torch.randint(0, 20, (64, 576), generator=g).float())
+    return q.bfloat16(), cache, scale, torch.randperm(300, generator=g)[:256].int().repeat(2, 1)
+
+
+def usual(g):
+    cache, scale = cpu_cache(g, 500, torch.randint(-8, -3, (500,), generator=g).float())
+    return torch.randn(2, 64, 576, generator=g).bfloat16(), cache, scale, torch.randperm(500, generator=g)[:400].int().repeat(2, 1)
+
+
+def growing(g):
+    """Scores that grow from tile to tile, or fall, and one outlier over a flat rest."""
+    N = 1024
+    cache, scale = cpu_cache(g, N, torch.full((N,), -6.0))
+    rope = torch.zeros(N, 64)
+    rope[:, 0], rope[:, 1], rope[700, 2] = torch.arange(N) / 16.0, torch.arange(N, 0, -1) / 16.0, 256.0
+    cache[:, 512:] = rope.bfloat16().view(torch.uint8)
+    q = torch.zeros(3, 64, 576)
+    q[0, :, 512], q[1, :, 513], q[2, :, 514] = torch.arange(64) / 4.0, 16.0, torch.arange(64) / 32.0
+    return q.bfloat16(), cache, scale, torch.arange(N, dtype=torch.int32).repeat(3, 1)
+
+
+DATA = [far_apart, queries_of_every_size, growing, usual]
+
+
+def with_weights(q, cache, scale, idx, made):
+    """The output when made() stands in for the weights P', whose largest of a head is `top`."""
+    out = []
+    code = cache[:, :512].contiguous().view(F8).double()
+    kv = values(cache, scale)
+    for i in range(idx.shape[0]):
+        at = idx[i].long()
+        p = torch.softmax(q[i].double() @ kv[at].t() * SCALE, -1)
+        w = p * scale[at].double() * (code[at] != 0).any(1)
+        top = w.amax(1, keepdim=True)
+        out.append(made(w / top) * top @ code[at])
+    return torch.stack(out)
+
+
+def e4m3(x):
+    return x.half().to(F8).double()
+
+
+def parts(top, lo):
+    """Weights (the largest 1) as e4m3 parts when the largest lies at 2^top."""
+    def made(w):
+        x = w * 2.0 ** top
+        hi = e4m3(x)
+        return (hi + (e4m3((x.half().double() - hi) * 16) / 16 if lo else 0)) / 2.0 ** top
+    return made
+
+
+@pytest.mark.parametrize("data", DATA)
+def test_bound_admits_two_parts_and_not_one(data):
+    """The bound lets hi + lo / 16 pass at either end of the reference's range, and not hi alone (on the CPU)."""
+    g = torch.Generator().manual_seed(37)
+    q, cache, scale, idx = data(g)
+    ref = attention64(q, cache, scale, idx)
+    b = bound(ref)
+    for top in (4.5, 6.0, 8.75):
+        assert bool(((with_weights(q, cache, scale, idx, parts(top, True)) - ref[0]).abs() <= b).all())
+        over = (with_weights(q, cache, scale, idx, parts(top, False)) - ref[0]).abs() > b
+        assert float(over.double().mean()) > 0.01
+    assert float((ref[0].abs() > b).double().mean()) > 0.5               # zeros do not pass
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("data", DATA)
+def test_attention_within_its_formats(dsa, data):
+    q, cache, scale, idx = data(torch.Generator().manual_seed(38))
+    both_ways(dsa, q.cuda(), cache.cuda(), scale.cuda(), idx.cuda())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [1, 127, 129, 1000, 2048])
+def test_attention_of_any_length_within_its_formats(dsa, K):
+    g = gen(K)
+    N = 2 * K + 3
+    cache, scale = make_cache(g, N, exponents=6)
+    idx = choose(g, [N, max(1, K // 3), N], N, K)
+    both_ways(dsa, randn(g, 3, 64, 576).bfloat16(), cache, scale, idx)
