@@ -20,7 +20,8 @@ _API = ("indexer_scores", "topk", "mla_sparse_attn_prefill", "mla_sparse_attn_de
         "mla_cache_write_q8", "mla_cache_read_q8", "mla_cache_read_q8_paged",
         "mla_sparse_attn_prefill_q8", "mla_sparse_attn_prefill_q8_paged", "mla_sparse_attn_decode_q8",
         "mla_sparse_attn_decode_q8_paged", "indexer_norm_rope",
-        "attn_workspace_size", "attn_q8_workspace_size", "device_status", "selftest_wait_timeout", "status_string", "load", "lib_path",
+        "attn_workspace_size", "attn_q8_workspace_size", "device_status", "selftest_wait_timeout",
+        "selftest_poll_timeout", "status_string", "load", "lib_path",
         "DsaError")
 
 __all__ = list(_API) + ["workloads", "build", "HostPrefill", "HostDecode", "sharding"]

@@ -64,6 +64,7 @@ SIGNATURES = {
     "dsa_indexer_source_layer": (ctypes.c_int, [_I, _I, _I]),
     "dsa_device_status": (ctypes.c_int32, [_P, ctypes.POINTER(ctypes.c_int32), _I]),
     "dsa_selftest_wait_timeout": (ctypes.c_int32, [_I, ctypes.c_uint64, _P]),
+    "dsa_selftest_poll_timeout": (ctypes.c_int32, [_I, ctypes.c_uint32, _P]),
 }
 
 _lock = threading.Lock()
@@ -638,6 +639,13 @@ def selftest_wait_timeout(spin: bool = False, limit_ns: int = 1_000_000, stream=
     and the timeout shows in device_status()."""
     rc = load().dsa_selftest_wait_timeout(1 if spin else 0, ctypes.c_uint64(int(limit_ns)), _stream(stream))
     _check("dsa_selftest_wait_timeout", rc)
+
+
+def selftest_poll_timeout(warp: bool = False, polls: int = 1 << 16, stream=None) -> None:
+    """The same for the waits of the 8-bit attention, which give up after a number of polls: one
+    thread's, or (warp) a warp's look at several barriers at once."""
+    rc = load().dsa_selftest_poll_timeout(1 if warp else 0, int(polls), _stream(stream))
+    _check("dsa_selftest_poll_timeout", rc)
 
 
 def device_status(reset: bool = True, stream=None) -> int:

@@ -145,6 +145,24 @@ __global__ void wait_timeout_selftest_kernel(int32_t* status, uint64_t limit_ns,
     else
         (void)mbar_wait(&bar, 0, abort_ptr, status, limit_ns);
 }
+
+// The same with the waits whose limit is a number of polls: one thread's, or a warp's look at seven barriers of which
+// none comes.
+__global__ void poll_timeout_selftest_kernel(int32_t* status, uint32_t polls, int warp) {
+    __shared__ __align__(8) uint64_t bar[7];
+    __shared__ int abort_flag;
+    const uint32_t lane = threadIdx.x;
+    if (lane == 0) {
+        for (int i = 0; i < 7; ++i) mbar_init(&bar[i], 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    if (warp)
+        (void)mbar_poll_warp(&bar[lane < 7 ? lane : 0], 0, lane, 7, 0x1f, &abort_flag, status, polls);
+    else if (lane == 0)
+        (void)mbar_poll(&bar[0], 0, &abort_flag, status, polls);
+}
 }  // namespace selftest
 
 extern "C" {
@@ -521,6 +539,15 @@ dsa_status_t dsa_selftest_wait_timeout(int spin, uint64_t limit_ns, void* stream
     dsa_status_t st = check_device();
     if (st != DSA_OK) return st;
     selftest::wait_timeout_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(device_status_ptr(), limit_ns, spin);
+    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+dsa_status_t dsa_selftest_poll_timeout(int warp, uint32_t polls, void* stream) {
+    if (warp != 0 && warp != 1) return DSA_ERR_INVALID_ARG;
+    if (polls == 0 || polls > kWaitLimitPolls) return DSA_ERR_INVALID_ARG;
+    dsa_status_t st = check_device();
+    if (st != DSA_OK) return st;
+    selftest::poll_timeout_selftest_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(device_status_ptr(), polls, warp);
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 

@@ -115,16 +115,32 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, v
 // mbar_wait_spin with the limit as a count of polls (each takes 30 cycles or more, so about 1 s at least):
 // no timer is read, whose first reading can outlast the wait itself, and few registers are held.
 constexpr uint32_t kWaitLimitPolls = 1u << 26;
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status) {
+__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort, int32_t* status,
+                                          uint32_t limit = kWaitLimitPolls) {
     uint32_t it = 0;
     while (!mbar_test_wait(bar, parity)) {
-        if ((++it & 255u) == 0 && (*abort || it >= kWaitLimitPolls)) {
-            if (it >= kWaitLimitPolls) raise_dev_error(status, DEV_ERR_TIMEOUT);
+        if ((++it & 255u) == 0 && (*abort || it >= limit)) {
+            if (it >= limit) raise_dev_error(status, DEV_ERR_TIMEOUT);
             *abort = 1;
             return false;
         }
     }
     return true;
+}
+// The same by a warp whose first `lanes` lanes each look at a barrier of their own (`mine`, in phase `parity`), until
+// all that `need` names (a bit a lane) have come: the bits of those that have, 0 when the wait gives up.
+__device__ __forceinline__ uint32_t mbar_poll_warp(uint64_t* mine, uint32_t parity, uint32_t lane, uint32_t lanes,
+                                                   uint32_t need, volatile int* abort, int32_t* status,
+                                                   uint32_t limit = kWaitLimitPolls) {
+    for (uint32_t it = 1;; ++it) {
+        const uint32_t got = __ballot_sync(0xffffffffu, lane < lanes && mbar_test_wait(mine, parity));
+        if ((got & need) == need) return got;
+        if ((it & 255u) == 0 && (*abort || it >= limit)) {
+            if (it >= limit && lane == 0) raise_dev_error(status, DEV_ERR_TIMEOUT);
+            *abort = 1;
+        }
+        if (__any_sync(0xffffffffu, (it & 255u) == 0 && *abort)) return 0;
+    }
 }
 
 // ---------------------------------------------------------------- grid dependencies

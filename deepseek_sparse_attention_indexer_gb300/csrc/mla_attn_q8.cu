@@ -390,18 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 uint64_t* mine = lane == 0 ? rope_full : lane == 3 ? s_free : lane == 4 ? q_full
                                  : lane < 3 ? ch + lane - 1 : lane < 7 ? ch + lane - 3 : ch;
                 const uint32_t mpar = lane == 0 ? gt & 1 : lane == 3 ? (gt & 1) ^ 1 : lane == 4 ? qi & 1 : par;
-                // all of the barriers `need` names: what has come of the seven, 0 when the wait gives up
-                auto poll = [&](uint32_t need) -> uint32_t {
-                    for (uint32_t it = 1;; ++it) {
-                        const uint32_t got = __ballot_sync(0xffffffffu, lane < 7 && mbar_test_wait(mine, mpar));
-                        if ((got & need) == need) return got;
-                        if ((it & 255u) == 0 && (*abort_flag || it >= kWaitLimitPolls)) {
-                            if (it >= kWaitLimitPolls && lane == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
-                            *abort_flag = 1;
-                        }
-                        if (__any_sync(0xffffffffu, (it & 255u) == 0 && *abort_flag)) return 0;
-                    }
-                };
+                auto poll = [&](uint32_t need) { return mbar_poll_warp(mine, mpar, lane, 7, need, abort_flag, p.status); };
                 const uint32_t got = poll(0x1f);
                 ok = got != 0;
                 if (!ok) break;

@@ -476,6 +476,15 @@ int dsa_indexer_source_layer(int layer, int topk_freq, int skip_offset);
 dsa_status_t dsa_selftest_wait_timeout(int spin, uint64_t limit_ns, void *stream);
 
 /*
+ * dsa_selftest_poll_timeout -- the same for the waits of the attention over the
+ * 8-bit cache, whose limit is a number of polls: one thread's (warp = 0), or a
+ * warp's that looks at seven barriers at once (warp = 1).  `polls` is rounded up
+ * to a multiple of 256; the kernels wait 2^26 of them, a second or more.
+ * Errors (host): as above, unless warp is 0 or 1 and 0 < polls <= 2^26.
+ */
+dsa_status_t dsa_selftest_poll_timeout(int warp, uint32_t polls, void *stream);
+
+/*
  * dsa_device_status -- synchronise `stream`, then read (and if `reset` is
  * non-zero, clear) the sticky device error word.  *code_out receives DSA_OK,
  * DSA_ERR_DEVICE_TIMEOUT or DSA_ERR_DEVICE_BOUNDS (timeout wins if both).

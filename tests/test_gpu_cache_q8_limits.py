@@ -357,3 +357,32 @@ def test_attention_of_any_length_within_its_formats(dsa, K):
     cache, scale = make_cache(g, N, exponents=6)
     idx = choose(g, [N, max(1, K // 3), N], N, K)
     both_ways(dsa, randn(g, 3, 64, 576).bfloat16(), cache, scale, idx)
+
+
+# ------------------------------------------------------------------------------------------------ waits
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("warp", [False, True])
+def test_polled_waits_give_up(dsa, warp):
+    """Both forms of the attention's wait, on barriers nothing arrives on, give up after their polls and record
+    DSA_ERR_DEVICE_TIMEOUT (6); the attention then runs as before."""
+    g = gen(39)
+    cache, scale = make_cache(g, 200)
+    idx = torch.arange(200, dtype=torch.int32, device="cuda")[None].contiguous()
+    q = randn(g, 1, 64, 576).bfloat16()
+    want = dsa.mla_sparse_attn_prefill_q8(q, cache, scale, idx, SCALE)
+    assert dsa.device_status() == 0
+    for polls in (1, 256, 100000):
+        dsa.selftest_poll_timeout(warp=warp, polls=polls)
+        assert dsa.device_status() == 6
+        assert dsa.device_status() == 0                                   # read and cleared
+    assert torch.equal(dsa.mla_sparse_attn_prefill_q8(q, cache, scale, idx, SCALE), want)
+    assert dsa.device_status() == 0
+
+
+def test_polled_wait_selftest_refusals():
+    """A form other than 0 or 1 and a limit outside 1 .. 2^26 are refused on the host (DSA_ERR_INVALID_ARG)."""
+    from deepseek_sparse_attention_indexer_gb300 import _build, _lib
+    f = _lib.load(_build.build()).dsa_selftest_poll_timeout
+    for warp, polls in ((2, 256), (-1, 256), (0, 0), (1, 0), (0, (1 << 26) + 1), (1, 1 << 31)):
+        assert f(warp, polls, None) == 1
