@@ -4,7 +4,7 @@
 // section 5: indexer_rope_interleave).
 //   y = (x - [mean]) * rsqrt(mean((x - [mean])^2) + eps) * w + b,
 //   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin) for the 32 pairs of dims 0..63
-// 16.9 KB a token in and out, a few operations an element.  4096 tokens with both norms (69 MB) take 13.3 us, 5.2 TB/s,
+// 16.9 KB a token in and out, a few operations an element.  4096 tokens with both norms (69 MB) take 13.1 us, 5.3 TB/s,
 // eight 16-byte loads of a lane in flight: with four 14.0, with two 16.3, with one 24; CTAs of 64 threads, so that
 // a token's end leaves few lanes waiting (256 threads: 14.5 against 14.0, four loads).  8 tokens take 2.1 us, 1.7
 // with two loads: less than the time the host needs to issue the call, so one form serves both.

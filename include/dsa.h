@@ -55,7 +55,8 @@ enum {
     DSA_ERR_MISALIGNED = 3,          /* base pointer or row stride not 16-byte aligned */
     DSA_ERR_WORKSPACE_TOO_SMALL = 4, /* ws_bytes below the matching *_workspace_size() */
     DSA_ERR_CUDA = 5,                /* a CUDA runtime call or launch failed */
-    DSA_ERR_DEVICE_TIMEOUT = 6,      /* (device word) an in-kernel wait hit its limit */
+    DSA_ERR_DEVICE_TIMEOUT = 6,      /* (device word) an in-kernel wait hit its limit, or a kernel did not run
+                                        because its shared memory lay unaligned */
     DSA_ERR_DEVICE_BOUNDS = 7,       /* (device word) an index outside the cache was met */
     DSA_ERR_UNSUPPORTED_DEVICE = 8,  /* current device is not compute capability 10.3 */
     DSA_ERR_SCRATCH_TOO_SMALL = 9    /* request does not fit the library's fixed device scratch */
@@ -357,6 +358,9 @@ dsa_status_t mla_cache_read_q8_paged(const void *cache, const float *cache_scale
  * written, do not count here).  Latent dims of a query must be finite
  * and at most 448 * 2^64 in magnitude (larger ones, infinities among them, are
  * cut near there); a NaN makes its head's output and lse NaN.
+ * A query that is cut is summed in another order than one that runs whole: its
+ * bits, not its error, depend on the number of rows and its place among them.
+ * The same call gives the same bits every time.
  * Two calls at once need a workspace each, also on one stream when two threads
  * issue them: a split call is two kernels.
  */
@@ -391,7 +395,8 @@ dsa_status_t mla_sparse_attn_decode_q8_paged(const void *q, const void *cache, c
  *
  *   norm DSA_NORM_RMS:    y = x * rsqrt(mean(x^2) + eps) * w + b
  *   norm DSA_NORM_LAYER:  y = (x - mean(x)) * rsqrt(var(x) + eps) * w + b
- *   over the 128 dims of a head (float32; a null b adds nothing), then dims 0..63 turned by the
+ *   over the 128 dims of a head (float32, its squares too: a head of elements above 1e18, or so small that
+ *   their squares and eps are 0, is not normalised rightly; a null b adds nothing), then dims 0..63 turned by the
  *   angle of pos[r] as in mla_cache_write_q8, dims 64..127 kept; rounded to bf16
  *   q        bf16, token r's 32 heads of 128 at q + r * q_stride (elements; >= 4096, a multiple of 8)
  *   k        bf16, token r's 128 dims at k + r * k_stride (>= 128, a multiple of 8)
