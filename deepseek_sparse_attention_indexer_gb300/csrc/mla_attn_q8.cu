@@ -38,8 +38,8 @@
 //     bf16 path's merge kernel.  Merging inside a thread-block cluster was slower: reading the other CTAs' parts from
 //     distributed shared memory took 13 thousand cycles, storing them there 20 thousand, and a cluster barrier
 //     with the parts in global memory made a call of 8 sequences 18.2 us, against 14.9 with the merge kernel.
-//   * Measured: 4096 queries of 2048 keys 1.14 ms (0.52 of the bf16 matrix peak for the 1088 products a key and
-//     head), decode of 256 sequences 103 us, of 8 14.6 us, of one 12.9 us.  About 5000 cycles a tile of 128 keys:
+//   * Measured: 4096 queries of 2048 keys 1.13 ms (0.52 of the bf16 matrix peak for the 1088 products a key and
+//     head), decode of 256 sequences 102 us, of 8 14.3 us, of one 12.9 us.  About 5000 cycles a tile of 128 keys:
 //     the loop copy, QK, softmax, PV of a stage is 10 thousand, and two stages fit.  Leaving out the vote and the
 //     softmax's reads of shared memory took 1.18 to 1.11 ms, half of PV or of QK 1.25 to 1.15.
 #include <cuda.h>
@@ -86,8 +86,9 @@ constexpr float kLeastExponent = -126.f;           // ex2_approx gives 0 below
 constexpr float kSmallScale = 0x1p-20f;            // below it the row sum looks at P' < 2^-126
 // A row of zeros is written with scale 1, but any scale stands for the same row: taken is the smallest, so that the
 // row, which adds nothing to the value sum, takes none of e4m3's range from the others.  Only rows of scale 1 or more,
-// few among a normalised latent's (about 2^-6), are looked at.  A look at every row's first codes made 4096 queries 1.14 ->
-// 1.22 ms; as it is, a cache of such rows alone pays 1.18 -> 1.30 ms (float32 output).
+// few among a normalised latent's (about 2^-6), are looked at.  4096 queries, ms: 1.13, with every hundredth row of zeros
+// 1.14, every tenth 1.34, zeros alone 3.97; a cache whose every row has scale 1, float32 output, 1.17 -> 1.32.  A look
+// at every row's first codes took 1.22; a lane alone at its row of zeros, after the wait, 2.19 for every hundredth.
 constexpr float kZeroRowScale = 0x1p-64f;
 
 // smem layout
@@ -244,14 +245,22 @@ struct RowStream {
     }
 };
 
-// Whether a row's 512 latent dims are zeros of either sign.
-__device__ __forceinline__ bool latent_is_zero(const uint8_t* row) {
-#pragma unroll 1
-    for (int i = 0; i < kQ8Latent; i += 16) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + i));
-        if (((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0) return false;
+__device__ __forceinline__ bool codes_are_zero(const uint8_t* at) {   // 16 codes, zeros of either sign
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
+    return ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) == 0;
+}
+
+// The scale sc of the lane's row, or kZeroRowScale where the row's latent dims are zeros, by a warp: each lane looks at
+// its row's first codes, and the warp together at the rows that begin with zeros.  (Two or four rows at once took
+// registers that the kernel has not: 1.13 -> 1.15, 1.17 ms without any such row.)
+__device__ __forceinline__ float row_scale(const uint8_t* cache, int row, float sc, uint32_t lane) {
+    const bool maybe = sc >= 1.f && codes_are_zero(cache + (int64_t)row * kQ8Row);
+    for (uint32_t m = __ballot_sync(0xffffffffu, maybe); m; m &= m - 1) {
+        const int l = __ffs(m) - 1;
+        const int64_t r = __shfl_sync(0xffffffffu, row, l);
+        if (__all_sync(0xffffffffu, codes_are_zero(cache + r * kQ8Row + 16 * lane)) && (int)lane == l) sc = kZeroRowScale;
     }
-    return true;
+    return sc;
 }
 
 // Query head h from its bf16 dims to its e4m3 parts, in place, by a warp: lane l holds dims 16 l .. 16 l + 15.
@@ -554,8 +563,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     for (int i = 0; i < 4; ++i) ldg_nc_v8(src + 32 * i, k + 8 * i);
                     sc = __ldg(p.cache_scale + row);
                 }
+                sc = row_scale(p.cache, row, sc, lane);
                 if (g > 0 && !wait(s_full, (g - 1) & 1)) break;   // QK of the tile before is complete
-                if (sc >= 1.f && latent_is_zero(p.cache + (int64_t)row * kQ8Row)) sc = kZeroRowScale;
                 tc_fence_after();
                 __syncwarp();
                 tmem_st32(tmem_base + TM_K + (static_cast<uint32_t>(32 * gw) << 16), k);

@@ -200,6 +200,12 @@ def test_rows_of_zeros_take_no_range(dsa, c):
     idx = torch.arange(N, dtype=torch.int32, device="cuda").repeat(2, 1)
     idx[1] = idx[1].flip(0)
     both_ways(dsa, q, cache, scale, idx)
+    many = torch.rand(N, generator=g, device="cuda") < 0.5                # half of the rows, one tile of nothing else
+    many[128:256] = True
+    many[300] = False
+    cache[many, :512], scale[many] = 0, 1.0
+    scale[300] = 1.0 if c < -20 else scale[300]                           # scale 1 and no zeros
+    both_ways(dsa, q, cache, scale, idx)
     only = torch.tensor([[3, 130, 200]], dtype=torch.int32, device="cuda")
     out, _, _ = both_ways(dsa, q[:1].contiguous(), cache, scale, only)
     assert bool((out == 0).all())
