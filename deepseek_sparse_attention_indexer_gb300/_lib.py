@@ -67,6 +67,9 @@ SIGNATURES = {
     "dsa_selftest_poll_timeout": (ctypes.c_int32, [_I, ctypes.c_uint32, _P]),
 }
 
+# the calls over the 4-bit cache take what those over the 8-bit one take
+SIGNATURES.update({name.replace("_q8", "_q4"): sig for name, sig in SIGNATURES.items() if "_q8" in name})
+
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
 
@@ -307,9 +310,10 @@ def mla_sparse_attn_prefill_paged(q: torch.Tensor, kv_pool: torch.Tensor, block_
     return (out, lse) if want_lse else out
 
 
-# ----------------------------------------------------------------------------- the 8-bit latent cache
+# ----------------------------------------------------------------------------- the 8-bit and 4-bit latent caches
 
 Q8_ROW = 640        # bytes of a cache row: 512 e4m3 latent dims | 64 bf16 rope dims
+Q4_ROW = 416        # 512 latent dims of four bits | 32 block scales | 64 bf16 rope dims
 NORMS = {"rms": 0, "layer": 1}
 
 
@@ -323,7 +327,7 @@ _U8 = frozenset((torch.uint8,))
 
 @functools.lru_cache(maxsize=4096)
 def _q8_workspace_bytes(dev: int, rows: int, top_k: int) -> int:
-    """The library's answer for a device and two sizes."""
+    """The library's answer for a device and two sizes, the same for a 4-bit cache."""
     return int(load().mla_sparse_attn_q8_workspace_size(rows, top_k))
 
 
@@ -370,17 +374,33 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _q8_rows(cache: torch.Tensor) -> int:
-    """Rows of an 8-bit cache (uint8, last dim 640)."""
-    if cache.shape[-1] != Q8_ROW:
-        _bad("the cache is uint8 with rows of 640 bytes")
-    return cache.numel() // Q8_ROW
+def _cache_rows(cache: torch.Tensor, row: int) -> int:
+    """Rows of an 8-bit or 4-bit cache (uint8, last dim `row` bytes)."""
+    if cache.shape[-1] != row:
+        _bad(f"the cache is uint8 with rows of {row} bytes")
+    return cache.numel() // row
 
 
 def _max_pos(cos_sin: torch.Tensor) -> int:
     if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
         _bad("cos_sin is float32 [max_pos, 64]")
     return cos_sin.shape[0]
+
+
+def _cache_write(name: str, row: int, kv_a, norm_w, eps, cos_sin, pos, slots, cache, cache_scale, interleave, stream) -> None:
+    dev = _current_device()
+    R, width = kv_a.shape
+    if width != 576:
+        _bad("kv_a is [R, 576]")
+    p, ld = _rows(kv_a, dev, (1,), "kv_a")
+    rows, n_pos = _cache_rows(cache, row), _max_pos(cos_sin)
+    rc = getattr(_lib or load(), name)(
+        p, ld if R > 1 else 576, _p(norm_w, dev, _F32, 512, "norm_w"), eps, _p(cos_sin, dev, _F32, n_pos * 64, "cos_sin"), n_pos,
+        1 if interleave else 0, _p(pos, dev, _I32, R, "pos"), _p(slots, dev, _I32, R, "slots"), R,
+        _p(cache, dev, _U8, rows * row, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"), rows,
+        _stream_on(dev, stream))
+    if rc:
+        raise DsaError(name, rc)
 
 
 def mla_cache_write_q8(kv_a: torch.Tensor, norm_w: torch.Tensor, eps: float, cos_sin: torch.Tensor, pos: torch.Tensor,
@@ -391,34 +411,39 @@ def mla_cache_write_q8(kv_a: torch.Tensor, norm_w: torch.Tensor, eps: float, cos
     kv_a [R, 576] bf16 (rows may be strided), norm_w [512] f32, cos_sin [max_pos, 64] f32 (32 cosines |
     32 sines a position), pos and slots [R] int32 (a negative slot skips the token; slots differ), cache
     uint8 [..., 640], cache_scale f32 [...]."""
+    _cache_write("mla_cache_write_q8", Q8_ROW, kv_a, norm_w, eps, cos_sin, pos, slots, cache, cache_scale, interleave, stream)
+
+
+def mla_cache_write_q4(kv_a: torch.Tensor, norm_w: torch.Tensor, eps: float, cos_sin: torch.Tensor, pos: torch.Tensor,
+                       slots: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor, interleave: bool = True,
+                       stream=None) -> None:
+    """mla_cache_write_q8 into the 4-bit cache: cache uint8 [..., 416], cache_scale f32 [...]."""
+    _cache_write("mla_cache_write_q4", Q4_ROW, kv_a, norm_w, eps, cos_sin, pos, slots, cache, cache_scale, interleave, stream)
+
+
+def _cache_read(name: str, row: int, cache, cache_scale, slots, out, stream) -> torch.Tensor:
     dev = _current_device()
-    R, width = kv_a.shape
-    if width != 576:
-        _bad("kv_a is [R, 576]")
-    p, ld = _rows(kv_a, dev, (1,), "kv_a")
-    rows, n_pos = _q8_rows(cache), _max_pos(cos_sin)
-    rc = (_lib or load()).mla_cache_write_q8(
-        p, ld if R > 1 else 576, _p(norm_w, dev, _F32, 512, "norm_w"), eps, _p(cos_sin, dev, _F32, n_pos * 64, "cos_sin"), n_pos,
-        1 if interleave else 0, _p(pos, dev, _I32, R, "pos"), _p(slots, dev, _I32, R, "slots"), R,
-        _p(cache, dev, _U8, rows * Q8_ROW, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"), rows,
-        _stream_on(dev, stream))
+    R, rows = slots.numel(), _cache_rows(cache, row)
+    if out is None:
+        out = _new((R, 576), torch.bfloat16, cache.device, stream)
+    rc = getattr(_lib or load(), name)(
+        _p(cache, dev, _U8, rows * row, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"), rows,
+        _p(slots, dev, _I32, R, "slots"), R, _p(out, dev, _BITS16, R * 576, "out"), _stream_on(dev, stream))
     if rc:
-        raise DsaError("mla_cache_write_q8", rc)
+        raise DsaError(name, rc)
+    return out
 
 
 def mla_cache_read_q8(cache: torch.Tensor, cache_scale: torch.Tensor, slots: torch.Tensor,
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out [R, 576] bf16: the rows `slots` [R] int32 of the 8-bit cache (zeros for a negative slot)."""
-    dev = _current_device()
-    R, rows = slots.numel(), _q8_rows(cache)
-    if out is None:
-        out = _new((R, 576), torch.bfloat16, cache.device, stream)
-    rc = (_lib or load()).mla_cache_read_q8(
-        _p(cache, dev, _U8, rows * Q8_ROW, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"), rows,
-        _p(slots, dev, _I32, R, "slots"), R, _p(out, dev, _BITS16, R * 576, "out"), _stream_on(dev, stream))
-    if rc:
-        raise DsaError("mla_cache_read_q8", rc)
-    return out
+    return _cache_read("mla_cache_read_q8", Q8_ROW, cache, cache_scale, slots, out, stream)
+
+
+def mla_cache_read_q4(cache: torch.Tensor, cache_scale: torch.Tensor, slots: torch.Tensor,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out [R, 576] bf16: the rows `slots` [R] int32 of the 4-bit cache (zeros for a negative slot)."""
+    return _cache_read("mla_cache_read_q4", Q4_ROW, cache, cache_scale, slots, out, stream)
 
 
 def _table(block_table: torch.Tensor, B: int) -> int:
@@ -428,36 +453,49 @@ def _table(block_table: torch.Tensor, B: int) -> int:
     return block_table.shape[1]
 
 
-def mla_cache_read_q8_paged(cache: torch.Tensor, cache_scale: torch.Tensor, kv_len: torch.Tensor,
-                            block_table: torch.Tensor, page_size: int, Nmax: int,
-                            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """out [B, Nmax, 576] bf16: the kv_len[b] rows of each sequence of a paged 8-bit cache; later rows
-    of a given `out` stay as they are (a new one has zeros there)."""
+def _cache_read_paged(name: str, row: int, cache, cache_scale, kv_len, block_table, page_size, Nmax, out, stream) -> torch.Tensor:
     dev = _current_device()
-    B, rows = kv_len.numel(), _q8_rows(cache)
+    B, rows = kv_len.numel(), _cache_rows(cache, row)
     stride = _table(block_table, B)
     if out is None:
         out = _new((B, Nmax, 576), torch.bfloat16, cache.device, stream)
         with torch.cuda.stream(torch.cuda.ExternalStream(_stream_on(dev, stream))):
             out.zero_()
-    rc = (_lib or load()).mla_cache_read_q8_paged(
-        _p(cache, dev, _U8, rows * Q8_ROW, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"),
+    rc = getattr(_lib or load(), name)(
+        _p(cache, dev, _U8, rows * row, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"),
         _p(kv_len, dev, _I32, B, "kv_len"), _p(block_table, dev, _I32, B * stride, "block_table"), stride, page_size,
         rows // page_size if page_size > 0 else 0, B, Nmax, _p(out, dev, _BITS16, B * Nmax * 576, "out"),
         _stream_on(dev, stream))
     if rc:
-        raise DsaError("mla_cache_read_q8_paged", rc)
+        raise DsaError(name, rc)
     return out
 
 
-def _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream):
-    """Checks and output buffers the 8-bit attention calls share: the device, the sizes, the tensors to return
+def mla_cache_read_q8_paged(cache: torch.Tensor, cache_scale: torch.Tensor, kv_len: torch.Tensor,
+                            block_table: torch.Tensor, page_size: int, Nmax: int,
+                            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out [B, Nmax, 576] bf16: the kv_len[b] rows of each sequence of a paged 8-bit cache; later rows
+    of a given `out` stay as they are (a new one has zeros there)."""
+    return _cache_read_paged("mla_cache_read_q8_paged", Q8_ROW, cache, cache_scale, kv_len, block_table, page_size,
+                             Nmax, out, stream)
+
+
+def mla_cache_read_q4_paged(cache: torch.Tensor, cache_scale: torch.Tensor, kv_len: torch.Tensor,
+                            block_table: torch.Tensor, page_size: int, Nmax: int,
+                            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """mla_cache_read_q8_paged of a paged 4-bit cache (uint8 [num_pages * page_size, 416])."""
+    return _cache_read_paged("mla_cache_read_q4_paged", Q4_ROW, cache, cache_scale, kv_len, block_table, page_size,
+                             Nmax, out, stream)
+
+
+def _attn_low(row, q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream):
+    """Checks and output buffers the attention calls over rows of `row` bytes share: the device, the sizes, the tensors to return
     and the pointers of q, cache, cache_scale, idx, out, lse."""
     dev = _current_device()
     rows, heads, width = q.shape
     if heads != 64 or width != 576:
         _bad("q is bf16 [rows, 64, 576]")
-    top_k, n = idx.shape[-1], _q8_rows(cache)
+    top_k, n = idx.shape[-1], _cache_rows(cache, row)
     if out is None:
         if out_dtype not in (torch.float32, torch.bfloat16):
             _bad(f"attention output must be float32 or bf16, got {out_dtype}")
@@ -466,13 +504,18 @@ def _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse, out_dtype, stream):
         lse = _new((rows, 64), torch.float32, q.device, stream)
     f32 = out.dtype is torch.float32
     return (dev, rows, top_k, n, out, lse, DSA_OUT_F32 if f32 else DSA_OUT_BF16, _p(q, dev, _BITS16, rows * 36864, "q"),
-            _p(cache, dev, _U8, n * Q8_ROW, "cache"), _p(cache_scale, dev, _F32, n, "cache_scale"),
+            _p(cache, dev, _U8, n * row, "cache"), _p(cache_scale, dev, _F32, n, "cache_scale"),
             _p(idx, dev, _I32, rows * top_k, "idx"), _p(out, dev, _F32 if f32 else _BITS16, rows * 32768, "out"),
             _opt(lse, dev, _F32, rows * 64, "lse"))
 
 
 def attn_q8_workspace_size(rows: int, top_k: int) -> int:
     """Bytes an attention call of so many queries over an 8-bit cache takes on the current device (0: none)."""
+    return _q8_workspace_bytes(_current_device(), rows, top_k)
+
+
+def attn_q4_workspace_size(rows: int, top_k: int) -> int:
+    """The same for a 4-bit cache."""
     return _q8_workspace_bytes(_current_device(), rows, top_k)
 
 
@@ -506,18 +549,47 @@ def _q8_workspace(workspace, rows, top_k, dev, device, stream):
     return workspace, workspace.data_ptr(), workspace.nbytes
 
 
+def _attn_prefill(name, row, q, cache, cache_scale, idx, scale, out, lse, want_lse, stream, out_dtype, workspace):
+    dev, L, top_k, N, out, lse, od, pq, pc, ps, pi, po, pl = _attn_low(row, q, cache, cache_scale, idx, out, lse,
+                                                                       want_lse, out_dtype, stream)
+    workspace, pw, n_ws = _q8_workspace(workspace, L, top_k, dev, q.device, stream)
+    rc = getattr(_lib or load(), name)(pq, pc, ps, pi, L, N, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))
+    if rc:
+        raise DsaError(name, rc)
+    return (out, lse) if want_lse else out
+
+
 def mla_sparse_attn_prefill_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor, idx: torch.Tensor,
                                scale: float, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                                want_lse: bool = False, stream=None, out_dtype=torch.float32,
                                workspace: Optional[torch.Tensor] = None):
     """mla_sparse_attn_prefill over an 8-bit cache: cache uint8 [N, 640], cache_scale f32 [N]."""
-    dev, L, top_k, N, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
-                                                                      out_dtype, stream)
+    return _attn_prefill("mla_sparse_attn_prefill_q8", Q8_ROW, q, cache, cache_scale, idx, scale, out, lse, want_lse,
+                         stream, out_dtype, workspace)
+
+
+def mla_sparse_attn_prefill_q4(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor, idx: torch.Tensor,
+                               scale: float, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                               want_lse: bool = False, stream=None, out_dtype=torch.float32,
+                               workspace: Optional[torch.Tensor] = None):
+    """mla_sparse_attn_prefill over a 4-bit cache: cache uint8 [N, 416], cache_scale f32 [N]."""
+    return _attn_prefill("mla_sparse_attn_prefill_q4", Q4_ROW, q, cache, cache_scale, idx, scale, out, lse, want_lse,
+                         stream, out_dtype, workspace)
+
+
+def _attn_prefill_paged(name, row, q, cache, cache_scale, block_table, page_size, idx, scale, N, out, lse, want_lse,
+                        stream, out_dtype, workspace):
+    dev, L, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_low(row, q, cache, cache_scale, idx, out, lse,
+                                                                       want_lse, out_dtype, stream)
+    pages = block_table.numel()
+    if page_size > 0 and pages < -(-N // page_size):
+        _bad("block_table holds ceil(N / page_size) pages")
     workspace, pw, n_ws = _q8_workspace(workspace, L, top_k, dev, q.device, stream)
-    rc = (_lib or load()).mla_sparse_attn_prefill_q8(pq, pc, ps, pi, L, N, top_k, scale, po, od, pl, pw, n_ws,
-                                                     _stream_on(dev, stream))
+    rc = getattr(_lib or load(), name)(
+        pq, pc, ps, _p(block_table, dev, _I32, pages, "block_table"), page_size, n // page_size if page_size > 0 else 0, pi,
+        L, N, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))
     if rc:
-        raise DsaError("mla_sparse_attn_prefill_q8", rc)
+        raise DsaError(name, rc)
     return (out, lse) if want_lse else out
 
 
@@ -527,17 +599,32 @@ def mla_sparse_attn_prefill_q8_paged(q: torch.Tensor, cache: torch.Tensor, cache
                                      want_lse: bool = False, stream=None, out_dtype=torch.float32,
                                      workspace: Optional[torch.Tensor] = None):
     """mla_sparse_attn_prefill_paged over an 8-bit pool: cache uint8 [num_pages * page_size, 640]."""
-    dev, L, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
-                                                                      out_dtype, stream)
-    pages = block_table.numel()
-    if page_size > 0 and pages < -(-N // page_size):
-        _bad("block_table holds ceil(N / page_size) pages")
-    workspace, pw, n_ws = _q8_workspace(workspace, L, top_k, dev, q.device, stream)
-    rc = (_lib or load()).mla_sparse_attn_prefill_q8_paged(
-        pq, pc, ps, _p(block_table, dev, _I32, pages, "block_table"), page_size, n // page_size if page_size > 0 else 0, pi,
-        L, N, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))
+    return _attn_prefill_paged("mla_sparse_attn_prefill_q8_paged", Q8_ROW, q, cache, cache_scale, block_table,
+                               page_size, idx, scale, N, out, lse, want_lse, stream, out_dtype, workspace)
+
+
+def mla_sparse_attn_prefill_q4_paged(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor,
+                                     block_table: torch.Tensor, page_size: int, idx: torch.Tensor, scale: float, N: int,
+                                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                                     want_lse: bool = False, stream=None, out_dtype=torch.float32,
+                                     workspace: Optional[torch.Tensor] = None):
+    """mla_sparse_attn_prefill_paged over a 4-bit pool: cache uint8 [num_pages * page_size, 416]."""
+    return _attn_prefill_paged("mla_sparse_attn_prefill_q4_paged", Q4_ROW, q, cache, cache_scale, block_table,
+                               page_size, idx, scale, N, out, lse, want_lse, stream, out_dtype, workspace)
+
+
+def _attn_decode(name, row, q, cache, cache_scale, kv_len, idx, scale, out, lse, workspace, want_lse, stream,
+                 out_dtype):
+    dev, B, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_low(row, q, cache, cache_scale, idx, out, lse,
+                                                                       want_lse, out_dtype, stream)
+    if cache.dim() != 3 or cache.shape[0] != B:
+        _bad("the cache is uint8 [B, Nmax, %d]" % row)
+    workspace, pw, n_ws = _q8_workspace(workspace, B, top_k, dev, q.device, stream)
+    rc = getattr(_lib or load(), name)(
+        pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), pi, B, cache.shape[1], top_k, scale, po, od, pl,
+        pw, n_ws, _stream_on(dev, stream))
     if rc:
-        raise DsaError("mla_sparse_attn_prefill_q8_paged", rc)
+        raise DsaError(name, rc)
     return (out, lse) if want_lse else out
 
 
@@ -546,16 +633,30 @@ def mla_sparse_attn_decode_q8(q: torch.Tensor, cache: torch.Tensor, cache_scale:
                               lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                               want_lse: bool = False, stream=None, out_dtype=torch.float32):
     """mla_sparse_attn_decode over an 8-bit cache: cache uint8 [B, Nmax, 640], cache_scale f32 [B, Nmax]."""
-    dev, B, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
-                                                                      out_dtype, stream)
-    if cache.dim() != 3 or cache.shape[0] != B:
-        _bad("the cache is uint8 [B, Nmax, 640]")
+    return _attn_decode("mla_sparse_attn_decode_q8", Q8_ROW, q, cache, cache_scale, kv_len, idx, scale, out, lse,
+                        workspace, want_lse, stream, out_dtype)
+
+
+def mla_sparse_attn_decode_q4(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor, kv_len: torch.Tensor,
+                              idx: torch.Tensor, scale: float, out: Optional[torch.Tensor] = None,
+                              lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                              want_lse: bool = False, stream=None, out_dtype=torch.float32):
+    """mla_sparse_attn_decode over a 4-bit cache: cache uint8 [B, Nmax, 416], cache_scale f32 [B, Nmax]."""
+    return _attn_decode("mla_sparse_attn_decode_q4", Q4_ROW, q, cache, cache_scale, kv_len, idx, scale, out, lse,
+                        workspace, want_lse, stream, out_dtype)
+
+
+def _attn_decode_paged(name, row, q, cache, cache_scale, kv_len, block_table, page_size, idx, scale, Nmax, out, lse,
+                       workspace, want_lse, stream, out_dtype):
+    dev, B, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_low(row, q, cache, cache_scale, idx, out, lse,
+                                                                       want_lse, out_dtype, stream)
+    stride = _table(block_table, B)
     workspace, pw, n_ws = _q8_workspace(workspace, B, top_k, dev, q.device, stream)
-    rc = (_lib or load()).mla_sparse_attn_decode_q8(
-        pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), pi, B, cache.shape[1], top_k, scale, po, od, pl,
-        pw, n_ws, _stream_on(dev, stream))
+    rc = getattr(_lib or load(), name)(
+        pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), _p(block_table, dev, _I32, B * stride, "block_table"), stride,
+        page_size, n // page_size if page_size > 0 else 0, pi, B, Nmax, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))
     if rc:
-        raise DsaError("mla_sparse_attn_decode_q8", rc)
+        raise DsaError(name, rc)
     return (out, lse) if want_lse else out
 
 
@@ -565,16 +666,18 @@ def mla_sparse_attn_decode_q8_paged(q: torch.Tensor, cache: torch.Tensor, cache_
                                     lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                                     want_lse: bool = False, stream=None, out_dtype=torch.float32):
     """mla_sparse_attn_decode_paged over an 8-bit pool: cache uint8 [num_pages * page_size, 640]."""
-    dev, B, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_q8(q, cache, cache_scale, idx, out, lse, want_lse,
-                                                                      out_dtype, stream)
-    stride = _table(block_table, B)
-    workspace, pw, n_ws = _q8_workspace(workspace, B, top_k, dev, q.device, stream)
-    rc = (_lib or load()).mla_sparse_attn_decode_q8_paged(
-        pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), _p(block_table, dev, _I32, B * stride, "block_table"), stride,
-        page_size, n // page_size if page_size > 0 else 0, pi, B, Nmax, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))
-    if rc:
-        raise DsaError("mla_sparse_attn_decode_q8_paged", rc)
-    return (out, lse) if want_lse else out
+    return _attn_decode_paged("mla_sparse_attn_decode_q8_paged", Q8_ROW, q, cache, cache_scale, kv_len, block_table,
+                              page_size, idx, scale, Nmax, out, lse, workspace, want_lse, stream, out_dtype)
+
+
+def mla_sparse_attn_decode_q4_paged(q: torch.Tensor, cache: torch.Tensor, cache_scale: torch.Tensor,
+                                    kv_len: torch.Tensor, block_table: torch.Tensor, page_size: int, idx: torch.Tensor,
+                                    scale: float, Nmax: int, out: Optional[torch.Tensor] = None,
+                                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                                    want_lse: bool = False, stream=None, out_dtype=torch.float32):
+    """mla_sparse_attn_decode_paged over a 4-bit pool: cache uint8 [num_pages * page_size, 416]."""
+    return _attn_decode_paged("mla_sparse_attn_decode_q4_paged", Q4_ROW, q, cache, cache_scale, kv_len, block_table,
+                              page_size, idx, scale, Nmax, out, lse, workspace, want_lse, stream, out_dtype)
 
 
 def indexer_norm_rope(q: torch.Tensor, k: torch.Tensor, k_w: Optional[torch.Tensor], k_b: Optional[torch.Tensor],

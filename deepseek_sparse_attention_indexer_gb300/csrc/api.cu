@@ -358,7 +358,7 @@ dsa_status_t mla_sparse_attn_decode_noalloc(const void* q, const void* kv, const
 }
 
 namespace {
-// Host checks the 8-bit attention calls share.
+// Host checks the 8-bit and 4-bit attention calls share.
 dsa_status_t check_attn_q8(const void* q, const void* cache, const float* cache_scale, const int32_t* idx, int rows,
                            int N, int top_k, float scale, const void* out, int out_dtype) {
     if (!q || !cache || !cache_scale || !idx || !out) return DSA_ERR_INVALID_ARG;
@@ -374,6 +374,8 @@ dsa_status_t check_attn_q8(const void* q, const void* cache, const float* cache_
 bool eps_ok(float eps) { return eps >= 0.f && eps < 3.0e38f; }
 }  // namespace
 
+size_t mla_sparse_attn_q4_workspace_size(int rows, int top_k) { return mla_sparse_attn_q8_workspace_size(rows, top_k); }
+
 size_t mla_sparse_attn_q8_workspace_size(int rows, int top_k) {
     if (rows < 1 || top_k < 1 || top_k > DSA_MAX_TOPK || check_device() != DSA_OK) return 0;
     return attn_q8_workspace(rows, top_k);
@@ -386,23 +388,24 @@ dsa_status_t check_workspace(const void* workspace, size_t have, size_t need) {
 }
 }  // namespace
 
-dsa_status_t mla_sparse_attn_prefill_q8(const void* q, const void* cache, const float* cache_scale,
-                                        const int32_t* idx, int L, int N, int top_k, float scale, void* out,
-                                        int out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+namespace {
+// The attention calls over the 8-bit cache, and (q4) over the 4-bit one.
+dsa_status_t attn_prefill(bool q4, const void* q, const void* cache, const float* cache_scale, const int32_t* idx,
+                          int L, int N, int top_k, float scale, void* out, int out_dtype, float* lse,
+                          void* workspace, size_t ws_bytes, void* stream) {
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
     if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(L, top_k))) != DSA_OK) return st;
-    return launch_attn_q8_prefill(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32, lse,
-                                  workspace, PageTable{}, static_cast<cudaStream_t>(stream));
+    return launch_attn_q8_prefill(q, cache, cache_scale, q4, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32,
+                                  lse, workspace, PageTable{}, static_cast<cudaStream_t>(stream));
 }
 
-dsa_status_t mla_sparse_attn_prefill_q8_paged(const void* q, const void* cache, const float* cache_scale,
-                                              const int32_t* block_table, int page_size, int num_pages,
-                                              const int32_t* idx, int L, int N, int top_k, float scale, void* out,
-                                              int out_dtype, float* lse, void* workspace, size_t ws_bytes,
-                                              void* stream) {
+dsa_status_t attn_prefill_paged(bool q4, const void* q, const void* cache, const float* cache_scale,
+                                const int32_t* block_table, int page_size, int num_pages, const int32_t* idx,
+                                int L, int N, int top_k, float scale, void* out, int out_dtype, float* lse,
+                                void* workspace, size_t ws_bytes, void* stream) {
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
     PageTable pt;
@@ -411,14 +414,13 @@ dsa_status_t mla_sparse_attn_prefill_q8_paged(const void* q, const void* cache, 
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
     if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(L, top_k))) != DSA_OK) return st;
-    return launch_attn_q8_prefill(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32, lse,
-                                  workspace, pt, static_cast<cudaStream_t>(stream));
+    return launch_attn_q8_prefill(q, cache, cache_scale, q4, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32,
+                                  lse, workspace, pt, static_cast<cudaStream_t>(stream));
 }
 
-dsa_status_t mla_sparse_attn_decode_q8(const void* q, const void* cache, const float* cache_scale,
-                                       const int32_t* kv_len, const int32_t* idx, int B, int Nmax, int top_k,
-                                       float scale, void* out, int out_dtype, float* lse, void* workspace,
-                                       size_t ws_bytes, void* stream) {
+dsa_status_t attn_decode(bool q4, const void* q, const void* cache, const float* cache_scale,
+                         const int32_t* kv_len, const int32_t* idx, int B, int Nmax, int top_k, float scale,
+                         void* out, int out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
     if (!kv_len) return DSA_ERR_INVALID_ARG;
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, B, Nmax, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
@@ -426,16 +428,15 @@ dsa_status_t mla_sparse_attn_decode_q8(const void* q, const void* cache, const f
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
     if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(B, top_k))) != DSA_OK) return st;
-    return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
+    return launch_attn_q8_decode(q, cache, cache_scale, q4, kv_len, idx, B, Nmax, top_k, scale, out,
                                  out_dtype == DSA_OUT_F32, lse, workspace, PageTable{},
                                  static_cast<cudaStream_t>(stream));
 }
 
-dsa_status_t mla_sparse_attn_decode_q8_paged(const void* q, const void* cache, const float* cache_scale,
-                                             const int32_t* kv_len, const int32_t* block_table, int bt_stride,
-                                             int page_size, int num_pages, const int32_t* idx, int B, int Nmax,
-                                             int top_k, float scale, void* out, int out_dtype, float* lse,
-                                             void* workspace, size_t ws_bytes, void* stream) {
+dsa_status_t attn_decode_paged(bool q4, const void* q, const void* cache, const float* cache_scale,
+                               const int32_t* kv_len, const int32_t* block_table, int bt_stride, int page_size,
+                               int num_pages, const int32_t* idx, int B, int Nmax, int top_k, float scale,
+                               void* out, int out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
     if (!kv_len) return DSA_ERR_INVALID_ARG;
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, B, Nmax, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
@@ -445,8 +446,75 @@ dsa_status_t mla_sparse_attn_decode_q8_paged(const void* q, const void* cache, c
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
     if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(B, top_k))) != DSA_OK) return st;
-    return launch_attn_q8_decode(q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out,
+    return launch_attn_q8_decode(q, cache, cache_scale, q4, kv_len, idx, B, Nmax, top_k, scale, out,
                                  out_dtype == DSA_OUT_F32, lse, workspace, pt, static_cast<cudaStream_t>(stream));
+}
+}  // namespace
+
+dsa_status_t mla_sparse_attn_prefill_q8(const void* q, const void* cache, const float* cache_scale,
+                                        const int32_t* idx, int L, int N, int top_k, float scale, void* out,
+                                        int out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    return attn_prefill(false, q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype, lse, workspace,
+                        ws_bytes, stream);
+}
+
+dsa_status_t mla_sparse_attn_prefill_q4(const void* q, const void* cache, const float* cache_scale,
+                                        const int32_t* idx, int L, int N, int top_k, float scale, void* out,
+                                        int out_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+    return attn_prefill(true, q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype, lse, workspace,
+                        ws_bytes, stream);
+}
+
+dsa_status_t mla_sparse_attn_prefill_q8_paged(const void* q, const void* cache, const float* cache_scale,
+                                              const int32_t* block_table, int page_size, int num_pages,
+                                              const int32_t* idx, int L, int N, int top_k, float scale, void* out,
+                                              int out_dtype, float* lse, void* workspace, size_t ws_bytes,
+                                              void* stream) {
+    return attn_prefill_paged(false, q, cache, cache_scale, block_table, page_size, num_pages, idx, L, N, top_k,
+                              scale, out, out_dtype, lse, workspace, ws_bytes, stream);
+}
+
+dsa_status_t mla_sparse_attn_prefill_q4_paged(const void* q, const void* cache, const float* cache_scale,
+                                              const int32_t* block_table, int page_size, int num_pages,
+                                              const int32_t* idx, int L, int N, int top_k, float scale, void* out,
+                                              int out_dtype, float* lse, void* workspace, size_t ws_bytes,
+                                              void* stream) {
+    return attn_prefill_paged(true, q, cache, cache_scale, block_table, page_size, num_pages, idx, L, N, top_k,
+                              scale, out, out_dtype, lse, workspace, ws_bytes, stream);
+}
+
+dsa_status_t mla_sparse_attn_decode_q8(const void* q, const void* cache, const float* cache_scale,
+                                       const int32_t* kv_len, const int32_t* idx, int B, int Nmax, int top_k,
+                                       float scale, void* out, int out_dtype, float* lse, void* workspace,
+                                       size_t ws_bytes, void* stream) {
+    return attn_decode(false, q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out, out_dtype, lse,
+                       workspace, ws_bytes, stream);
+}
+
+dsa_status_t mla_sparse_attn_decode_q4(const void* q, const void* cache, const float* cache_scale,
+                                       const int32_t* kv_len, const int32_t* idx, int B, int Nmax, int top_k,
+                                       float scale, void* out, int out_dtype, float* lse, void* workspace,
+                                       size_t ws_bytes, void* stream) {
+    return attn_decode(true, q, cache, cache_scale, kv_len, idx, B, Nmax, top_k, scale, out, out_dtype, lse,
+                       workspace, ws_bytes, stream);
+}
+
+dsa_status_t mla_sparse_attn_decode_q8_paged(const void* q, const void* cache, const float* cache_scale,
+                                             const int32_t* kv_len, const int32_t* block_table, int bt_stride,
+                                             int page_size, int num_pages, const int32_t* idx, int B, int Nmax,
+                                             int top_k, float scale, void* out, int out_dtype, float* lse,
+                                             void* workspace, size_t ws_bytes, void* stream) {
+    return attn_decode_paged(false, q, cache, cache_scale, kv_len, block_table, bt_stride, page_size, num_pages,
+                             idx, B, Nmax, top_k, scale, out, out_dtype, lse, workspace, ws_bytes, stream);
+}
+
+dsa_status_t mla_sparse_attn_decode_q4_paged(const void* q, const void* cache, const float* cache_scale,
+                                             const int32_t* kv_len, const int32_t* block_table, int bt_stride,
+                                             int page_size, int num_pages, const int32_t* idx, int B, int Nmax,
+                                             int top_k, float scale, void* out, int out_dtype, float* lse,
+                                             void* workspace, size_t ws_bytes, void* stream) {
+    return attn_decode_paged(true, q, cache, cache_scale, kv_len, block_table, bt_stride, page_size, num_pages, idx,
+                             B, Nmax, top_k, scale, out, out_dtype, lse, workspace, ws_bytes, stream);
 }
 
 dsa_status_t mla_cache_write_q8(const void* kv_a, int64_t kv_a_stride, const float* norm_w, float eps,
@@ -465,20 +533,21 @@ dsa_status_t mla_cache_write_q8(const void* kv_a, int64_t kv_a_stride, const flo
                                  cache_scale, (int)cache_rows, static_cast<cudaStream_t>(stream));
 }
 
-dsa_status_t mla_cache_read_q8(const void* cache, const float* cache_scale, int64_t cache_rows, const int32_t* slots,
-                               int R, void* out, void* stream) {
+dsa_status_t mla_cache_read_q8(const void* cache, const float* cache_scale, int64_t cache_rows,
+                               const int32_t* slots, int R, void* out, void* stream) {
     if (!cache || !cache_scale || !slots || !out) return DSA_ERR_INVALID_ARG;
     if (R < 1 || cache_rows < 1) return DSA_ERR_INVALID_ARG;
     if (cache_rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
     dsa_status_t st = check_device();
     if (st != DSA_OK) return st;
-    return launch_cache_read_q8(cache, cache_scale, (int)cache_rows, slots, R, out, static_cast<cudaStream_t>(stream));
+    return launch_cache_read_q8(cache, cache_scale, (int)cache_rows, slots, R, out,
+                                static_cast<cudaStream_t>(stream));
 }
 
 dsa_status_t mla_cache_read_q8_paged(const void* cache, const float* cache_scale, const int32_t* kv_len,
-                                     const int32_t* block_table, int bt_stride, int page_size, int num_pages, int B,
-                                     int Nmax, void* out, void* stream) {
+                                     const int32_t* block_table, int bt_stride, int page_size, int num_pages,
+                                     int B, int Nmax, void* out, void* stream) {
     if (!cache || !cache_scale || !kv_len || !out) return DSA_ERR_INVALID_ARG;
     if (B < 1 || Nmax < 1) return DSA_ERR_INVALID_ARG;
     PageTable pt;
@@ -487,7 +556,51 @@ dsa_status_t mla_cache_read_q8_paged(const void* cache, const float* cache_scale
     if ((long long)B * bt_stride > 0x7FFFFFFFLL || (long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
-    return launch_cache_read_q8_paged(cache, cache_scale, kv_len, B, Nmax, out, pt, static_cast<cudaStream_t>(stream));
+    return launch_cache_read_q8_paged(cache, cache_scale, kv_len, B, Nmax, out, pt,
+                                      static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_cache_write_q4(const void* kv_a, int64_t kv_a_stride, const float* norm_w, float eps,
+                                const float* cos_sin, int max_pos, int interleave, const int32_t* pos,
+                                const int32_t* slots, int R, void* cache, float* cache_scale, int64_t cache_rows,
+                                void* stream) {
+    if (!kv_a || !norm_w || !cos_sin || !pos || !slots || !cache || !cache_scale) return DSA_ERR_INVALID_ARG;
+    if (R < 1 || max_pos < 1 || cache_rows < 1 || kv_a_stride < DSA_QK_DIM || !eps_ok(eps)) return DSA_ERR_INVALID_ARG;
+    if (interleave != 0 && interleave != 1) return DSA_ERR_INVALID_ARG;
+    if (cache_rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(kv_a) || !aligned16(norm_w) || !aligned16(cos_sin) || !aligned32(cache) || kv_a_stride % 8)
+        return DSA_ERR_MISALIGNED;
+    dsa_status_t st = check_device();
+    if (st != DSA_OK) return st;
+    return launch_cache_write_q4(kv_a, kv_a_stride, norm_w, eps, cos_sin, max_pos, interleave, pos, slots, R, cache,
+                                 cache_scale, (int)cache_rows, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_cache_read_q4(const void* cache, const float* cache_scale, int64_t cache_rows,
+                               const int32_t* slots, int R, void* out, void* stream) {
+    if (!cache || !cache_scale || !slots || !out) return DSA_ERR_INVALID_ARG;
+    if (R < 1 || cache_rows < 1) return DSA_ERR_INVALID_ARG;
+    if (cache_rows > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    dsa_status_t st = check_device();
+    if (st != DSA_OK) return st;
+    return launch_cache_read_q4(cache, cache_scale, (int)cache_rows, slots, R, out,
+                                static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_cache_read_q4_paged(const void* cache, const float* cache_scale, const int32_t* kv_len,
+                                     const int32_t* block_table, int bt_stride, int page_size, int num_pages,
+                                     int B, int Nmax, void* out, void* stream) {
+    if (!cache || !cache_scale || !kv_len || !out) return DSA_ERR_INVALID_ARG;
+    if (B < 1 || Nmax < 1) return DSA_ERR_INVALID_ARG;
+    PageTable pt;
+    dsa_status_t st = make_page_table(block_table, bt_stride, page_size, num_pages, Nmax, &pt);
+    if (st != DSA_OK) return st;
+    if ((long long)B * bt_stride > 0x7FFFFFFFLL || (long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned32(cache) || !aligned16(out)) return DSA_ERR_MISALIGNED;
+    if ((st = check_device()) != DSA_OK) return st;
+    return launch_cache_read_q4_paged(cache, cache_scale, kv_len, B, Nmax, out, pt,
+                                      static_cast<cudaStream_t>(stream));
 }
 
 dsa_status_t dsa_indexer_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int norm,

@@ -87,16 +87,25 @@ dsa_status_t launch_cache_read_q8(const void* cache, const float* cache_scale, i
                                   int R, void* out, cudaStream_t stream);
 dsa_status_t launch_cache_read_q8_paged(const void* cache, const float* cache_scale, const int32_t* kv_len, int B,
                                         int Nmax, void* out, const PageTable& pages, cudaStream_t stream);
-dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, const int32_t* idx,
-                                    int L, int N, int top_k, float scale, void* out, int out_f32, float* lse,
-                                    void* workspace, const PageTable& pages, cudaStream_t stream);
+dsa_status_t launch_cache_write_q4(const void* kv_a, int64_t kv_a_stride, const float* norm_w, float eps,
+                                   const float* cos_sin, int max_pos, int interleave, const int32_t* pos,
+                                   const int32_t* slots, int R, void* cache, float* cache_scale, int cache_rows,
+                                   cudaStream_t stream);
+dsa_status_t launch_cache_read_q4(const void* cache, const float* cache_scale, int cache_rows, const int32_t* slots,
+                                  int R, void* out, cudaStream_t stream);
+dsa_status_t launch_cache_read_q4_paged(const void* cache, const float* cache_scale, const int32_t* kv_len, int B,
+                                        int Nmax, void* out, const PageTable& pages, cudaStream_t stream);
+// The attention over the 8-bit cache, or (q4) over the 4-bit one.
+dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, bool q4,
+                                    const int32_t* idx, int L, int N, int top_k, float scale, void* out, int out_f32,
+                                    float* lse, void* workspace, const PageTable& pages, cudaStream_t stream);
 size_t attn_q8_workspace(int rows, int top_k);
 // Merge of nsplit partial (normalised output, lse) pairs a sequence.
 dsa_status_t launch_decode_combine(const float* part_o, const float* part_lse, int B, int nsplit, void* out, int out_f32,
                                    float* lse, cudaStream_t stream);
-dsa_status_t launch_attn_q8_decode(const void* q, const void* cache, const float* cache_scale, const int32_t* kv_len,
-                                   const int32_t* idx, int B, int Nmax, int top_k, float scale, void* out,
-                                   int out_f32, float* lse, void* workspace, const PageTable& pages,
+dsa_status_t launch_attn_q8_decode(const void* q, const void* cache, const float* cache_scale, bool q4,
+                                   const int32_t* kv_len, const int32_t* idx, int B, int Nmax, int top_k, float scale,
+                                   void* out, int out_f32, float* lse, void* workspace, const PageTable& pages,
                                    cudaStream_t stream);
 dsa_status_t launch_indexer_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int norm,
                                       const float* q_w, const float* q_b, const float* k_w, const float* k_b,

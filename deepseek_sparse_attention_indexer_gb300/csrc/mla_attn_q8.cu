@@ -47,7 +47,7 @@
 #include <atomic>
 #include <cmath>
 
-#include "dsa_q8.cuh"
+#include "dsa_q4.cuh"
 #include "mla_attn_common.cuh"
 
 namespace dsa {
@@ -107,7 +107,8 @@ constexpr int OFF_RED = OFF_QS + 4 * kH * 4;       // float [4][64]
 constexpr int OFF_MNEG = OFF_RED + 4 * kH * 4;     // float [64]: minus the references
 constexpr int OFF_DELTA = OFF_MNEG + kH * 4;       // float [64]: how far a reference has just risen
 constexpr int OFF_INVL = OFF_DELTA + kH * 4;       // float [64]
-constexpr int OFF_BAR = OFF_INVL + kH * 4;
+constexpr int OFF_TABLE = OFF_INVL + kH * 4;       // uint2 [37]: the magnitudes of 4-bit codes as e4m3, by block byte
+constexpr int OFF_BAR = OFF_TABLE + (kQ4Scales + 1) * 8;
 // barriers: full[8], free[4], rope_full, s_full, s_free, p_full, q_free, q_raw, q_full
 constexpr int kSlots = kStages * kChunks;
 constexpr int kBars = kSlots + 2 * kStages + 7;
@@ -134,9 +135,19 @@ constexpr uint32_t IDESC_PV = idesc_e4m3_scaled_f32(128, 64, true, true);
 
 __device__ __align__(16) uint8_t g_no_row[kQ8Latent];   // zeros, the latent dims of a slot without a row
 
+// The two caches: bytes of a row, where its rope dims begin.
+template <bool Q4>
+struct Rows {
+    static constexpr int kBytes = Q4 ? kQ4Row : kQ8Row;
+    static constexpr int kRope = Q4 ? kQ4Rope : kQ8Latent;
+    // the lane's share of a row's codes, and whether they stand for zeros of either sign
+    static constexpr int kLaneCodes = Q4 ? kQ4Codes / 32 : kQ8Latent / 32;
+};
+static_assert(kQ4Rope <= kQ8Latent, "g_no_row holds the codes and blocks of a 4-bit row");
+
 struct AttnQ8Params : AttnShape {
     const __nv_bfloat16* q;    // [rows][64][576]
-    const uint8_t* cache;      // 640-byte rows
+    const uint8_t* cache;      // 640-byte or 416-byte rows
     const float* cache_scale;
     void* out;                 // final: [rows][64][512], float32 or bf16 (out_f32)
     int out_f32;
@@ -245,7 +256,12 @@ struct RowStream {
     }
 };
 
-__device__ __forceinline__ bool codes_are_zero(const uint8_t* at) {   // 16 codes, zeros of either sign
+template <bool Q4>
+__device__ __forceinline__ bool codes_are_zero(const uint8_t* at) {   // kLaneCodes bytes, zeros of either sign
+    if (Q4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+        return ((v.x | v.y) & kQ4Magnitudes) == 0;
+    }
     const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
     return ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) == 0;
 }
@@ -253,12 +269,15 @@ __device__ __forceinline__ bool codes_are_zero(const uint8_t* at) {   // 16 code
 // The scale sc of the lane's row, or kZeroRowScale where the row's latent dims are zeros, by a warp: each lane looks at
 // its row's first codes, and the warp together at the rows that begin with zeros.  (Two or four rows at once took
 // registers that the kernel has not: 1.13 -> 1.15, 1.17 ms without any such row.)
+template <bool Q4>
 __device__ __forceinline__ float row_scale(const uint8_t* cache, int row, float sc, uint32_t lane) {
-    const bool maybe = sc >= 1.f && codes_are_zero(cache + (int64_t)row * kQ8Row);
+    constexpr int kBytes = Rows<Q4>::kBytes;
+    const bool maybe = sc >= 1.f && codes_are_zero<Q4>(cache + (int64_t)row * kBytes);
     for (uint32_t m = __ballot_sync(0xffffffffu, maybe); m; m &= m - 1) {
         const int l = __ffs(m) - 1;
         const int64_t r = __shfl_sync(0xffffffffu, row, l);
-        if (__all_sync(0xffffffffu, codes_are_zero(cache + r * kQ8Row + 16 * lane)) && (int)lane == l) sc = kZeroRowScale;
+        const bool zero = codes_are_zero<Q4>(cache + r * kBytes + Rows<Q4>::kLaneCodes * lane);
+        if (__all_sync(0xffffffffu, zero) && (int)lane == l) sc = kZeroRowScale;
     }
     return sc;
 }
@@ -306,7 +325,8 @@ __device__ __noinline__ void zero_item(const AttnQ8Params& p, int row, int split
 }
 
 // SPLIT: one item a CTA, a part of a query; else persistent CTAs, whole queries and then parts.
-template <bool SPLIT>
+// Q4: the 4-bit cache, whose rows are expanded to the same e4m3 tile on their way to shared memory.
+template <bool SPLIT, bool Q4>
 __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_constant__ CUtensorMap tmap_q, const AttnQ8Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {   // the operands' swizzle counts from 1 KB boundaries; there is no room to round up
@@ -338,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&full[i], kGatherWarps * 32);   // one cp.async arrival per gather thread
+            mbar_init(&full[i], Q4 ? kGatherWarps : kGatherWarps * 32);   // one cp.async arrival per gather thread
         }
         for (int i = 0; i < 2 * kStages; ++i) mbar_init(&freed[i], kPvIssuers);   // both issuers' commits of a chunk
         mbar_init(rope_full, kRopeWarps);
@@ -370,6 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         tmem_st16(a + TM_LO, v);
         tmem_st_wait();
     }
+    if (Q4 && threadIdx.x <= kQ4Scales)
+        reinterpret_cast<uint2*>(smem + OFF_TABLE)[threadIdx.x] =
+            threadIdx.x < kQ4Scales ? q4_table(q4_block_scale(threadIdx.x)) : make_uint2(0, 0);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -508,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
     } else if (warp >= kFirstGather && warp < kFirstWorker) {
         // ------------------------------------------------------------ gather: latent rows, rope rows, queries
         setmaxnreg_dec<kGatherRegs>();
+        constexpr int kBytes = Rows<Q4>::kBytes;
         const bool is_rope = warp >= kFirstRope;
         const int gw = (warp - kFirstGather) & 3; // rows 32 gw .. 32 gw + 31 of a tile
         const int qh0 = kQHeads * (warp - kFirstGather);
@@ -548,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             const int row1 = more ? rs.resolve(p) : -1;
             const bool first1 = rs.first, has1 = more;
             // a row of a large cache into L2 a tile before it is copied (by the time of the copy HBM has answered)
-            if (p.l2_prefetch && !is_rope && row1 >= 0) l2_prefetch_bulk(p.cache + (int64_t)row1 * kQ8Row, kQ8Row);
+            if (p.l2_prefetch && !is_rope && row1 >= 0) l2_prefetch_bulk(p.cache + (int64_t)row1 * kBytes, kBytes);
             more = more && rs.fetch(p, lane, base);
             if (is_rope) {
                 // A lane carries one key's 64 rope dims (128 bytes) through registers into its lane of tensor memory:
@@ -558,12 +582,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
 #pragma unroll
                 for (int i = 0; i < 32; ++i) k[i] = 0;
                 if (row >= 0) {
-                    const uint8_t* src = p.cache + (int64_t)row * kQ8Row + kQ8Latent;
+                    const uint8_t* src = p.cache + (int64_t)row * kBytes + Rows<Q4>::kRope;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) ldg_nc_v8(src + 32 * i, k + 8 * i);
                     sc = __ldg(p.cache_scale + row);
                 }
-                sc = row_scale(p.cache, row, sc, lane);
+                sc = row_scale<Q4>(p.cache, row, sc, lane);
                 if (g > 0 && !wait(s_full, (g - 1) & 1)) break;   // QK of the tile before is complete
                 tc_fence_after();
                 __syncwarp();
@@ -576,6 +600,43 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(rope_full);
+            } else if (Q4) {
+                // A lane expands 32 dims of each of its rows a half tile: 16 bytes of codes, two block bytes.  The two
+                // pieces that it stores lie in one chunk; lanes of the half's second chunk begin with the odd one, so
+                // that the eight lanes of a row meet no bank twice.
+                const uint8_t* mine = row < 0 ? g_no_row : p.cache + (int64_t)row * kBytes;
+                const uint2* table = reinterpret_cast<const uint2*>(smem + OFF_TABLE);
+                bool ok = true;
+#pragma unroll 1
+                for (int half = 0; ok && half < 2; ++half) {
+                    uint4 code[8];
+                    uint32_t block[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint8_t* src = reinterpret_cast<const uint8_t*>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), 4 * i + ci));
+                        code[i] = ldg_nc_v4(src + 128 * half + 16 * cc);
+                        block[i] = __ldg(reinterpret_cast<const uint16_t*>(src + kQ4Codes + 16 * half) + cc);
+                    }
+                    if (!(ok = wait(&freed[2 * (g & 1) + half], ((g >> 1) & 1) ^ 1))) break;
+                    const int odd = cc >> 2, chunk = 2 * half + odd;
+                    uint8_t* dst = smem + OFF_LAT + (g & 1) * (kChunks * kBlk) + chunk * kBlk + (32 * gw + ci) * 128;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint2 t0 = table[min(block[i] & 0xffu, (uint32_t)kQ4Scales)];
+                        const uint2 t1 = table[min(block[i] >> 8, (uint32_t)kQ4Scales)];
+                        const uint2 a = q4_expand(code[i].x, t0), b = q4_expand(code[i].y, t0);
+                        const uint2 c = q4_expand(code[i].z, t1), d = q4_expand(code[i].w, t1);
+                        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
+                        const int sw = 4 * (i & 1) + ci, pc = 2 * (cc & 3);    // row % 8, the first of the two pieces
+                        *reinterpret_cast<uint4*>(dst + i * 512 + (((pc + odd) ^ sw) << 4)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4*>(dst + i * 512 + (((pc + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane < 2) mbar_arrive(&full[4 * (g & 1) + 2 * half + lane]);
+                }
+                if (!ok) break;
             } else {
                 const uint8_t* mine = row < 0 ? g_no_row : p.cache + (int64_t)row * kQ8Row;
                 const uint8_t* src[8];
@@ -943,26 +1004,26 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
 }
 
 // Shared-memory limit of a kernel, raised once a device.
-template <bool SPLIT>
+template <bool SPLIT, bool Q4>
 dsa_status_t prepare_kernel() {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> done[kMaxDevices];
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DSA_ERR_CUDA;
     if (done[dev].load(std::memory_order_acquire)) return DSA_OK;
-    const dsa_status_t st = ensure_smem_attr(reinterpret_cast<const void*>(mla_attn_q8_kernel<SPLIT>), kSmemBytes);
+    const dsa_status_t st = ensure_smem_attr(reinterpret_cast<const void*>(mla_attn_q8_kernel<SPLIT, Q4>), kSmemBytes);
     if (st == DSA_OK) done[dev].store(true, std::memory_order_release);
     return st;
 }
 
-template <bool SPLIT>
+template <bool SPLIT, bool Q4>
 dsa_status_t launch(const AttnQ8Params& p, cudaStream_t stream) {
-    dsa_status_t st = prepare_kernel<SPLIT>();
+    dsa_status_t st = prepare_kernel<SPLIT, Q4>();
     if (st != DSA_OK) return st;
     CUtensorMap tq;
     if ((st = make_tmap_bf16_2d(&tq, p.q, DSA_QK_DIM, (uint64_t)p.rows * kH, DSA_QK_DIM * 2, 64, kH)) != DSA_OK) return st;
     const int sms = device_sm_count();
-    if (launch_pdl(mla_attn_q8_kernel<SPLIT>, dim3(p.n_items < sms ? p.n_items : sms), dim3(kThreads), kSmemBytes, stream,
+    if (launch_pdl(mla_attn_q8_kernel<SPLIT, Q4>, dim3(p.n_items < sms ? p.n_items : sms), dim3(kThreads), kSmemBytes, stream,
                    tq, p) != cudaSuccess)
         return DSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
@@ -994,8 +1055,8 @@ Cut cut_rows(int rows, int top_k) {
 // tiles or more to run ahead in; a prefetch of rows that L2 holds, or of few tiles, only takes from the copies.
 // Without / with, us: 1216 queries at 16k keys (10 MB) 349 / 355, at 131k (84 MB) 379 / 375, at 1M 412 / 397;
 // decode of 152 sequences of 8k 63.3 / 62.8, of 304 of 32k 122.4 / 120.0, of 32 of 131k (4 tiles an item) 29.7 / 30.4.
-int want_l2_prefetch(int64_t keys, int split_len) {
-    return split_len >= 8 * kTile && (size_t)keys * kQ8Row > device_l2_bytes() / 2 ? 1 : 0;
+int want_l2_prefetch(int64_t keys, int split_len, int row_bytes) {
+    return split_len >= 8 * kTile && (size_t)keys * row_bytes > device_l2_bytes() / 2 ? 1 : 0;
 }
 
 AttnQ8Params base_params(const void* q, const void* cache, const float* cache_scale, const int32_t* idx, int Nmax,
@@ -1016,6 +1077,7 @@ AttnQ8Params base_params(const void* q, const void* cache, const float* cache_sc
     return p;
 }
 
+template <bool Q4>
 dsa_status_t launch_rows(AttnQ8Params p, int rows, void* workspace, cudaStream_t stream) {
     const Cut c = cut_rows(rows, p.top_k);
     p.rows = rows;
@@ -1023,10 +1085,11 @@ dsa_status_t launch_rows(AttnQ8Params p, int rows, void* workspace, cudaStream_t
     p.nsplit = c.splits;
     p.split_len = c.each * kTile;
     p.n_items = c.whole + c.cut * c.splits;
-    p.l2_prefetch = want_l2_prefetch((p.prefill ? 1 : (int64_t)rows) * p.Nmax, c.whole > 0 ? p.top_k : p.split_len);
+    p.l2_prefetch = want_l2_prefetch((p.prefill ? 1 : (int64_t)rows) * p.Nmax, c.whole > 0 ? p.top_k : p.split_len,
+                                    Rows<Q4>::kBytes);
     p.part_o = static_cast<float*>(workspace);
     p.part_lse = p.part_o + (size_t)c.cut * c.splits * kH * kDv;
-    const dsa_status_t st = c.whole > 0 ? launch<false>(p, stream) : launch<true>(p, stream);
+    const dsa_status_t st = c.whole > 0 ? launch<false, Q4>(p, stream) : launch<true, Q4>(p, stream);
     if (st != DSA_OK || c.cut == 0) return st;
     void* out = static_cast<char*>(p.out) + (int64_t)c.whole * kH * kDv * (p.out_f32 ? 4 : 2);
     float* lse = p.lse ? p.lse + (int64_t)c.whole * kH : nullptr;
@@ -1040,21 +1103,21 @@ size_t attn_q8_workspace(int rows, int top_k) {
     return (size_t)c.cut * c.splits * kH * (kDv + 1) * sizeof(float);
 }
 
-dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, const int32_t* idx,
-                                    int L, int N, int top_k, float scale, void* out, int out_f32, float* lse,
-                                    void* workspace, const PageTable& pages, cudaStream_t stream) {
+dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, bool q4,
+                                    const int32_t* idx, int L, int N, int top_k, float scale, void* out, int out_f32,
+                                    float* lse, void* workspace, const PageTable& pages, cudaStream_t stream) {
     AttnQ8Params p = base_params(q, cache, cache_scale, idx, N, top_k, scale, out, out_f32, lse, pages);
     p.prefill = 1;
-    return launch_rows(p, L, workspace, stream);
+    return q4 ? launch_rows<true>(p, L, workspace, stream) : launch_rows<false>(p, L, workspace, stream);
 }
 
-dsa_status_t launch_attn_q8_decode(const void* q, const void* cache, const float* cache_scale, const int32_t* kv_len,
-                                   const int32_t* idx, int B, int Nmax, int top_k, float scale, void* out,
-                                   int out_f32, float* lse, void* workspace, const PageTable& pages,
+dsa_status_t launch_attn_q8_decode(const void* q, const void* cache, const float* cache_scale, bool q4,
+                                   const int32_t* kv_len, const int32_t* idx, int B, int Nmax, int top_k, float scale,
+                                   void* out, int out_f32, float* lse, void* workspace, const PageTable& pages,
                                    cudaStream_t stream) {
     AttnQ8Params p = base_params(q, cache, cache_scale, idx, Nmax, top_k, scale, out, out_f32, lse, pages);
     p.kv_len = kv_len;
-    return launch_rows(p, B, workspace, stream);
+    return q4 ? launch_rows<true>(p, B, workspace, stream) : launch_rows<false>(p, B, workspace, stream);
 }
 
 }  // namespace dsa

@@ -45,6 +45,7 @@ extern "C" {
 #define DSA_V_HEAD_DIM 256
 #define DSA_MAX_TOPK 2048
 #define DSA_Q8_ROW_BYTES 640   /* a row of the 8-bit latent cache */
+#define DSA_Q4_ROW_BYTES 416   /* a row of the 4-bit latent cache */
 
 typedef int32_t dsa_status_t;
 
@@ -379,6 +380,80 @@ dsa_status_t mla_sparse_attn_decode_q8(const void *q, const void *cache, const f
                                        int top_k, float scale, void *out, int out_dtype, float *lse,
                                        void *workspace, size_t ws_bytes, void *stream);
 dsa_status_t mla_sparse_attn_decode_q8_paged(const void *q, const void *cache, const float *cache_scale,
+                                             const int32_t *kv_len, const int32_t *block_table,
+                                             int bt_stride, int page_size, int num_pages,
+                                             const int32_t *idx, int B, int Nmax, int top_k, float scale,
+                                             void *out, int out_dtype, float *lse, void *workspace,
+                                             size_t ws_bytes, void *stream);
+
+/*
+ * The 4-bit latent cache.  A key's row takes 416 bytes (a bf16 row 1152, an 8-bit one 640):
+ *
+ *   cache[row]        bytes 0..255:   the 512 latent dims, four bits each
+ *                     bytes 256..287: a scale byte for each block of 16 dims
+ *                     bytes 288..415: the 64 rotated rope dims, bf16
+ *   cache_scale[row]  f32
+ *
+ * A dim is +-M * S * cache_scale[row], M one of 0, 1/2, 1, 3/2, 2, 3, 4, 6 (index 0..7: a float of two
+ * exponent bits and one fraction bit), S the block's scale: byte 3 a + m with m < 3, a < 12 stands for
+ * (1 + m / 4) * 2^(a - 6), 36 and above for 0.  Of the four bytes of dims 8 g .. 8 g + 7, byte i holds the
+ * index of dim 8 g + 2 i in bits 0-2 and of dim 8 g + 2 i + 1 in bits 4-6, the sign of dim 8 g + 4 + i in
+ * bit 3 and of dim 8 g + i in bit 7.  Every byte pattern is a valid row.  M * S is an e4m3 number, whatever
+ * M and S: a row of this cache is one of the 8-bit cache in fewer bytes, and the calls below compute what
+ * the calls over the 8-bit cache compute of those values.  As written by mla_cache_write_q4 the scale is a
+ * power of two, which makes every stored value exactly a bf16 number; readers take any positive finite
+ * scale in [2^-64, 2^64].  `cache` is 32-byte aligned.  Rows are addressed as in the bf16 cache (dense
+ * [B, Nmax] rows or pages of a pool; rows * 416 may pass 2^32).  No counterpart on the pages.
+ */
+
+/*
+ * mla_cache_write_q4 -- mla_cache_write_q8 into the 4-bit cache: u and the rope dims as there, then
+ *
+ *   s_b  = the smallest (1 + m / 4) * 2^j with m in {0, 1, 2} and max|u| of block b <= 6 s_b
+ *   k    = J - 5, J the largest j of the row's blocks, clamped to -64..64; -64 for a row of zeros
+ *   S_b  = s_b * 2^-k, cut to the largest S there is; 2^-6 for a block that needs less
+ *   M    = |u| / (S_b * 2^k) to the nearest, ties to the even index, saturating;  cache_scale = 2^k
+ *
+ * (u as a float32 rounded to odd, so that every comparison is as with u itself; below 2^-149 u is 0.)
+ * Arguments, bounds and errors are those of mla_cache_write_q8 (rows of 416 bytes).
+ */
+dsa_status_t mla_cache_write_q4(const void *kv_a, int64_t kv_a_stride, const float *norm_w, float eps,
+                                const float *cos_sin, int max_pos, int interleave, const int32_t *pos,
+                                const int32_t *slots, int R, void *cache, float *cache_scale,
+                                int64_t cache_rows, void *stream);
+
+/*
+ * mla_cache_read_q4, mla_cache_read_q4_paged -- rows of the 4-bit cache back as bf16 rows (exact for
+ * power-of-two scales); arguments, bounds and errors are those of mla_cache_read_q8 and its paged form.
+ */
+dsa_status_t mla_cache_read_q4(const void *cache, const float *cache_scale, int64_t cache_rows,
+                               const int32_t *slots, int R, void *out, void *stream);
+dsa_status_t mla_cache_read_q4_paged(const void *cache, const float *cache_scale, const int32_t *kv_len,
+                                     const int32_t *block_table, int bt_stride, int page_size,
+                                     int num_pages, int B, int Nmax, void *out, void *stream);
+
+/*
+ * mla_sparse_attn_*_q4 -- the attention over the 4-bit cache, read directly: arguments, checks,
+ * workspaces (mla_sparse_attn_q4_workspace_size) and precision are those of the call over the 8-bit
+ * cache of the same name, and so are the bits of the result where both caches hold the same values.
+ * (Rows of zeros of scale 1 or more, which leave the others all of a probability's range, are those
+ * whose codes are zeros; one whose block bytes make them zeros is not looked for.)
+ */
+size_t mla_sparse_attn_q4_workspace_size(int rows, int top_k);
+dsa_status_t mla_sparse_attn_prefill_q4(const void *q, const void *cache, const float *cache_scale,
+                                        const int32_t *idx, int L, int N, int top_k, float scale,
+                                        void *out, int out_dtype, float *lse, void *workspace,
+                                        size_t ws_bytes, void *stream);
+dsa_status_t mla_sparse_attn_prefill_q4_paged(const void *q, const void *cache, const float *cache_scale,
+                                              const int32_t *block_table, int page_size, int num_pages,
+                                              const int32_t *idx, int L, int N, int top_k, float scale,
+                                              void *out, int out_dtype, float *lse, void *workspace,
+                                              size_t ws_bytes, void *stream);
+dsa_status_t mla_sparse_attn_decode_q4(const void *q, const void *cache, const float *cache_scale,
+                                       const int32_t *kv_len, const int32_t *idx, int B, int Nmax,
+                                       int top_k, float scale, void *out, int out_dtype, float *lse,
+                                       void *workspace, size_t ws_bytes, void *stream);
+dsa_status_t mla_sparse_attn_decode_q4_paged(const void *q, const void *cache, const float *cache_scale,
                                              const int32_t *kv_len, const int32_t *block_table,
                                              int bt_stride, int page_size, int num_pages,
                                              const int32_t *idx, int B, int Nmax, int top_k, float scale,
