@@ -46,6 +46,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "dsa_q4.cuh"
 #include "mla_attn_common.cuh"
@@ -73,7 +74,6 @@ constexpr int kLaunchRegs = 72, kIssueRegs = 56, kGatherRegs = 64, kWorkerRegs =
 static_assert(kThreads * kLaunchRegs >=
                   32 * (kFirstGather * kIssueRegs + (kGatherWarps + kRopeWarps) * kGatherRegs + kWorkerWarps * kWorkerRegs),
               "registers of the CTA");
-constexpr int kQHeads = kH / (kGatherWarps + kRopeWarps);   // query heads a gather or rope warp converts
 static_assert(kGatherWarps == 4 && kRopeWarps == 4, "a warp of either kind has 32 rows of a tile, one a lane");
 constexpr int kHG = kH / (kWorkerWarps / 4);       // 16 heads a worker warp
 constexpr int kGroupThreads = 4 * 32;              // the four warps sharing a head group
@@ -107,8 +107,8 @@ constexpr int OFF_RED = OFF_QS + 4 * kH * 4;       // float [4][64]
 constexpr int OFF_MNEG = OFF_RED + 4 * kH * 4;     // float [64]: minus the references
 constexpr int OFF_DELTA = OFF_MNEG + kH * 4;       // float [64]: how far a reference has just risen
 constexpr int OFF_INVL = OFF_DELTA + kH * 4;       // float [64]
-constexpr int OFF_TABLE = OFF_INVL + kH * 4;       // uint2 [37]: the magnitudes of 4-bit codes as e4m3, by block byte
-constexpr int OFF_BAR = OFF_TABLE + (kQ4Scales + 1) * 8;
+constexpr int OFF_TABLE = OFF_INVL + kH * 4;       // uint2 [256]: the magnitudes of 4-bit codes as e4m3, by block byte
+constexpr int OFF_BAR = OFF_TABLE + 256 * 8;
 // barriers: full[8], free[4], rope_full, s_full, s_free, p_full, q_free, q_raw, q_full
 constexpr int kSlots = kStages * kChunks;
 constexpr int kBars = kSlots + 2 * kStages + 7;
@@ -333,6 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         if (threadIdx.x == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
         return;
     }
+    // warps that convert a whole query: latent and rope warps; the rope warps of the 4-bit cache have no registers for it
+    constexpr int kConverters = Q4 ? kGatherWarps : kGatherWarps + kRopeWarps;
     float2* sc_s = reinterpret_cast<float2*>(smem + OFF_SC);
     float* ic_s = reinterpret_cast<float*>(smem + OFF_IC);
     int* small_s = reinterpret_cast<int*>(smem + OFF_SMALL);
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         mbar_init(p_full, kWorkerWarps);
         mbar_init(q_free, 1);
         mbar_init(q_raw, 1);
-        mbar_init(q_full, SPLIT ? kWorkerWarps : kGatherWarps + kRopeWarps);
+        mbar_init(q_full, SPLIT ? kWorkerWarps : kConverters);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         tmem_st16(a + TM_LO, v);
         tmem_st_wait();
     }
-    if (Q4 && threadIdx.x <= kQ4Scales)
+    if (Q4 && threadIdx.x < 256)
         reinterpret_cast<uint2*>(smem + OFF_TABLE)[threadIdx.x] =
             threadIdx.x < kQ4Scales ? q4_table(q4_block_scale(threadIdx.x)) : make_uint2(0, 0);
     tc_fence_before();
@@ -424,7 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                                  : lane < 3 ? ch + lane - 1 : lane < 7 ? ch + lane - 3 : ch;
                 const uint32_t mpar = lane == 0 ? gt & 1 : lane == 3 ? (gt & 1) ^ 1 : lane == 4 ? qi & 1 : par;
                 auto poll = [&](uint32_t need) { return mbar_poll_warp(mine, mpar, lane, 7, need, abort_flag, p.status); };
-                const uint32_t got = poll(0x1f);
+                // 4-bit rows: the warps that bring the rope rows expand chunks 2 and 3 before them, so the rope product is last.
+                constexpr uint32_t kFirst = Q4 ? 0x1e : 0x1f, kRest = Q4 ? 0x61 : 0x60;
+                const uint32_t got = poll(kFirst);
                 ok = got != 0;
                 if (!ok) break;
                 const uint32_t lat = base + (OFF_LAT >> 4) + (gt & 1) * (kChunks * kBlk >> 4);
@@ -437,24 +441,29 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                 fence_proxy_async_smem();   // of every lane that saw a barrier, before the lane that issues
                 __syncwarp();
                 tc_fence_after();
-                if (lane == 0) {
-                    chunk(0);
-                    chunk(1);
+                auto rope = [&] {
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)       // 16 dims a step, the keys from tensor memory
                         mma_bf16_ts_lo(tmem_base + TM_R, tmem_base + TM_K + 8 * kk, base + (OFF_QR >> 4) + 2 * kk, kDescHi,
                                        IDESC_ROPE, kk ? 1u : 0u);
+                };
+                if (lane == 0) {
+                    chunk(0);
+                    chunk(1);
+                    if (!Q4) rope();
                 }
                 __syncwarp();
-                if ((got & 0x60) != 0x60) {
-                    ok = poll(0x60) != 0;
+                if ((got & kRest) != kRest) {
+                    ok = poll(kRest) != 0;
                     if (!ok) break;
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
+                if (Q4) tc_fence_after();
                 if (lane == 0) {
                     chunk(2);
                     chunk(3);
+                    if (Q4) rope();
                     mbar_arrive(s_full);
                     mma_commit(s_full);
                     if (t == T - 1) mma_commit(q_free);
@@ -530,10 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
         }
     } else if (warp >= kFirstGather && warp < kFirstWorker) {
         // ------------------------------------------------------------ gather: latent rows, rope rows, queries
-        setmaxnreg_dec<kGatherRegs>();
         constexpr int kBytes = Rows<Q4>::kBytes;
         const bool is_rope = warp >= kFirstRope;
         const int gw = (warp - kFirstGather) & 3; // rows 32 gw .. 32 gw + 31 of a tile
+        constexpr int kQHeads = kH / kConverters;   // a warp's
         const int qh0 = kQHeads * (warp - kFirstGather);
         const uint32_t smem_base = smem_u32(smem);
         // One thread polls (the roles' pollers on different schedulers), a named barrier releases the four warps.  (A
@@ -544,127 +553,156 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             if (gw == (is_rope ? 2 : 1) && lane == 0) ok = mbar_poll(bar, parity, abort_flag, p.status);
             return named_bar_and(kGatherBar + (is_rope ? 1 : 0), 128, ok);
         };
-        int qi = 0, qbuf = 0;
+        int qi = 0;
         auto convert = [&]() -> bool {            // the warp's heads of the item's query, once it has landed
             if (!wait(q_raw, qi & 1)) return false;
 #pragma unroll 2
-            for (int i = 0; i < kQHeads; ++i) convert_head(smem, qbuf, qh0 + i, p.scale_log2, lane);
+            for (int i = 0; i < kQHeads; ++i) convert_head(smem, qi & 3, qh0 + i, p.scale_log2, lane);
             ++qi;
-            qbuf = (qbuf + 1) & 3;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
             return true;
         };
 
-        RowStream rs;
-        const int base = 32 * gw + (int)lane;
-        // `has`: there is a tile to copy, `row` its row; `more`: one is fetched behind it
-        bool has = rs.fetch(p, lane, base);
-        int row = has ? rs.resolve(p) : -1;
-        bool first = rs.first, more = has && rs.fetch(p, lane, base);
-        // latent rows: a warp instruction copies a 128-byte block of four different rows, 8 lanes a row; this lane's
-        // rows are 32 gw + 4 i + l / 8
-        const int ci = (int)(lane >> 3), cc = (int)(lane & 7);
-        const uint32_t dst0 = smem_base + OFF_LAT + (uint32_t)((32 * gw + ci) * 128);
-        const uint32_t sw0 = (uint32_t)((cc ^ ci) << 4), sw1 = (uint32_t)((cc ^ (4 + ci)) << 4);
-        for (int g = 0; has; ++g) {
-            const int row1 = more ? rs.resolve(p) : -1;
-            const bool first1 = rs.first, has1 = more;
-            // a row of a large cache into L2 a tile before it is copied (by the time of the copy HBM has answered)
-            if (p.l2_prefetch && !is_rope && row1 >= 0) l2_prefetch_bulk(p.cache + (int64_t)row1 * kBytes, kBytes);
-            more = more && rs.fetch(p, lane, base);
-            if (is_rope) {
-                // A lane carries one key's 64 rope dims (128 bytes) through registers into its lane of tensor memory:
-                // the loads run ahead, and only the store waits for QK of the tile before.
-                uint32_t k[32];
-                float sc = kZeroRowScale;         // of a page outside the pool
+        auto gather = [&](auto role) {            // of the latent rows, or the rope rows
+            constexpr bool kRope = decltype(role)::value;
+            RowStream rs;
+            const int base = 32 * gw + (int)lane;
+            // `has`: there is a tile to copy, `row` its row; `more`: one is fetched behind it
+            bool has = rs.fetch(p, lane, base);
+            int row = has ? rs.resolve(p) : -1;
+            bool first = rs.first, more = has && rs.fetch(p, lane, base);
+            // latent rows: a warp instruction copies a 128-byte block of four different rows, 8 lanes a row; this lane's
+            // rows are 32 gw + 4 i + l / 8
+            const int ci = (int)(lane >> 3), cc = (int)(lane & 7);
+            const uint32_t dst0 = smem_base + OFF_LAT + (uint32_t)((32 * gw + ci) * 128);
+            const uint32_t sw0 = (uint32_t)((cc ^ ci) << 4), sw1 = (uint32_t)((cc ^ (4 + ci)) << 4);
+            // 4-bit rows: the latent warps expand chunks 0 and 1, the rope warps 2 and 3, a lane its own row.  Its codes and
+            // block bytes are in registers when their place comes free.  (A row's pieces on eight lanes, as the copies of
+            // 8-bit rows have them, took 16 shuffles and twice the loads.)  The eight lanes of a store's phase have eight
+            // different rows mod 8: by the swizzle no bank twice.
+            constexpr int kChunk = kRope ? 2 : 0;     // the first of the warp's two
+            uint32_t x0[16], x1[16], block[4];
+            auto load = [&](uint32_t (&x)[16], const uint8_t* src, int c) {
+                ldg_nc_v8(src + 64 * c, x);
+                ldg_nc_v8(src + 64 * c + 32, x + 8);
+            };
+            auto expand = [&](const uint32_t (&x)[16], int g, int c) {
+                const uint32_t table = smem_base + OFF_TABLE;
+                const uint32_t dst = smem_base + OFF_LAT + (g & 1) * (kChunks * kBlk) + c * kBlk + base * 128 + ((base & 7) << 4);
+                // A table's load is ahead of the store before it.
+                uint2 t = lds_v2(table + 8 * (block[2 * (c - kChunk)] & 0xff));
 #pragma unroll
-                for (int i = 0; i < 32; ++i) k[i] = 0;
-                if (row >= 0) {
+                for (int i = 0; i < 8; ++i) {
+                    uint2 u = t;
+                    if (i < 7) u = lds_v2(table + 8 * __byte_perm(block[2 * (c - kChunk) + ((i + 1) >> 2)], 0, 0x4440 + ((i + 1) & 3)));
+                    const uint2 a = q4_expand(x[2 * i], t), b = q4_expand(x[2 * i + 1], t);
+                    sts_v4(dst ^ (i << 4), a.x, a.y, b.x, b.y);
+                    t = u;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[4 * (g & 1) + c]);
+            };
+            constexpr int kEarly = 2;                 // quarters of the rope dims loaded while a chunk is expanded
+            float sc1 = kZeroRowScale;                // the scale of the rope warps' next row
+            auto load_row = [&](int row) {
+                const uint8_t* src = row < 0 ? g_no_row : p.cache + (int64_t)row * kBytes;
+                const uint4 b = ldg_nc_v4(src + kQ4Codes + 8 * kChunk);
+                block[0] = b.x;
+                block[1] = b.y;
+                block[2] = b.z;
+                block[3] = b.w;
+                load(x0, src, kChunk);
+                load(x1, src, kChunk + 1);
+                if (kRope) sc1 = row >= 0 ? ldg_nc_f32(p.cache_scale + row) : kZeroRowScale;
+            };
+            if constexpr (Q4) load_row(row);
+            for (int g = 0; has; ++g) {
+                const int row1 = more ? rs.resolve(p) : -1;
+                const bool first1 = rs.first, has1 = more;
+                // a row of a large cache into L2 a tile before it is copied (by the time of the copy HBM has answered)
+                if (p.l2_prefetch && !kRope && row1 >= 0) l2_prefetch_bulk(p.cache + (int64_t)row1 * kBytes, kBytes);
+                more = more && rs.fetch(p, lane, base);
+                if constexpr (kRope) {
+                    // A lane carries one key's 64 rope dims (128 bytes) through registers into its lane of tensor memory:
+                    // the loads run ahead, and only the store waits for QK of the tile before.
+                    uint32_t k[32];
+                    float sc = kZeroRowScale;         // of a page outside the pool
                     const uint8_t* src = p.cache + (int64_t)row * kBytes + Rows<Q4>::kRope;
+                    auto load_k = [&](int from, int to) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ldg_nc_v8(src + 32 * i, k + 8 * i);
-                    sc = __ldg(p.cache_scale + row);
-                }
-                sc = row_scale<Q4>(p.cache, row, sc, lane);
-                if (g > 0 && !wait(s_full, (g - 1) & 1)) break;   // QK of the tile before is complete
-                tc_fence_after();
-                __syncwarp();
-                tmem_st32(tmem_base + TM_K + (static_cast<uint32_t>(32 * gw) << 16), k);
-                sc_s[(g & 1) * kTile + base] = row == -1 ? make_float2(0.f, -INFINITY) : make_float2(sc, lg2_approx(sc));
-                ic_s[(g & 3) * kTile + base] = row == -1 ? 0.f : 1.f / sc;
-                const bool small = __any_sync(0xffffffffu, row != -1 && sc < kSmallScale);
-                if (lane == 0) small_s[(g & 3) * 4 + gw] = small;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(rope_full);
-            } else if (Q4) {
-                // A lane expands 32 dims of each of its rows a half tile: 16 bytes of codes, two block bytes.  The two
-                // pieces that it stores lie in one chunk; lanes of the half's second chunk begin with the odd one, so
-                // that the eight lanes of a row meet no bank twice.
-                const uint8_t* mine = row < 0 ? g_no_row : p.cache + (int64_t)row * kBytes;
-                const uint2* table = reinterpret_cast<const uint2*>(smem + OFF_TABLE);
-                bool ok = true;
-#pragma unroll 1
-                for (int half = 0; ok && half < 2; ++half) {
-                    uint4 code[8];
-                    uint32_t block[8];
+                        for (int i = 8 * from; i < 8 * to; ++i) k[i] = 0;
+                        if (row >= 0)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint8_t* src = reinterpret_cast<const uint8_t*>(
-                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), 4 * i + ci));
-                        code[i] = ldg_nc_v4(src + 128 * half + 16 * cc);
-                        block[i] = __ldg(reinterpret_cast<const uint16_t*>(src + kQ4Codes + 16 * half) + cc);
+                            for (int i = from; i < to; ++i) ldg_nc_v8(src + 32 * i, k + 8 * i);
+                    };
+                    if constexpr (Q4) {
+                        if (!wait(&freed[2 * (g & 1) + 1], ((g >> 1) & 1) ^ 1)) break;
+                        expand(x0, g, 2);
+                        load_k(0, kEarly);
+                        expand(x1, g, 3);
+                        load_k(kEarly, 4);
+                        sc = sc1;
+                    } else {
+                        load_k(0, 4);
+                        if (row >= 0) sc = __ldg(p.cache_scale + row);
                     }
-                    if (!(ok = wait(&freed[2 * (g & 1) + half], ((g >> 1) & 1) ^ 1))) break;
-                    const int odd = cc >> 2, chunk = 2 * half + odd;
-                    uint8_t* dst = smem + OFF_LAT + (g & 1) * (kChunks * kBlk) + chunk * kBlk + (32 * gw + ci) * 128;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint2 t0 = table[min(block[i] & 0xffu, (uint32_t)kQ4Scales)];
-                        const uint2 t1 = table[min(block[i] >> 8, (uint32_t)kQ4Scales)];
-                        const uint2 a = q4_expand(code[i].x, t0), b = q4_expand(code[i].y, t0);
-                        const uint2 c = q4_expand(code[i].z, t1), d = q4_expand(code[i].w, t1);
-                        const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
-                        const int sw = 4 * (i & 1) + ci, pc = 2 * (cc & 3);    // row % 8, the first of the two pieces
-                        *reinterpret_cast<uint4*>(dst + i * 512 + (((pc + odd) ^ sw) << 4)) = odd ? hi : lo;
-                        *reinterpret_cast<uint4*>(dst + i * 512 + (((pc + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
-                    }
-                    fence_proxy_async_smem();
+                    sc = row_scale<Q4>(p.cache, row, sc, lane);
+                    if (g > 0 && !wait(s_full, (g - 1) & 1)) break;   // QK of the tile before is complete
+                    tc_fence_after();
                     __syncwarp();
-                    if (lane < 2) mbar_arrive(&full[4 * (g & 1) + 2 * half + lane]);
-                }
-                if (!ok) break;
-            } else {
-                const uint8_t* mine = row < 0 ? g_no_row : p.cache + (int64_t)row * kQ8Row;
-                const uint8_t* src[8];
+                    tmem_st32(tmem_base + TM_K + (static_cast<uint32_t>(32 * gw) << 16), k);
+                    sc_s[(g & 1) * kTile + base] = row == -1 ? make_float2(0.f, -INFINITY) : make_float2(sc, lg2_approx(sc));
+                    ic_s[(g & 3) * kTile + base] = row == -1 ? 0.f : 1.f / sc;
+                    const bool small = __any_sync(0xffffffffu, row != -1 && sc < kSmallScale);
+                    if (lane == 0) small_s[(g & 3) * 4 + gw] = small;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(rope_full);
+                } else if constexpr (Q4) {
+                    if (!wait(&freed[2 * (g & 1)], ((g >> 1) & 1) ^ 1)) break;
+                    expand(x0, g, 0);
+                    expand(x1, g, 1);
+                } else {
+                    const uint8_t* mine = row < 0 ? g_no_row : p.cache + (int64_t)row * kQ8Row;
+                    const uint8_t* src[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    src[i] = reinterpret_cast<const uint8_t*>(__shfl_sync(
-                                 0xffffffffu, reinterpret_cast<unsigned long long>(mine), 4 * i + ci)) + cc * 16;
-                const uint32_t dst = dst0 + (g & 1) * (kChunks * kBlk);
-                bool ok = true;
+                    for (int i = 0; i < 8; ++i)
+                        src[i] = reinterpret_cast<const uint8_t*>(__shfl_sync(
+                                     0xffffffffu, reinterpret_cast<unsigned long long>(mine), 4 * i + ci)) + cc * 16;
+                    const uint32_t dst = dst0 + (g & 1) * (kChunks * kBlk);
+                    bool ok = true;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    ok = ok && wait(&freed[2 * (g & 1) + half], ((g >> 1) & 1) ^ 1);
-                    if (ok) {
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && wait(&freed[2 * (g & 1) + half], ((g >> 1) & 1) ^ 1);
+                        if (ok) {
 #pragma unroll
-                        for (int c = 2 * half; c < 2 * half + 2; ++c) {
+                            for (int c = 2 * half; c < 2 * half + 2; ++c) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                cp_async_16(dst + c * kBlk + i * 512 + ((i & 1) ? sw1 : sw0), src[i] + c * 128);
-                            cp_async_arrive_noinc(&full[4 * (g & 1) + c]);
+                                for (int i = 0; i < 8; ++i)
+                                    cp_async_16(dst + c * kBlk + i * 512 + ((i & 1) ? sw1 : sw0), src[i] + c * 128);
+                                cp_async_arrive_noinc(&full[4 * (g & 1) + c]);
+                            }
                         }
                     }
+                    if (!ok) break;
                 }
-                if (!ok) break;
+                if (!(Q4 && kRope) && !SPLIT && first && !convert()) break;   // split: the workers, idle so far, convert the only query
+                row = row1;
+                first = first1;
+                has = has1;
+                if constexpr (Q4) load_row(row);
             }
-            if (!SPLIT && first && !convert()) break;   // split: the workers, idle so far, convert the only query
-            row = row1;
-            first = first1;
-            has = has1;
+        };
+        if (is_rope) {
+            setmaxnreg_dec<kGatherRegs>();
+            gather(std::true_type{});
+        } else {
+            setmaxnreg_dec<kGatherRegs>();
+            gather(std::false_type{});
         }
         cp_async_wait_all();
     } else if (warp >= kFirstWorker) {
