@@ -67,8 +67,9 @@ SIGNATURES = {
     "dsa_selftest_poll_timeout": (ctypes.c_int32, [_I, ctypes.c_uint32, _P]),
 }
 
-# the calls over the 4-bit cache take what those over the 8-bit one take
+# the calls over the 4-bit cache take what those over the 8-bit one take, the workspace's size the keys too
 SIGNATURES.update({name.replace("_q8", "_q4"): sig for name, sig in SIGNATURES.items() if "_q8" in name})
+SIGNATURES["mla_sparse_attn_q4_workspace_size"] = (_SZ, [_I, _I, _I])
 
 _lock = threading.Lock()
 _lib: Optional[ctypes.CDLL] = None
@@ -327,8 +328,13 @@ _U8 = frozenset((torch.uint8,))
 
 @functools.lru_cache(maxsize=4096)
 def _q8_workspace_bytes(dev: int, rows: int, top_k: int) -> int:
-    """The library's answer for a device and two sizes, the same for a 4-bit cache."""
+    """The library's answer for a device and two sizes."""
     return int(load().mla_sparse_attn_q8_workspace_size(rows, top_k))
+
+
+@functools.lru_cache(maxsize=4096)
+def _q4_workspace_bytes(dev: int, rows: int, top_k: int, N: int) -> int:
+    return int(load().mla_sparse_attn_q4_workspace_size(rows, top_k, N))
 
 
 def _current_device() -> int:
@@ -514,9 +520,9 @@ def attn_q8_workspace_size(rows: int, top_k: int) -> int:
     return _q8_workspace_bytes(_current_device(), rows, top_k)
 
 
-def attn_q4_workspace_size(rows: int, top_k: int) -> int:
-    """The same for a 4-bit cache."""
-    return _q8_workspace_bytes(_current_device(), rows, top_k)
+def attn_q4_workspace_size(rows: int, top_k: int, N: int = 0) -> int:
+    """The same for a 4-bit cache; N: the keys of a prefill's cache, 0 for a decode call."""
+    return _q4_workspace_bytes(_current_device(), rows, top_k, N)
 
 
 # Workspaces of the attention by (device, stream), a set for each thread: calls that one thread makes on one stream run in
@@ -530,13 +536,16 @@ class _Workspaces(threading.local):
 _workspaces = _Workspaces()
 
 
-def _q8_workspace(workspace, rows, top_k, dev, device, stream):
+_KEPT_WORKSPACE = 64 << 20      # larger ones (the rows of a long 4-bit cache) go back to the allocator
+
+
+def _low_workspace(row, workspace, rows, top_k, N, dev, device, stream):
     """(tensor to keep until the call, pointer, bytes)."""
     if workspace is None:
-        need = _q8_workspace_bytes(dev, rows, top_k)
+        need = _q8_workspace_bytes(dev, rows, top_k) if row == Q8_ROW else _q4_workspace_bytes(dev, rows, top_k, N)
         if need == 0:
             return None, None, 0
-        if stream is None and not torch.cuda.is_current_stream_capturing():
+        if stream is None and need <= _KEPT_WORKSPACE and not torch.cuda.is_current_stream_capturing():
             key = (dev, torch._C._cuda_getCurrentRawStream(dev))
             by_stream = _workspaces.by_stream
             workspace = by_stream.get(key)
@@ -552,7 +561,7 @@ def _q8_workspace(workspace, rows, top_k, dev, device, stream):
 def _attn_prefill(name, row, q, cache, cache_scale, idx, scale, out, lse, want_lse, stream, out_dtype, workspace):
     dev, L, top_k, N, out, lse, od, pq, pc, ps, pi, po, pl = _attn_low(row, q, cache, cache_scale, idx, out, lse,
                                                                        want_lse, out_dtype, stream)
-    workspace, pw, n_ws = _q8_workspace(workspace, L, top_k, dev, q.device, stream)
+    workspace, pw, n_ws = _low_workspace(row, workspace, L, top_k, N, dev, q.device, stream)
     rc = getattr(_lib or load(), name)(pq, pc, ps, pi, L, N, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))
     if rc:
         raise DsaError(name, rc)
@@ -584,7 +593,7 @@ def _attn_prefill_paged(name, row, q, cache, cache_scale, block_table, page_size
     pages = block_table.numel()
     if page_size > 0 and pages < -(-N // page_size):
         _bad("block_table holds ceil(N / page_size) pages")
-    workspace, pw, n_ws = _q8_workspace(workspace, L, top_k, dev, q.device, stream)
+    workspace, pw, n_ws = _low_workspace(row, workspace, L, top_k, N, dev, q.device, stream)
     rc = getattr(_lib or load(), name)(
         pq, pc, ps, _p(block_table, dev, _I32, pages, "block_table"), page_size, n // page_size if page_size > 0 else 0, pi,
         L, N, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))
@@ -619,7 +628,7 @@ def _attn_decode(name, row, q, cache, cache_scale, kv_len, idx, scale, out, lse,
                                                                        want_lse, out_dtype, stream)
     if cache.dim() != 3 or cache.shape[0] != B:
         _bad("the cache is uint8 [B, Nmax, %d]" % row)
-    workspace, pw, n_ws = _q8_workspace(workspace, B, top_k, dev, q.device, stream)
+    workspace, pw, n_ws = _low_workspace(row, workspace, B, top_k, 0, dev, q.device, stream)
     rc = getattr(_lib or load(), name)(
         pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), pi, B, cache.shape[1], top_k, scale, po, od, pl,
         pw, n_ws, _stream_on(dev, stream))
@@ -651,7 +660,7 @@ def _attn_decode_paged(name, row, q, cache, cache_scale, kv_len, block_table, pa
     dev, B, top_k, n, out, lse, od, pq, pc, ps, pi, po, pl = _attn_low(row, q, cache, cache_scale, idx, out, lse,
                                                                        want_lse, out_dtype, stream)
     stride = _table(block_table, B)
-    workspace, pw, n_ws = _q8_workspace(workspace, B, top_k, dev, q.device, stream)
+    workspace, pw, n_ws = _low_workspace(row, workspace, B, top_k, 0, dev, q.device, stream)
     rc = getattr(_lib or load(), name)(
         pq, pc, ps, _p(kv_len, dev, _I32, B, "kv_len"), _p(block_table, dev, _I32, B * stride, "block_table"), stride,
         page_size, n // page_size if page_size > 0 else 0, pi, B, Nmax, top_k, scale, po, od, pl, pw, n_ws, _stream_on(dev, stream))

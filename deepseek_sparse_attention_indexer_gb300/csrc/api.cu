@@ -374,7 +374,10 @@ dsa_status_t check_attn_q8(const void* q, const void* cache, const float* cache_
 bool eps_ok(float eps) { return eps >= 0.f && eps < 3.0e38f; }
 }  // namespace
 
-size_t mla_sparse_attn_q4_workspace_size(int rows, int top_k) { return mla_sparse_attn_q8_workspace_size(rows, top_k); }
+size_t mla_sparse_attn_q4_workspace_size(int rows, int top_k, int N) {
+    if (rows < 1 || top_k < 1 || top_k > DSA_MAX_TOPK || N < 0 || check_device() != DSA_OK) return 0;
+    return attn_q4_workspace(rows, top_k, N);
+}
 
 size_t mla_sparse_attn_q8_workspace_size(int rows, int top_k) {
     if (rows < 1 || top_k < 1 || top_k > DSA_MAX_TOPK || check_device() != DSA_OK) return 0;
@@ -395,9 +398,12 @@ dsa_status_t attn_prefill(bool q4, const void* q, const void* cache, const float
                           void* workspace, size_t ws_bytes, void* stream) {
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
-    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace) ||
+        (q4 && !aligned32(workspace)))
+        return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
-    if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(L, top_k))) != DSA_OK) return st;
+    if ((st = check_workspace(workspace, ws_bytes, q4 ? attn_q4_workspace(L, top_k, N) : attn_q8_workspace(L, top_k))) != DSA_OK)
+        return st;
     return launch_attn_q8_prefill(q, cache, cache_scale, q4, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32,
                                   lse, workspace, PageTable{}, static_cast<cudaStream_t>(stream));
 }
@@ -411,9 +417,12 @@ dsa_status_t attn_prefill_paged(bool q4, const void* q, const void* cache, const
     PageTable pt;
     const int stride = page_size > 0 ? (int)(((long long)N + page_size - 1) / page_size) : 0;
     if ((st = make_page_table(block_table, stride, page_size, num_pages, N, &pt)) != DSA_OK) return st;
-    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace)) return DSA_ERR_MISALIGNED;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace) ||
+        (q4 && !aligned32(workspace)))
+        return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
-    if ((st = check_workspace(workspace, ws_bytes, attn_q8_workspace(L, top_k))) != DSA_OK) return st;
+    if ((st = check_workspace(workspace, ws_bytes, q4 ? attn_q4_workspace(L, top_k, N) : attn_q8_workspace(L, top_k))) != DSA_OK)
+        return st;
     return launch_attn_q8_prefill(q, cache, cache_scale, q4, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32,
                                   lse, workspace, pt, static_cast<cudaStream_t>(stream));
 }

@@ -128,7 +128,39 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
 }
 
+// One warp a row: lane l expands block l to 16 e4m3 bytes and copies rope dims 2l, 2l+1: row j of the 8-bit cache.
+__global__ void __launch_bounds__(kWarps * 32)
+    cache_expand_q4_kernel(const uint8_t* cache, const float* scale, int N, uint8_t* out, float* out_scale,
+                           const PageTable pt) {
+    griddep_wait();
+    const int j = blockIdx.x * kWarps + threadIdx.x / 32;
+    const int lane = threadIdx.x & 31;
+    if (j >= N) return;
+    const int64_t row = pt.table ? paged_row(pt, 0, j) : j;
+    if (row < 0) return;                       // a page outside the pool: the attention does not read its rows
+    const uint8_t* src = cache + row * kQ4Row;
+    uint8_t* dst = out + (int64_t)j * kQ8Row;
+    const uint2 c = __ldg(reinterpret_cast<const uint2*>(src) + lane);
+    const uint32_t b = __ldg(src + kQ4Codes + lane);
+    const uint32_t pe = __ldg(reinterpret_cast<const uint32_t*>(src + kQ4Rope) + lane);
+    const float s = __ldg(scale + row);
+    const uint2 t = b < kQ4Scales ? q4_table(q4_block_scale(b)) : make_uint2(0, 0);
+    const uint2 x = q4_expand(c.x, t), y = q4_expand(c.y, t);
+    reinterpret_cast<uint4*>(dst)[lane] = make_uint4(x.x, x.y, y.x, y.y);
+    reinterpret_cast<uint32_t*>(dst + kQ8Latent)[lane] = pe;
+    if (lane == 0) out_scale[j] = s;
+}
+
 }  // namespace
+
+dsa_status_t launch_cache_expand_q4(const void* cache, const float* cache_scale, int N, void* out, float* out_scale,
+                                    const PageTable& pages, cudaStream_t stream) {
+    if (launch_pdl(cache_expand_q4_kernel, dim3(ceil_div(N, kWarps)), dim3(kWarps * 32), 0, stream,
+                   static_cast<const uint8_t*>(cache), cache_scale, N, static_cast<uint8_t*>(out), out_scale,
+                   pages) != cudaSuccess)
+        return DSA_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
 
 dsa_status_t launch_cache_write_q4(const void* kv_a, int64_t kv_a_stride, const float* norm_w, float eps,
                                    const float* cos_sin, int max_pos, int interleave, const int32_t* pos,

@@ -95,11 +95,15 @@ dsa_status_t launch_cache_read_q4(const void* cache, const float* cache_scale, i
                                   int R, void* out, cudaStream_t stream);
 dsa_status_t launch_cache_read_q4_paged(const void* cache, const float* cache_scale, const int32_t* kv_len, int B,
                                         int Nmax, void* out, const PageTable& pages, cudaStream_t stream);
+// Rows 0 .. N - 1 of a sequence of the 4-bit cache as rows of the 8-bit cache, dense.
+dsa_status_t launch_cache_expand_q4(const void* cache, const float* cache_scale, int N, void* out, float* out_scale,
+                                    const PageTable& pages, cudaStream_t stream);
 // The attention over the 8-bit cache, or (q4) over the 4-bit one.
 dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, bool q4,
                                     const int32_t* idx, int L, int N, int top_k, float scale, void* out, int out_f32,
                                     float* lse, void* workspace, const PageTable& pages, cudaStream_t stream);
 size_t attn_q8_workspace(int rows, int top_k);
+size_t attn_q4_workspace(int rows, int top_k, int N);   // N: keys of a prefill's cache; decode 0
 // Merge of nsplit partial (normalised output, lse) pairs a sequence.
 dsa_status_t launch_decode_combine(const float* part_o, const float* part_lse, int B, int nsplit, void* out, int out_f32,
                                    float* lse, cudaStream_t stream);

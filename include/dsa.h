@@ -433,13 +433,16 @@ dsa_status_t mla_cache_read_q4_paged(const void *cache, const float *cache_scale
                                      int num_pages, int B, int Nmax, void *out, void *stream);
 
 /*
- * mla_sparse_attn_*_q4 -- the attention over the 4-bit cache, read directly: arguments, checks,
- * workspaces (mla_sparse_attn_q4_workspace_size) and precision are those of the call over the 8-bit
- * cache of the same name, and so are the bits of the result where both caches hold the same values.
- * (Rows of zeros of scale 1 or more, which leave the others all of a probability's range, are those
- * whose codes are zeros; one whose block bytes make them zeros is not looked for.)
+ * mla_sparse_attn_*_q4 -- the attention over the 4-bit cache: arguments, checks and precision are those
+ * of the call over the 8-bit cache of the same name, and so are the bits of the result where both
+ * caches hold the same values.  (Rows of zeros of scale 1 or more, which leave the others all of a
+ * probability's range, are those whose codes are zeros; one whose block bytes make them zeros is
+ * looked for only by a prefill whose queries select each key several times over.)
+ * Workspace: as there, of mla_sparse_attn_q4_workspace_size(rows, top_k, N) bytes, N the keys of a
+ * prefill's cache and 0 for a decode call.  A prefill whose queries select each key several times over
+ * holds the N rows in it as 8-bit ones (644 bytes a key); its workspace is 32-byte aligned.
  */
-size_t mla_sparse_attn_q4_workspace_size(int rows, int top_k);
+size_t mla_sparse_attn_q4_workspace_size(int rows, int top_k, int N);
 dsa_status_t mla_sparse_attn_prefill_q4(const void *q, const void *cache, const float *cache_scale,
                                         const int32_t *idx, int L, int N, int top_k, float scale,
                                         void *out, int out_dtype, float *lse, void *workspace,

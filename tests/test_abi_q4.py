@@ -96,4 +96,4 @@ def test_decode_refusals(lib):
     refusals(lib.mla_sparse_attn_decode_q4_paged, names, good,
              {INVALID: [{"table": None}, {"stride": 0}, {"N": 257}, {"pages": 0}], SHAPE: [{"page": 100}]})
     for B, top_k in ((0, 64), (-1, 64), (4, 0), (4, 2049)):
-        assert lib.mla_sparse_attn_q4_workspace_size(B, top_k) == 0
+        assert lib.mla_sparse_attn_q4_workspace_size(B, top_k, 0) == 0

@@ -487,6 +487,48 @@ def test_attention_records_keys_outside_the_cache(dsa):
     assert dsa.device_status() == 7
 
 
+@pytest.mark.parametrize("L,expanded", [(4, False), (150, True)])
+def test_prefill_records_pages_outside_the_pool(dsa, L, expanded):
+    """Also where the cache is expanded first: a selected key on a page outside the pool is a row of zeros and recorded,
+    a page that no query selects may be anything."""
+    g = gen(16)
+    N, K, page = 1000, 900, 16
+    assert (dsa.attn_q4_workspace_size(L, K, N) > dsa.attn_q8_workspace_size(L, K)) == expanded
+    cache, scale = make_cache(g, N)
+    pool, pscale, table, pages = paged(g, cache[None], scale[None], [N], page)
+    q = randn(g, L, 64, 576).bfloat16()
+    idx = choose(g, [N - 32] * L, N - 32, K)
+    want = dsa.mla_sparse_attn_prefill_q4_paged(q, pool, pscale, table[0], page, idx, SCALE, N, want_lse=True)
+    table[0, -1], table[0, -2] = -1, pages                                # keys that nothing selects
+    got = dsa.mla_sparse_attn_prefill_q4_paged(q, pool, pscale, table[0], page, idx, SCALE, N, want_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and dsa.device_status() == 0
+    table[0, 3] = pages
+    got = dsa.mla_sparse_attn_prefill_q4_paged(q, pool, pscale, table[0], page, idx, SCALE, N, want_lse=True)
+    assert dsa.device_status() == 7
+    gone = cache.clone()
+    gone[3 * page:4 * page] = 0
+    twin = dsa.mla_sparse_attn_prefill_q4(q, gone, scale, idx, SCALE, want_lse=True)
+    close(got[0], got[1], attention64(q, lambda s: values(gone, scale)[idx[s].clamp(min=0).long()], idx >= 0, SCALE))
+    close(twin[0], twin[1], attention64(q, lambda s: values(gone, scale)[idx[s].clamp(min=0).long()], idx >= 0, SCALE))
+
+
+def test_prefill_workspace(dsa):
+    """The size the library names is enough and needed; a given workspace gives the same bits."""
+    g = gen(17)
+    L, N, K = 160, 700, 640
+    cache, scale = make_cache(g, N, exponents=1)
+    q, idx = randn(g, L, 64, 576).bfloat16(), choose(g, [N] * L, N, K)
+    want = dsa.mla_sparse_attn_prefill_q4(q, cache, scale, idx, SCALE)
+    need = dsa.attn_q4_workspace_size(L, K, N)
+    assert need > dsa.attn_q8_workspace_size(L, K)
+    ws = torch.full((need + 256,), 0xEE, dtype=torch.uint8, device="cuda")
+    got = dsa.mla_sparse_attn_prefill_q4(q, cache, scale, idx, SCALE, workspace=ws[:need])
+    assert torch.equal(got, want) and bool((ws[need:] == 0xEE).all()) and dsa.device_status() == 0
+    for bad in (ws[:need - 1], ws[16:]):
+        with pytest.raises(dsa.DsaError):
+            dsa.mla_sparse_attn_prefill_q4(q, cache, scale, idx, SCALE, workspace=bad)
+
+
 def test_offsets_past_32_bits(dsa):
     """Rows past the 2^32nd byte of the cache."""
     g = gen(13)
