@@ -65,6 +65,11 @@ SIGNATURES = {
     "dsa_device_status": (ctypes.c_int32, [_P, ctypes.POINTER(ctypes.c_int32), _I]),
     "dsa_selftest_wait_timeout": (ctypes.c_int32, [_I, ctypes.c_uint64, _P]),
     "dsa_selftest_poll_timeout": (ctypes.c_int32, [_I, ctypes.c_uint32, _P]),
+    "mla_key_weights_workspace_size": (_SZ, [_I]),
+    "mla_key_weights_prefill": (ctypes.c_int32, [_P, _P, _P, _I, _P, _I, _I, _P, _P, _I, _I, _I, _F, _P, _I, _P, _SZ, _P]),
+    "mla_key_weights_decode": (ctypes.c_int32, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _F, _P, _I, _P]),
+    "dsa_cache_evict_plan": (ctypes.c_int32, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "dsa_cache_move_rows": (ctypes.c_int32, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _P]),
 }
 
 # the calls over the 4-bit cache take what those over the 8-bit one take, the workspace's size the keys too
@@ -688,6 +693,175 @@ def mla_sparse_attn_decode_q4_paged(q: torch.Tensor, cache: torch.Tensor, cache_
     return _attn_decode_paged("mla_sparse_attn_decode_q4_paged", Q4_ROW, q, cache, cache_scale, kv_len, block_table,
                               page_size, idx, scale, Nmax, out, lse, workspace, want_lse, stream, out_dtype)
 
+
+# ----------------------------------------------------------------------------- eviction by attention weight
+
+_ROW_FORMATS = {Q8_ROW: 1, Q4_ROW: 2}                       # of a uint8 cache, by its row's bytes
+
+
+def _weights_cache(cache, cache_scale, dev):
+    """(rows, pointer, scales' pointer, row format) of a bf16, 8-bit or 4-bit cache."""
+    if cache.dtype in _BITS16 and cache.shape[-1] == 576:
+        if cache_scale is not None:
+            _bad("a bf16 cache has no scales")
+        rows = cache.numel() // 576
+        return rows, _p(cache, dev, _BITS16, rows * 576, "cache"), None, 0
+    row = cache.shape[-1]
+    fmt = _ROW_FORMATS.get(row, -1) if cache.dtype is torch.uint8 else -1
+    if fmt < 0:
+        _bad("the cache is bf16 [..., 576], uint8 [..., 640] or uint8 [..., 416]")
+    if cache_scale is None:
+        _bad("cache_scale is f32, one a row")
+    rows = cache.numel() // row
+    return rows, _p(cache, dev, _U8, rows * row, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"), fmt
+
+
+def _weights_args(q, idx, lse, dev):
+    rows, heads, width = q.shape
+    if heads != 64 or width != 576:
+        _bad("q is bf16 [rows, 64, 576]")
+    top_k = idx.shape[-1]
+    return (rows, top_k, _p(q, dev, _BITS16, rows * 36864, "q"), _p(idx, dev, _I32, rows * top_k, "idx"),
+            _p(lse, dev, _F32, rows * 64, "lse"))
+
+
+def mla_key_weights_prefill(q: torch.Tensor, cache: torch.Tensor, idx: torch.Tensor, lse: torch.Tensor, scale: float,
+                            acc: Optional[torch.Tensor] = None, cache_scale: Optional[torch.Tensor] = None,
+                            block_table: Optional[torch.Tensor] = None, page_size: int = 0, N: Optional[int] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The attention weight that each of a sequence's N keys received from the queries q [L, 64, 576], summed over
+    queries and heads: a new f32 [N], or added to `acc`.
+
+    idx [L, top_k] and lse [L, 64] as the attention took and returned them; cache bf16 [N, 576], or uint8 [N, 640] or
+    [N, 416] with cache_scale, or a pool of such rows with block_table and page_size (and N)."""
+    dev = _current_device()
+    rows, pc, ps, fmt = _weights_cache(cache, cache_scale, dev)
+    L, top_k, pq, pi, pl = _weights_args(q, idx, lse, dev)
+    pt = pages = None
+    if block_table is not None:
+        if N is None or page_size < 1:
+            _bad("a paged cache needs N and page_size")
+        pages = block_table.numel()
+        if pages < -(-N // page_size):
+            _bad("block_table holds ceil(N / page_size) pages")
+        pt = _p(block_table, dev, _I32, pages, "block_table")
+    elif N is None:
+        N = rows
+    elif N != rows:
+        _bad("the cache has N rows")
+    fresh = acc is None
+    if fresh:
+        acc = _new((N,), torch.float32, q.device, stream)
+    if workspace is None:
+        workspace = _new((N * 8,), torch.uint8, q.device, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _bad("the workspace is contiguous on the current CUDA device")
+    rc = (_lib or load()).mla_key_weights_prefill(
+        pq, pc, ps, fmt, pt, page_size if pt else 0, rows // page_size if pt else 0, pi, pl, L, N, top_k, scale,
+        _p(acc, dev, _F32, N, "acc"), 0 if fresh else 1, workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream))
+    if rc:
+        raise DsaError("mla_key_weights_prefill", rc)
+    return acc
+
+
+def mla_key_weights_decode(q: torch.Tensor, cache: torch.Tensor, kv_len: torch.Tensor, idx: torch.Tensor,
+                           lse: torch.Tensor, scale: float, acc: Optional[torch.Tensor] = None,
+                           cache_scale: Optional[torch.Tensor] = None, block_table: Optional[torch.Tensor] = None,
+                           page_size: int = 0, Nmax: Optional[int] = None, stream=None) -> torch.Tensor:
+    """The same for B sequences of one query each, q [B, 64, 576]: a new f32 [B, Nmax], or added to `acc`.
+
+    cache [B, Nmax, row], or a pool with block_table [B, pages] and page_size (and Nmax)."""
+    dev = _current_device()
+    rows, pc, ps, fmt = _weights_cache(cache, cache_scale, dev)
+    B, top_k, pq, pi, pl = _weights_args(q, idx, lse, dev)
+    pt, stride = None, 0
+    if block_table is not None:
+        if Nmax is None or page_size < 1:
+            _bad("a paged cache needs Nmax and page_size")
+        stride = _table(block_table, B)
+        pt = _p(block_table, dev, _I32, B * stride, "block_table")
+    elif cache.dim() != 3 or cache.shape[0] != B or (Nmax is not None and Nmax != cache.shape[1]):
+        _bad("the cache is [B, Nmax, row]")
+    else:
+        Nmax = cache.shape[1]
+    fresh = acc is None
+    if fresh:
+        acc = _new((B, Nmax), torch.float32, q.device, stream)
+    rc = (_lib or load()).mla_key_weights_decode(
+        pq, pc, ps, fmt, _p(kv_len, dev, _I32, B, "kv_len"), pt, stride, page_size if pt else 0,
+        rows // page_size if pt else 0, pi, pl, B, Nmax, top_k, scale, _p(acc, dev, _F32, B * Nmax, "acc"),
+        0 if fresh else 1, _stream_on(dev, stream))
+    if rc:
+        raise DsaError("mla_key_weights_decode", rc)
+    return acc
+
+
+def cache_evict_plan(acc: torch.Tensor, pos: torch.Tensor, kv_len: torch.Tensor, keep: int, recent: int = 0,
+                     sink: int = 0, stream=None):
+    """(src, dst, left): the moves that leave `keep` keys of each longer sequence, int32 [B, min(keep, Nmax - keep)]
+    padded with -1, and the keys left [B].
+
+    acc f32 [B, Nmax] (weights), pos int32 [B, Nmax] (positions), kv_len [B].  The `recent` latest positions and
+    those below `sink` stay, then the heaviest keys, equal ones the lower index first."""
+    dev = _current_device()
+    if acc.dim() != 2:
+        _bad("acc is f32 [B, Nmax]")
+    B, Nmax = acc.shape
+    if not 1 <= keep < Nmax:
+        _bad("1 <= keep < Nmax")
+    moves = min(keep, Nmax - keep)
+    src, dst = _new((B, moves), torch.int32, acc.device, stream), _new((B, moves), torch.int32, acc.device, stream)
+    left = _new((B,), torch.int32, acc.device, stream)
+    rc = (_lib or load()).dsa_cache_evict_plan(
+        _p(acc, dev, _F32, B * Nmax, "acc"), _p(pos, dev, _I32, B * Nmax, "pos"), _p(kv_len, dev, _I32, B, "kv_len"), B, Nmax,
+        keep, recent, sink, src.data_ptr(), dst.data_ptr(), left.data_ptr(), _stream_on(dev, stream))
+    if rc:
+        raise DsaError("dsa_cache_evict_plan", rc)
+    return src, dst, left
+
+
+def cache_move_rows(src: torch.Tensor, dst: torch.Tensor, dense=(), paged=(), block_table: Optional[torch.Tensor] = None,
+                    page_size: int = 0, stream=None) -> None:
+    """Row dst[b, i] of sequence b becomes its row src[b, i] in every tensor given, in place: `dense` ones [B, Nmax, ...],
+    `paged` ones pools [num_pages * page_size, ...] with block_table [B, pages].  At most 8 tensors, rows of a multiple
+    of 4 bytes."""
+    dev = _current_device()
+    if src.dim() != 2 or dst.shape != src.shape:
+        _bad("src and dst are int32 [B, moves]")
+    B, moves = src.shape
+    n = len(dense) + len(paged)
+    if not 1 <= n <= 8:
+        _bad("1 to 8 tensors")
+    Nmax, rows, ptrs, sizes = None, None, [], []
+    for t in dense:
+        if t.get_device() != dev or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != B or Nmax not in (None, t.shape[1]):
+            _bad("dense tensors are contiguous [B, Nmax, ...] on the current CUDA device")
+        Nmax = t.shape[1]
+        ptrs.append(t.data_ptr())
+        sizes.append(t.nbytes // (B * Nmax) if B * Nmax else 0)
+    pt, stride = None, 0
+    if paged:
+        if block_table is None or page_size < 1:
+            _bad("paged tensors need block_table and page_size")
+        stride = _table(block_table, B)
+        pt = _p(block_table, dev, _I32, B * stride, "block_table")
+        for t in paged:
+            if t.get_device() != dev or not t.is_contiguous() or t.dim() < 1 or rows not in (None, t.shape[0]):
+                _bad("paged tensors are contiguous [num_pages * page_size, ...] on the current CUDA device")
+            rows = t.shape[0]
+            ptrs.append(t.data_ptr())
+            sizes.append(t.nbytes // rows if rows else 0)
+        if Nmax is None:
+            Nmax = stride * page_size
+    rc = (_lib or load()).dsa_cache_move_rows(
+        _p(src, dev, _I32, B * moves, "src"), _p(dst, dev, _I32, B * moves, "dst"), B, moves, Nmax, n, (_P * n)(*ptrs),
+        (_I * n)(*sizes), (_I * n)(*([0] * len(dense) + [1] * len(paged))), pt, stride, page_size if pt else 0,
+        rows // page_size if pt else 0, _stream_on(dev, stream))
+    if rc:
+        raise DsaError("dsa_cache_move_rows", rc)
+
+
+# ----------------------------------------------------------------------------- around the attention
 
 def indexer_norm_rope(q: torch.Tensor, k: torch.Tensor, k_w: Optional[torch.Tensor], k_b: Optional[torch.Tensor],
                       eps: float, cos_sin: torch.Tensor, pos: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,

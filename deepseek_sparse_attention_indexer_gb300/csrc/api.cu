@@ -637,6 +637,97 @@ dsa_status_t dsa_indexer_norm_rope(const void* q, int64_t q_stride, const void* 
                                     static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+// Host checks the two calls for the keys' weights share.
+dsa_status_t check_key_weights(const void* q, const void* cache, const float* cache_scale, int row_format,
+                               const int32_t* idx, const float* lse, int rows, int N, int top_k, float scale,
+                               const float* acc, int accumulate) {
+    if (row_format != DSA_ROWS_BF16 && row_format != DSA_ROWS_Q8 && row_format != DSA_ROWS_Q4) return DSA_ERR_INVALID_ARG;
+    if (!q || !cache || !idx || !lse || !acc || (row_format != DSA_ROWS_BF16) != (cache_scale != nullptr))
+        return DSA_ERR_INVALID_ARG;
+    if (rows < 1 || N < 1 || (accumulate != 0 && accumulate != 1)) return DSA_ERR_INVALID_ARG;
+    if (top_k < 1 || top_k > DSA_MAX_TOPK) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if ((long long)rows * DSA_HEADS > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!(scale > 0.f) || !(scale < 1e30f)) return DSA_ERR_INVALID_ARG;
+    return DSA_OK;
+}
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+}  // namespace
+
+size_t mla_key_weights_workspace_size(int N) { return N < 1 ? 0 : (size_t)N * 8; }
+
+dsa_status_t mla_key_weights_prefill(const void* q, const void* cache, const float* cache_scale, int row_format,
+                                     const int32_t* block_table, int page_size, int num_pages, const int32_t* idx,
+                                     const float* lse, int L, int N, int top_k, float scale, float* acc,
+                                     int accumulate, void* workspace, size_t ws_bytes, void* stream) {
+    dsa_status_t st = check_key_weights(q, cache, cache_scale, row_format, idx, lse, L, N, top_k, scale, acc, accumulate);
+    if (st != DSA_OK) return st;
+    PageTable pt{};
+    const int stride = page_size > 0 ? (int)(((long long)N + page_size - 1) / page_size) : 0;
+    if (block_table && (st = make_page_table(block_table, stride, page_size, num_pages, N, &pt)) != DSA_OK) return st;
+    if (!aligned16(q) || !aligned32(cache) || !aligned8(workspace)) return DSA_ERR_MISALIGNED;
+    if ((st = check_workspace(workspace, ws_bytes, mla_key_weights_workspace_size(N))) != DSA_OK) return st;
+    if ((st = check_device()) != DSA_OK) return st;
+    return launch_key_weights_prefill(row_format, q, cache, cache_scale, idx, lse, L, N, top_k, scale, acc, accumulate,
+                                      workspace, pt, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t mla_key_weights_decode(const void* q, const void* cache, const float* cache_scale, int row_format,
+                                    const int32_t* kv_len, const int32_t* block_table, int bt_stride, int page_size,
+                                    int num_pages, const int32_t* idx, const float* lse, int B, int Nmax, int top_k,
+                                    float scale, float* acc, int accumulate, void* stream) {
+    if (!kv_len) return DSA_ERR_INVALID_ARG;
+    dsa_status_t st = check_key_weights(q, cache, cache_scale, row_format, idx, lse, B, Nmax, top_k, scale, acc, accumulate);
+    if (st != DSA_OK) return st;
+    PageTable pt{};
+    if (block_table) {
+        if ((st = make_page_table(block_table, bt_stride, page_size, num_pages, Nmax, &pt)) != DSA_OK) return st;
+        if ((long long)B * bt_stride > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    }
+    if ((long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(q) || !aligned32(cache)) return DSA_ERR_MISALIGNED;
+    if ((st = check_device()) != DSA_OK) return st;
+    return launch_key_weights_decode(row_format, q, cache, cache_scale, kv_len, idx, lse, B, Nmax, top_k, scale, acc,
+                                     accumulate, pt, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t dsa_cache_evict_plan(const float* acc, const int32_t* pos, const int32_t* kv_len, int B, int Nmax, int keep,
+                                  int recent, int sink, int32_t* src, int32_t* dst, int32_t* left, void* stream) {
+    if (!acc || !pos || !kv_len || !src || !dst || !left || src == dst) return DSA_ERR_INVALID_ARG;
+    if (B < 1 || Nmax < 2 || keep < 1 || keep >= Nmax || recent < 0 || sink < 0) return DSA_ERR_INVALID_ARG;
+    if ((long long)recent + sink > keep) return DSA_ERR_INVALID_ARG;
+    if ((long long)B * Nmax > 0x7FFFFFFFLL || B > (1 << 27)) return DSA_ERR_UNSUPPORTED_SHAPE;
+    dsa_status_t st = check_device();
+    if (st != DSA_OK) return st;
+    return launch_evict_plan(acc, pos, kv_len, B, Nmax, keep, recent, sink, src, dst, left, static_cast<cudaStream_t>(stream));
+}
+
+dsa_status_t dsa_cache_move_rows(const int32_t* src, const int32_t* dst, int B, int moves, int Nmax, int count,
+                                 void* const* tensors, const int* row_bytes, const int* paged,
+                                 const int32_t* block_table, int bt_stride, int page_size, int num_pages, void* stream) {
+    if (!src || !dst || !tensors || !row_bytes || !paged) return DSA_ERR_INVALID_ARG;
+    if (B < 1 || moves < 1 || Nmax < 1 || count < 1) return DSA_ERR_INVALID_ARG;
+    if (count > DSA_MAX_MOVED || B > 65535) return DSA_ERR_UNSUPPORTED_SHAPE;
+    if ((long long)B * moves > 0x7FFFFFFFLL || (long long)B * Nmax > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    bool any_paged = false;
+    for (int i = 0; i < count; ++i) {
+        if (!tensors[i] || row_bytes[i] < 4 || (paged[i] != 0 && paged[i] != 1)) return DSA_ERR_INVALID_ARG;
+        if (row_bytes[i] % 4 || !aligned4(tensors[i])) return DSA_ERR_MISALIGNED;
+        any_paged = any_paged || paged[i];
+    }
+    PageTable pt{};
+    dsa_status_t st;
+    if (any_paged) {
+        if ((st = make_page_table(block_table, bt_stride, page_size, num_pages, Nmax, &pt)) != DSA_OK) return st;
+        if ((long long)B * bt_stride > 0x7FFFFFFFLL) return DSA_ERR_UNSUPPORTED_SHAPE;
+    }
+    if ((st = check_device()) != DSA_OK) return st;
+    return launch_move_rows(src, dst, B, moves, Nmax, count, tensors, row_bytes, paged, pt,
+                            static_cast<cudaStream_t>(stream));
+}
+
 dsa_status_t mla_value_up_proj(const void* o, const void* wv_b, int R, void* v, void* stream) {
     if (!o || !wv_b || !v) return DSA_ERR_INVALID_ARG;
     if (R < 1) return DSA_ERR_INVALID_ARG;

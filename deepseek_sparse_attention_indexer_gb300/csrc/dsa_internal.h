@@ -116,6 +116,19 @@ dsa_status_t launch_indexer_norm_rope(const void* q, int64_t q_stride, const voi
                                       float eps, const float* cos_sin, int max_pos, int interleave,
                                       const int32_t* pos, const int32_t* slots, int R, void* q_out, void* k_cache,
                                       int cache_rows, cudaStream_t stream);
+dsa_status_t launch_key_weights_prefill(int format, const void* q, const void* cache, const float* cache_scale,
+                                        const int32_t* idx, const float* lse, int L, int N, int top_k, float scale,
+                                        float* acc, int accumulate, void* workspace, const PageTable& pages,
+                                        cudaStream_t stream);
+dsa_status_t launch_key_weights_decode(int format, const void* q, const void* cache, const float* cache_scale,
+                                       const int32_t* kv_len, const int32_t* idx, const float* lse, int B, int Nmax,
+                                       int top_k, float scale, float* acc, int accumulate, const PageTable& pages,
+                                       cudaStream_t stream);
+dsa_status_t launch_evict_plan(const float* acc, const int32_t* pos, const int32_t* kv_len, int B, int Nmax, int keep,
+                               int recent, int sink, int32_t* src, int32_t* dst, int32_t* left, cudaStream_t stream);
+dsa_status_t launch_move_rows(const int32_t* src, const int32_t* dst, int B, int most, int Nmax, int count,
+                              void* const* tensors, const int* row_bytes, const int* paged, const PageTable& pages,
+                              cudaStream_t stream);
 dsa_status_t launch_value_up_proj(const void* o, const void* wv_b, int R, void* v, cudaStream_t stream);
 
 }  // namespace dsa

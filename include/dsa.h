@@ -464,6 +464,89 @@ dsa_status_t mla_sparse_attn_decode_q4_paged(const void *q, const void *cache, c
                                              size_t ws_bytes, void *stream);
 
 /*
+ * Eviction.  A long context's cache is cut to a budget of keys by the attention weight that each key
+ * has received: mla_key_weights_* sums it up (next to the attention, from its lse), dsa_cache_evict_plan
+ * chooses the keys that stay, dsa_cache_move_rows closes the gaps in every tensor that holds a row a
+ * key.  The order of a sequence's keys is not kept: its positions are a tensor of their own.  No
+ * counterpart on the pages.
+ */
+#define DSA_ROWS_BF16 0   /* 1152-byte rows, no cache_scale */
+#define DSA_ROWS_Q8 1     /* the 8-bit cache */
+#define DSA_ROWS_Q4 2     /* the 4-bit cache */
+#define DSA_MAX_MOVED 8
+
+/*
+ * mla_key_weights_prefill, mla_key_weights_decode -- the attention weight of each key:
+ *
+ *   w[j] = sum over i with j in idx[i] and heads h of exp(scale * q[i,h,:] . k_j - lse[i,h])
+ *   acc[j] = w[j] (accumulate 0), acc[j] + w[j] (accumulate 1)
+ *
+ * with q, cache, idx, kv_len, block_table and scale as given to the attention call that returned lse.
+ *   cache        bf16, 8-bit or 4-bit rows (row_format), 32-byte aligned; cache_scale for the latter two
+ *   block_table  pages as in the attention calls, or NULL: dense rows
+ *   lse          f32 [L, 64] or [B, 64]; a lse of other keys than the selected (the log of the sum over
+ *                several caches' parts) gives the weights relative to those
+ *   acc          f32 [N], or [B, Nmax]: the sums of sequence b's keys; every key's is written with accumulate 0
+ * Products are exact and accumulated in float32.  A key's weight in one query is at most 128 (64 heads'
+ * probabilities are at most 64); a NaN counts 0.  Entries of idx behind the cache are recorded as
+ * DSA_ERR_DEVICE_BOUNDS and skipped, negative ones skipped; a key given twice in a query counts twice.
+ * Prefill adds whole numbers of 2^-shift, L * 128 * 2^shift <= 2^62, in a workspace of
+ * mla_key_weights_workspace_size(N) bytes (8-byte aligned): the sums do not depend on any order, and so
+ * the same call gives the same bits.  Decode needs none, and has each sequence's keys once.
+ * Errors (host): DSA_ERR_INVALID_ARG for a null pointer (a cache_scale with bf16 rows too), sizes < 1, a
+ * scale that is not positive and finite, accumulate not 0 or 1; DSA_ERR_UNSUPPORTED_SHAPE for top_k and
+ * sizes as in the attention calls; DSA_ERR_MISALIGNED; DSA_ERR_WORKSPACE_TOO_SMALL.
+ */
+size_t mla_key_weights_workspace_size(int N);
+dsa_status_t mla_key_weights_prefill(const void *q, const void *cache, const float *cache_scale,
+                                     int row_format, const int32_t *block_table, int page_size,
+                                     int num_pages, const int32_t *idx, const float *lse, int L, int N,
+                                     int top_k, float scale, float *acc, int accumulate,
+                                     void *workspace, size_t ws_bytes, void *stream);
+dsa_status_t mla_key_weights_decode(const void *q, const void *cache, const float *cache_scale,
+                                    int row_format, const int32_t *kv_len, const int32_t *block_table,
+                                    int bt_stride, int page_size, int num_pages, const int32_t *idx,
+                                    const float *lse, int B, int Nmax, int top_k, float scale,
+                                    float *acc, int accumulate, void *stream);
+
+/*
+ * dsa_cache_evict_plan -- which keys of each sequence stay, and the moves that close the gaps.
+ * Of sequence b's kv_len[b] keys (at most Nmax), if they are more than `keep`, stay
+ *   the `recent` latest positions and those below `sink` (recent + sink <= keep), and
+ *   the heaviest of the others by acc, `keep` in all; equal weights rank the lower index first, a NaN below
+ *   every other weight.  (Positions of a sequence differ; if more than `keep` keys are protected all the
+ *   same, those of lowest index stay.)
+ * The i-th place below keep, in ascending order, whose key goes is filled from the i-th key from keep on
+ * that stays: src[b, i] and dst[b, i], M = min(keep, Nmax - keep) entries a sequence, -1 behind the last.
+ * No row is source and destination, so the moves may run in any order.
+ *   acc   f32 [B, Nmax], pos int32 [B, Nmax], kv_len int32 [B]; only a sequence's own keys are read
+ *   src, dst  int32 [B, M];  left  int32 [B]: min(kv_len[b], keep), the keys after the moves
+ * Errors (host): DSA_ERR_INVALID_ARG for a null pointer, src equal to dst, B < 1, keep outside 1 .. Nmax - 1,
+ * recent or sink < 0 or together above keep; DSA_ERR_UNSUPPORTED_SHAPE for B * Nmax > 2^31 - 1.
+ */
+dsa_status_t dsa_cache_evict_plan(const float *acc, const int32_t *pos, const int32_t *kv_len, int B,
+                                  int Nmax, int keep, int recent, int sink, int32_t *src, int32_t *dst,
+                                  int32_t *left, void *stream);
+
+/*
+ * dsa_cache_move_rows -- row dst[b, i] of sequence b becomes row src[b, i], in up to 8 tensors at once
+ * (latent rows, their scales, indexer keys, weights, positions): every pair with both entries >= 0.
+ * A call's destinations of a sequence differ, and none is a source (a plan's are so); pages that hold
+ * moved rows belong to one sequence.
+ *   src, dst   int32 [B, moves] (device)
+ *   tensors    host array of `count` device pointers (4-byte aligned); row_bytes: bytes of a row each, a
+ *              multiple of 4; paged: 0 for [B, Nmax, ...] rows, 1 for a pool addressed through block_table
+ * An entry >= Nmax or a page outside the pool is recorded as DSA_ERR_DEVICE_BOUNDS and not moved.
+ * Errors (host): DSA_ERR_INVALID_ARG for a null pointer or a size < 1, row_bytes < 4, paged not 0 or 1;
+ * DSA_ERR_UNSUPPORTED_SHAPE for count > 8, B > 65535, products above 2^31 - 1, page sizes as in
+ * the paged calls; DSA_ERR_MISALIGNED.
+ */
+dsa_status_t dsa_cache_move_rows(const int32_t *src, const int32_t *dst, int B, int moves, int Nmax,
+                                 int count, void *const *tensors, const int *row_bytes, const int *paged,
+                                 const int32_t *block_table, int bt_stride, int page_size,
+                                 int num_pages, void *stream);
+
+/*
  * dsa_indexer_norm_rope -- the indexer's queries and keys of R new tokens from
  * their projections: norm and rotation of each head in one pass, the queries
  * written as dsa_indexer_scores takes them and the keys scattered to the key
