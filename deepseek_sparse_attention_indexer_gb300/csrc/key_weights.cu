@@ -6,17 +6,18 @@
 // spent on values.  A pass of the scores alone (576 products a key and head, against 1088 for the attention).
 //
 // How (GB300 design):
-//   * Keys sit on the 128 lanes of tensor memory, S^T = K . Q^T (M = 128 keys, N = 64 heads), so that a thread of the
+//   * S^T = K . Q^T with the keys on the 128 lanes of tensor memory (M = 128 keys, N = 64 heads), so that a thread of the
 //     epilogue has one key's 64 scores and its sum over heads needs no other thread.
-//   * The rows of every format go through registers into tensor memory as bf16, as the A operand of the MMA, 64 dims
-//     (32 columns) a slot of a ring of eight: e4m3 and 4-bit numbers times their block's scale are bf16 numbers, and the
-//     row's scale is applied to the sum (the rope dims, which it does not scale, have an accumulator of their own).
-//     Shared memory holds queries only, and its port is free for the MMA's reads of them.
-//   * Four lanes load a row's 64 dims, 16 each, and store them with the 16-lane shape, whose columns a thread holds in
-//     pairs: the MMA sees a chunk's dims in another order, four at a time transposed, and so does the query, which is
-//     brought into that order on its way to shared memory.  (A lane a row is the order of the 32-lane shape, and a
-//     load instruction then touches 32 lines in place of 8.)
-//   * Roles: warp 0 issues MMAs, warps 1-3 load queries, 16 warps gather, 8 do the epilogue (4 a tile, in turn).
+//   * A tile's rows go to shared memory as bf16, 64 dims a slot, nine slots for the 576: bf16 rows by cp.async, whose
+//     copies in flight hold no registers, e4m3 and 4-bit rows through registers.  Their numbers, times their block's
+//     scale, are bf16 numbers; the row's scale is applied to the sum, and the rope dims, which it does not scale, have
+//     an accumulator of their own.  (Rows through registers into tensor memory, as the MMA's A operand, left too few
+//     bytes in flight: 1.24 ms for 4096 queries of 2048 bf16 rows.)
+//   * One query stands in shared memory; a chunk of the next one is loaded when the last tile's MMAs have read it.
+//   * An MMA of N = 64 takes its issuer 57 cycles, whatever N, a commit 200 and a look at the barriers 550: two issuers,
+//     each with an accumulator of its own for its dims, and barriers for four groups of chunks in place of nine.
+//   * Roles: warps 0 and 2 issue MMAs, warp 1 loads queries (TMA), 8 warps gather bf16 rows, 16 the others, 8 do the
+//     epilogue, 4 a tile, in turn.
 //   * Decode adds a key's weight to its float32 sum: one thread a key (the same key twice adds the same number twice).
 //     A prefill's queries meet at keys in any order, so they add whole numbers, 2^-shift each, in 64 bits, and a second
 //     kernel makes floats of them: the same bits every time.
@@ -36,25 +37,34 @@ constexpr int kQDim = DSA_QK_DIM;                  // 576
 constexpr int kDims = 64;                          // dims of a chunk
 constexpr int kChunks = kQDim / kDims;             // 9, the last one the rope dims
 constexpr int kQBlk = kH * 128;                    // 8 KB: 64 heads x 64 dims
-constexpr int kSlots = 8;                          // chunks in tensor memory
-constexpr int kLoadWarps = 3, kGatherWarps = 16, kEpiWarps = 8;
-constexpr int kFirstGather = 1 + kLoadWarps;
-constexpr int kFirstEpi = kFirstGather + kGatherWarps;
-constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
-constexpr int kGroups = kGatherWarps / 4;          // four warps, one a lane quadrant, fill a chunk
+constexpr int kBlk = 128 * 128;                    // 16 KB: 128 keys x 64 dims
+constexpr int kEpiWarps = 8;
+template <int FMT>
+struct Roles {                                     // warps 0 and 2 MMA, 1 queries, 3 none, then gather, then epilogue
+    static constexpr int kGather = FMT == DSA_ROWS_BF16 ? 8 : 16;
+    static constexpr int kFirstEpi = 4 + kGather;
+    static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+};
 
-constexpr int OFF_Q = 0;                           // 2 queries
-constexpr int OFF_LSE = OFF_Q + 2 * kChunks * kQBlk;   // float [2][64]: -lse log2(e)
-constexpr int OFF_BAR = OFF_LSE + 2 * kH * 4;
-// barriers: full[8], empty[8], acc_full[2], acc_free[2], q_full[2], q_free[2]
-constexpr int kBars = 2 * kSlots + 8;
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + kChunks * kQBlk;
+constexpr int OFF_LSE = OFF_K + kChunks * kBlk;    // float [8][64]: -lse log2(e), a copy an epilogue warp
+constexpr int OFF_BAR = OFF_LSE + kEpiWarps * kH * 4;
+// barriers: full[4], empty[4], q_full[4], q_free[4], acc_full[2], acc_free[2]
+constexpr int kParts = 4;                          // chunks 0 1, 2 3 (first issuer); 4 5, 6 7 8 (second)
+constexpr int kBars = 4 * kParts + 4;
+__device__ __forceinline__ constexpr int part_begin(int g) { return 2 * g; }
+__device__ __forceinline__ constexpr int part_end(int g) { return g == kParts - 1 ? kChunks : 2 * g + 2; }
 constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
 constexpr int kSmemBytes = OFF_ABORT + 4;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
 
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t TM_A = 0;                       // ring: 8 x 32 columns
-constexpr uint32_t TM_D = 256;                     // 2 x (64 latent, 64 rope)
+// accumulators of a tile, two tiles: chunks 0 to 3, chunks 4 and up, and, where it is not among those, the rope chunk
+template <int FMT>
+struct Acc {
+    static constexpr uint32_t kCols = FMT == DSA_ROWS_BF16 ? 128 : 192, kAlloc = FMT == DSA_ROWS_BF16 ? 256 : 512;
+};
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 128-byte swizzle, 8-row groups 1 KB apart
 constexpr uint32_t IDESC = idesc_bf16_f32(128, 64, false, false);
 
@@ -94,15 +104,6 @@ __device__ __forceinline__ int64_t key_row(const WeightParams& p, const Item& I,
     return paged_row(p.pages, I.batch, j);
 }
 
-__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -129,16 +130,14 @@ __device__ __forceinline__ void q4_to_bf16(uint32_t w, uint32_t scale, uint32_t*
     }
 }
 
-// dims 16 j .. 16 j + 15 of chunk c of a row, as they lie in the cache; zeros without a row
+// Dims 16 j .. 16 j + 15 of chunk c of a row of the 8-bit or 4-bit cache as they lie there; zeros without a row.
 template <int FMT>
-__device__ __forceinline__ void load_dims(const WeightParams& p, int64_t row, int c, int j, uint32_t (&x)[8]) {
+__device__ __forceinline__ void load_dims(const WeightParams& p, int row, int c, int j, uint32_t (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0;
     if (row < 0) return;
-    const uint8_t* src = p.cache + row * Row<FMT>::kBytes;
-    if (FMT == DSA_ROWS_BF16) {
-        ldg_nc_v8(src + 128 * c + 32 * j, x);
-    } else if (c == kChunks - 1) {                 // the rope dims of the other formats are bf16, too
+    const uint8_t* src = p.cache + (int64_t)row * Row<FMT>::kBytes;
+    if (c == kChunks - 1) {                        // the rope dims, bf16
         ldg_nc_v8(src + (FMT == DSA_ROWS_Q8 ? kQ8Latent : kQ4Rope) + 32 * j, x);
     } else if (FMT == DSA_ROWS_Q8) {
         const uint4 v = ldg_nc_v4(src + 64 * c + 16 * j);
@@ -154,7 +153,7 @@ __device__ __forceinline__ void load_dims(const WeightParams& p, int64_t row, in
 // the same as bf16
 template <int FMT>
 __device__ __forceinline__ void widen(int c, uint32_t (&x)[8]) {
-    if (FMT == DSA_ROWS_BF16 || c == kChunks - 1) return;
+    if (c == kChunks - 1) return;
     if (FMT == DSA_ROWS_Q8) {
         const uint32_t w[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -170,39 +169,41 @@ __device__ __forceinline__ void widen(int c, uint32_t (&x)[8]) {
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const WeightParams p) {
+__global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
+    key_weights_kernel(const __grid_constant__ CUtensorMap tmap_q, const WeightParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
-    if (smem_u32(smem) & 1023u) {   // the operand's swizzle counts from 1 KB boundaries
+    if (smem_u32(smem) & 1023u) {   // the operands' swizzle counts from 1 KB boundaries
         if (threadIdx.x == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
         return;
     }
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
-    uint64_t* empty = full + kSlots;
-    uint64_t* acc_full = empty + kSlots;
+    uint64_t* empty = full + kParts;
+    uint64_t* q_full = empty + kParts;
+    uint64_t* q_free = q_full + kParts;
+    uint64_t* acc_full = q_free + kParts;
     uint64_t* acc_free = acc_full + 2;
-    uint64_t* q_full = acc_free + 2;
-    uint64_t* q_free = q_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+    constexpr int kFirstEpi = Roles<FMT>::kFirstEpi, kGroups = Roles<FMT>::kGather / 4;
     const int warp = threadIdx.x / 32;
     const uint32_t lane = lane_id();
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&full[i], 4);
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(&full[i], FMT == DSA_ROWS_BF16 ? 128 : 4);   // the copies' arrivals, or a warp's
             mbar_init(&empty[i], 1);
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_free[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_full[i], 2);
             mbar_init(&acc_free[i], 4);
-            mbar_init(&q_full[i], kLoadWarps);
-            mbar_init(&q_free[i], 1 + kEpiWarps);  // the MMAs, and every warp of the epilogue once an item
         }
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 0) {
-        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_alloc(tmem_slot, Acc<FMT>::kAlloc);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -229,115 +230,136 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const WeightPa
         }
     };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ MMA issuer
-        int n = 0, gt = 0, qi = 0;
+    // Chunk c of every tile lies in slot c; the slots' barriers are in the phase of the tile, gt, the query's of the item, qi.
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------------------------------ MMA issuers
+        // One look at all barriers, a lane each (a poll between MMAs waits until the tensor core has taken those before
+        // it): lanes 0, 1 the keys' parts, 2, 3 the query's, 4 the accumulator.
+        const int g0 = warp;                       // the issuer's parts g0, g0 + 1
+        int gt = 0, qi = 0;
+        const uint32_t base = (smem_u32(smem) >> 4) | ((16u >> 4) << 16);
         items([&](const Item&, int T) {
-            bool ok = wait(&q_full[qi & 1], (qi >> 1) & 1);
-            const uint32_t q_lo = ((smem_u32(smem + OFF_Q) + (qi & 1) * (kChunks * kQBlk)) >> 4) | ((16u >> 4) << 16);
-            for (int t = 0; ok && t < T; ++t, ++gt) {
-                ok = wait(&acc_free[gt & 1], ((gt >> 1) & 1) ^ 1);
-                const uint32_t d = tmem_base + TM_D + 128 * (gt & 1);
-                for (int c = 0; ok && c < kChunks; ++c, ++n) {
-                    ok = wait(&full[n % kSlots], (n / kSlots) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const bool rope = FMT != DSA_ROWS_BF16 && c == kChunks - 1;
+            for (int t = 0; t < T; ++t, ++gt) {
+                const uint32_t acc = tmem_base + Acc<FMT>::kCols * (gt & 1), d = acc + (g0 ? 64 : 0);
+                uint64_t* mine = lane < 2 ? &full[g0 + lane] : lane < 4 ? &q_full[g0 + lane - 2] : &acc_free[gt & 1];
+                const uint32_t parity = lane < 2 ? gt & 1 : lane < 4 ? qi & 1 : ((gt >> 1) & 1) ^ 1;
+                uint32_t got = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16_ts_lo(d + (rope ? 64 : 0), tmem_base + TM_A + 32 * (n % kSlots) + 8 * k,
-                                           q_lo + c * (kQBlk >> 4) + 2 * k, kDescHi, IDESC, ((c && !rope) || k) ? 1u : 0u);
-                        mma_commit(&empty[n % kSlots]);
-                        if (c == kChunks - 1) {
-                            mma_commit(&acc_full[gt & 1]);
-                            if (t == T - 1) mma_commit(&q_free[qi & 1]);
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t need = 5u << h | 16u;
+                    if ((got & need) != need) {
+                        got = mbar_poll_warp(mine, parity, lane, 5, need, abort_flag, p.status);
+                        if (got == 0) return false;
+                        fence_proxy_async_smem();  // of every lane that saw a barrier, before the lane that issues
+                        tc_fence_after();
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        const int g = g0 + h;
+                        for (int c = part_begin(g); c < part_end(g); ++c) {
+                            const bool rope = FMT != DSA_ROWS_BF16 && c == kChunks - 1;
+                            const bool first = c == part_begin(g0) || rope;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_bf16_ss_lo(rope ? acc + 128 : d, base + ((OFF_K + c * kBlk) >> 4) + 2 * k, kDescHi,
+                                               base + ((OFF_Q + c * kQBlk) >> 4) + 2 * k, kDescHi, IDESC, first && k == 0 ? 0u : 1u);
                         }
+                        mma_commit(&empty[g]);
+                        if (t == T - 1) mma_commit(&q_free[g]);
                     }
                     __syncwarp();
                 }
+                if (lane == 0) mma_commit(&acc_full[gt & 1]);
+                __syncwarp();
             }
             ++qi;
-            return ok;
+            return true;
         });
-    } else if (warp < kFirstGather) {
-        // ------------------------------------------------------------ queries
-        const int lt = (warp - 1) * 32 + (int)lane;
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ queries (TMA)
         int qi = 0;
         items([&](const Item& I, int) {
-            if (!wait(&q_free[qi & 1], ((qi >> 1) & 1) ^ 1)) return false;
-            const __nv_bfloat16* src = p.q + (int64_t)I.row * (kH * kQDim);
-            uint8_t* dst = smem + OFF_Q + (qi & 1) * (kChunks * kQBlk);
-            // 16 dims a step: head h, chunk c, piece j; its four dims 4 b.. go to 8-byte unit 4 b + j of the row
-#pragma unroll 4
-            for (int i = lt; i < kH * kChunks * 4; i += kLoadWarps * 32) {
-                const int h = i / (kChunks * 4), r = i % (kChunks * 4), c = r / 4, j = r % 4;
-                const uint4 u = ldg_nc_v4(src + h * kQDim + 16 * r), v = ldg_nc_v4(src + h * kQDim + 16 * r + 8);
-                const uint2 w[4] = {{u.x, u.y}, {u.z, u.w}, {v.x, v.y}, {v.z, v.w}};
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    *reinterpret_cast<uint2*>(dst + c * kQBlk + h * 128 + (((2 * b + (j >> 1)) ^ (h & 7)) << 4) + 8 * (j & 1)) = w[b];
+            for (int g = 0; g < kParts; ++g) {
+                if (!wait(&q_free[g], (qi & 1) ^ 1)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[g], (part_end(g) - part_begin(g)) * kQBlk);
+                    for (int c = part_begin(g); c < part_end(g); ++c)
+                        tma_load_2d(smem + OFF_Q + c * kQBlk, &tmap_q, &q_full[g], c * kDims, I.row * kH);
+                }
+                __syncwarp();
             }
-            if (lt < kH)
-                reinterpret_cast<float*>(smem + OFF_LSE)[(qi & 1) * kH + lt] =
-                    -1.4426950408889634f * __ldg(p.lse + (int64_t)I.row * kH + lt);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[qi & 1]);
             ++qi;
             return true;
         });
-    } else if (warp < kFirstEpi) {
+    } else if (warp >= 4 && warp < kFirstEpi) {
         // ------------------------------------------------------------ gather
-        const int quad = warp & 3, group = (warp - kFirstGather) >> 2;
-        const int j = (int)(lane & 3);
-        const uint32_t at = tmem_base + TM_A + (static_cast<uint32_t>(quad * 32) << 16);
-        int n0 = 0;                                // chunks of the tiles before
+        // Four warps, 32 rows each, fill a chunk: bf16 rows eight lanes a row, 16 bytes each, two sets of warps with two
+        // parts each; the others four lanes a row, 16 dims each, a set a part.
+        constexpr int kLanes = FMT == DSA_ROWS_BF16 ? 8 : 4, kRows = kLanes;
+        constexpr int kOwn = kParts / kGroups;
+        const int quad = warp & 3, g0 = ((warp - 4) >> 2) * kOwn;
+        const int j = (int)lane % kLanes, r0 = quad * 32 + (int)lane / kLanes;   // rows r0 + 32 / kLanes * i
+        int gt = 0;
         items([&](const Item& I, int T) {
-            for (int t = 0; t < T; ++t, n0 += kChunks) {
-                int64_t row[4];
+            const int32_t* idx = p.idx + (int64_t)I.row * p.top_k;
+            for (int t = 0; t < T; ++t, ++gt) {
+                int row[kRows];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {      // rows l / 4 + 8 i of the quadrant
-                    const int slot = I.slot0 + t * kTile + quad * 32 + 8 * i + (int)(lane >> 2);
-                    row[i] = key_row(p, I, slot < I.slot_end ? __ldg(p.idx + (int64_t)I.row * p.top_k + slot) : -1);
+                for (int i = 0; i < kRows; ++i) {
+                    const int slot = I.slot0 + t * kTile + r0 + 32 / kLanes * i;
+                    row[i] = slot < I.slot_end ? __ldg(idx + slot) : -1;
                 }
-                for (int c = (group - n0 % kGroups + kGroups) % kGroups; c < kChunks; c += kGroups) {
-                    const int n = n0 + c;
-                    uint32_t x[4][8];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) load_dims<FMT>(p, row[i], c, j, x[i]);
-                    if (!wait(&empty[n % kSlots], ((n / kSlots) & 1) ^ 1)) return false;
-                    tc_fence_after();
+                for (int i = 0; i < kRows; ++i) row[i] = (int)key_row(p, I, row[i]);
+                if constexpr (FMT == DSA_ROWS_BF16) {
+#pragma unroll 1
+                    for (int g = g0; g < g0 + kOwn; ++g) {
+                        if (!wait(&empty[g], (gt & 1) ^ 1)) return false;
+                        for (int c = part_begin(g); c < part_end(g); ++c) {
+                            const uint32_t dst = smem_u32(smem + OFF_K) + c * kBlk + r0 * 128;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) widen<FMT>(c, x[i]);
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {  // 16 lanes: rows of i = 2 f and 2 f + 1
-                        uint32_t r[16];
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            r[4 * b] = x[2 * f][2 * b];
-                            r[4 * b + 1] = x[2 * f][2 * b + 1];
-                            r[4 * b + 2] = x[2 * f + 1][2 * b];
-                            r[4 * b + 3] = x[2 * f + 1][2 * b + 1];
+                            for (int i = 0; i < kRows; ++i) {
+                                const uint8_t* src = p.cache + (int64_t)max(row[i], 0) * Row<FMT>::kBytes + 128 * c + 16 * j;
+                                cp_async_16(dst + i * 512 + ((j ^ ((r0 + 4 * i) & 7)) << 4), src, row[i] >= 0 ? 16u : 0u);
+                            }
                         }
-                        tmem_st_16x256b_x4(at + 32 * (n % kSlots) + (16u * f << 16), r);
+                        cp_async_arrive_noinc(&full[g]);
                     }
-                    tmem_st_wait();
-                    tc_fence_before();
+                } else {
+                    uint32_t x[kRows][8];
+                    const int g = g0, r = (int)lane / kLanes;   // row % 8
+                    for (int c = part_begin(g); c < part_end(g); ++c) {
+#pragma unroll
+                        for (int i = 0; i < kRows; ++i) load_dims<FMT>(p, row[i], c, j, x[i]);
+                        if (c == part_begin(g) && !wait(&empty[g], (gt & 1) ^ 1)) return false;
+                        uint8_t* dst = smem + OFF_K + c * kBlk + r0 * 128;
+#pragma unroll
+                        for (int i = 0; i < kRows; ++i) {
+                            widen<FMT>(c, x[i]);
+                            *reinterpret_cast<uint4*>(dst + i * 1024 + (((2 * j) ^ r) << 4)) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
+                            *reinterpret_cast<uint4*>(dst + i * 1024 + (((2 * j + 1) ^ r) << 4)) = make_uint4(x[i][4], x[i][5], x[i][6], x[i][7]);
+                        }
+                    }
+                    fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[n % kSlots]);
+                    if (lane == 0) mbar_arrive(&full[g]);
                 }
             }
             return true;
         });
-    } else {
+        cp_async_wait_all();
+    } else if (warp >= kFirstEpi) {
         // ------------------------------------------------------------ epilogue
         const int quad = warp & 3, set = (warp - kFirstEpi) >> 2;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
-        int gt = 0, qi = 0;
+        float2* nl = reinterpret_cast<float2*>(smem + OFF_LSE) + (warp - kFirstEpi) * (kH / 2);
+        int gt = 0;
         items([&](const Item& I, int T) {
-            // also of an item whose only tile is the other set's: no arrival ahead of its phase
-            if (!wait(&q_full[qi & 1], (qi >> 1) & 1)) return false;
+            const float* lse = p.lse + (int64_t)I.row * kH + 2 * lane;
+            const float l0 = __ldg(lse), l1 = __ldg(lse + 1);
+            __syncwarp();
+            nl[lane] = make_float2(-1.4426950408889634f * l0, -1.4426950408889634f * l1);
+            __syncwarp();
             for (int t = 0; t < T; ++t, ++gt) {
                 if ((gt & 1) != set) continue;
                 const int slot = I.slot0 + t * kTile + quad * 32 + (int)lane;
@@ -349,20 +371,21 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const WeightPa
                 const float2 sc = make_float2(p.scale_log2 * c, p.scale_log2 * c), sr = make_float2(p.scale_log2, p.scale_log2);
                 if (!wait(&acc_full[gt & 1], (gt >> 1) & 1)) return false;
                 tc_fence_after();
-                const float2* nl = reinterpret_cast<const float2*>(smem + OFF_LSE + (qi & 1) * kH * 4);
-                const uint32_t d = tmem_base + lane_addr + TM_D + 128 * (gt & 1);
+                const uint32_t d = tmem_base + lane_addr + Acc<FMT>::kCols * (gt & 1);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int h = 0; h < kH; h += 16) {
-                    uint32_t v[16], r[16];
-                    tmem_ld16(d + h, v);
-                    if (FMT != DSA_ROWS_BF16) tmem_ld16(d + 64 + h, r);
+                    uint32_t u[16], v[16], r[16];
+                    tmem_ld16(d + h, u);
+                    tmem_ld16(d + 64 + h, v);
+                    if (FMT != DSA_ROWS_BF16) tmem_ld16(d + 128 + h, r);
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         float2 x = nl[h / 2 + k];
                         if (FMT != DSA_ROWS_BF16)
                             x = __ffma2_rn(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sr, x);
+                        x = __ffma2_rn(make_float2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])), sc, x);
                         x = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sc, x);
                         sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
                     }
@@ -379,9 +402,6 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const WeightPa
                         atomicAdd(p.acc + (int64_t)I.batch * p.Nmax + key, w);
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_free[qi & 1]);
-            ++qi;
             return true;
         });
     }
@@ -390,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const WeightPa
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, kTmemCols);
+        tmem_dealloc(tmem_base, Acc<FMT>::kAlloc);
     }
 }
 
@@ -415,9 +435,12 @@ dsa_status_t launch(const WeightParams& p, cudaStream_t stream) {
         if (st != DSA_OK) return st;
         done[dev].store(true, std::memory_order_release);
     }
+    CUtensorMap tq;
+    const dsa_status_t st = make_tmap_bf16_2d(&tq, p.q, kQDim, (uint64_t)p.rows * kH, kQDim * 2, kDims, kH);
+    if (st != DSA_OK) return st;
     const int sms = device_sm_count();
-    if (launch_pdl(key_weights_kernel<FMT>, dim3(p.n_items < sms ? p.n_items : sms), dim3(kThreads), kSmemBytes, stream,
-                   p) != cudaSuccess)
+    if (launch_pdl(key_weights_kernel<FMT>, dim3(p.n_items < sms ? p.n_items : sms), dim3(Roles<FMT>::kThreads), kSmemBytes,
+                   stream, tq, p) != cudaSuccess)
         return DSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
