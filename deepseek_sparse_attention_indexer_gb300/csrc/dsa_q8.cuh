@@ -44,6 +44,28 @@ __device__ __forceinline__ int e4m3_scale_exponent(float amax) {
 }
 __device__ __forceinline__ float exp2_int(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
+// Four values as hi + lo / 16 in e4m3 (|x| <= 448): the four hi bytes, the four lo bytes.  The half-precision step
+// between keeps 11 bits, the difference x - hi is exact.
+__device__ __forceinline__ void split_e4m3x4(float x, float y, float z, float w, uint32_t& hi, uint32_t& lo) {
+    asm("{\n\t.reg .b32 a, b, p, q;\n\t.reg .b16 s, t;\n\t"
+        "cvt.rn.f16x2.f32 a, %3, %2;\n\t"
+        "cvt.rn.f16x2.f32 b, %5, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 s, a;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 t, b;\n\t"
+        "mov.b32 %0, {s, t};\n\t"
+        "cvt.rn.f16x2.e4m3x2 p, s;\n\t"
+        "cvt.rn.f16x2.e4m3x2 q, t;\n\t"
+        "sub.rn.f16x2 a, a, p;\n\t"
+        "sub.rn.f16x2 b, b, q;\n\t"
+        "mul.rn.f16x2 a, a, %6;\n\t"
+        "mul.rn.f16x2 b, b, %6;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 s, a;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 t, b;\n\t"
+        "mov.b32 %1, {s, t};\n\t}\n"
+        : "=&r"(hi), "=&r"(lo)
+        : "f"(x), "f"(y), "f"(z), "f"(w), "r"(0x4c004c00u));   // 16, twice
+}
+
 // Pool row of key j of sequence b, -1 when its page lies outside the pool.
 __device__ __forceinline__ int64_t paged_row(const PageTable& pt, int b, int j) {
     const int page = __ldg(pt.table + (int64_t)b * pt.stride + (j >> pt.shift));

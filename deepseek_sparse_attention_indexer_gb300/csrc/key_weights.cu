@@ -6,18 +6,17 @@
 // spent on values.  A pass of the scores alone (576 products a key and head, against 1088 for the attention).
 //
 // How (GB300 design):
-//   * S^T = K . Q^T with the keys on the 128 lanes of tensor memory (M = 128 keys, N = 64 heads), so that a thread of the
+//   * S^T = K . Q^T with the keys on the 128 lanes of tensor memory (M = 128 keys, heads as N), so that a thread of the
 //     epilogue has one key's 64 scores and its sum over heads needs no other thread.
-//   * A tile's rows go to shared memory as bf16, 64 dims a slot, nine slots for the 576: bf16 rows by cp.async, whose
-//     copies in flight hold no registers, e4m3 and 4-bit rows through registers.  Their numbers, times their block's
-//     scale, are bf16 numbers; the row's scale is applied to the sum, and the rope dims, which it does not scale, have
-//     an accumulator of their own.  (Rows through registers into tensor memory, as the MMA's A operand, left too few
-//     bytes in flight: 1.24 ms for 4096 queries of 2048 bf16 rows.)
-//   * One query stands in shared memory; a chunk of the next one is loaded when the last tile's MMAs have read it.
-//   * An MMA of N = 64 takes its issuer 57 cycles, whatever N, a commit 200 and a look at the barriers 550: two issuers,
-//     each with an accumulator of its own for its dims, and barriers for four groups of chunks in place of nine.
-//   * Roles: warps 0 and 2 issue MMAs, warp 1 loads queries (TMA), 8 warps gather bf16 rows, 16 the others, 8 do the
-//     epilogue, 4 a tile, in turn.
+//   * The gathered rows go to shared memory by cp.async, whose copies in flight hold no registers; the query stands there.
+//     (Rows through registers into tensor memory, as the MMA's A operand, left too few bytes in flight: 1.24 ms for 4096
+//     queries of 2048 bf16 rows.)
+//   * bf16 rows: nine chunks of 64 dims, a tile's in nine slots.  An MMA of N = 64 takes its issuer 57 cycles, whatever
+//     N, a commit 200 and a look at the barriers 550: two issuers, each with an accumulator of its own for its dims, and
+//     barriers for four groups of chunks in place of nine (1.22 -> 0.91 ms).
+//   * 8-bit and 4-bit rows: e4m3 products, the query as two e4m3 numbers, as in the attention over them (mla_attn_q8.cu):
+//     four chunks of 128 dims and the rope dims, 20 MMAs a tile in place of 36, two issuers with a tile in turn.  The
+//     row's scale and the query head's are applied to the sums.  4-bit rows are expanded on their way, a lane its own row.
 //   * Decode adds a key's weight to its float32 sum: one thread a key (the same key twice adds the same number twice).
 //     A prefill's queries meet at keys in any order, so they add whole numbers, 2^-shift each, in 64 bits, and a second
 //     kernel makes floats of them: the same bits every time.
@@ -34,46 +33,19 @@ namespace dsa {
 namespace {
 
 constexpr int kQDim = DSA_QK_DIM;                  // 576
-constexpr int kDims = 64;                          // dims of a chunk
-constexpr int kChunks = kQDim / kDims;             // 9, the last one the rope dims
-constexpr int kQBlk = kH * 128;                    // 8 KB: 64 heads x 64 dims
-constexpr int kBlk = 128 * 128;                    // 16 KB: 128 keys x 64 dims
-constexpr int kEpiWarps = 8;
-template <int FMT>
-struct Roles {                                     // warps 0 and 2 MMA, 1 queries, 3 none, then gather, then epilogue
-    static constexpr int kGather = FMT == DSA_ROWS_BF16 ? 8 : 16;
-    static constexpr int kFirstEpi = 4 + kGather;
-    static constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
-};
-
-constexpr int OFF_Q = 0;
-constexpr int OFF_K = OFF_Q + kChunks * kQBlk;
-constexpr int OFF_LSE = OFF_K + kChunks * kBlk;    // float [8][64]: -lse log2(e), a copy an epilogue warp
-constexpr int OFF_BAR = OFF_LSE + kEpiWarps * kH * 4;
-// barriers: full[4], empty[4], q_full[4], q_free[4], acc_full[2], acc_free[2]
-constexpr int kParts = 4;                          // chunks 0 1, 2 3 (first issuer); 4 5, 6 7 8 (second)
-constexpr int kBars = 4 * kParts + 4;
-__device__ __forceinline__ constexpr int part_begin(int g) { return 2 * g; }
-__device__ __forceinline__ constexpr int part_end(int g) { return g == kParts - 1 ? kChunks : 2 * g + 2; }
-constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
-constexpr int OFF_ABORT = OFF_TMEM + 4;
-constexpr int kSmemBytes = OFF_ABORT + 4;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
-
-// accumulators of a tile, two tiles: chunks 0 to 3, chunks 4 and up, and, where it is not among those, the rope chunk
-template <int FMT>
-struct Acc {
-    static constexpr uint32_t kCols = FMT == DSA_ROWS_BF16 ? 128 : 192, kAlloc = FMT == DSA_ROWS_BF16 ? 256 : 512;
-};
+constexpr int kBlk = 128 * 128;                    // 16 KB: 128 keys x 128 bytes
+constexpr int kQBlk = kH * 128;                    // 8 KB: 64 heads x 64 bf16 dims
+constexpr int kEpiWarps = 8;                       // four a tile, in turn
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 128-byte swizzle, 8-row groups 1 KB apart
-constexpr uint32_t IDESC = idesc_bf16_f32(128, 64, false, false);
-
+constexpr uint32_t IDESC_BF16 = idesc_bf16_f32(128, 64, false, false);
+constexpr uint32_t IDESC_E4M3 = idesc_e4m3_f32(128, 128, false, false);
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMostWeight = 128.f;               // of a query: 64 heads' probabilities, and room for their rounding
 
 struct WeightParams : AttnShape {
     const __nv_bfloat16* q;    // [rows][64][576]
     const uint8_t* cache;      // rows of the format's bytes
-    const float* cache_scale;  // q8, q4
+    const float* cache_scale;  // 8-bit, 4-bit
     const float* lse;          // [rows][64]
     float scale_log2;          // scale * log2(e)
     float* acc;                // decode: [B][Nmax]
@@ -81,11 +53,6 @@ struct WeightParams : AttnShape {
     float unit;                // 2^shift
     int32_t* status;
     PageTable pages;
-};
-
-template <int FMT>
-struct Row {
-    static constexpr int kBytes = FMT == DSA_ROWS_BF16 ? 2 * kQDim : FMT == DSA_ROWS_Q8 ? kQ8Row : kQ4Row;
 };
 
 __device__ __forceinline__ Item item_at(const WeightParams& p, int item) {
@@ -97,80 +64,132 @@ __device__ __forceinline__ Item item_at(const WeightParams& p, int item) {
     return it;
 }
 
-// Cache row of key j, -1 where there is none.
-__device__ __forceinline__ int64_t key_row(const WeightParams& p, const Item& I, int j) {
-    if (j < 0 || j >= I.bound) return -1;
-    if (!p.pages.table) return (int64_t)I.batch * p.Nmax + j;
-    return paged_row(p.pages, I.batch, j);
+// Selected key `slot` of the item, -1 where there is none; and the cache row of a key, -1 where there is none.
+__device__ __forceinline__ int key_at(const WeightParams& p, const Item& I, int slot) {
+    return slot < I.slot_end ? __ldg(p.idx + (int64_t)I.row * p.top_k + slot) : -1;
+}
+__device__ __forceinline__ int key_row(const WeightParams& p, const Item& I, int key) {
+    if (key < 0 || key >= I.bound) return -1;
+    if (!p.pages.table) return (int)((int64_t)I.batch * p.Nmax + key);
+    return (int)paged_row(p.pages, I.batch, key);
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-// four e4m3 codes as bf16: exponent and fraction in place, then the exponent's bias (a product with 2^120, exact, also
-// of the subnormal numbers)
-__device__ __forceinline__ void e4m3_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const uint32_t m = w & 0x7f7f7f7fu;
-    constexpr uint32_t k2_120 = 0x7b807b80u;
-    lo = mul_bf16x2((__byte_perm(w, 0, 0x1404) & 0x80008000u) | (__byte_perm(m, 0, 0x1404) >> 4), k2_120);
-    hi = mul_bf16x2((__byte_perm(w, 0, 0x3424) & 0x80008000u) | (__byte_perm(m, 0, 0x3424) >> 4), k2_120);
-}
-// eight 4-bit codes as bf16, times their block's scale (twice in `scale`)
-__device__ __forceinline__ void q4_to_bf16(uint32_t w, uint32_t scale, uint32_t* out) {
-    const uint32_t sel = w & kQ4Magnitudes;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t s = h ? sel >> 16 : sel;
-        const uint32_t top = __byte_perm(0x3f3f3f00u, 0x40404040u, s) | ((h ? w << 4 : w) & 0x80808080u);
-        const uint32_t low = __byte_perm(0xc0800000u, 0xc0804000u, s);
-        out[2 * h] = mul_bf16x2(__byte_perm(low, top, 0x5140), scale);
-        out[2 * h + 1] = mul_bf16x2(__byte_perm(low, top, 0x7362), scale);
+// Items with tiles, in the same order for every role: f(item, tiles) until it returns false.
+template <typename F>
+__device__ __forceinline__ void for_items(const WeightParams& p, uint32_t lane, F f) {
+    for (int s = 0;; ++s) {
+        const int it = nth_item(p, s);
+        if (it == -1) return;
+        if (it < 0) continue;
+        const Item I = item_at(p, it);
+        const int T = item_tiles(p, I, lane);
+        if (T > 0 && !f(I, T)) return;
     }
 }
 
-// Dims 16 j .. 16 j + 15 of chunk c of a row of the 8-bit or 4-bit cache as they lie there; zeros without a row.
-template <int FMT>
-__device__ __forceinline__ void load_dims(const WeightParams& p, int row, int c, int j, uint32_t (&x)[8]) {
+// The rows of a gathering lane, R a tile, tile after tile over all items, in two steps so that the loads of one are in
+// flight while the warp copies: fetch() loads the keys of the next tile, resolve() makes cache rows of them (a page
+// lookup when paged).
+template <int R>
+struct Feed {
+    int s = 0, tiles = 0;              // next item; tiles of the current one still to fetch
+    int slot = 0;                      // of the lane's first row in the next tile
+    Item I{};
+    int key[R], batch = 0, bound = 0;
+
+    __device__ __forceinline__ bool fetch(const WeightParams& p, uint32_t lane, int r0, int step) {
+        while (tiles == 0) {
+            const int it = nth_item(p, s++);
+            if (it == -1) return false;
+            if (it < 0) continue;
+            I = item_at(p, it);
+            tiles = item_tiles(p, I, lane);
+            slot = I.slot0 + r0;
+        }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0;
+        for (int i = 0; i < R; ++i) key[i] = key_at(p, I, slot + i * step);
+        batch = I.batch;
+        bound = I.bound;
+        slot += kTile;
+        --tiles;
+        return true;
+    }
+    __device__ __forceinline__ void resolve(const WeightParams& p, int (&row)[R]) const {
+        Item at{};
+        at.batch = batch;
+        at.bound = bound;
+#pragma unroll
+        for (int i = 0; i < R; ++i) row[i] = key_row(p, at, key[i]);
+    }
+};
+
+// One lane polls for its warp.
+__device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, uint32_t lane, volatile int* abort, int32_t* status) {
+    bool ok = true;
+    if (lane == 0) ok = mbar_poll(bar, parity, abort, status);
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// 128 bytes of each of the lane's rows (r0 + 4 i of the tile, eight lanes a row, this lane's 16 bytes the j-th) to a slot;
+// zeros for a row that is not there.
+__device__ __forceinline__ void copy_rows(const WeightParams& p, const int (&row)[8], int bytes, int at, uint32_t slot, int r0, int j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint8_t* src = p.cache + (int64_t)max(row[i], 0) * bytes + at + 16 * j;
+        cp_async_16(slot + r0 * 128 + i * 512 + ((j ^ ((r0 + 4 * i) & 7)) << 4), src, row[i] >= 0 ? 16u : 0u);
+    }
+}
+
+__device__ __forceinline__ void add_weight(const WeightParams& p, const Item& I, int key, int row, float2 sum) {
+    const float s = sum.x + sum.y;
+    const float w = s > 0.f ? fminf(s, kMostWeight) : 0.f;   // NaN: 0
     if (row < 0) return;
-    const uint8_t* src = p.cache + (int64_t)row * Row<FMT>::kBytes;
-    if (c == kChunks - 1) {                        // the rope dims, bf16
-        ldg_nc_v8(src + (FMT == DSA_ROWS_Q8 ? kQ8Latent : kQ4Rope) + 32 * j, x);
-    } else if (FMT == DSA_ROWS_Q8) {
-        const uint4 v = ldg_nc_v4(src + 64 * c + 16 * j);
-        x[0] = v.x;
-        x[1] = v.y;
-        x[2] = v.z;
-        x[3] = v.w;
-    } else {
-        ldg_nc_v2(src + 32 * c + 8 * j, x[0], x[1]);
-        x[2] = ldg_nc_u8(src + kQ4Codes + 4 * c + j);
-    }
-}
-// the same as bf16
-template <int FMT>
-__device__ __forceinline__ void widen(int c, uint32_t (&x)[8]) {
-    if (c == kChunks - 1) return;
-    if (FMT == DSA_ROWS_Q8) {
-        const uint32_t w[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) e4m3_to_bf16(w[i], x[2 * i], x[2 * i + 1]);
-    } else {
-        const uint32_t w0 = x[0], w1 = x[1], b = x[2];
-        // (1 + m/4) 2^(a - 6) as bf16: exponent 121 + a, fraction m/4
-        const uint32_t a = b / 3, m = b - 3 * a;
-        const uint32_t s = b < kQ4Scales ? (121 + a) << 7 | m << 5 : 0;
-        q4_to_bf16(w0, s | s << 16, x);
-        q4_to_bf16(w1, s | s << 16, x + 4);
-    }
+    if (p.prefill)
+        atomicAdd(p.sums + key, (unsigned long long)__float2ull_rn(w * p.unit));
+    else
+        atomicAdd(p.acc + (int64_t)I.batch * p.Nmax + key, w);
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
-    key_weights_kernel(const __grid_constant__ CUtensorMap tmap_q, const WeightParams p) {
+// A copy of -lse log2(e) of the item's heads for the calling warp.
+__device__ __forceinline__ void stage_lse(const WeightParams& p, const Item& I, float2* nl, uint32_t lane) {
+    const float* lse = p.lse + (int64_t)I.row * kH + 2 * lane;
+    const float l0 = __ldg(lse), l1 = __ldg(lse + 1);
+    __syncwarp();
+    nl[lane] = make_float2(-kLog2e * l0, -kLog2e * l1);
+    __syncwarp();
+}
+
+__device__ __forceinline__ float2 pair(const uint32_t (&v)[16], int k) {
+    return make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+}
+
+// ------------------------------------------------------------------------------------------------ bf16 rows
+
+namespace wide {
+
+constexpr int kChunks = kQDim / 64;                // 9
+constexpr int kParts = 4;                          // chunks 0 1, 2 3 (first issuer); 4 5, 6 7 8 (second)
+__device__ __forceinline__ constexpr int part_begin(int g) { return 2 * g; }
+__device__ __forceinline__ constexpr int part_end(int g) { return g == kParts - 1 ? kChunks : 2 * g + 2; }
+// warps 0 and 2 MMA, 1 queries, 3 none, 4-11 gather, 12-19 epilogue
+constexpr int kFirstGather = 4, kFirstEpi = 12, kThreads = 32 * (kFirstEpi + kEpiWarps);
+
+constexpr int OFF_Q = 0;
+constexpr int OFF_K = OFF_Q + kChunks * kQBlk;
+constexpr int OFF_LSE = OFF_K + kChunks * kBlk;    // float [8][64], a copy an epilogue warp
+constexpr int OFF_BAR = OFF_LSE + kEpiWarps * kH * 4;
+constexpr int kBars = 4 * kParts + 4;              // full[4], empty[4], q_full[4], q_free[4], acc_full[2], acc_free[2]
+constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
+constexpr int OFF_ABORT = OFF_TMEM + 4;
+constexpr int kSmemBytes = OFF_ABORT + 4;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+constexpr uint32_t kAccCols = 128, kTmemCols = 256;   // the issuers' accumulators of a tile, two tiles
+
+}  // namespace wide
+
+__global__ void __launch_bounds__(wide::kThreads, 1)
+    key_weights_bf16_kernel(const __grid_constant__ CUtensorMap tmap_q, const WeightParams p) {
+    using namespace wide;
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {   // the operands' swizzle counts from 1 KB boundaries
         if (threadIdx.x == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
@@ -184,13 +203,12 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     uint64_t* acc_free = acc_full + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
-    constexpr int kFirstEpi = Roles<FMT>::kFirstEpi, kGroups = Roles<FMT>::kGather / 4;
     const int warp = threadIdx.x / 32;
     const uint32_t lane = lane_id();
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kParts; ++i) {
-            mbar_init(&full[i], FMT == DSA_ROWS_BF16 ? 128 : 4);   // the copies' arrivals, or a warp's
+            mbar_init(&full[i], 128);              // the copies' arrivals, one a lane of four warps
             mbar_init(&empty[i], 1);
             mbar_init(&q_full[i], 1);
             mbar_init(&q_free[i], 1);
@@ -203,7 +221,7 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         fence_mbar_init();
     }
     if (warp == 0) {
-        tmem_alloc(tmem_slot, Acc<FMT>::kAlloc);
+        tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -211,24 +229,7 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     griddep_wait();
-
-    // One lane polls for its warp.
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        bool ok = true;
-        if (lane == 0) ok = mbar_poll(bar, parity, abort_flag, p.status);
-        return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    };
-    // Items with tiles, in the same order for every role: f(item, tiles) until it returns false.
-    auto items = [&](auto f) {
-        for (int s = 0;; ++s) {
-            const int it = nth_item(p, s);
-            if (it == -1) return;
-            if (it < 0) continue;
-            const Item I = item_at(p, it);
-            const int T = item_tiles(p, I, lane);
-            if (T > 0 && !f(I, T)) return;
-        }
-    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_poll(bar, parity, lane, abort_flag, p.status); };
 
     // Chunk c of every tile lies in slot c; the slots' barriers are in the phase of the tile, gt, the query's of the item, qi.
     if (warp == 0 || warp == 2) {
@@ -238,9 +239,9 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
         const int g0 = warp;                       // the issuer's parts g0, g0 + 1
         int gt = 0, qi = 0;
         const uint32_t base = (smem_u32(smem) >> 4) | ((16u >> 4) << 16);
-        items([&](const Item&, int T) {
+        for_items(p, lane, [&](const Item&, int T) {
             for (int t = 0; t < T; ++t, ++gt) {
-                const uint32_t acc = tmem_base + Acc<FMT>::kCols * (gt & 1), d = acc + (g0 ? 64 : 0);
+                const uint32_t d = tmem_base + kAccCols * (gt & 1) + (g0 ? 64 : 0);
                 uint64_t* mine = lane < 2 ? &full[g0 + lane] : lane < 4 ? &q_full[g0 + lane - 2] : &acc_free[gt & 1];
                 const uint32_t parity = lane < 2 ? gt & 1 : lane < 4 ? qi & 1 : ((gt >> 1) & 1) ^ 1;
                 uint32_t got = 0;
@@ -256,14 +257,12 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
                     }
                     if (lane == 0) {
                         const int g = g0 + h;
-                        for (int c = part_begin(g); c < part_end(g); ++c) {
-                            const bool rope = FMT != DSA_ROWS_BF16 && c == kChunks - 1;
-                            const bool first = c == part_begin(g0) || rope;
+                        for (int c = part_begin(g); c < part_end(g); ++c)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_bf16_ss_lo(rope ? acc + 128 : d, base + ((OFF_K + c * kBlk) >> 4) + 2 * k, kDescHi,
-                                               base + ((OFF_Q + c * kQBlk) >> 4) + 2 * k, kDescHi, IDESC, first && k == 0 ? 0u : 1u);
-                        }
+                                mma_bf16_ss_lo(d, base + ((OFF_K + c * kBlk) >> 4) + 2 * k, kDescHi,
+                                               base + ((OFF_Q + c * kQBlk) >> 4) + 2 * k, kDescHi, IDESC_BF16,
+                                               c == part_begin(g0) && k == 0 ? 0u : 1u);
                         mma_commit(&empty[g]);
                         if (t == T - 1) mma_commit(&q_free[g]);
                     }
@@ -278,129 +277,80 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ queries (TMA)
         int qi = 0;
-        items([&](const Item& I, int) {
+        for_items(p, lane, [&](const Item& I, int) {
             for (int g = 0; g < kParts; ++g) {
                 if (!wait(&q_free[g], (qi & 1) ^ 1)) return false;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&q_full[g], (part_end(g) - part_begin(g)) * kQBlk);
                     for (int c = part_begin(g); c < part_end(g); ++c)
-                        tma_load_2d(smem + OFF_Q + c * kQBlk, &tmap_q, &q_full[g], c * kDims, I.row * kH);
+                        tma_load_2d(smem + OFF_Q + c * kQBlk, &tmap_q, &q_full[g], 64 * c, I.row * kH);
                 }
                 __syncwarp();
             }
             ++qi;
             return true;
         });
-    } else if (warp >= 4 && warp < kFirstEpi) {
-        // ------------------------------------------------------------ gather
-        // Four warps, 32 rows each, fill a chunk: bf16 rows eight lanes a row, 16 bytes each, two sets of warps with two
-        // parts each; the others four lanes a row, 16 dims each, a set a part.
-        constexpr int kLanes = FMT == DSA_ROWS_BF16 ? 8 : 4, kRows = kLanes;
-        constexpr int kOwn = kParts / kGroups;
-        const int quad = warp & 3, g0 = ((warp - 4) >> 2) * kOwn;
-        const int j = (int)lane % kLanes, r0 = quad * 32 + (int)lane / kLanes;   // rows r0 + 32 / kLanes * i
-        int gt = 0;
-        items([&](const Item& I, int T) {
-            const int32_t* idx = p.idx + (int64_t)I.row * p.top_k;
-            for (int t = 0; t < T; ++t, ++gt) {
-                int row[kRows];
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    const int slot = I.slot0 + t * kTile + r0 + 32 / kLanes * i;
-                    row[i] = slot < I.slot_end ? __ldg(idx + slot) : -1;
-                }
-#pragma unroll
-                for (int i = 0; i < kRows; ++i) row[i] = (int)key_row(p, I, row[i]);
-                if constexpr (FMT == DSA_ROWS_BF16) {
+    } else if (warp >= kFirstGather && warp < kFirstEpi) {
+        // ------------------------------------------------------------ gather: two sets of four warps, two parts each
+        const int quad = warp & 3, g0 = (warp - kFirstGather) >> 2 << 1;
+        const int j = (int)lane & 7, r0 = quad * 32 + (int)(lane >> 3);
+        Feed<8> feed;
+        int row[8], next[8];
+        bool has = feed.fetch(p, lane, r0, 4), more = has;
+        if (has) {
+            feed.resolve(p, row);
+            more = feed.fetch(p, lane, r0, 4);
+        }
+        for (int gt = 0; has; ++gt) {
+            if (more) feed.resolve(p, next);
+            has = more;
+            more = more && feed.fetch(p, lane, r0, 4);
+            bool ok = true;
 #pragma unroll 1
-                    for (int g = g0; g < g0 + kOwn; ++g) {
-                        if (!wait(&empty[g], (gt & 1) ^ 1)) return false;
-                        for (int c = part_begin(g); c < part_end(g); ++c) {
-                            const uint32_t dst = smem_u32(smem + OFF_K) + c * kBlk + r0 * 128;
-#pragma unroll
-                            for (int i = 0; i < kRows; ++i) {
-                                const uint8_t* src = p.cache + (int64_t)max(row[i], 0) * Row<FMT>::kBytes + 128 * c + 16 * j;
-                                cp_async_16(dst + i * 512 + ((j ^ ((r0 + 4 * i) & 7)) << 4), src, row[i] >= 0 ? 16u : 0u);
-                            }
-                        }
-                        cp_async_arrive_noinc(&full[g]);
-                    }
-                } else {
-                    uint32_t x[kRows][8];
-                    const int g = g0, r = (int)lane / kLanes;   // row % 8
-                    for (int c = part_begin(g); c < part_end(g); ++c) {
-#pragma unroll
-                        for (int i = 0; i < kRows; ++i) load_dims<FMT>(p, row[i], c, j, x[i]);
-                        if (c == part_begin(g) && !wait(&empty[g], (gt & 1) ^ 1)) return false;
-                        uint8_t* dst = smem + OFF_K + c * kBlk + r0 * 128;
-#pragma unroll
-                        for (int i = 0; i < kRows; ++i) {
-                            widen<FMT>(c, x[i]);
-                            *reinterpret_cast<uint4*>(dst + i * 1024 + (((2 * j) ^ r) << 4)) = make_uint4(x[i][0], x[i][1], x[i][2], x[i][3]);
-                            *reinterpret_cast<uint4*>(dst + i * 1024 + (((2 * j + 1) ^ r) << 4)) = make_uint4(x[i][4], x[i][5], x[i][6], x[i][7]);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[g]);
-                }
+            for (int g = g0; ok && g < g0 + 2; ++g) {
+                if (!(ok = wait(&empty[g], (gt & 1) ^ 1))) break;
+                for (int c = part_begin(g); c < part_end(g); ++c)
+                    copy_rows(p, row, 2 * kQDim, 128 * c, smem_u32(smem) + OFF_K + c * kBlk, r0, j);
+                cp_async_arrive_noinc(&full[g]);
             }
-            return true;
-        });
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) row[i] = next[i];
+        }
         cp_async_wait_all();
     } else if (warp >= kFirstEpi) {
         // ------------------------------------------------------------ epilogue
         const int quad = warp & 3, set = (warp - kFirstEpi) >> 2;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         float2* nl = reinterpret_cast<float2*>(smem + OFF_LSE) + (warp - kFirstEpi) * (kH / 2);
+        const float2 sc = make_float2(p.scale_log2, p.scale_log2);
         int gt = 0;
-        items([&](const Item& I, int T) {
-            const float* lse = p.lse + (int64_t)I.row * kH + 2 * lane;
-            const float l0 = __ldg(lse), l1 = __ldg(lse + 1);
-            __syncwarp();
-            nl[lane] = make_float2(-1.4426950408889634f * l0, -1.4426950408889634f * l1);
-            __syncwarp();
+        for_items(p, lane, [&](const Item& I, int T) {
+            stage_lse(p, I, nl, lane);
             for (int t = 0; t < T; ++t, ++gt) {
                 if ((gt & 1) != set) continue;
-                const int slot = I.slot0 + t * kTile + quad * 32 + (int)lane;
-                const int key = slot < I.slot_end ? __ldg(p.idx + (int64_t)I.row * p.top_k + slot) : -1;
-                const int64_t row = key_row(p, I, key);
+                const int key = key_at(p, I, I.slot0 + t * kTile + quad * 32 + (int)lane), row = key_row(p, I, key);
                 if (key >= 0 && row < 0) raise_dev_error(p.status, DEV_ERR_BOUNDS);
-                float c = 1.f;
-                if (FMT != DSA_ROWS_BF16 && row >= 0) c = __ldg(p.cache_scale + row);
-                const float2 sc = make_float2(p.scale_log2 * c, p.scale_log2 * c), sr = make_float2(p.scale_log2, p.scale_log2);
                 if (!wait(&acc_full[gt & 1], (gt >> 1) & 1)) return false;
                 tc_fence_after();
-                const uint32_t d = tmem_base + lane_addr + Acc<FMT>::kCols * (gt & 1);
+                const uint32_t d = tmem_base + lane_addr + kAccCols * (gt & 1);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int h = 0; h < kH; h += 16) {
-                    uint32_t u[16], v[16], r[16];
+                    uint32_t u[16], v[16];
                     tmem_ld16(d + h, u);
                     tmem_ld16(d + 64 + h, v);
-                    if (FMT != DSA_ROWS_BF16) tmem_ld16(d + 128 + h, r);
                     tmem_ld_wait();
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        float2 x = nl[h / 2 + k];
-                        if (FMT != DSA_ROWS_BF16)
-                            x = __ffma2_rn(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), sr, x);
-                        x = __ffma2_rn(make_float2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1])), sc, x);
-                        x = __ffma2_rn(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), sc, x);
+                        const float2 x = __ffma2_rn(__fadd2_rn(pair(u, k), pair(v, k)), sc, nl[h / 2 + k]);
                         sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_free[gt & 1]);
-                const float s = sum.x + sum.y;
-                const float w = s > 0.f ? fminf(s, kMostWeight) : 0.f;   // NaN: 0
-                if (row >= 0) {
-                    if (p.prefill)
-                        atomicAdd(p.sums + key, (unsigned long long)__float2ull_rn(w * p.unit));
-                    else
-                        atomicAdd(p.acc + (int64_t)I.batch * p.Nmax + key, w);
-                }
+                add_weight(p, I, key, row, sum);
             }
             return true;
         });
@@ -410,7 +360,339 @@ __global__ void __launch_bounds__(Roles<FMT>::kThreads, 1)
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, Acc<FMT>::kAlloc);
+        tmem_dealloc(tmem_base, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------ 8-bit and 4-bit rows
+
+namespace low {
+
+constexpr int kChunks = 5;                         // four of 128 latent dims, the rope dims
+constexpr int kSlots = 9;                          // chunk n of the CTA lies in slot n % 9
+constexpr int kQueryWarps = 8;                     // eight heads each
+// warps 0 and 2 MMA, 1 and 3 none, 4-11 gather, 12-19 queries, 20-27 epilogue
+constexpr int kFirstGather = 4, kFirstQuery = 12, kFirstEpi = kFirstQuery + kQueryWarps;
+constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+// registers by warpgroups of what the launch holds
+constexpr int kLaunchRegs = 72, kIssueRegs = 56, kGatherRegs = 72, kQueryRegs = 88, kEpiRegs = 64;
+static_assert(32 * (4 * kIssueRegs + 8 * kGatherRegs + 8 * kQueryRegs + 8 * kEpiRegs) <= kThreads * kLaunchRegs, "registers of the CTA");
+
+constexpr int OFF_QHL = 0;                         // 4 chunks x (64 hi rows, 64 lo rows) x 128 B
+constexpr int OFF_QR = OFF_QHL + 4 * kBlk;         // rope dims of 64 heads, bf16
+constexpr int OFF_K = OFF_QR + kQBlk;
+constexpr int OFF_LSE = OFF_K + kSlots * kBlk;     // float [8][64], a copy an epilogue warp
+constexpr int OFF_QS = OFF_LSE + kEpiWarps * kH * 4;   // float [4][64]: scale log2(e) 2^k of a query's heads
+constexpr int OFF_TABLE = OFF_QS + 4 * kH * 4;     // uint2 [256]: the magnitudes of 4-bit codes as e4m3, by block byte
+constexpr int OFF_BAR = OFF_TABLE + 256 * 8;
+constexpr int kBars = 2 * kSlots + 3 + 4;          // full[9], empty[9], q_full, qr_full, q_free, acc_full[2], acc_free[2]
+constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
+constexpr int OFF_ABORT = OFF_TMEM + 4;
+constexpr int kSmemBytes = OFF_ABORT + 4;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+constexpr uint32_t kAccCols = 192, kTmemCols = 512;   // 64 hi, 64 lo, 64 rope of a tile, two tiles
+
+}  // namespace low
+
+template <bool Q4>
+__global__ void __launch_bounds__(low::kThreads, 1)
+    key_weights_e4m3_kernel(const __grid_constant__ CUtensorMap tmap_q, const WeightParams p) {
+    using namespace low;
+    constexpr int kBytes = Q4 ? kQ4Row : kQ8Row;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {   // the operands' swizzle counts from 1 KB boundaries
+        if (threadIdx.x == 0) raise_dev_error(p.status, DEV_ERR_TIMEOUT);
+        return;
+    }
+    float* qs_s = reinterpret_cast<float*>(smem + OFF_QS);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+    uint64_t* empty = full + kSlots;
+    uint64_t* q_full = empty + kSlots;
+    uint64_t* qr_full = q_full + 1;
+    uint64_t* q_free = q_full + 2;
+    uint64_t* acc_full = q_full + 3;
+    uint64_t* acc_free = acc_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_ABORT);
+    const int warp = threadIdx.x / 32;
+    const uint32_t lane = lane_id();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&full[i], 128);              // one arrival a lane of four warps: the copies', or its own
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(q_full, kQueryWarps);
+        mbar_init(qr_full, 1);
+        mbar_init(q_free, 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_free[i], 4);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(tmem_slot, kTmemCols);
+        tmem_relinquish();
+    }
+    if (Q4 && threadIdx.x < 256)
+        reinterpret_cast<uint2*>(smem + OFF_TABLE)[threadIdx.x] =
+            threadIdx.x < kQ4Scales ? q4_table(q4_block_scale(threadIdx.x)) : make_uint2(0, 0);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    griddep_wait();
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_poll(bar, parity, lane, abort_flag, p.status); };
+
+    if (warp < kFirstGather) setmaxnreg_dec<kIssueRegs>();
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------------------------------ MMA issuers, tiles in turn
+        // One look at all barriers: lanes 0-4 the chunks, 5 the query, 6 its rope dims, 7 the accumulator.
+        const int mine_of = warp >> 1;
+        int gt = 0, qi = 0;
+        const uint32_t base = (smem_u32(smem) >> 4) | ((16u >> 4) << 16);
+        for_items(p, lane, [&](const Item&, int T) {
+            bool used = false;
+            for (int t = 0; t < T; ++t, ++gt) {
+                if ((gt & 1) != mine_of) continue;
+                used = true;
+                const int n = kChunks * gt, at = n + (int)lane;
+                const uint32_t d = tmem_base + kAccCols * (gt & 1);
+                uint64_t* mine = lane < kChunks ? &full[at % kSlots] : lane == 5 ? q_full : lane == 6 ? qr_full : &acc_free[gt & 1];
+                const uint32_t parity = lane < kChunks ? at / kSlots & 1 : lane < 7 ? qi & 1 : ((gt >> 1) & 1) ^ 1;
+                uint32_t got = 0;
+                for (int c = 0; c < kChunks; ++c) {
+                    const uint32_t need = 0xe0u | 1u << c;
+                    if ((got & need) != need) {
+                        got = mbar_poll_warp(mine, parity, lane, 8, need, abort_flag, p.status);
+                        if (got == 0) return false;
+                        fence_proxy_async_smem();  // of every lane that saw a barrier, before the lane that issues
+                        tc_fence_after();
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        const int slot = (n + c) % kSlots;
+                        const uint32_t a = base + ((OFF_K + slot * kBlk) >> 4);
+                        if (c < 4) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)   // 32 dims a step
+                                mma_e4m3_ss_lo(d, a + 2 * k, kDescHi, base + ((OFF_QHL + c * kBlk) >> 4) + 2 * k, kDescHi,
+                                               IDESC_E4M3, (c | k) ? 1u : 0u);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)   // 16 dims a step
+                                mma_bf16_ss_lo(d + 128, a + 2 * k, kDescHi, base + (OFF_QR >> 4) + 2 * k, kDescHi, IDESC_BF16,
+                                               k ? 1u : 0u);
+                        }
+                        mma_commit(&empty[slot]);
+                    }
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    mma_commit(&acc_full[gt & 1]);
+                    if (t >= T - 2) mma_commit(q_free);   // the issuer's last tile of the item
+                }
+                __syncwarp();
+            }
+            if (!used) {                           // an item of one tile, the other's: no arrival ahead of its phase
+                if (!wait(q_full, qi & 1)) return false;
+                if (lane == 0) mbar_arrive(q_free);
+                __syncwarp();
+            }
+            ++qi;
+            return true;
+        });
+    } else if (warp >= kFirstGather && warp < kFirstQuery) {
+        // ------------------------------------------------------------ gather: two sets of four warps
+        // 8-bit rows: the sets copy every other chunk, eight lanes a row.  4-bit rows: the first expands chunks 0 and 2, the
+        // second 1 and 3, a lane its own row.
+        setmaxnreg_dec<kGatherRegs>();
+        const int quad = warp & 3, set = (warp - kFirstGather) >> 2;
+        const uint32_t ring = smem_u32(smem) + OFF_K;
+        int n = 0;                                 // the tile's first chunk
+        auto free = [&](int c) { return wait(&empty[(n + c) % kSlots], ((n + c) / kSlots & 1) ^ 1); };
+        if constexpr (!Q4) {
+            const int j = (int)lane & 7, r0 = quad * 32 + (int)(lane >> 3);
+            Feed<8> feed;
+            int row[8], next[8];
+            bool has = feed.fetch(p, lane, r0, 4), more = has;
+            if (has) {
+                feed.resolve(p, row);
+                more = feed.fetch(p, lane, r0, 4);
+            }
+            for (; has; n += kChunks) {
+                if (more) feed.resolve(p, next);
+                has = more;
+                more = more && feed.fetch(p, lane, r0, 4);
+                bool ok = true;
+#pragma unroll 1
+                for (int c = (n ^ set) & 1; c < kChunks; c += 2) {   // the rope dims follow the latent dims, 128 bytes too
+                    if (!(ok = free(c))) break;
+                    copy_rows(p, row, kBytes, 128 * c, ring + (n + c) % kSlots * kBlk, r0, j);
+                    cp_async_arrive_noinc(&full[(n + c) % kSlots]);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) row[i] = next[i];
+            }
+        } else {
+            const int r = quad * 32 + (int)lane;   // the lane's row of a tile
+            const uint32_t table = smem_u32(smem) + OFF_TABLE;
+            Feed<1> feed;
+            int row[1], next[1];
+            uint32_t x[2][16], b[2][2];
+            auto load = [&] {                      // both chunks' codes, ahead of the waits for their places
+                const uint8_t* src = p.cache + (int64_t)max(row[0], 0) * kBytes;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = set + 2 * h;
+                    ldg_nc_v8(src + 64 * c, x[h]);
+                    ldg_nc_v8(src + 64 * c + 32, x[h] + 8);
+                    ldg_nc_v2(src + kQ4Codes + 8 * c, b[h][0], b[h][1]);
+                }
+            };
+            bool has = feed.fetch(p, lane, r, 0), more = has;
+            if (has) {
+                feed.resolve(p, row);
+                load();
+                more = feed.fetch(p, lane, r, 0);
+            }
+            for (; has; n += kChunks) {
+                if (more) feed.resolve(p, next);
+                has = more;
+                more = more && feed.fetch(p, lane, r, 0);
+                bool ok = true;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = set + 2 * h;
+                    if (!(ok = ok && free(c))) break;
+                    if (row[0] < 0) b[h][0] = b[h][1] = 0xffffffffu;   // zeros
+                    const uint32_t dst = ring + (n + c) % kSlots * kBlk + r * 128 + ((r & 7) << 4);
+                    uint2 tb = lds_v2(table + 8 * (b[h][0] & 0xff));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {  // a table's load is ahead of the store before it
+                        uint2 ahead = tb;
+                        if (i < 7) ahead = lds_v2(table + 8 * __byte_perm(b[h][(i + 1) >> 2], 0, 0x4440 + ((i + 1) & 3)));
+                        const uint2 u = q4_expand(x[h][2 * i], tb), v = q4_expand(x[h][2 * i + 1], tb);
+                        sts_v4(dst ^ (i << 4), u.x, u.y, v.x, v.y);
+                        tb = ahead;
+                    }
+                    fence_proxy_async_smem();
+                    mbar_arrive(&full[(n + c) % kSlots]);
+                }
+                if (ok && ((n ^ set) & 1) == 0) {  // the rope dims by the sets in turn
+                    if ((ok = free(4))) {
+                        const uint8_t* src = p.cache + (int64_t)max(row[0], 0) * kBytes + kQ4Rope;
+                        const uint32_t dst = ring + (n + 4) % kSlots * kBlk + r * 128 + ((r & 7) << 4);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) cp_async_16(dst ^ (i << 4), src + 16 * i, row[0] >= 0 ? 16u : 0u);
+                        cp_async_arrive_noinc(&full[(n + 4) % kSlots]);
+                    }
+                }
+                if (!ok) break;
+                row[0] = next[0];
+                if (has) load();
+            }
+        }
+        cp_async_wait_all();
+    } else if (warp >= kFirstQuery && warp < kFirstEpi) {
+        // ------------------------------------------------------------ queries
+        // Eight heads a warp, dims 16 l .. 16 l + 15 a lane, in registers before their place comes free.
+        setmaxnreg_inc<kQueryRegs>();
+        constexpr int kOwn = kH / kQueryWarps;
+        const int h0 = (warp - kFirstQuery) * kOwn;
+        int qi = 0;
+        for_items(p, lane, [&](const Item& I, int) {
+            const __nv_bfloat16* src = p.q + ((int64_t)I.row * kH + h0) * kQDim + 16 * lane;
+            uint4 a[kOwn], b[kOwn];
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                a[i] = ldg_nc_v4(src + i * kQDim);
+                b[i] = ldg_nc_v4(src + i * kQDim + 8);
+            }
+            if (!wait(q_free, (qi & 1) ^ 1)) return false;
+            if (warp == kFirstQuery && lane == 0) {
+                mbar_arrive_expect_tx(qr_full, kQBlk);
+                tma_load_2d(smem + OFF_QR, &tmap_q, qr_full, kQ8Latent, I.row * kH);
+            }
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                const int h = h0 + i;
+                const uint32_t w[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
+                float amax = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+                // magnitudes compare as their bit patterns do
+                const int e = e4m3_scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
+                const float inv = exp2_int(-e);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    split_e4m3x4(bf16_lo(w[2 * k]) * inv, bf16_hi(w[2 * k]) * inv, bf16_lo(w[2 * k + 1]) * inv,
+                                 bf16_hi(w[2 * k + 1]) * inv, hi[k], lo[k]);
+                uint8_t* d = smem + OFF_QHL + (int)(lane >> 3) * kBlk + h * 128 + (((int)(lane & 7) ^ (h & 7)) << 4);
+                *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(d + kH * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (lane == 0) qs_s[(qi & 3) * kH + h] = p.scale_log2 * exp2_int(e);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            ++qi;
+            return true;
+        });
+    } else if (warp >= kFirstEpi) {
+        // ------------------------------------------------------------ epilogue
+        setmaxnreg_dec<kEpiRegs>();
+        const int quad = warp & 3, set = (warp - kFirstEpi) >> 2;
+        const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+        float2* nl = reinterpret_cast<float2*>(smem + OFF_LSE) + (warp - kFirstEpi) * (kH / 2);
+        const float2 sr = make_float2(p.scale_log2, p.scale_log2), sixteenth = make_float2(0.0625f, 0.0625f);
+        int gt = 0, qi = 0;
+        for_items(p, lane, [&](const Item& I, int T) {
+            stage_lse(p, I, nl, lane);
+            const float2* qs = reinterpret_cast<const float2*>(qs_s + (qi & 3) * kH);
+            for (int t = 0; t < T; ++t, ++gt) {
+                if ((gt & 1) != set) continue;
+                const int key = key_at(p, I, I.slot0 + t * kTile + quad * 32 + (int)lane), row = key_row(p, I, key);
+                if (key >= 0 && row < 0) raise_dev_error(p.status, DEV_ERR_BOUNDS);
+                const float c = row >= 0 ? __ldg(p.cache_scale + row) : 0.f;
+                if (!wait(&acc_full[gt & 1], (gt >> 1) & 1)) return false;
+                tc_fence_after();
+                const uint32_t d = tmem_base + lane_addr + kAccCols * (gt & 1);
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int h = 0; h < kH; h += 16) {
+                    uint32_t hi[16], lo[16], ro[16];
+                    tmem_ld16(d + h, hi);
+                    tmem_ld16(d + 64 + h, lo);
+                    tmem_ld16(d + 128 + h, ro);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float2 x = __ffma2_rn(__ffma2_rn(pair(lo, k), sixteenth, pair(hi, k)),
+                                                    __fmul2_rn(qs[h / 2 + k], make_float2(c, c)),
+                                                    __ffma2_rn(pair(ro, k), sr, nl[h / 2 + k]));
+                        sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_free[gt & 1]);
+                add_weight(p, I, key, row, sum);
+            }
+            ++qi;
+            return true;
+        });
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, kTmemCols);
     }
 }
 
@@ -424,31 +706,32 @@ __global__ void __launch_bounds__(256)
     acc[j] = accumulate ? acc[j] + w : w;
 }
 
-template <int FMT>
+using Kernel = void (*)(const CUtensorMap, const WeightParams);
+
+template <Kernel KERNEL, int THREADS, int SMEM>
 dsa_status_t launch(const WeightParams& p, cudaStream_t stream) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> done[kMaxDevices];
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return DSA_ERR_CUDA;
     if (!done[dev].load(std::memory_order_acquire)) {
-        const dsa_status_t st = ensure_smem_attr(reinterpret_cast<const void*>(key_weights_kernel<FMT>), kSmemBytes);
+        const dsa_status_t st = ensure_smem_attr(reinterpret_cast<const void*>(KERNEL), SMEM);
         if (st != DSA_OK) return st;
         done[dev].store(true, std::memory_order_release);
     }
     CUtensorMap tq;
-    const dsa_status_t st = make_tmap_bf16_2d(&tq, p.q, kQDim, (uint64_t)p.rows * kH, kQDim * 2, kDims, kH);
+    const dsa_status_t st = make_tmap_bf16_2d(&tq, p.q, kQDim, (uint64_t)p.rows * kH, kQDim * 2, 64, kH);
     if (st != DSA_OK) return st;
     const int sms = device_sm_count();
-    if (launch_pdl(key_weights_kernel<FMT>, dim3(p.n_items < sms ? p.n_items : sms), dim3(Roles<FMT>::kThreads), kSmemBytes,
-                   stream, tq, p) != cudaSuccess)
+    if (launch_pdl(KERNEL, dim3(p.n_items < sms ? p.n_items : sms), dim3(THREADS), SMEM, stream, tq, p) != cudaSuccess)
         return DSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 dsa_status_t launch_format(int format, const WeightParams& p, cudaStream_t stream) {
-    return format == DSA_ROWS_BF16 ? launch<DSA_ROWS_BF16>(p, stream)
-           : format == DSA_ROWS_Q8 ? launch<DSA_ROWS_Q8>(p, stream)
-                                   : launch<DSA_ROWS_Q4>(p, stream);
+    return format == DSA_ROWS_BF16 ? launch<key_weights_bf16_kernel, wide::kThreads, wide::kSmemBytes>(p, stream)
+           : format == DSA_ROWS_Q8 ? launch<key_weights_e4m3_kernel<false>, low::kThreads, low::kSmemBytes>(p, stream)
+                                   : launch<key_weights_e4m3_kernel<true>, low::kThreads, low::kSmemBytes>(p, stream);
 }
 
 // Parts of a query's tiles: whole queries where they fill the SMs, else so many parts that the items do.
@@ -473,7 +756,7 @@ WeightParams base_params(const void* q, const void* cache, const float* cache_sc
     p.cache = static_cast<const uint8_t*>(cache);
     p.cache_scale = cache_scale;
     p.lse = lse;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    p.scale_log2 = scale * kLog2e;
     p.status = device_status_ptr();
     p.pages = pages;
     return p;

@@ -189,28 +189,6 @@ __device__ __forceinline__ float lg2_approx(float x) {
     return y;
 }
 
-// Four values as hi + lo / 16 in e4m3 (|x| <= 448): the four hi bytes, the four lo bytes.  The half-precision step
-// between keeps 11 bits, the difference x - hi is exact.
-__device__ __forceinline__ void split_e4m3x4(float x, float y, float z, float w, uint32_t& hi, uint32_t& lo) {
-    asm("{\n\t.reg .b32 a, b, p, q;\n\t.reg .b16 s, t;\n\t"
-        "cvt.rn.f16x2.f32 a, %3, %2;\n\t"
-        "cvt.rn.f16x2.f32 b, %5, %4;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 s, a;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 t, b;\n\t"
-        "mov.b32 %0, {s, t};\n\t"
-        "cvt.rn.f16x2.e4m3x2 p, s;\n\t"
-        "cvt.rn.f16x2.e4m3x2 q, t;\n\t"
-        "sub.rn.f16x2 a, a, p;\n\t"
-        "sub.rn.f16x2 b, b, q;\n\t"
-        "mul.rn.f16x2 a, a, %6;\n\t"
-        "mul.rn.f16x2 b, b, %6;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 s, a;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 t, b;\n\t"
-        "mov.b32 %1, {s, t};\n\t}\n"
-        : "=&r"(hi), "=&r"(lo)
-        : "f"(x), "f"(y), "f"(z), "f"(w), "r"(0x4c004c00u));   // 16, twice
-}
-
 // The rows of this CTA's tiles, tile after tile, one a lane (row `base` of a tile), in two steps so that the
 // loads of one are in flight while the caller works: fetch() loads the selected key of the next tile,
 // resolve() turns it into a cache row (a page lookup when paged).
