@@ -24,6 +24,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "dsa_q4.cuh"
 #include "mla_attn_common.cuh"
@@ -123,22 +124,33 @@ struct Feed {
     }
 };
 
-// One lane polls for its warp.
+// All lanes look once; where the phase has not come, one lane polls for its warp.
 __device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, uint32_t lane, volatile int* abort, int32_t* status) {
+    if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
     bool ok = true;
     if (lane == 0) ok = mbar_poll(bar, parity, abort, status);
     return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
-// 128 bytes of each of the lane's rows (r0 + 4 i of the tile, eight lanes a row, this lane's 16 bytes the j-th) to a slot;
-// zeros for a row that is not there.
-__device__ __forceinline__ void copy_rows(const WeightParams& p, const int (&row)[8], int bytes, int at, uint32_t slot, int r0, int j) {
+__device__ __align__(16) uint8_t g_no_row[2 * kQDim];   // zeros, the row of a key that is not there
+
+// 128 bytes of each of the lane's rows (r0 + 4 i of the tile, eight lanes a row, this lane's 16 bytes the j-th: src) to a
+// slot.  One instruction a row: the gathering warps' instructions are what a tile of bf16 or 8-bit rows waits for.
+struct RowCopy {
+    const uint8_t* src[8];
+    uint32_t even, odd;                            // offsets in a slot of the rows of even and of odd i, less 512 i
+
+    __device__ __forceinline__ RowCopy(int r0, int j)
+        : even(r0 * 128 + ((j ^ (r0 & 7)) << 4)), odd(r0 * 128 + ((j ^ (r0 & 7) ^ 4) << 4)) {}
+    __device__ __forceinline__ void point(const WeightParams& p, const int (&row)[8], int bytes, int j) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint8_t* src = p.cache + (int64_t)max(row[i], 0) * bytes + at + 16 * j;
-        cp_async_16(slot + r0 * 128 + i * 512 + ((j ^ ((r0 + 4 * i) & 7)) << 4), src, row[i] >= 0 ? 16u : 0u);
+        for (int i = 0; i < 8; ++i) src[i] = (row[i] < 0 ? g_no_row : p.cache + (int64_t)row[i] * bytes) + 16 * j;
     }
-}
+    __device__ __forceinline__ void copy(int at, uint32_t slot) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) cp_async_16(slot + ((i & 1) ? odd : even) + i * 512, src[i] + at);
+    }
+};
 
 __device__ __forceinline__ void add_weight(const WeightParams& p, const Item& I, int key, int row, float2 sum) {
     const float s = sum.x + sum.y;
@@ -294,28 +306,37 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
         // ------------------------------------------------------------ gather: two sets of four warps, two parts each
         const int quad = warp & 3, g0 = (warp - kFirstGather) >> 2 << 1;
         const int j = (int)lane & 7, r0 = quad * 32 + (int)(lane >> 3);
+        const uint32_t keys = smem_u32(smem) + OFF_K;
         Feed<8> feed;
-        int row[8], next[8];
+        RowCopy rows(r0, j);
+        int row[8];
         bool has = feed.fetch(p, lane, r0, 4), more = has;
         if (has) {
             feed.resolve(p, row);
             more = feed.fetch(p, lane, r0, 4);
         }
         for (int gt = 0; has; ++gt) {
-            if (more) feed.resolve(p, next);
+            rows.point(p, row, 2 * kQDim, j);
+            if (more) feed.resolve(p, row);
             has = more;
             more = more && feed.fetch(p, lane, r0, 4);
             bool ok = true;
-#pragma unroll 1
-            for (int g = g0; ok && g < g0 + 2; ++g) {
-                if (!(ok = wait(&empty[g], (gt & 1) ^ 1))) break;
-                for (int c = part_begin(g); c < part_end(g); ++c)
-                    copy_rows(p, row, 2 * kQDim, 128 * c, smem_u32(smem) + OFF_K + c * kBlk, r0, j);
+            auto part = [&](auto which) {          // the chunks as constants: offsets in the instructions
+                constexpr int g = decltype(which)::value;
+                ok = ok && wait(&empty[g], (gt & 1) ^ 1);
+                if (!ok) return;
+#pragma unroll
+                for (int c = part_begin(g); c < part_end(g); ++c) rows.copy(128 * c, keys + c * kBlk);
                 cp_async_arrive_noinc(&full[g]);
+            };
+            if (g0 == 0) {
+                part(std::integral_constant<int, 0>{});
+                part(std::integral_constant<int, 1>{});
+            } else {
+                part(std::integral_constant<int, 2>{});
+                part(std::integral_constant<int, 3>{});
             }
             if (!ok) break;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) row[i] = next[i];
         }
         cp_async_wait_all();
     } else if (warp >= kFirstEpi) {
@@ -462,19 +483,22 @@ __global__ void __launch_bounds__(low::kThreads, 1)
                 const uint32_t d = tmem_base + kAccCols * (gt & 1);
                 uint64_t* mine = lane < kChunks ? &full[at % kSlots] : lane == 5 ? q_full : lane == 6 ? qr_full : &acc_free[gt & 1];
                 const uint32_t parity = lane < kChunks ? at / kSlots & 1 : lane < 7 ? qi & 1 : ((gt >> 1) & 1) ^ 1;
+                const int slot0 = n % kSlots;
                 uint32_t got = 0;
+                bool ok = true;
+#pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     const uint32_t need = 0xe0u | 1u << c;
-                    if ((got & need) != need) {
+                    if (ok && (got & need) != need) {
                         got = mbar_poll_warp(mine, parity, lane, 8, need, abort_flag, p.status);
-                        if (got == 0) return false;
+                        ok = got != 0;
                         fence_proxy_async_smem();  // of every lane that saw a barrier, before the lane that issues
                         tc_fence_after();
                         __syncwarp();
                     }
-                    if (lane == 0) {
-                        const int slot = (n + c) % kSlots;
-                        const uint32_t a = base + ((OFF_K + slot * kBlk) >> 4);
+                    if (lane == 0 && ok) {
+                        const int slot = slot0 + c - (slot0 + c >= kSlots ? kSlots : 0);
+                        const uint32_t a = base + (OFF_K >> 4) + slot * (kBlk >> 4);
                         if (c < 4) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k)   // 32 dims a step
@@ -490,6 +514,7 @@ __global__ void __launch_bounds__(low::kThreads, 1)
                     }
                     __syncwarp();
                 }
+                if (!ok) return false;
                 if (lane == 0) {
                     mma_commit(&acc_full[gt & 1]);
                     if (t >= T - 2) mma_commit(q_free);   // the issuer's last tile of the item
@@ -516,26 +541,27 @@ __global__ void __launch_bounds__(low::kThreads, 1)
         if constexpr (!Q4) {
             const int j = (int)lane & 7, r0 = quad * 32 + (int)(lane >> 3);
             Feed<8> feed;
-            int row[8], next[8];
+            RowCopy rows(r0, j);
+            int row[8];
             bool has = feed.fetch(p, lane, r0, 4), more = has;
             if (has) {
                 feed.resolve(p, row);
                 more = feed.fetch(p, lane, r0, 4);
             }
             for (; has; n += kChunks) {
-                if (more) feed.resolve(p, next);
+                rows.point(p, row, kBytes, j);
+                if (more) feed.resolve(p, row);
                 has = more;
                 more = more && feed.fetch(p, lane, r0, 4);
                 bool ok = true;
-#pragma unroll 1
-                for (int c = (n ^ set) & 1; c < kChunks; c += 2) {   // the rope dims follow the latent dims, 128 bytes too
-                    if (!(ok = free(c))) break;
-                    copy_rows(p, row, kBytes, 128 * c, ring + (n + c) % kSlots * kBlk, r0, j);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {   // the rope dims follow the latent dims, 128 bytes too
+                    if (((n + c) & 1) != set) continue;
+                    if (!(ok = ok && free(c))) break;
+                    rows.copy(128 * c, ring + (n + c) % kSlots * kBlk);
                     cp_async_arrive_noinc(&full[(n + c) % kSlots]);
                 }
                 if (!ok) break;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) row[i] = next[i];
             }
         } else {
             const int r = quad * 32 + (int)lane;   // the lane's row of a tile
@@ -599,18 +625,35 @@ __global__ void __launch_bounds__(low::kThreads, 1)
         cp_async_wait_all();
     } else if (warp >= kFirstQuery && warp < kFirstEpi) {
         // ------------------------------------------------------------ queries
-        // Eight heads a warp, dims 16 l .. 16 l + 15 a lane, in registers before their place comes free.
+        // Eight heads a warp, dims 16 l .. 16 l + 15 a lane, loaded and split before their place comes free.
         setmaxnreg_inc<kQueryRegs>();
         constexpr int kOwn = kH / kQueryWarps;
         const int h0 = (warp - kFirstQuery) * kOwn;
         int qi = 0;
         for_items(p, lane, [&](const Item& I, int) {
             const __nv_bfloat16* src = p.q + ((int64_t)I.row * kH + h0) * kQDim + 16 * lane;
-            uint4 a[kOwn], b[kOwn];
+            uint32_t hi[kOwn][4], lo[kOwn][4];
 #pragma unroll
             for (int i = 0; i < kOwn; ++i) {
-                a[i] = ldg_nc_v4(src + i * kQDim);
-                b[i] = ldg_nc_v4(src + i * kQDim + 8);
+                const uint4 a = ldg_nc_v4(src + i * kQDim), b = ldg_nc_v4(src + i * kQDim + 8);
+                hi[i][0] = a.x, hi[i][1] = a.y, hi[i][2] = a.z, hi[i][3] = a.w;
+                lo[i][0] = b.x, lo[i][1] = b.y, lo[i][2] = b.z, lo[i][3] = b.w;
+            }
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                const uint32_t w[8] = {hi[i][0], hi[i][1], hi[i][2], hi[i][3], lo[i][0], lo[i][1], lo[i][2], lo[i][3]};
+                float amax = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
+                // magnitudes compare as their bit patterns do
+                const int e = e4m3_scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
+                const float inv = exp2_int(-e);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    split_e4m3x4(bf16_lo(w[2 * k]) * inv, bf16_hi(w[2 * k]) * inv, bf16_lo(w[2 * k + 1]) * inv,
+                                 bf16_hi(w[2 * k + 1]) * inv, hi[i][k], lo[i][k]);
+                // (a place of four: the epilogue may be at the tiles of the item before the last)
+                if (lane == 0) qs_s[(qi & 3) * kH + h0 + i] = p.scale_log2 * exp2_int(e);
             }
             if (!wait(q_free, (qi & 1) ^ 1)) return false;
             if (warp == kFirstQuery && lane == 0) {
@@ -620,22 +663,9 @@ __global__ void __launch_bounds__(low::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kOwn; ++i) {
                 const int h = h0 + i;
-                const uint32_t w[8] = {a[i].x, a[i].y, a[i].z, a[i].w, b[i].x, b[i].y, b[i].z, b[i].w};
-                float amax = 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k]))));
-                // magnitudes compare as their bit patterns do
-                const int e = e4m3_scale_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
-                const float inv = exp2_int(-e);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    split_e4m3x4(bf16_lo(w[2 * k]) * inv, bf16_hi(w[2 * k]) * inv, bf16_lo(w[2 * k + 1]) * inv,
-                                 bf16_hi(w[2 * k + 1]) * inv, hi[k], lo[k]);
                 uint8_t* d = smem + OFF_QHL + (int)(lane >> 3) * kBlk + h * 128 + (((int)(lane & 7) ^ (h & 7)) << 4);
-                *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(d + kH * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                if (lane == 0) qs_s[(qi & 3) * kH + h] = p.scale_log2 * exp2_int(e);
+                *reinterpret_cast<uint4*>(d) = make_uint4(hi[i][0], hi[i][1], hi[i][2], hi[i][3]);
+                *reinterpret_cast<uint4*>(d + kH * 128) = make_uint4(lo[i][0], lo[i][1], lo[i][2], lo[i][3]);
             }
             fence_proxy_async_smem();
             __syncwarp();
