@@ -32,10 +32,11 @@ __all__ = list(_API) + ["workloads", "build", "HostPrefill", "HostDecode", "shar
 
 
 def __getattr__(name):
-    # torch is imported only when a library call is first used
+    # torch is imported only when a library call is first used; from then on the call is a name of the package
     if name in _API:
         from . import _lib
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)
+        return value
     if name == "build":
         from ._build import build
         return build

@@ -810,8 +810,11 @@ def cache_evict_plan(acc: torch.Tensor, pos: torch.Tensor, kv_len: torch.Tensor,
     if not 1 <= keep < Nmax:
         _bad("1 <= keep < Nmax")
     moves = min(keep, Nmax - keep)
-    src, dst = _new((B, moves), torch.int32, acc.device, stream), _new((B, moves), torch.int32, acc.device, stream)
-    left = _new((B,), torch.int32, acc.device, stream)
+    src = _new((B, moves), torch.int32, acc.device, stream)
+    if stream is None:
+        dst, left = torch.empty_like(src), torch.empty_like(kv_len)
+    else:
+        dst, left = _new((B, moves), torch.int32, acc.device, stream), _new((B,), torch.int32, acc.device, stream)
     rc = (_lib or load()).dsa_cache_evict_plan(
         _p(acc, dev, _F32, B * Nmax, "acc"), _p(pos, dev, _I32, B * Nmax, "pos"), _p(kv_len, dev, _I32, B, "kv_len"), B, Nmax,
         keep, recent, sink, src.data_ptr(), dst.data_ptr(), left.data_ptr(), _stream_on(dev, stream))
@@ -826,39 +829,50 @@ def cache_move_rows(src: torch.Tensor, dst: torch.Tensor, dense=(), paged=(), bl
     `paged` ones pools [num_pages * page_size, ...] with block_table [B, pages].  At most 8 tensors, rows of a multiple
     of 4 bytes."""
     dev = _current_device()
-    if src.dim() != 2 or dst.shape != src.shape:
+    if src.dim() != 2:
         _bad("src and dst are int32 [B, moves]")
     B, moves = src.shape
-    n = len(dense) + len(paged)
-    if not 1 <= n <= 8:
-        _bad("1 to 8 tensors")
-    Nmax, rows, ptrs, sizes = None, None, [], []
+    Nmax, ptrs, sizes = None, [], []
     for t in dense:
-        if t.get_device() != dev or not t.is_contiguous() or t.dim() < 2 or t.shape[0] != B or Nmax not in (None, t.shape[1]):
+        shape = t.shape
+        if (len(shape) < 2 or shape[0] != B or Nmax not in (None, shape[1]) or t.get_device() != dev or not t.is_contiguous()):
             _bad("dense tensors are contiguous [B, Nmax, ...] on the current CUDA device")
-        Nmax = t.shape[1]
+        Nmax = shape[1]
         ptrs.append(t.data_ptr())
-        sizes.append(t.nbytes // (B * Nmax) if B * Nmax else 0)
-    pt, stride = None, 0
+        sizes.append(t.stride(1) * t.element_size())
+    pt, stride, pages = None, 0, 0
     if paged:
         if block_table is None or page_size < 1:
             _bad("paged tensors need block_table and page_size")
         stride = _table(block_table, B)
         pt = _p(block_table, dev, _I32, B * stride, "block_table")
+        rows = None
         for t in paged:
-            if t.get_device() != dev or not t.is_contiguous() or t.dim() < 1 or rows not in (None, t.shape[0]):
+            shape = t.shape
+            if len(shape) < 1 or rows not in (None, shape[0]) or t.get_device() != dev or not t.is_contiguous():
                 _bad("paged tensors are contiguous [num_pages * page_size, ...] on the current CUDA device")
-            rows = t.shape[0]
+            rows = shape[0]
             ptrs.append(t.data_ptr())
-            sizes.append(t.nbytes // rows if rows else 0)
+            sizes.append(t.stride(0) * t.element_size())
+        pages = rows // page_size
         if Nmax is None:
             Nmax = stride * page_size
+    n = len(ptrs)
+    if not 1 <= n <= 8:
+        _bad("1 to 8 tensors")
+    bytes_, kinds = _move_arrays(tuple(sizes), len(dense))
     rc = (_lib or load()).dsa_cache_move_rows(
         _p(src, dev, _I32, B * moves, "src"), _p(dst, dev, _I32, B * moves, "dst"), B, moves, Nmax, n, (_P * n)(*ptrs),
-        (_I * n)(*sizes), (_I * n)(*([0] * len(dense) + [1] * len(paged))), pt, stride, page_size if pt else 0,
-        rows // page_size if pt else 0, _stream_on(dev, stream))
+        bytes_, kinds, pt, stride, page_size if pt else 0, pages, _stream_on(dev, stream))
     if rc:
         raise DsaError("dsa_cache_move_rows", rc)
+
+
+@functools.lru_cache(maxsize=256)
+def _move_arrays(sizes, dense: int):
+    """Row bytes and kinds (0 dense, 1 paged) of a call's tensors, as the library takes them; only read there."""
+    n = len(sizes)
+    return (_I * n)(*sizes), (_I * n)(*([0] * dense + [1] * (n - dense)))
 
 
 # ----------------------------------------------------------------------------- around the attention

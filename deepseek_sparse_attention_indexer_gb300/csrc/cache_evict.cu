@@ -11,7 +11,10 @@
 // thread, which has a run of keys, the ranks of its equal keys, its gaps and its movers.  No sort, no atomics whose order
 // shows.  It is a chain of latencies: three histograms, four cluster barriers.
 //
-// Moves: a warp a move, all tensors of the call in one launch.
+// Moves: a warp a run of entries, all tensors of the call in one launch.  The rows lie apart in HBM, so it is bytes in
+// flight that count: the run's indices and pages are looked up a lane each, and a lane loads its pieces of two moves, all
+// tensors, before it stores the first.  (A warp an entry: entries behind a sequence's last move, most of them, took 73 of 99
+// us for 64 sequences of up to 16k keys.)
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -49,34 +52,32 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 
 __device__ __forceinline__ int padded(int i) { return i + (i >> 5); }   // runs of a power of two start in different banks
 
-// Sum of x over the threads before this one; total over all.
-__device__ __forceinline__ int scan_block(int x, int* warp_sums, int& total) {
+// Sums of x and y over the threads before this one, in their place; the totals over all.
+__device__ __forceinline__ int2 scan_block(int2& x, int2* warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int s = x;
+    auto scan_warp = [&](int2 v) {
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const int y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-    }
+        for (int o = 1; o < 32; o *= 2) {
+            const int a = __shfl_up_sync(0xffffffffu, v.x, o), b = __shfl_up_sync(0xffffffffu, v.y, o);
+            if (lane >= o) v = make_int2(v.x + a, v.y + b);
+        }
+        return v;
+    };
+    const int2 own = scan_warp(x);
     __syncthreads();                               // readers of the last scan are done
-    if (lane == 31) warp_sums[warp] = s;
+    if (lane == 31) warp_sums[warp] = own;
     __syncthreads();
-    int w = warp_sums[lane];                       // kThreads / 32 = 32 warps
-    int before = 0, all = 0;
-#pragma unroll
-    for (int o = 0; o < 32; ++o) {
-        const int v = __shfl_sync(0xffffffffu, w, o);
-        if (o < warp) before += v;
-        all += v;
-    }
-    total = all;
-    return before + s - x;
+    const int2 w = scan_warp(warp_sums[lane]);     // of kThreads / 32 = 32 warps
+    const int before = max(warp - 1, 0);
+    const int bx = __shfl_sync(0xffffffffu, w.x, before), by = __shfl_sync(0xffffffffu, w.y, before);
+    x = make_int2(own.x - x.x + (warp ? bx : 0), own.y - x.y + (warp ? by : 0));
+    return make_int2(__shfl_sync(0xffffffffu, w.x, 31), __shfl_sync(0xffffffffu, w.y, 31));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanParams p) {
     extern __shared__ uint32_t keys_s[];
     __shared__ int hist[2][kBins];
-    __shared__ int warp_sums[32];
+    __shared__ int2 warp_sums[32];
     __shared__ int share[4];                       // read by the other blocks: largest position, gaps, movers
     __shared__ int found[2];                       // bin, keys of larger digits
     cg::cluster_group cluster = cg::this_cluster();
@@ -96,26 +97,30 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanParam
     const float* acc = p.acc + (int64_t)b * p.Nmax + j0;
     const int32_t* pos = p.pos + (int64_t)b * p.Nmax + j0;
 
+    // Largest position; the weights' keys beside it where they are held.
+    const bool held = len <= p.smem_keys;
     int newest = INT32_MIN;
+    for (int i = t; i < len; i += kThreads) {
+        if (held) keys_s[padded(i)] = order_key(__ldg(acc + i));
+        newest = max(newest, __ldg(pos + i));
+    }
     if (p.recent > 0) {
-        for (int i = t; i < len; i += kThreads) newest = max(newest, __ldg(pos + i));
         newest = __reduce_max_sync(0xffffffffu, newest);
-        if ((t & 31) == 0) warp_sums[t >> 5] = newest;
+        if ((t & 31) == 0) warp_sums[t >> 5].x = newest;
         __syncthreads();
         if (t < 32) {
-            const int m = __reduce_max_sync(0xffffffffu, warp_sums[t]);
+            const int m = __reduce_max_sync(0xffffffffu, warp_sums[t].x);
             if (t == 0) share[0] = m;
         }
         cluster.sync();
         for (int r = 0; r < C; ++r) newest = max(newest, cluster.map_shared_rank(share, r)[0]);
     }
     const int64_t oldest_recent = (int64_t)newest - p.recent;   // positions above it are protected
-    auto make = [&](int i) -> uint32_t {
+    auto make = [&](int i) -> uint32_t {           // a thread's own keys, as it wrote them
         const int at = __ldg(pos + i);
         if ((p.recent > 0 && at > oldest_recent) || at < p.sink) return 0xffffffffu;
-        return order_key(__ldg(acc + i));
+        return held ? keys_s[padded(i)] : order_key(__ldg(acc + i));
     };
-    const bool held = len <= p.smem_keys;
     auto key = [&](int i) -> uint32_t { return held ? keys_s[padded(i)] : make(i); };
 
     // Radix select: `prefix` the digits found so far, `want` how many of the keys that share them stay.
@@ -146,15 +151,15 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanParam
             own[i] = 0;
             for (int r = 0; r < C; ++r) own[i] += cluster.map_shared_rank(h, r)[bin];
         }
-        int total;
-        int before = scan_block(own[0] + own[1], warp_sums, total);
+        int2 before = make_int2(own[0] + own[1], 0);
+        scan_block(before, warp_sums);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (before < want && before + own[i] >= want) {
+            if (before.x < want && before.x + own[i] >= want) {
                 found[0] = kBins - 1 - (2 * t + i);
-                found[1] = before;
+                found[1] = before.x;
             }
-            before += own[i];
+            before.x += own[i];
         }
         __syncthreads();
         const int bin = found[0];
@@ -166,9 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanParam
 
     // A run of keys a thread: ranks of the equal ones, then what goes below `keep` and what stays behind it.
     const int run = (len + kThreads - 1) / kThreads, r0 = min(len, t * run), r1 = min(len, r0 + run);
-    int eq = 0, total;
-    for (int i = r0; i < r1; ++i) eq += key(i) == prefix;
-    const int eq0 = equal_before + scan_block(eq, warp_sums, total);
+    int2 eq = make_int2(0, 0);
+    for (int i = r0; i < r1; ++i) eq.x += key(i) == prefix;
+    scan_block(eq, warp_sums);
+    const int eq0 = equal_before + eq.x;
     auto each = [&](auto f) {
         int e = eq0;
         for (int i = r0; i < r1; ++i) {
@@ -177,16 +183,16 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanParam
             f(j0 + i, stays);
         }
     };
-    int gaps = 0, movers = 0;
+    int2 own = make_int2(0, 0);                    // gaps, movers
     each([&](int j, bool stays) {
-        gaps += j < p.keep && !stays;
-        movers += j >= p.keep && stays;
+        own.x += j < p.keep && !stays;
+        own.y += j >= p.keep && stays;
     });
-    int all_gaps, all_movers;
-    int gap = scan_block(gaps, warp_sums, all_gaps), mover = scan_block(movers, warp_sums, all_movers);
+    const int2 all = scan_block(own, warp_sums);
+    int gap = own.x, mover = own.y;
     if (t == 0) {
-        share[1] = all_gaps;
-        share[2] = all_movers;
+        share[1] = all.x;
+        share[2] = all.y;
     }
     cluster.sync();
     int count = 0;
@@ -208,58 +214,114 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanParam
 }
 
 constexpr int kMoveWarps = 8;
+constexpr int kAhead = 3;                          // pieces of 16 bytes of a move that a lane loads before it stores
 
 struct MoveParams {
     const int32_t* src;
     const int32_t* dst;
     int most, Nmax, count;
-    uint8_t* base[DSA_MAX_MOVED];
+    int run;                                       // entries a warp, at most 32
+    uint8_t* base[DSA_MAX_MOVED];                  // tensors of 16-byte pieces first
     int bytes[DSA_MAX_MOVED];
     int paged[DSA_MAX_MOVED];                      // 1: rows of a pool
+    int wide;                                      // tensors whose rows are whole 16-byte pieces
+    int pieces, words;                             // of a row of all those; 4-byte words of a row of the others
     PageTable pages;
     int32_t* status;
 };
 
-__global__ void __launch_bounds__(kMoveWarps * 32) move_rows_kernel(const __grid_constant__ MoveParams p) {
-    griddep_wait();
-    const int m = blockIdx.x * kMoveWarps + threadIdx.x / 32, lane = threadIdx.x & 31;
-    if (m >= p.most) return;
-    const int b = blockIdx.y;
-    const int from = __ldg(p.src + (int64_t)b * p.most + m), to = __ldg(p.dst + (int64_t)b * p.most + m);
-    if (from < 0 || to < 0) return;
-    if (from >= p.Nmax || to >= p.Nmax) {
-        if (lane == 0) raise_dev_error(p.status, DEV_ERR_BOUNDS);
-        return;
-    }
-    int64_t pf = -1, pt = -1;
-    if (p.pages.table) {
-        pf = paged_row(p.pages, b, from);
-        pt = paged_row(p.pages, b, to);
-    }
-    for (int i = 0; i < p.count; ++i) {
-        const int64_t f = p.paged[i] ? pf : (int64_t)b * p.Nmax + from, t = p.paged[i] ? pt : (int64_t)b * p.Nmax + to;
-        if (f < 0 || t < 0) {
-            if (lane == 0) raise_dev_error(p.status, DEV_ERR_BOUNDS);
-            continue;
+// Piece (or word) u of a move: its tensor and the offset in the row, bytes of `size`; false behind the last.
+__device__ __forceinline__ bool find_piece(const MoveParams& p, int u, int first, int last, int size, int& tensor, int& at) {
+    for (int i = first; i < last; ++i) {
+        const int n = p.bytes[i] / size;
+        if (u < n) {
+            tensor = i;
+            at = u * size;
+            return true;
         }
-        const int bytes = p.bytes[i];
-        const uint8_t* s = p.base[i] + f * bytes;
-        uint8_t* d = p.base[i] + t * bytes;
-        if (bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(p.base[i]) & 15) == 0) {
-            int at = lane * 16;
-            for (; at + 1024 < bytes; at += 1536) {   // three loads in flight
-                uint4 v[3];
+        u -= n;
+    }
+    return false;
+}
+
+__global__ void __launch_bounds__(kMoveWarps * 32, 4) move_rows_kernel(const __grid_constant__ MoveParams p) {
+    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const int m = (blockIdx.x * kMoveWarps + threadIdx.x / 32) * p.run + lane;
+    griddep_wait();
+    int from = -1, to = -1;
+    if (lane < p.run && m < p.most) {
+        from = __ldg(p.src + (int64_t)b * p.most + m);
+        to = __ldg(p.dst + (int64_t)b * p.most + m);
+    }
+    bool ok = from >= 0 && to >= 0;
+    if (!__any_sync(0xffffffffu, ok)) return;
+    bool bad = ok && (from >= p.Nmax || to >= p.Nmax);
+    ok = ok && !bad;
+    int pf = -1, pt = -1;                          // rows of a pool (below 2^31)
+    if (ok && p.pages.table) {
+        pf = (int)paged_row(p.pages, b, from);
+        pt = (int)paged_row(p.pages, b, to);
+        bad = pf < 0 || pt < 0;
+    }
+    const bool pool = pf >= 0 && pt >= 0;          // else the paged tensors are left out
+    if (bad) raise_dev_error(p.status, DEV_ERR_BOUNDS);
+    // the lane's pieces, the same of every move
+    int tensor[kAhead + 1], at[kAhead + 1];
+    bool mine[kAhead + 1];
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    if (at + 512 * k < bytes) v[k] = *reinterpret_cast<const uint4*>(s + at + 512 * k);
+    for (int k = 0; k < kAhead; ++k) mine[k] = find_piece(p, lane + 32 * k, 0, p.wide, 16, tensor[k], at[k]);
+    mine[kAhead] = find_piece(p, lane, p.wide, p.count, 4, tensor[kAhead], at[kAhead]);
+
+    struct Move {
+        int f, t, pf, pt;
+        bool pool;
+    };
+    auto row = [&](const Move& v, int i, bool dest) {
+        const int64_t r = p.paged[i] ? (dest ? v.pt : v.pf) : (int64_t)b * p.Nmax + (dest ? v.t : v.f);
+        return p.base[i] + r * p.bytes[i];
+    };
+    uint32_t left = __ballot_sync(0xffffffffu, ok);
+    while (left) {
+        Move mv[2];
+        bool have[2];
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    if (at + 512 * k < bytes) *reinterpret_cast<uint4*>(d + at + 512 * k) = v[k];
+        for (int i = 0; i < 2; ++i) {
+            have[i] = left != 0;
+            const int l = left ? __ffs(left) - 1 : 0;
+            left &= left - 1;
+            mv[i] = Move{__shfl_sync(0xffffffffu, from, l), __shfl_sync(0xffffffffu, to, l), __shfl_sync(0xffffffffu, pf, l),
+                         __shfl_sync(0xffffffffu, pt, l), __shfl_sync(0xffffffffu, (int)pool, l) != 0};
+        }
+        uint4 v[2][kAhead];
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (have[i] && mine[k] && (mv[i].pool || !p.paged[tensor[k]]))
+                    v[i][k] = *reinterpret_cast<const uint4*>(row(mv[i], tensor[k], false) + at[k]);
+            if (have[i] && mine[kAhead] && (mv[i].pool || !p.paged[tensor[kAhead]]))
+                w[i] = *reinterpret_cast<const uint32_t*>(row(mv[i], tensor[kAhead], false) + at[kAhead]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!have[i]) break;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (mine[k] && (mv[i].pool || !p.paged[tensor[k]]))
+                    *reinterpret_cast<uint4*>(row(mv[i], tensor[k], true) + at[k]) = v[i][k];
+            if (mine[kAhead] && (mv[i].pool || !p.paged[tensor[kAhead]]))
+                *reinterpret_cast<uint32_t*>(row(mv[i], tensor[kAhead], true) + at[kAhead]) = w[i];
+            for (int u = lane + 32 * kAhead; u < p.pieces; u += 32) {   // longer rows
+                int j, o;
+                if (!find_piece(p, u, 0, p.wide, 16, j, o) || (!mv[i].pool && p.paged[j])) continue;
+                *reinterpret_cast<uint4*>(row(mv[i], j, true) + o) = *reinterpret_cast<const uint4*>(row(mv[i], j, false) + o);
             }
-            for (; at < bytes; at += 512) *reinterpret_cast<uint4*>(d + at) = *reinterpret_cast<const uint4*>(s + at);
-        } else {
-            for (int at = lane * 4; at < bytes; at += 128)
-                *reinterpret_cast<uint32_t*>(d + at) = *reinterpret_cast<const uint32_t*>(s + at);
+            for (int u = lane + 32; u < p.words; u += 32) {
+                int j, o;
+                if (!find_piece(p, u, p.wide, p.count, 4, j, o) || (!mv[i].pool && p.paged[j])) continue;
+                *reinterpret_cast<uint32_t*>(row(mv[i], j, true) + o) = *reinterpret_cast<const uint32_t*>(row(mv[i], j, false) + o);
+            }
         }
     }
 }
@@ -269,8 +331,13 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_rows_kernel(const __grid
 dsa_status_t launch_evict_plan(const float* acc, const int32_t* pos, const int32_t* kv_len, int B, int Nmax, int keep,
                                int recent, int sink, int32_t* src, int32_t* dst, int32_t* left, cudaStream_t stream) {
     PlanParams p{acc, pos, kv_len, Nmax, keep, recent, sink, keep < Nmax - keep ? keep : Nmax - keep, 0, src, dst, left};
-    int cluster = 1;
-    while (cluster < 8 && Nmax > 2048 * cluster) cluster *= 2;
+    // Blocks a sequence: one for 4096 keys, four for 32k, eight beyond (1 sequence of 4k / 16k / 64k keys, us: 1 block 17 /
+    // 31 / -, 2 16.7 / 23 / 51, 4 18 / 21 / 35, 8 24 / 26 / 32), but no more than one block an SM at once (64 of 16k: 1 block
+    // 31, 2 23, 4 44, 8 140), and enough that a part fits shared memory (one of 64k in one block 305).
+    const int sms = device_sm_count();
+    int cluster = Nmax <= 4096 ? 1 : Nmax <= 32768 ? 4 : 8;
+    while (cluster > 1 && (long long)B * cluster * 9 > sms * 8) cluster /= 2;   // (clusters leave some SMs)
+    while (cluster < 8 && ceil_div(Nmax, cluster) >= kKeysInSmem) cluster *= 2;
     const int part = ceil_div(Nmax, cluster);
     p.smem_keys = part < kKeysInSmem ? part : 0;
     const int smem = p.smem_keys ? (p.smem_keys + p.smem_keys / 32 + 1) * 4 : 0;
@@ -309,15 +376,26 @@ dsa_status_t launch_move_rows(const int32_t* src, const int32_t* dst, int B, int
     p.dst = dst;
     p.most = most;
     p.Nmax = Nmax;
-    p.count = count;
-    for (int i = 0; i < count; ++i) {
-        p.base[i] = static_cast<uint8_t*>(tensors[i]);
-        p.bytes[i] = row_bytes[i];
-        p.paged[i] = paged[i];
+    for (int pass = 0; pass < 2; ++pass) {         // the tensors of whole 16-byte pieces, then the others
+        for (int i = 0; i < count; ++i) {
+            const bool wide = row_bytes[i] % 16 == 0 && aligned16(tensors[i]);
+            if (wide != (pass == 0)) continue;
+            const int at = p.count++;
+            p.base[at] = static_cast<uint8_t*>(tensors[i]);
+            p.bytes[at] = row_bytes[i];
+            p.paged[at] = paged[i];
+            (wide ? p.pieces : p.words) += row_bytes[i] / (wide ? 16 : 4);
+            if (wide) p.wide = p.count;
+        }
     }
     p.pages = pages;
     p.status = device_status_ptr();
-    if (launch_pdl(move_rows_kernel, dim3(ceil_div(most, kMoveWarps), B), dim3(kMoveWarps * 32), 0, stream, p) != cudaSuccess)
+    // A warp an entry while there are no more than four rounds of the 32 warps an SM holds, up to eight entries a warp
+    // beyond.  One / eight a warp, us: 16k entries (8k moves) 4.5 / 9, 524k (80k) 99 / 44.
+    const long long entries = (long long)B * most, at_once = 128LL * device_sm_count();
+    p.run = 1;
+    while (p.run < 8 && entries > at_once * p.run) p.run *= 2;
+    if (launch_pdl(move_rows_kernel, dim3(ceil_div(most, kMoveWarps * p.run), B), dim3(kMoveWarps * 32), 0, stream, p) != cudaSuccess)
         return DSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

@@ -133,7 +133,7 @@ constexpr uint32_t IDESC_QK = idesc_e4m3_f32(128, 128, false, false);
 constexpr uint32_t IDESC_ROPE = idesc_bf16_f32(128, 64, false, false);
 constexpr uint32_t IDESC_PV = idesc_e4m3_scaled_f32(128, 64, true, true);
 
-__device__ __align__(16) uint8_t g_no_row[kQ8Latent];   // zeros, the latent dims of a slot without a row
+__device__ __align__(32) uint8_t g_no_row[kQ8Latent];   // zeros, the latent dims of a slot without a row
 
 // The two caches: bytes of a row, where its rope dims begin.
 template <bool Q4>
@@ -609,13 +609,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
                     // the loads run ahead, and only the store waits for QK of the tile before.
                     uint32_t k[32];
                     float sc = kZeroRowScale;         // of a page outside the pool
-                    const uint8_t* src = p.cache + (int64_t)row * kBytes + Rows<Q4>::kRope;
+                    const uint8_t* src = row < 0 ? g_no_row : p.cache + (int64_t)row * kBytes + Rows<Q4>::kRope;
                     auto load_k = [&](int from, int to) {
 #pragma unroll
-                        for (int i = 8 * from; i < 8 * to; ++i) k[i] = 0;
-                        if (row >= 0)
-#pragma unroll
-                            for (int i = from; i < to; ++i) ldg_nc_v8(src + 32 * i, k + 8 * i);
+                        for (int i = from; i < to; ++i) ldg_nc_v8(src + 32 * i, k + 8 * i);
                     };
                     if constexpr (Q4) {
                         if (!wait(&freed[2 * (g & 1) + 1], ((g >> 1) & 1) ^ 1)) break;
