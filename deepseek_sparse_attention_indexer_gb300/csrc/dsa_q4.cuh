@@ -29,11 +29,17 @@ __device__ __forceinline__ float q4_block_scale(uint32_t byte) {   // of a block
 __device__ __forceinline__ uint2 q4_table(float x) {
     return make_uint2(pack_e4m3x4(0.f, 0.5f * x, x, 1.5f * x), pack_e4m3x4(2.f * x, 3.f * x, 4.f * x, 6.f * x));
 }
+// The bytes of (x, y) that the low four nibbles of sel name, each below 8 (an instruction; the intrinsic masks first)
+__device__ __forceinline__ uint32_t select_bytes(uint32_t x, uint32_t y, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(sel));
+    return r;
+}
 // Eight codes as e4m3 bytes, by the table of their block
 __device__ __forceinline__ uint2 q4_expand(uint32_t w, uint2 table) {
     const uint32_t sel = w & kQ4Magnitudes;
-    return make_uint2(__byte_perm(table.x, table.y, sel) | (w & 0x80808080u),
-                      __byte_perm(table.x, table.y, sel >> 16) | ((w << 4) & 0x80808080u));
+    return make_uint2(select_bytes(table.x, table.y, sel) | (w & 0x80808080u),
+                      select_bytes(table.x, table.y, sel >> 16) | ((w << 4) & 0x80808080u));
 }
 
 }  // namespace dsa
