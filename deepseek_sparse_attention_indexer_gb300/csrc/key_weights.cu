@@ -12,8 +12,8 @@
 //     (Rows through registers into tensor memory, as the MMA's A operand, left too few bytes in flight: 1.24 ms for 4096
 //     queries of 2048 bf16 rows.)
 //   * bf16 rows: nine chunks of 64 dims, a tile's in nine slots.  An MMA of N = 64 takes its issuer 57 cycles, whatever
-//     N, a commit 200 and a look at the barriers 550: two issuers, each with an accumulator of its own for its dims, and
-//     barriers for four groups of chunks in place of nine (1.22 -> 0.91 ms).
+//     N, and a look at the barriers 550: two issuers, and barriers for four groups of chunks, each with an accumulator
+//     of its own, in place of nine (1.22 -> 0.91 ms).
 //   * 8-bit and 4-bit rows: e4m3 products, the query as two e4m3 numbers, as in the attention over them (mla_attn_q8.cu):
 //     four chunks of 128 dims and the rope dims, 20 MMAs a tile in place of 36, two issuers with a tile in turn.  The
 //     row's scale and the query head's are applied to the sums.  4-bit rows are expanded on their way, a lane its own row.
@@ -195,7 +195,9 @@ constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
 constexpr int OFF_ABORT = OFF_TMEM + 4;
 constexpr int kSmemBytes = OFF_ABORT + 4;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
-constexpr uint32_t kAccCols = 128, kTmemCols = 256;   // the issuers' accumulators of a tile, two tiles
+// An accumulator a part, two tiles: the tensor core cuts a sum where it adds to it, and 8 to 12 additions each, summed here
+// rounded to nearest, are nearer than 16 to 20 (error against float64, 8 sequences, 1.1e-6 -> 5e-7, for 4% of the time).
+constexpr uint32_t kAccCols = 64 * kParts, kTmemCols = 2 * kAccCols;
 
 }  // namespace wide
 
@@ -253,7 +255,7 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
         const uint32_t base = (smem_u32(smem) >> 4) | ((16u >> 4) << 16);
         for_items(p, lane, [&](const Item&, int T) {
             for (int t = 0; t < T; ++t, ++gt) {
-                const uint32_t d = tmem_base + kAccCols * (gt & 1) + (g0 ? 64 : 0);
+                const uint32_t d = tmem_base + kAccCols * (gt & 1);
                 uint64_t* mine = lane < 2 ? &full[g0 + lane] : lane < 4 ? &q_full[g0 + lane - 2] : &acc_free[gt & 1];
                 const uint32_t parity = lane < 2 ? gt & 1 : lane < 4 ? qi & 1 : ((gt >> 1) & 1) ^ 1;
                 uint32_t got = 0;
@@ -272,9 +274,9 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                         for (int c = part_begin(g); c < part_end(g); ++c)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_bf16_ss_lo(d, base + ((OFF_K + c * kBlk) >> 4) + 2 * k, kDescHi,
+                                mma_bf16_ss_lo(d + 64 * g, base + ((OFF_K + c * kBlk) >> 4) + 2 * k, kDescHi,
                                                base + ((OFF_Q + c * kQBlk) >> 4) + 2 * k, kDescHi, IDESC_BF16,
-                                               c == part_begin(g0) && k == 0 ? 0u : 1u);
+                                               c == part_begin(g) && k == 0 ? 0u : 1u);
                         mma_commit(&empty[g]);
                         if (t == T - 1) mma_commit(&q_free[g]);
                     }
@@ -359,12 +361,18 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < kH; h += 16) {
                     uint32_t u[16], v[16];
+                    float2 s[8];
                     tmem_ld16(d + h, u);
                     tmem_ld16(d + 64 + h, v);
                     tmem_ld_wait();
 #pragma unroll
+                    for (int k = 0; k < 8; ++k) s[k] = __fadd2_rn(pair(u, k), pair(v, k));
+                    tmem_ld16(d + 128 + h, u);
+                    tmem_ld16(d + 192 + h, v);
+                    tmem_ld_wait();
+#pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float2 x = __ffma2_rn(__fadd2_rn(pair(u, k), pair(v, k)), sc, nl[h / 2 + k]);
+                        const float2 x = __ffma2_rn(__fadd2_rn(s[k], __fadd2_rn(pair(u, k), pair(v, k))), sc, nl[h / 2 + k]);
                         sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
                     }
                 }
