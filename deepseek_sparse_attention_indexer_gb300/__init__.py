@@ -23,7 +23,7 @@ _API = ("indexer_scores", "topk", "mla_sparse_attn_prefill", "mla_sparse_attn_de
         "mla_cache_write_q4", "mla_cache_read_q4", "mla_cache_read_q4_paged",
         "mla_sparse_attn_prefill_q4", "mla_sparse_attn_prefill_q4_paged", "mla_sparse_attn_decode_q4",
         "mla_sparse_attn_decode_q4_paged", "attn_q4_workspace_size",
-        "mla_key_weights_prefill", "mla_key_weights_decode", "cache_evict_plan", "cache_move_rows",
+        "mla_key_weights_prefill", "mla_key_weights_decode", "key_weights_workspace_size", "cache_evict_plan", "cache_move_rows",
         "attn_workspace_size", "attn_q8_workspace_size", "device_status", "selftest_wait_timeout",
         "selftest_poll_timeout", "status_string", "load", "lib_path",
         "DsaError")

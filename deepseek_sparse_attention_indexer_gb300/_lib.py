@@ -65,7 +65,7 @@ SIGNATURES = {
     "dsa_device_status": (ctypes.c_int32, [_P, ctypes.POINTER(ctypes.c_int32), _I]),
     "dsa_selftest_wait_timeout": (ctypes.c_int32, [_I, ctypes.c_uint64, _P]),
     "dsa_selftest_poll_timeout": (ctypes.c_int32, [_I, ctypes.c_uint32, _P]),
-    "mla_key_weights_workspace_size": (_SZ, [_I]),
+    "mla_key_weights_workspace_size": (_SZ, [_I, _I, _I, _I]),
     "mla_key_weights_prefill": (ctypes.c_int32, [_P, _P, _P, _I, _P, _I, _I, _P, _P, _I, _I, _I, _F, _P, _I, _P, _SZ, _P]),
     "mla_key_weights_decode": (ctypes.c_int32, [_P, _P, _P, _I, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _F, _P, _I, _P]),
     "dsa_cache_evict_plan": (ctypes.c_int32, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
@@ -716,6 +716,12 @@ def _weights_cache(cache, cache_scale, dev):
     return rows, _p(cache, dev, _U8, rows * row, "cache"), _p(cache_scale, dev, _F32, rows, "cache_scale"), fmt
 
 
+@functools.lru_cache(maxsize=4096)
+def key_weights_workspace_size(L: int, top_k: int, N: int, row_format: int = 0) -> int:
+    """Bytes mla_key_weights_prefill takes; row_format 0 bf16 rows, 1 8-bit, 2 4-bit."""
+    return int(load().mla_key_weights_workspace_size(row_format, L, N, top_k))
+
+
 def _weights_args(q, idx, lse, dev):
     rows, heads, width = q.shape
     if heads != 64 or width != 576:
@@ -753,7 +759,7 @@ def mla_key_weights_prefill(q: torch.Tensor, cache: torch.Tensor, idx: torch.Ten
     if fresh:
         acc = _new((N,), torch.float32, q.device, stream)
     if workspace is None:
-        workspace = _new((N * 8,), torch.uint8, q.device, stream)
+        workspace = _new((key_weights_workspace_size(L, top_k, N, fmt),), torch.uint8, q.device, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         _bad("the workspace is contiguous on the current CUDA device")
     rc = (_lib or load()).mla_key_weights_prefill(

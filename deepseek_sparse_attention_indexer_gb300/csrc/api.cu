@@ -652,11 +652,13 @@ dsa_status_t check_key_weights(const void* q, const void* cache, const float* ca
     return DSA_OK;
 }
 
-bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 }  // namespace
 
-size_t mla_key_weights_workspace_size(int N) { return N < 1 ? 0 : (size_t)N * 8; }
+size_t mla_key_weights_workspace_size(int row_format, int L, int N, int top_k) {
+    if (row_format < DSA_ROWS_BF16 || row_format > DSA_ROWS_Q4 || L < 1 || N < 1 || top_k < 1 || top_k > DSA_MAX_TOPK) return 0;
+    return key_weights_workspace(row_format, L, N, top_k);
+}
 
 dsa_status_t mla_key_weights_prefill(const void* q, const void* cache, const float* cache_scale, int row_format,
                                      const int32_t* block_table, int page_size, int num_pages, const int32_t* idx,
@@ -667,8 +669,8 @@ dsa_status_t mla_key_weights_prefill(const void* q, const void* cache, const flo
     PageTable pt{};
     const int stride = page_size > 0 ? (int)(((long long)N + page_size - 1) / page_size) : 0;
     if (block_table && (st = make_page_table(block_table, stride, page_size, num_pages, N, &pt)) != DSA_OK) return st;
-    if (!aligned16(q) || !aligned32(cache) || !aligned8(workspace)) return DSA_ERR_MISALIGNED;
-    if ((st = check_workspace(workspace, ws_bytes, mla_key_weights_workspace_size(N))) != DSA_OK) return st;
+    if (!aligned16(q) || !aligned32(cache) || !aligned32(workspace)) return DSA_ERR_MISALIGNED;
+    if ((st = check_workspace(workspace, ws_bytes, key_weights_workspace(row_format, L, N, top_k))) != DSA_OK) return st;
     if ((st = check_device()) != DSA_OK) return st;
     return launch_key_weights_prefill(row_format, q, cache, cache_scale, idx, lse, L, N, top_k, scale, acc, accumulate,
                                       workspace, pt, static_cast<cudaStream_t>(stream));

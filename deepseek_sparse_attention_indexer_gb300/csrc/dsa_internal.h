@@ -62,6 +62,7 @@ struct PageTable {
 };
 
 inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+inline size_t round_up(size_t n) { return (n + 255) / 256 * 256; }   // parts of a workspace
 
 // Launch entry points implemented in the kernel files.
 dsa_status_t launch_indexer(const void* q_idx, const void* k_idx, const float* w, const int32_t* q_pos0,
@@ -116,6 +117,7 @@ dsa_status_t launch_indexer_norm_rope(const void* q, int64_t q_stride, const voi
                                       float eps, const float* cos_sin, int max_pos, int interleave,
                                       const int32_t* pos, const int32_t* slots, int R, void* q_out, void* k_cache,
                                       int cache_rows, cudaStream_t stream);
+size_t key_weights_workspace(int format, int L, int N, int top_k);
 dsa_status_t launch_key_weights_prefill(int format, const void* q, const void* cache, const float* cache_scale,
                                         const int32_t* idx, const float* lse, int L, int N, int top_k, float scale,
                                         float* acc, int accumulate, void* workspace, const PageTable& pages,

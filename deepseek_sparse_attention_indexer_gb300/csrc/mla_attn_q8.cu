@@ -1117,8 +1117,6 @@ dsa_status_t launch_rows(AttnQ8Params p, int rows, void* workspace, cudaStream_t
 // 2016 / 1593.
 bool want_expanded(int rows, int top_k, int N) { return (long long)rows * top_k >= 3LL * N + 24576; }
 
-size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
-
 }  // namespace
 
 size_t attn_q8_workspace(int rows, int top_k) {

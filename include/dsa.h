@@ -491,13 +491,15 @@ dsa_status_t mla_sparse_attn_decode_q4_paged(const void *q, const void *cache, c
  * probabilities are at most 64); a NaN counts 0.  Entries of idx behind the cache are recorded as
  * DSA_ERR_DEVICE_BOUNDS and skipped, negative ones skipped; a key given twice in a query counts twice.
  * Prefill adds whole numbers of 2^-shift, L * 128 * 2^shift <= 2^62, in a workspace of
- * mla_key_weights_workspace_size(N) bytes (8-byte aligned): the sums do not depend on any order, and so
- * the same call gives the same bits.  Decode needs none, and has each sequence's keys once.
+ * mla_key_weights_workspace_size(row_format, L, N, top_k) bytes (32-byte aligned): the sums do not depend
+ * on any order, and so the same call gives the same bits.  (A prefill over the 4-bit cache whose queries
+ * select each key many times holds the N rows there as 8-bit ones.)  Decode needs none, and has each
+ * sequence's keys once.
  * Errors (host): DSA_ERR_INVALID_ARG for a null pointer (a cache_scale with bf16 rows too), sizes < 1, a
  * scale that is not positive and finite, accumulate not 0 or 1; DSA_ERR_UNSUPPORTED_SHAPE for top_k and
  * sizes as in the attention calls; DSA_ERR_MISALIGNED; DSA_ERR_WORKSPACE_TOO_SMALL.
  */
-size_t mla_key_weights_workspace_size(int N);
+size_t mla_key_weights_workspace_size(int row_format, int L, int N, int top_k);
 dsa_status_t mla_key_weights_prefill(const void *q, const void *cache, const float *cache_scale,
                                      int row_format, const int32_t *block_table, int page_size,
                                      int num_pages, const int32_t *idx, const float *lse, int L, int N,

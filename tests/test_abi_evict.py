@@ -38,8 +38,11 @@ def test_key_weights_prefill_refusals(lib):
     good = (P, P, P, 2, P, 64, 8, P, P, 4, 256, 64, 0.0625, P, 0, P, 1 << 20, None)
     refusals(lib.mla_key_weights_prefill, names, good, WEIGHTS_BAD)
     refusals(lib.mla_key_weights_prefill, names, good,
-             {INVALID: [{"ws": None}, {"pages": 0}], ALIGN: [{"ws": P + 4}], SMALL: [{"bytes": 256 * 8 - 1}]})
-    assert lib.mla_key_weights_workspace_size(256) == 2048 and lib.mla_key_weights_workspace_size(0) == 0
+             {INVALID: [{"ws": None}, {"pages": 0}], ALIGN: [{"ws": P + 16}], SMALL: [{"bytes": 256 * 8 - 1}]})
+    size = lib.mla_key_weights_workspace_size
+    assert size(2, 4, 256, 64) == size(0, 4096, 256, 64) == size(1, 4096, 256, 64) == 2048
+    assert size(2, 4096, 256, 64) >= 256 * (8 + 640 + 4)                  # the rows expanded
+    assert size(3, 4, 256, 64) == size(-1, 4, 256, 64) == size(0, 0, 256, 64) == size(0, 4, 0, 64) == size(0, 4, 256, 2049) == 0
 
 
 def test_key_weights_decode_refusals(lib):

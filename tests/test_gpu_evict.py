@@ -278,6 +278,40 @@ def test_weights_record_keys_outside_the_cache(dsa, fmt):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("page", [0, 16])
+def test_weights_over_expanded_rows(dsa, page):
+    """A 4-bit prefill that selects each key many times: the weights of the 8-bit rows of the same values; a page outside
+    the pool is recorded where a query selects it, and only there."""
+    g = gen(8)
+    N, L, K = 500, 320, 450
+    assert dsa.key_weights_workspace_size(L, K, N, 2) > N * 648
+    cache, scale = make_cache(g, "q4", N)
+    eight = torch.cat([(values("q4", cache, scale)[:, :512] / scale[:, None].double()).float().to(F8).view(torch.uint8), cache[:, 288:]], 1)
+    idx, q, lse = choose(g, [N - 20] * L, N, K), randn(g, L, 64, 576).bfloat16(), torch.full((L, 64), 6.0, device="cuda")
+    want = dsa.mla_key_weights_prefill(q, eight, idx, lse, SCALE, cache_scale=scale)
+    if not page:
+        assert torch.equal(dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale), want)
+        ws = torch.full((dsa.key_weights_workspace_size(L, K, N, 2) + 64,), 0xEE, dtype=torch.uint8, device="cuda")
+        got = dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale, workspace=ws[:-64])
+        assert torch.equal(got, want) and bool((ws[-64:] == 0xEE).all())
+        # as many queries as are read directly, a few at a time
+        few = torch.zeros(N, device="cuda", dtype=torch.float64)
+        for i in range(0, L, 8):
+            few += dsa.mla_key_weights_prefill(q[i:i + 8], cache, idx[i:i + 8], lse[i:i + 8], SCALE, cache_scale=scale).double()
+        assert bool(((few - want.double()).abs() <= 2.0 ** -22 * want.double()).all())   # roundings to float32: 41 of them
+        return
+    pool, pscale, table, pages = paged(g, cache[None], scale[None], [N], page)
+    table[0, -1] = pages                                                  # keys that nothing selects
+    call = lambda: dsa.mla_key_weights_prefill(q, pool, idx, lse, SCALE, cache_scale=pscale, block_table=table[0],  # noqa: E731
+                                               page_size=page, N=N)
+    assert torch.equal(call(), want) and dsa.device_status() == 0
+    table[0, 2] = -1
+    got = call()
+    assert dsa.device_status() == 7
+    want[2 * page:3 * page] = 0.0
+    assert torch.equal(got, want)
+
+
 def test_weights_past_32_bits(dsa):
     g = gen(6)
     N = (1 << 32) // 1152 + 3000
@@ -357,7 +391,7 @@ def check_plan(dsa, acc, pos, kv_len, keep, recent, sink):
 
 PLANS = [(1, 2, 1, 0, 0), (3, 3, 2, 1, 1), (70, 100, 37, 5, 2), (2, 2048, 2047, 100, 4), (5, 2049, 1, 1, 0), (5, 2049, 1000, 0, 0),
          (3, 5000, 4999, 0, 7), (8, 4096, 2048, 256, 4), (2, 16385, 8000, 8000, 0), (40, 9001, 3000, 300, 3), (1, 70001, 65536, 4096, 4),
-         (1, 400001, 100000, 512, 4)]
+         (1, 389000, 200000, 1000, 0), (1, 400001, 100000, 512, 4)]
 
 
 @pytest.mark.parametrize("B,N,keep,recent,sink", PLANS)
