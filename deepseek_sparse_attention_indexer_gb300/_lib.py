@@ -845,7 +845,7 @@ def cache_move_rows(src: torch.Tensor, dst: torch.Tensor, dense=(), paged=(), bl
             _bad("dense tensors are contiguous [B, Nmax, ...] on the current CUDA device")
         Nmax = shape[1]
         ptrs.append(t.data_ptr())
-        sizes.append(t.stride(1) * t.element_size())
+        sizes.append(t.nbytes // max(B * Nmax, 1))
     pt, stride, pages = None, 0, 0
     if paged:
         if block_table is None or page_size < 1:
@@ -859,7 +859,7 @@ def cache_move_rows(src: torch.Tensor, dst: torch.Tensor, dense=(), paged=(), bl
                 _bad("paged tensors are contiguous [num_pages * page_size, ...] on the current CUDA device")
             rows = shape[0]
             ptrs.append(t.data_ptr())
-            sizes.append(t.stride(0) * t.element_size())
+            sizes.append(t.nbytes // max(rows, 1))
         pages = rows // page_size
         if Nmax is None:
             Nmax = stride * page_size

@@ -522,6 +522,23 @@ def test_moves_record_what_is_out_of_range(dsa):
     assert dsa.device_status() == 7 and torch.equal(pool, before)
 
 
+def test_moves_of_odd_tensors(dsa):
+    """A sequence of one row, whose strides say nothing; bases that are not 16-byte aligned; a row of 4000 bytes."""
+    one = torch.arange(6, dtype=torch.int32, device="cuda").view(3, 2).t()[:1].t()     # [3, 1], strides of a wider tensor
+    one = one.as_strided((3, 1), (1, 77))
+    assert one.is_contiguous()
+    before = one.clone()
+    dsa.cache_move_rows(i32(0, 0, 0)[:, None].contiguous(), i32(0, 0, 0)[:, None].contiguous(), dense=(one,))
+    assert torch.equal(one, before)
+    flat = torch.arange(1 + 2 * 8 * 8, dtype=torch.int32, device="cuda")
+    odd, long = flat[1:].view(2, 8, 8), torch.arange(2 * 8 * 1000, dtype=torch.int32, device="cuda").view(2, 8, 1000)
+    want = odd.clone(), long.clone()
+    for t in want:
+        t[0, 1], t[1, 2], t[1, 0] = t[0, 6].clone(), t[1, 7].clone(), t[1, 4].clone()
+    dsa.cache_move_rows(i32(6, -1, 7, 4).view(2, 2), i32(1, -1, 2, 0).view(2, 2), dense=(odd, long))
+    assert torch.equal(odd, want[0]) and torch.equal(long, want[1]) and int(flat[0]) == 0 and dsa.device_status() == 0
+
+
 def test_moves_past_32_bits(dsa):
     N = (1 << 32) // 2048 + 4000
     t = torch.zeros(1, N, 512, dtype=torch.int32, device="cuda")
