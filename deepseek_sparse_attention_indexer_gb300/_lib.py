@@ -786,6 +786,8 @@ def mla_key_weights_decode(q: torch.Tensor, cache: torch.Tensor, kv_len: torch.T
             _bad("a paged cache needs Nmax and page_size")
         stride = _table(block_table, B)
         pt = _p(block_table, dev, _I32, B * stride, "block_table")
+        if stride < 1:                  # its pointer may be null, which would stand for dense rows
+            _bad("block_table is int32 [B, pages]")
     elif cache.dim() != 3 or cache.shape[0] != B or (Nmax is not None and Nmax != cache.shape[1]):
         _bad("the cache is [B, Nmax, row]")
     else:
@@ -823,7 +825,7 @@ def cache_evict_plan(acc: torch.Tensor, pos: torch.Tensor, kv_len: torch.Tensor,
         dst, left = _new((B, moves), torch.int32, acc.device, stream), _new((B,), torch.int32, acc.device, stream)
     rc = (_lib or load()).dsa_cache_evict_plan(
         _p(acc, dev, _F32, B * Nmax, "acc"), _p(pos, dev, _I32, B * Nmax, "pos"), _p(kv_len, dev, _I32, B, "kv_len"), B, Nmax,
-        keep, recent, sink, src.data_ptr(), dst.data_ptr(), left.data_ptr(), _stream_on(dev, stream))
+        keep, min(recent, Nmax), min(sink, Nmax), src.data_ptr(), dst.data_ptr(), left.data_ptr(), _stream_on(dev, stream))
     if rc:
         raise DsaError("dsa_cache_evict_plan", rc)
     return src, dst, left
@@ -864,8 +866,8 @@ def cache_move_rows(src: torch.Tensor, dst: torch.Tensor, dense=(), paged=(), bl
         if Nmax is None:
             Nmax = stride * page_size
     n = len(ptrs)
-    if not 1 <= n <= 8:
-        _bad("1 to 8 tensors")
+    if not 1 <= n <= 8 or max(sizes) > 1 << 20:
+        _bad("1 to 8 tensors, rows of at most 1 MB")
     bytes_, kinds = _move_arrays(tuple(sizes), len(dense))
     rc = (_lib or load()).dsa_cache_move_rows(
         _p(src, dev, _I32, B * moves, "src"), _p(dst, dev, _I32, B * moves, "dst"), B, moves, Nmax, n, (_P * n)(*ptrs),

@@ -716,6 +716,7 @@ dsa_status_t dsa_cache_move_rows(const int32_t* src, const int32_t* dst, int B, 
     bool any_paged = false;
     for (int i = 0; i < count; ++i) {
         if (!tensors[i] || row_bytes[i] < 4 || (paged[i] != 0 && paged[i] != 1)) return DSA_ERR_INVALID_ARG;
+        if (row_bytes[i] > (1 << 20)) return DSA_ERR_UNSUPPORTED_SHAPE;
         if (row_bytes[i] % 4 || !aligned4(tensors[i])) return DSA_ERR_MISALIGNED;
         any_paged = any_paged || paged[i];
     }

@@ -487,10 +487,11 @@ dsa_status_t mla_sparse_attn_decode_q4_paged(const void *q, const void *cache, c
  *   lse          f32 [L, 64] or [B, 64]; a lse of other keys than the selected (the log of the sum over
  *                several caches' parts) gives the weights relative to those
  *   acc          f32 [N], or [B, Nmax]: the sums of sequence b's keys; every key's is written with accumulate 0
- * Products are exact and accumulated in float32.  A key's weight in one query is at most 128 (64 heads'
+ * Products are exact and accumulated in float32.  The weight of an entry of idx is at most 128 (64 heads'
  * probabilities are at most 64); a NaN counts 0.  Entries of idx behind the cache are recorded as
  * DSA_ERR_DEVICE_BOUNDS and skipped, negative ones skipped; a key given twice in a query counts twice.
- * Prefill adds whole numbers of 2^-shift, L * 128 * 2^shift <= 2^62, in a workspace of
+ * Prefill adds whole numbers of 2^-shift, L * 128 * 2^shift <= 2^62 (64 bits hold a key that every
+ * query has up to four times, whatever lse; any that lse counts as often), in a workspace of
  * mla_key_weights_workspace_size(row_format, L, N, top_k) bytes (32-byte aligned): the sums do not depend
  * on any order, and so the same call gives the same bits.  (A prefill over the 4-bit cache whose queries
  * select each key many times holds the N rows there as 8-bit ones.)  Decode needs none, and has each
@@ -540,8 +541,8 @@ dsa_status_t dsa_cache_evict_plan(const float *acc, const int32_t *pos, const in
  *              multiple of 4; paged: 0 for [B, Nmax, ...] rows, 1 for a pool addressed through block_table
  * An entry >= Nmax or a page outside the pool is recorded as DSA_ERR_DEVICE_BOUNDS and not moved.
  * Errors (host): DSA_ERR_INVALID_ARG for a null pointer or a size < 1, row_bytes < 4, paged not 0 or 1;
- * DSA_ERR_UNSUPPORTED_SHAPE for count > 8, B > 65535, products above 2^31 - 1, page sizes as in
- * the paged calls; DSA_ERR_MISALIGNED.
+ * DSA_ERR_UNSUPPORTED_SHAPE for count > 8, rows above 1 MB, B > 65535, products above 2^31 - 1, page
+ * sizes as in the paged calls; DSA_ERR_MISALIGNED.
  */
 dsa_status_t dsa_cache_move_rows(const int32_t *src, const int32_t *dst, int B, int moves, int Nmax,
                                  int count, void *const *tensors, const int *row_bytes, const int *paged,

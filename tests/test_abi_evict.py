@@ -80,7 +80,8 @@ def test_move_rows_refusals(lib):
                 {"sizes": (4, 0)}, {"sizes": (-4, 4)}, {"kinds": (0, 2)}):
         assert call(**bad) == INVALID, bad
     for bad in ({"B": 65536}, {"page": 24}, {"moves": 1 << 30}, {"Nmax": 1 << 30, "page": 65536, "stride": 1 << 14, "pages": 1 << 15},
-                {"ptrs": (P,) * 9, "sizes": (4,) * 9, "kinds": (0,) * 9}):
+                {"ptrs": (P,) * 9, "sizes": (4,) * 9, "kinds": (0,) * 9}, {"sizes": (4, (1 << 20) + 4)},
+                {"sizes": ((1 << 31) - 4, 4)}):
         assert call(**bad) == SHAPE, bad
     for bad in ({"sizes": (4, 6)}, {"ptrs": (P + 2, P)}):
         assert call(**bad) == ALIGN, bad

@@ -622,6 +622,8 @@ def test_wrapper_refusals(dsa):
                 dict(block_table=i32(0, 0).view(2, 1)), dict(acc=torch.zeros(2, 9, device="cuda")), dict(kv_len=kv_len.cpu()), dict(Nmax=9)):
         with pytest.raises(ValueError):
             dsa.mla_key_weights_decode(**{**good, **bad})
+    with pytest.raises(ValueError):                                       # a table of no pages is not a dense cache
+        dsa.mla_key_weights_decode(**{**good, "cache": kv[0]}, block_table=i32().view(2, 0), page_size=16, Nmax=64)
     flat = dict(q=q, cache=kv[0], idx=idx, lse=lse, scale=SCALE)
     dsa.mla_key_weights_prefill(**flat)
     for bad in (dict(N=9), dict(block_table=i32(0)), dict(block_table=i32(0), page_size=16, N=17), dict(idx=idx.long()),
@@ -636,9 +638,12 @@ def test_wrapper_refusals(dsa):
             dsa.cache_evict_plan(**{**dict(acc=acc, pos=pos, kv_len=kv_len, keep=4), **bad})
     with pytest.raises(dsa.DsaError):
         dsa.cache_evict_plan(acc, pos, kv_len, 4, recent=3, sink=2)
+    with pytest.raises(dsa.DsaError):
+        dsa.cache_evict_plan(acc, pos, kv_len, 4, recent=1 << 32)          # not a number of 32 bits
     src, dst, _ = dsa.cache_evict_plan(acc, pos, kv_len, 4)
     for bad in (dict(), dict(dense=(acc, pos[:1])), dict(dense=(acc[:, :4],)), dict(paged=(acc,)), dict(dense=(acc,) * 9),
-                dict(dense=(acc, torch.zeros(2, 9, device="cuda"))), dict(dense=(acc.cpu(),))):
+                dict(dense=(acc, torch.zeros(2, 9, device="cuda"))), dict(dense=(acc.cpu(),)),
+                dict(dense=(torch.empty(2, 8, (1 << 18) + 1, device="cuda"),))):
         with pytest.raises(ValueError):
             dsa.cache_move_rows(src, dst, **bad)
     with pytest.raises(dsa.DsaError):
