@@ -203,11 +203,10 @@ __device__ __forceinline__ uint4 ldg_nc_v4(const void* p) {
     return v;
 }
 
-// A byte, 8 bytes, a float: not loaded later than written, as the compiler may a plain load.
-__device__ __forceinline__ uint32_t ldg_nc_u8(const void* p) {
-    uint32_t v;
-    asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(v) : "l"(p));
-    return v;
+// 16 bytes, 8 bytes, a float: not loaded later than written, as the compiler may a plain load.  They allocate in L1: what
+// another warp reads of the same sectors hits there.
+__device__ __forceinline__ void ldg_nc_v4(const void* p, uint32_t (&r)[4]) {
+    asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
 }
 __device__ __forceinline__ void ldg_nc_v2(const void* p, uint32_t& x, uint32_t& y) {
     asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "l"(p));

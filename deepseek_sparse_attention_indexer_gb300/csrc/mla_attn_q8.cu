@@ -588,11 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_attn_q8_kernel(const __grid_c
             float sc1 = kZeroRowScale;                // the scale of the rope warps' next row
             auto load_row = [&](int row) {
                 const uint8_t* src = row < 0 ? g_no_row : p.cache + (int64_t)row * kBytes;
-                const uint4 b = ldg_nc_v4(src + kQ4Codes + 8 * kChunk);
-                block[0] = b.x;
-                block[1] = b.y;
-                block[2] = b.z;
-                block[3] = b.w;
+                // (a sector that the latent and the rope warps share: without L1, decode of 256 sequences 145 -> 148.5 us)
+                ldg_nc_v4(src + kQ4Codes + 8 * kChunk, block);
                 load(x0, src, kChunk);
                 load(x1, src, kChunk + 1);
                 if (kRope) sc1 = row >= 0 ? ldg_nc_f32(p.cache_scale + row) : kZeroRowScale;
