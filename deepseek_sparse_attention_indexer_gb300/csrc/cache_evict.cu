@@ -9,12 +9,14 @@
 // are order-preserving 32-bit keys in shared memory, protected ones the largest; a radix select (11 + 11 + 10 bits,
 // the blocks' histograms summed through distributed shared memory) finds the last one that stays, and two scans give each
 // thread, which has a run of keys, the ranks of its equal keys, its gaps and its movers.  No sort, no atomics whose order
-// shows.  It is a chain of latencies: three histograms, four cluster barriers.
+// shows.  It is a chain of latencies: three histograms, four cluster barriers (8 sequences of 4096 keys 12.9 us, 64 of 16k
+// 18.9).
 //
 // Moves: a warp a run of entries, all tensors of the call in one launch.  The rows lie apart in HBM, so it is bytes in
 // flight that count: the run's indices and pages are looked up a lane each, and a lane loads its pieces of two moves, all
 // tensors, before it stores the first.  (A warp an entry: entries behind a sequence's last move, most of them, took 73 of 99
-// us for 64 sequences of up to 16k keys.)
+// us for 64 sequences of up to 16k keys.)  80 thousand moves of 1416 bytes, 226 MB read and written: 16 us behind the plan, not
+// far from HBM's copy rate with part of it still in L2.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -331,11 +333,12 @@ __global__ void __launch_bounds__(kMoveWarps * 32, 4) move_rows_kernel(const __g
 dsa_status_t launch_evict_plan(const float* acc, const int32_t* pos, const int32_t* kv_len, int B, int Nmax, int keep,
                                int recent, int sink, int32_t* src, int32_t* dst, int32_t* left, cudaStream_t stream) {
     PlanParams p{acc, pos, kv_len, Nmax, keep, recent, sink, keep < Nmax - keep ? keep : Nmax - keep, 0, src, dst, left};
-    // Blocks a sequence: one for 4096 keys, four for 32k, eight beyond (1 sequence of 4k / 16k / 64k keys, us: 1 block 17 /
-    // 31 / -, 2 16.7 / 23 / 51, 4 18 / 21 / 35, 8 24 / 26 / 32), but no more than one block an SM at once (64 of 16k: 1 block
-    // 31, 2 23, 4 44, 8 140), and enough that a part fits shared memory (one of 64k in one block 305).
+    // Blocks a sequence: one for 4096 keys, two for 8192, four for 32k, eight beyond (a sequence of 4k / 8k / 16k / 32k / 64k
+    // keys, us: 1 block 13.1 / 16.9 / 25.6 / 42.3 / -, 2 13.1 / 14.7 / 18.6 / 27.2 / 44.3, 4 14.5 / 15.8 / 17.3 / 21.2 / 30.1, 8
+    // 21.2 / 21.7 / 23.0 / 24.7 / 28.6), but no more than one block an SM at once (64 sequences of 16k: 1 block 26, 2 18.8, 4
+    // 36, 8 118), and enough that a part fits shared memory (one of 64k in one block 305).
     const int sms = device_sm_count();
-    int cluster = Nmax <= 4096 ? 1 : Nmax <= 32768 ? 4 : 8;
+    int cluster = Nmax <= 4096 ? 1 : Nmax <= 8192 ? 2 : Nmax <= 32768 ? 4 : 8;
     while (cluster > 1 && (long long)B * cluster * 9 > sms * 8) cluster /= 2;   // (clusters leave some SMs)
     while (cluster < 8 && ceil_div(Nmax, cluster) >= kKeysInSmem) cluster *= 2;
     const int part = ceil_div(Nmax, cluster);
