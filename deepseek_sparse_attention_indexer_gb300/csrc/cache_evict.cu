@@ -12,11 +12,12 @@
 // shows.  It is a chain of latencies: three histograms, four cluster barriers (8 sequences of 4096 keys 12.9 us, 64 of 16k
 // 18.9).
 //
-// Moves: a warp a run of entries, all tensors of the call in one launch.  The rows lie apart in HBM, so it is bytes in
-// flight that count: the run's indices and pages are looked up a lane each, and a lane loads its pieces of two moves, all
-// tensors, before it stores the first.  (A warp an entry: entries behind a sequence's last move, most of them, took 73 of 99
-// us for 64 sequences of up to 16k keys.)  80 thousand moves of 1416 bytes, 226 MB read and written: 16 us behind the plan, not
-// far from HBM's copy rate with part of it still in L2.
+// Moves: all tensors of the call in one launch of as many warps as the SMs hold.  The rows lie apart in HBM, so it is bytes
+// in flight that count: 32 entries' indices and pages are looked up at once, a lane each, and a lane loads its pieces of two
+// moves, all tensors, before it stores the first.  Most entries lie behind a sequence's last move, and sequences have few
+// or many, so a warp takes entries from all over.  79,491 moves of 1416 bytes in 64 sequences' 524,288 entries 43 us (225 MB,
+// 5.2 TB/s; a run of eight entries a warp 53, an entry a warp 99), 8175 in 8 sequences' 16,384 4.8 us (a warp an entry 7.6);
+// four blocks an SM, which spill, 44 and 5.0, two with four moves in flight 45 and 4.7.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -215,14 +216,13 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanParam
     cluster.sync();                                // no block leaves while its shared memory is read
 }
 
-constexpr int kMoveWarps = 8;
+constexpr int kMoveWarps = 8, kMoveBlocks = 3;     // warps a block, blocks an SM
 constexpr int kAhead = 3;                          // pieces of 16 bytes of a move that a lane loads before it stores
 
 struct MoveParams {
     const int32_t* src;
     const int32_t* dst;
-    int most, Nmax, count;
-    int run;                                       // entries a warp, at most 32
+    int B, most, Nmax, count;
     uint8_t* base[DSA_MAX_MOVED];                  // tensors of 16-byte pieces first
     int bytes[DSA_MAX_MOVED];
     int paged[DSA_MAX_MOVED];                      // 1: rows of a pool
@@ -246,83 +246,94 @@ __device__ __forceinline__ bool find_piece(const MoveParams& p, int u, int first
     return false;
 }
 
-__global__ void __launch_bounds__(kMoveWarps * 32, 4) move_rows_kernel(const __grid_constant__ MoveParams p) {
-    const int lane = threadIdx.x & 31, b = blockIdx.y;
-    const int m = (blockIdx.x * kMoveWarps + threadIdx.x / 32) * p.run + lane;
+__global__ void __launch_bounds__(kMoveWarps * 32, kMoveBlocks) move_rows_kernel(const __grid_constant__ MoveParams p) {
+    const int lane = threadIdx.x & 31;
     griddep_wait();
-    int from = -1, to = -1;
-    if (lane < p.run && m < p.most) {
-        from = __ldg(p.src + (int64_t)b * p.most + m);
-        to = __ldg(p.dst + (int64_t)b * p.most + m);
+    // The lane's pieces, the same of every move: where they lie in row 0 of their tensors, the tensors' bytes a row.
+    uint8_t* at[kAhead + 1];
+    int bytes[kAhead + 1];
+    bool paged[kAhead + 1];
+#pragma unroll
+    for (int k = 0; k <= kAhead; ++k) {
+        int i, o;
+        const bool mine = k < kAhead ? find_piece(p, lane + 32 * k, 0, p.wide, 16, i, o) : find_piece(p, lane, p.wide, p.count, 4, i, o);
+        at[k] = mine ? p.base[i] + o : nullptr;
+        bytes[k] = mine ? p.bytes[i] : 0;
+        paged[k] = mine && p.paged[i];
     }
-    bool ok = from >= 0 && to >= 0;
-    if (!__any_sync(0xffffffffu, ok)) return;
-    bool bad = ok && (from >= p.Nmax || to >= p.Nmax);
-    ok = ok && !bad;
-    int pf = -1, pt = -1;                          // rows of a pool (below 2^31)
-    if (ok && p.pages.table) {
-        pf = (int)paged_row(p.pages, b, from);
-        pt = (int)paged_row(p.pages, b, to);
-        bad = pf < 0 || pt < 0;
-    }
-    const bool pool = pf >= 0 && pt >= 0;          // else the paged tensors are left out
-    if (bad) raise_dev_error(p.status, DEV_ERR_BOUNDS);
-    // the lane's pieces, the same of every move
-    int tensor[kAhead + 1], at[kAhead + 1];
-    bool mine[kAhead + 1];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) mine[k] = find_piece(p, lane + 32 * k, 0, p.wide, 16, tensor[k], at[k]);
-    mine[kAhead] = find_piece(p, lane, p.wide, p.count, 4, tensor[kAhead], at[kAhead]);
-
-    struct Move {
-        int f, t, pf, pt;
-        bool pool;
+    struct Move {                                  // rows of the dense tensors and of the pools, -1: left out
+        int from[2], to[2];
     };
-    auto row = [&](const Move& v, int i, bool dest) {
-        const int64_t r = p.paged[i] ? (dest ? v.pt : v.pf) : (int64_t)b * p.Nmax + (dest ? v.t : v.f);
-        return p.base[i] + r * p.bytes[i];
-    };
-    uint32_t left = __ballot_sync(0xffffffffu, ok);
-    while (left) {
-        Move mv[2];
-        bool have[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            have[i] = left != 0;
-            const int l = left ? __ffs(left) - 1 : 0;
-            left &= left - 1;
-            mv[i] = Move{__shfl_sync(0xffffffffu, from, l), __shfl_sync(0xffffffffu, to, l), __shfl_sync(0xffffffffu, pf, l),
-                         __shfl_sync(0xffffffffu, pt, l), __shfl_sync(0xffffffffu, (int)pool, l) != 0};
-        }
-        uint4 v[2][kAhead];
-        uint32_t w[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (have[i] && mine[k] && (mv[i].pool || !p.paged[tensor[k]]))
-                    v[i][k] = *reinterpret_cast<const uint4*>(row(mv[i], tensor[k], false) + at[k]);
-            if (have[i] && mine[kAhead] && (mv[i].pool || !p.paged[tensor[kAhead]]))
-                w[i] = *reinterpret_cast<const uint32_t*>(row(mv[i], tensor[kAhead], false) + at[kAhead]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (!have[i]) break;
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (mine[k] && (mv[i].pool || !p.paged[tensor[k]]))
-                    *reinterpret_cast<uint4*>(row(mv[i], tensor[k], true) + at[k]) = v[i][k];
-            if (mine[kAhead] && (mv[i].pool || !p.paged[tensor[kAhead]]))
-                *reinterpret_cast<uint32_t*>(row(mv[i], tensor[kAhead], true) + at[kAhead]) = w[i];
-            for (int u = lane + 32 * kAhead; u < p.pieces; u += 32) {   // longer rows
-                int j, o;
-                if (!find_piece(p, u, 0, p.wide, 16, j, o) || (!mv[i].pool && p.paged[j])) continue;
-                *reinterpret_cast<uint4*>(row(mv[i], j, true) + o) = *reinterpret_cast<const uint4*>(row(mv[i], j, false) + o);
+    auto from = [](const Move& v, bool paged) { return paged ? v.from[1] : v.from[0]; };
+    auto to = [](const Move& v, bool paged) { return paged ? v.to[1] : v.to[0]; };
+    // Entry e is the (e / B)-th of a sequence; a warp's are as many apart as there are warps, 32 looked up at a time.  The
+    // sequences in turn, one further at each place, so that a warp meets all of them whatever the number of warps.
+    const uint32_t warps = gridDim.x * kMoveWarps, B = p.B, entries = B * p.most;   // entries < 2^31
+    for (uint32_t e0 = blockIdx.x * kMoveWarps + threadIdx.x / 32; e0 < entries; e0 += 32 * warps) {
+        const uint32_t e = e0 + lane * warps;
+        Move own{{-1, -1}, {-1, -1}};
+        if (e < entries) {
+            const uint32_t m = e / B;
+            const int b = (int)((e + m) % B);
+            const int from = __ldg(p.src + (int64_t)b * p.most + m), to = __ldg(p.dst + (int64_t)b * p.most + m);
+            bool bad = false;
+            if (from >= 0 && to >= 0 && !(bad = from >= p.Nmax || to >= p.Nmax)) {
+                own.from[0] = b * p.Nmax + from;   // below 2^31, as the rows of a pool
+                own.to[0] = b * p.Nmax + to;
+                if (p.pages.table) {
+                    own.from[1] = (int)paged_row(p.pages, b, from);
+                    own.to[1] = (int)paged_row(p.pages, b, to);
+                    bad = own.from[1] < 0 || own.to[1] < 0;
+                    if (bad) own.from[1] = -1;     // the paged tensors are left out
+                }
             }
-            for (int u = lane + 32; u < p.words; u += 32) {
-                int j, o;
-                if (!find_piece(p, u, p.wide, p.count, 4, j, o) || (!mv[i].pool && p.paged[j])) continue;
-                *reinterpret_cast<uint32_t*>(row(mv[i], j, true) + o) = *reinterpret_cast<const uint32_t*>(row(mv[i], j, false) + o);
+            if (bad) raise_dev_error(p.status, DEV_ERR_BOUNDS);
+        }
+        uint32_t left = __ballot_sync(0xffffffffu, own.from[0] >= 0);
+        while (left) {
+            Move mv[2];
+            uint4 v[2][kAhead];
+            uint32_t w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int l = left ? __ffs(left) - 1 : 0;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int f = __shfl_sync(0xffffffffu, own.from[j], l);
+                    mv[i].from[j] = left ? f : -1;
+                    mv[i].to[j] = __shfl_sync(0xffffffffu, own.to[j], l);
+                }
+                left &= left - 1;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (at[k] && from(mv[i], paged[k]) >= 0)
+                        v[i][k] = *reinterpret_cast<const uint4*>(at[k] + (int64_t)from(mv[i], paged[k]) * bytes[k]);
+                if (at[kAhead] && from(mv[i], paged[kAhead]) >= 0)
+                    w[i] = *reinterpret_cast<const uint32_t*>(at[kAhead] + (int64_t)from(mv[i], paged[kAhead]) * bytes[kAhead]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (at[k] && from(mv[i], paged[k]) >= 0)
+                        *reinterpret_cast<uint4*>(at[k] + (int64_t)to(mv[i], paged[k]) * bytes[k]) = v[i][k];
+                if (at[kAhead] && from(mv[i], paged[kAhead]) >= 0)
+                    *reinterpret_cast<uint32_t*>(at[kAhead] + (int64_t)to(mv[i], paged[kAhead]) * bytes[kAhead]) = w[i];
+                for (int u = lane + 32 * kAhead; u < p.pieces; u += 32) {   // longer rows
+                    int j, o;
+                    if (!find_piece(p, u, 0, p.wide, 16, j, o) || from(mv[i], p.paged[j]) < 0) continue;
+                    *reinterpret_cast<uint4*>(p.base[j] + (int64_t)to(mv[i], p.paged[j]) * p.bytes[j] + o) =
+                        *reinterpret_cast<const uint4*>(p.base[j] + (int64_t)from(mv[i], p.paged[j]) * p.bytes[j] + o);
+                }
+                for (int u = lane + 32; u < p.words; u += 32) {
+                    int j, o;
+                    if (!find_piece(p, u, p.wide, p.count, 4, j, o) || from(mv[i], p.paged[j]) < 0) continue;
+                    *reinterpret_cast<uint32_t*>(p.base[j] + (int64_t)to(mv[i], p.paged[j]) * p.bytes[j] + o) =
+                        *reinterpret_cast<const uint32_t*>(p.base[j] + (int64_t)from(mv[i], p.paged[j]) * p.bytes[j] + o);
+                }
             }
         }
     }
@@ -377,6 +388,7 @@ dsa_status_t launch_move_rows(const int32_t* src, const int32_t* dst, int B, int
     MoveParams p{};
     p.src = src;
     p.dst = dst;
+    p.B = B;
     p.most = most;
     p.Nmax = Nmax;
     for (int pass = 0; pass < 2; ++pass) {         // the tensors of whole 16-byte pieces, then the others
@@ -393,12 +405,8 @@ dsa_status_t launch_move_rows(const int32_t* src, const int32_t* dst, int B, int
     }
     p.pages = pages;
     p.status = device_status_ptr();
-    // A warp an entry while there are no more than four rounds of the 32 warps an SM holds, up to eight entries a warp
-    // beyond.  One / eight a warp, us: 16k entries (8k moves) 4.5 / 9, 524k (80k) 99 / 44.
-    const long long entries = (long long)B * most, at_once = 128LL * device_sm_count();
-    p.run = 1;
-    while (p.run < 8 && entries > at_once * p.run) p.run *= 2;
-    if (launch_pdl(move_rows_kernel, dim3(ceil_div(most, kMoveWarps * p.run), B), dim3(kMoveWarps * 32), 0, stream, p) != cudaSuccess)
+    const int blocks = kMoveBlocks * device_sm_count(), need = (int)(((long long)B * most + kMoveWarps - 1) / kMoveWarps);
+    if (launch_pdl(move_rows_kernel, dim3(need < blocks ? need : blocks), dim3(kMoveWarps * 32), 0, stream, p) != cudaSuccess)
         return DSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
