@@ -591,10 +591,10 @@ __global__ void __launch_bounds__(low::kThreads, 1)
             bool has = feed.fetch(p, lane, r, 0), more = has;
             if (has) {
                 feed.resolve(p, row);
-                load();
                 more = feed.fetch(p, lane, r, 0);
             }
             for (; has; n += kChunks) {
+                load();                            // (at the loop's end the loads were waited for there: 56 us for 52)
                 if (more) feed.resolve(p, next);
                 has = more;
                 more = more && feed.fetch(p, lane, r, 0);
@@ -628,7 +628,6 @@ __global__ void __launch_bounds__(low::kThreads, 1)
                 }
                 if (!ok) break;
                 row[0] = next[0];
-                if (has) load();
             }
         }
         cp_async_wait_all();
