@@ -20,6 +20,10 @@
 //   * Decode adds a key's weight to its float32 sum: one thread a key (the same key twice adds the same number twice).
 //     A prefill's queries meet at keys in any order, so they add whole numbers, 2^-shift each, in 64 bits, and a second
 //     kernel makes floats of them: the same bits every time.
+//   * Measured: 4096 queries of 2048 of 16k keys 0.77 ms over bf16 rows (0.41 of the bf16 matrix peak, 12.5 TB/s gathered from
+//     L2), 0.87 over 8-bit, 0.88 over 4-bit rows; decode of 128 sequences of up to 8192 keys 52 us over 4-bit, 44 over 8-bit
+//     rows, of 8 over bf16 rows 7.8.  Bound by the instructions of the gathering warps (the issue slots are half busy, a
+//     warp gets one every 13 cycles), over 4-bit rows by the expansion.
 #include <cuda.h>
 
 #include <atomic>
