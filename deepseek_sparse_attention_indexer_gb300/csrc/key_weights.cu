@@ -93,39 +93,36 @@ __device__ __forceinline__ void for_items(const WeightParams& p, uint32_t lane, 
     }
 }
 
-// The rows of a gathering lane, R a tile, tile after tile over all items, in two steps so that the loads of one are in
-// flight while the warp copies: fetch() loads the keys of the next tile, resolve() makes cache rows of them (a page
-// lookup when paged).
-template <int R>
+// The row of a gathering lane, one a tile, tile after tile over all items, in two steps so that the loads of one are in
+// flight while the warp copies: fetch() loads the key of the next tile, resolve() makes a cache row of it (a page lookup
+// when paged).
 struct Feed {
     int s = 0, tiles = 0;              // next item; tiles of the current one still to fetch
-    int slot = 0;                      // of the lane's first row in the next tile
+    int slot = 0;                      // of the lane's row in the next tile
     Item I{};
-    int key[R], batch = 0, bound = 0;
+    int key = -1, batch = 0, bound = 0;
 
-    __device__ __forceinline__ bool fetch(const WeightParams& p, uint32_t lane, int r0, int step) {
+    __device__ __forceinline__ bool fetch(const WeightParams& p, uint32_t lane, int r) {
         while (tiles == 0) {
             const int it = nth_item(p, s++);
             if (it == -1) return false;
             if (it < 0) continue;
             I = item_at(p, it);
             tiles = item_tiles(p, I, lane);
-            slot = I.slot0 + r0;
+            slot = I.slot0 + r;
         }
-#pragma unroll
-        for (int i = 0; i < R; ++i) key[i] = key_at(p, I, slot + i * step);
+        key = key_at(p, I, slot);
         batch = I.batch;
         bound = I.bound;
         slot += kTile;
         --tiles;
         return true;
     }
-    __device__ __forceinline__ void resolve(const WeightParams& p, int (&row)[R]) const {
+    __device__ __forceinline__ int resolve(const WeightParams& p) const {
         Item at{};
         at.batch = batch;
         at.bound = bound;
-#pragma unroll
-        for (int i = 0; i < R; ++i) row[i] = key_row(p, p.pages, at, key[i]);
+        return key_row(p, p.pages, at, key);
     }
 };
 
@@ -140,16 +137,21 @@ __device__ __forceinline__ bool warp_poll(uint64_t* bar, uint32_t parity, uint32
 __device__ __align__(16) uint8_t g_no_row[2 * kQDim];   // zeros, the row of a key that is not there
 
 // 128 bytes of each of the lane's rows (r0 + 4 i of the tile, eight lanes a row, this lane's 16 bytes the j-th: src) to a
-// slot.  One instruction a row: the gathering warps' instructions are what a tile of bf16 or 8-bit rows waits for.
+// slot.  One instruction a row, and a row looked up by one lane: the gathering warps' instructions are what a tile of bf16
+// or 8-bit rows waits for.
 struct RowCopy {
     const uint8_t* src[8];
     uint32_t even, odd;                            // offsets in a slot of the rows of even and of odd i, less 512 i
 
     __device__ __forceinline__ RowCopy(int r0, int j)
         : even(r0 * 128 + ((j ^ (r0 & 7)) << 4)), odd(r0 * 128 + ((j ^ (r0 & 7) ^ 4) << 4)) {}
-    __device__ __forceinline__ void point(const WeightParams& p, const int (&row)[8], int bytes, int j) {
+    // row: the cache row of the warp's lane-th row of the tile
+    __device__ __forceinline__ void point(const WeightParams& p, int row, int bytes, int j, uint32_t lane) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) src[i] = (row[i] < 0 ? g_no_row : p.cache + (int64_t)row[i] * bytes) + 16 * j;
+        for (int i = 0; i < 8; ++i) {
+            const int r = __shfl_sync(0xffffffffu, row, 4 * i + (int)(lane >> 3));
+            src[i] = (r < 0 ? g_no_row : p.cache + (int64_t)r * bytes) + 16 * j;
+        }
     }
     __device__ __forceinline__ void copy(int at, uint32_t slot) const {
 #pragma unroll
@@ -314,19 +316,20 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
         const int quad = warp & 3, g0 = (warp - kFirstGather) >> 2 << 1;
         const int j = (int)lane & 7, r0 = quad * 32 + (int)(lane >> 3);
         const uint32_t keys = smem_u32(smem) + OFF_K;
-        Feed<8> feed;
+        const int r = quad * 32 + (int)lane;       // the row the lane looks up
+        Feed feed;
         RowCopy rows(r0, j);
-        int row[8];
-        bool has = feed.fetch(p, lane, r0, 4), more = has;
+        int row = -1;
+        bool has = feed.fetch(p, lane, r), more = has;
         if (has) {
-            feed.resolve(p, row);
-            more = feed.fetch(p, lane, r0, 4);
+            row = feed.resolve(p);
+            more = feed.fetch(p, lane, r);
         }
         for (int gt = 0; has; ++gt) {
-            rows.point(p, row, 2 * kQDim, j);
-            if (more) feed.resolve(p, row);
+            rows.point(p, row, 2 * kQDim, j, lane);
+            if (more) row = feed.resolve(p);
             has = more;
-            more = more && feed.fetch(p, lane, r0, 4);
+            more = more && feed.fetch(p, lane, r);
             bool ok = true;
             auto part = [&](auto which) {          // the chunks as constants: offsets in the instructions
                 constexpr int g = decltype(which)::value;
@@ -553,19 +556,20 @@ __global__ void __launch_bounds__(low::kThreads, 1)
         auto free = [&](int c) { return wait(&empty[(n + c) % kSlots], ((n + c) / kSlots & 1) ^ 1); };
         if constexpr (!Q4) {
             const int j = (int)lane & 7, r0 = quad * 32 + (int)(lane >> 3);
-            Feed<8> feed;
+            const int r = quad * 32 + (int)lane;   // the row the lane looks up
+            Feed feed;
             RowCopy rows(r0, j);
-            int row[8];
-            bool has = feed.fetch(p, lane, r0, 4), more = has;
+            int row = -1;
+            bool has = feed.fetch(p, lane, r), more = has;
             if (has) {
-                feed.resolve(p, row);
-                more = feed.fetch(p, lane, r0, 4);
+                row = feed.resolve(p);
+                more = feed.fetch(p, lane, r);
             }
             for (; has; n += kChunks) {
-                rows.point(p, row, kBytes, j);
-                if (more) feed.resolve(p, row);
+                rows.point(p, row, kBytes, j, lane);
+                if (more) row = feed.resolve(p);
                 has = more;
-                more = more && feed.fetch(p, lane, r0, 4);
+                more = more && feed.fetch(p, lane, r);
                 bool ok = true;
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {   // the rope dims follow the latent dims, 128 bytes too
@@ -579,11 +583,11 @@ __global__ void __launch_bounds__(low::kThreads, 1)
         } else {
             const int r = quad * 32 + (int)lane;   // the lane's row of a tile
             const uint32_t table = smem_u32(smem) + OFF_TABLE;
-            Feed<1> feed;
-            int row[1], next[1];
+            Feed feed;
+            int row = -1, next = -1;
             uint32_t x[2][16], b[2][2];
             auto load = [&] {                      // both chunks' codes, ahead of the waits for their places
-                const uint8_t* src = p.cache + (int64_t)max(row[0], 0) * kBytes;
+                const uint8_t* src = p.cache + (int64_t)max(row, 0) * kBytes;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int c = set + 2 * h;
@@ -592,22 +596,22 @@ __global__ void __launch_bounds__(low::kThreads, 1)
                     ldg_nc_v2(src + kQ4Codes + 8 * c, b[h][0], b[h][1]);
                 }
             };
-            bool has = feed.fetch(p, lane, r, 0), more = has;
+            bool has = feed.fetch(p, lane, r), more = has;
             if (has) {
-                feed.resolve(p, row);
-                more = feed.fetch(p, lane, r, 0);
+                row = feed.resolve(p);
+                more = feed.fetch(p, lane, r);
             }
             for (; has; n += kChunks) {
                 load();                            // (at the loop's end the loads were waited for there: 56 us for 52)
-                if (more) feed.resolve(p, next);
+                if (more) next = feed.resolve(p);
                 has = more;
-                more = more && feed.fetch(p, lane, r, 0);
+                more = more && feed.fetch(p, lane, r);
                 bool ok = true;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int c = set + 2 * h;
                     if (!(ok = ok && free(c))) break;
-                    if (row[0] < 0) b[h][0] = b[h][1] = 0xffffffffu;   // zeros
+                    if (row < 0) b[h][0] = b[h][1] = 0xffffffffu;   // zeros
                     const uint32_t dst = ring + (n + c) % kSlots * kBlk + r * 128 + ((r & 7) << 4);
                     uint2 tb = lds_v2(table + 8 * (b[h][0] & 0xff));
 #pragma unroll
@@ -623,15 +627,15 @@ __global__ void __launch_bounds__(low::kThreads, 1)
                 }
                 if (ok && ((n ^ set) & 1) == 0) {  // the rope dims by the sets in turn
                     if ((ok = free(4))) {
-                        const uint8_t* src = p.cache + (int64_t)max(row[0], 0) * kBytes + kQ4Rope;
+                        const uint8_t* src = p.cache + (int64_t)max(row, 0) * kBytes + kQ4Rope;
                         const uint32_t dst = ring + (n + 4) % kSlots * kBlk + r * 128 + ((r & 7) << 4);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) cp_async_16(dst ^ (i << 4), src + 16 * i, row[0] >= 0 ? 16u : 0u);
+                        for (int i = 0; i < 8; ++i) cp_async_16(dst ^ (i << 4), src + 16 * i, row >= 0 ? 16u : 0u);
                         cp_async_arrive_noinc(&full[(n + 4) % kSlots]);
                     }
                 }
                 if (!ok) break;
-                row[0] = next[0];
+                row = next;
             }
         }
         cp_async_wait_all();

@@ -475,7 +475,8 @@ def moved_by_hand(t, src, dst, rows):
     return t
 
 
-@pytest.mark.parametrize("B,N,keep,page", [(1, 2, 1, 0), (3, 100, 40, 16), (9, 1000, 700, 64), (2, 9000, 4000, 256)])
+@pytest.mark.parametrize("B,N,keep,page", [(1, 2, 1, 0), (3, 100, 40, 16), (9, 1000, 700, 64), (2, 9000, 4000, 256),
+                                           (700, 40, 20, 16), (5000, 3, 2, 0)])
 def test_moves(dsa, B, N, keep, page):
     """Rows of 4 to 2048 bytes, 16-byte ones and others, dense and paged in one call; all other rows stay."""
     g = gen(B * N)
