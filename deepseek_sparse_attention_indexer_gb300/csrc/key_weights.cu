@@ -178,7 +178,8 @@ __device__ __forceinline__ void stage_lse(const WeightParams& p, const Item& I, 
     __syncwarp();
 }
 
-__device__ __forceinline__ float2 pair(const uint32_t (&v)[16], int k) {
+template <int N>
+__device__ __forceinline__ float2 pair(const uint32_t (&v)[N], int k) {
     return make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
 }
 
@@ -378,15 +379,17 @@ __global__ void __launch_bounds__(wide::kThreads, 1)
                     tmem_ld16(d + 128 + h, u);
                     tmem_ld16(d + 192 + h, v);
                     tmem_ld_wait();
+                    if (h == kH - 16) {            // all read: free before the last exponentials
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_free[gt & 1]);
+                    }
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const float2 x = __ffma2_rn(__fadd2_rn(s[k], __fadd2_rn(pair(u, k), pair(v, k))), sc, nl[h / 2 + k]);
                         sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_free[gt & 1]);
                 add_weight(p, I, key, row, sum);
             }
             return true;
@@ -711,24 +714,35 @@ __global__ void __launch_bounds__(low::kThreads, 1)
                 tc_fence_after();
                 const uint32_t d = tmem_base + lane_addr + kAccCols * (gt & 1);
                 float2 sum = make_float2(0.f, 0.f);
+                // Eight heads' columns are loaded while those before are summed, and the accumulator is free when the last have
+                // come (4096 queries 0.75 -> 0.70 ms).  (The registers pass through an empty statement after the wait, so that no use comes before it.)
+                uint32_t v[2][3][8];
+                auto load = [&](int h) {
 #pragma unroll
-                for (int h = 0; h < kH; h += 16) {
-                    uint32_t hi[16], lo[16], ro[16];
-                    tmem_ld16(d + h, hi);
-                    tmem_ld16(d + 64 + h, lo);
-                    tmem_ld16(d + 128 + h, ro);
+                    for (int part = 0; part < 3; ++part) tmem_ld8(d + 64 * part + h, v[h / 8 & 1][part]);
+                };
+                load(0);
+#pragma unroll
+                for (int h = 0; h < kH; h += 8) {
+                    uint32_t (&u)[3][8] = v[h / 8 & 1];
                     tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float2 x = __ffma2_rn(__ffma2_rn(pair(lo, k), sixteenth, pair(hi, k)),
+                    for (int k = 0; k < 24; ++k) asm volatile("" : "+r"(u[k / 8][k % 8]));
+                    if (h < kH - 8) {
+                        load(h + 8);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&acc_free[gt & 1]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 x = __ffma2_rn(__ffma2_rn(pair(u[1], k), sixteenth, pair(u[0], k)),
                                                     __fmul2_rn(qs[h / 2 + k], make_float2(c, c)),
-                                                    __ffma2_rn(pair(ro, k), sr, nl[h / 2 + k]));
+                                                    __ffma2_rn(pair(u[2], k), sr, nl[h / 2 + k]));
                         sum = __fadd2_rn(sum, make_float2(ex2_approx(x.x), ex2_approx(x.y)));
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_free[gt & 1]);
                 add_weight(p, I, key, row, sum);
             }
             ++qi;
