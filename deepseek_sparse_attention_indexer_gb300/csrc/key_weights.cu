@@ -20,10 +20,11 @@
 //   * Decode adds a key's weight to its float32 sum: one thread a key (the same key twice adds the same number twice).
 //     A prefill's queries meet at keys in any order, so they add whole numbers, 2^-shift each, in 64 bits, and a second
 //     kernel makes floats of them: the same bits every time.
-//   * Measured: 4096 queries of 2048 of 16k keys 0.77 ms over bf16 rows (0.41 of the bf16 matrix peak, 12.5 TB/s gathered from
-//     L2), 0.87 over 8-bit, 0.88 over 4-bit rows; decode of 128 sequences of up to 8192 keys 52 us over 4-bit, 44 over 8-bit
-//     rows, of 8 over bf16 rows 7.8.  Bound by the instructions of the gathering warps (the issue slots are half busy, a
-//     warp gets one every 13 cycles), over 4-bit rows by the expansion.
+//   * Measured: 4096 queries of 2048 of 16k keys 0.76 ms over bf16 rows (0.42 of the bf16 matrix peak, 12.7 TB/s gathered from
+//     L2), 0.70 over 8-bit and 4-bit rows; decode of 128 sequences of up to 8192 keys 52 us over 4-bit, 38 over 8-bit, 54 over
+//     bf16 rows, of 8 over bf16 rows 7.5.  What bounds it (traces): bf16 rows the bytes in flight, one tile's 147 KB for the 3500
+//     cycles of copy (2000), MMA and barriers; 8-bit rows the MMA phases of the two issuers, which fall together and then
+//     wait together for the epilogue (3100 cycles a tile); 4-bit rows in decode the expansion.
 #include <cuda.h>
 
 #include <atomic>
@@ -824,11 +825,12 @@ WeightParams base_params(const void* q, const void* cache, const float* cache_sc
     return p;
 }
 
-// A prefill over the 4-bit cache expands its rows to 8-bit ones first where the queries select each key ten times or more:
-// a selected key then costs 0.103 ns in place of 0.127, a key of the cache 0.2 ns and the launch 2 us (4096 queries of 2048 of
-// 16k keys 1067 -> 878 us).
+// A prefill over the 4-bit cache expands its rows to 8-bit ones first where the queries select each key six times or more:
+// a selected key then costs 0.09 ns in place of 0.127, a key of the cache 0.2 ns and the launch 2 us.  Direct / expanded, us: 16
+// queries of 2048 of 2k keys 13.0 / 13.3, 32 17.6 / 16.0; 64 of 8k 26 / 22; 304 of 16k 79 / 58, of 65k (9.5 times each) 81 / 68;
+// 608 of 131k (9.5) 164 / 138; 2432 of 262k 690 / 506.
 bool want_expanded(int format, int L, int N, int top_k) {
-    return format == DSA_ROWS_Q4 && (long long)L * top_k >= 10LL * N + 131072;
+    return format == DSA_ROWS_Q4 && (long long)L * top_k >= 6LL * N + 49152;
 }
 
 }  // namespace
