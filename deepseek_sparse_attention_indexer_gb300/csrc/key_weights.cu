@@ -412,6 +412,10 @@ namespace low {
 constexpr int kChunks = 5;                         // four of 128 latent dims, the rope dims
 constexpr int kSlots = 9;                          // chunk n of the CTA lies in slot n % 9
 constexpr int kQueryWarps = 8;                     // eight heads each
+// Places of the query heads' scales.  Those of item n are written when the MMAs of item n - 2 are known to be done.  With items
+// of one tile these waited only for accumulators that the epilogue gives free before its last reads of the scales: of items
+// n - 4 and, by the other set of warps, n - 5.  So six places at least.
+constexpr int kScalePlaces = 8;
 // warps 0 and 2 MMA, 1 and 3 none, 4-11 gather, 12-19 queries, 20-27 epilogue
 constexpr int kFirstGather = 4, kFirstQuery = 12, kFirstEpi = kFirstQuery + kQueryWarps;
 constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
@@ -423,8 +427,8 @@ constexpr int OFF_QHL = 0;                         // 4 chunks x (64 hi rows, 64
 constexpr int OFF_QR = OFF_QHL + 4 * kBlk;         // rope dims of 64 heads, bf16
 constexpr int OFF_K = OFF_QR + kQBlk;
 constexpr int OFF_LSE = OFF_K + kSlots * kBlk;     // float [8][64], a copy an epilogue warp
-constexpr int OFF_QS = OFF_LSE + kEpiWarps * kH * 4;   // float [4][64]: scale log2(e) 2^k of a query's heads
-constexpr int OFF_TABLE = OFF_QS + 4 * kH * 4;     // uint2 [256]: the magnitudes of 4-bit codes as e4m3, by block byte
+constexpr int OFF_QS = OFF_LSE + kEpiWarps * kH * 4;   // float [8][64]: scale log2(e) 2^k of a query's heads
+constexpr int OFF_TABLE = OFF_QS + kScalePlaces * kH * 4;   // uint2 [256]: the magnitudes of 4-bit codes as e4m3, by block byte
 constexpr int OFF_BAR = OFF_TABLE + 256 * 8;
 constexpr int kBars = 2 * kSlots + 3 + 4;          // full[9], empty[9], q_full, qr_full, q_free, acc_full[2], acc_free[2]
 constexpr int OFF_TMEM = OFF_BAR + kBars * 8;
@@ -672,8 +676,7 @@ __global__ void __launch_bounds__(low::kThreads, 1)
                 for (int k = 0; k < 4; ++k)
                     split_e4m3x4(bf16_lo(w[2 * k]) * inv, bf16_hi(w[2 * k]) * inv, bf16_lo(w[2 * k + 1]) * inv,
                                  bf16_hi(w[2 * k + 1]) * inv, hi[i][k], lo[i][k]);
-                // (a place of four: the epilogue may be at the tiles of the item before the last)
-                if (lane == 0) qs_s[(qi & 3) * kH + h0 + i] = p.scale_log2 * exp2_int(e);
+                if (lane == 0) qs_s[(qi & (kScalePlaces - 1)) * kH + h0 + i] = p.scale_log2 * exp2_int(e);
             }
             if (!wait(q_free, (qi & 1) ^ 1)) return false;
             if (warp == kFirstQuery && lane == 0) {
@@ -703,7 +706,7 @@ __global__ void __launch_bounds__(low::kThreads, 1)
         int gt = 0, qi = 0;
         for_items(p, lane, [&](const Item& I, int T) {
             stage_lse(p, I, nl, lane);
-            const float2* qs = reinterpret_cast<const float2*>(qs_s + (qi & 3) * kH);
+            const float2* qs = reinterpret_cast<const float2*>(qs_s + (qi & (kScalePlaces - 1)) * kH);
             for (int t = 0; t < T; ++t, ++gt) {
                 if ((gt & 1) != set) continue;
                 const int key = key_at(p, I, I.slot0 + t * kTile + quad * 32 + (int)lane);

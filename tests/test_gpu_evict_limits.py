@@ -1,0 +1,101 @@
+"""The keys' weights where a CTA takes many queries and where the heads of a query differ in size, against float64.
+
+Tolerances, from the arithmetic: those of test_gpu_evict.py (576 float32 additions of a score, off by at most 576 * 2^-24 of the
+sum S of its terms' absolute values, roundings of numbers up to S + |lse|, the exponential's and the sums'), but a head's own S
+and lse in place of the largest.  Over 8-bit and 4-bit rows the query's latent dims enter as hi + lo / 16 in e4m3, exact where
+a dim is 2^-14 of its head's largest or more; below, lo ends at steps of 2^-9, so a dim is off by at most 2^-10 / 16 beside a
+largest of at least 224: 2^-21.8 of it, taken as 2^-21.  A score is off by that times scale * the sum of the key's |latent dims|.
+"""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_evict import SCALE, choose, gen, make_cache, randn, values  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from deepseek_sparse_attention_indexer_gb300 import _build, _lib
+    _build.build()
+    _lib.load()
+    _lib.device_status(reset=True)
+    yield _lib
+    _lib.device_status(reset=True)
+
+
+def weights64(q, rows, idx, split):
+    """(lse f32 [R, 64], weights [R, K] in float64 with that lse, bounds [R, K]): rows(slice) [r, K, 576] float64; split: the
+    query is held as two e4m3 numbers."""
+    lse, w, bound = [], [], []
+    for i in range(0, q.shape[0], 32):
+        kv, ok = rows(slice(i, i + 32)), (idx[i:i + 32] >= 0)[:, None]
+        kv, qq = torch.where(ok[:, 0, :, None], kv, 0.0), q[i:i + 32].double()
+        x = torch.where(ok, torch.einsum("rhd,rkd->rhk", qq, kv) * SCALE, -math.inf)
+        S = torch.einsum("rhd,rkd->rhk", qq.abs(), kv.abs()) * SCALE
+        l32 = torch.logsumexp(x, -1).float()
+        fine = torch.where(torch.isneginf(l32), 0.0, l32.double())
+        off = 576 * 2.0 ** -24 * S + 2.0 ** -22 * (S + fine.abs()[..., None])
+        if split:
+            off = off + 2.0 ** -21 * SCALE * qq[..., :512].abs().amax(-1)[..., None] * kv[..., :512].abs().sum(-1)[:, None]
+        p = torch.exp(x - fine[..., None])
+        lse.append(l32)
+        w.append(p.sum(1))
+        bound.append((p * (torch.expm1(off) + 2.0 ** -17)).sum(1))
+    return torch.cat(lse), torch.cat(w), torch.cat(bound)
+
+
+def summed(x, idx, n):
+    """[R, K] numbers of selected keys added up over all rows, [n]."""
+    out = torch.zeros(n, dtype=torch.float64, device="cuda")
+    return out.index_add_(0, idx.clamp(min=0).long().flatten(), torch.where(idx >= 0, x, 0.0).flatten())
+
+
+def sized_queries(g, rows):
+    """Heads of every size from 1 down to 2^-12, drawn anew for each query."""
+    return (randn(g, rows, 64, 576) * torch.exp2(-torch.randint(0, 13, (rows, 64, 1), generator=g, device="cuda").float())).bfloat16()
+
+
+# ------------------------------------------------------------------------------------------------ many queries a CTA
+
+@pytest.mark.parametrize("fmt,N", [("bf16", 1024), ("q8", 1024), ("q4", 1024), ("q4", 20000)])
+def test_prefill_of_many_short_queries(dsa, fmt, N):
+    """Nine queries of one tile a CTA (4-bit rows expanded, and read directly): each with its own heads' scales."""
+    g = gen(N)
+    L, K = 1300, 128
+    cache, scale = make_cache(g, fmt, N)
+    idx, q = choose(g, [N - (i * 7919) % 100 if i % 50 else 0 for i in range(L)], N, K), sized_queries(g, L)
+    assert (dsa.key_weights_workspace_size(L, K, N, 2) > 8 * N) == (N == 1024)
+    kv = values(fmt, cache, scale)
+    lse, w, bound = weights64(q, lambda s: kv[idx[s].clamp(min=0).long()], idx, fmt != "bf16")
+    want, bound = summed(w, idx, N), summed(bound, idx, N)
+    got = dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale)
+    assert dsa.device_status() == 0
+    assert bool(((got.double() - want).abs() <= bound + 2 * L * L * 2.0 ** -56).all()), float(((got.double() - want).abs() / bound).nan_to_num().max())
+    for _ in range(20):
+        assert torch.equal(dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale), got)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q8", "q4"])
+def test_decode_of_many_short_sequences(dsa, fmt):
+    g = gen(2)
+    B, N, K = 1300, 140, 128
+    lens = [(b * 7919) % (N + 1) for b in range(B)]
+    cache, scale = make_cache(g, fmt, B * N)
+    idx, q, kv_len = choose(g, lens, N, K), sized_queries(g, B), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    first = torch.arange(B, device="cuda")[:, None] * N
+    at = torch.where(idx >= 0, idx + first, -1)
+    kv = values(fmt, cache, scale)
+    lse, w, bound = weights64(q, lambda s: kv[at[s].clamp(min=0)], idx, fmt != "bf16")
+    want, bound = summed(w, at, B * N).view(B, N), summed(bound, at, B * N).view(B, N)
+    cache, scale = cache.view(B, N, -1), None if scale is None else scale.view(B, N)
+    got = dsa.mla_key_weights_decode(q, cache, kv_len, idx, lse, SCALE, cache_scale=scale)
+    assert dsa.device_status() == 0
+    assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).nan_to_num().max())
+    for _ in range(20):
+        assert torch.equal(dsa.mla_key_weights_decode(q, cache, kv_len, idx, lse, SCALE, cache_scale=scale), got)
