@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(low::kThreads, 1)
         mbar_init(qr_full, 1);
         mbar_init(q_free, 2);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_full[i], 2);              // the issuer: its commit, and that it has seen the query's scales
             mbar_init(&acc_free[i], 4);
         }
         *abort_flag = 0;
@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(low::kThreads, 1)
                 }
                 if (!ok) return false;
                 if (lane == 0) {
+                    mbar_arrive(&acc_full[gt & 1]);
                     mma_commit(&acc_full[gt & 1]);
                     if (t >= T - 2) mma_commit(q_free);   // the issuer's last tile of the item
                 }

@@ -81,6 +81,26 @@ def test_prefill_of_many_short_queries(dsa, fmt, N):
         assert torch.equal(dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale), got)
 
 
+@pytest.mark.parametrize("fmt,N", [("bf16", 3000), ("q8", 3000), ("q4", 3000), ("q4", 100000)])
+def test_prefill_of_many_queries_of_all_lengths(dsa, fmt, N):
+    """Six queries a CTA of none to six tiles each, one tile and several next to each other."""
+    g = gen(N + 1)
+    L, K = 900, 700
+    cache, scale = make_cache(g, fmt, N)
+    q, many = sized_queries(g, L), torch.randint(0, K + 1, (L, 1), generator=g, device="cuda")
+    many[::3] = many[::3] % 129
+    idx = choose(g, [N] * L, N, K).masked_fill(torch.arange(K, device="cuda") >= many, -1)
+    assert (dsa.key_weights_workspace_size(L, K, N, 2) > 8 * N) == (N == 3000)
+    kv = values(fmt, cache, scale)
+    lse, w, bound = weights64(q, lambda s: kv[idx[s].clamp(min=0).long()], idx, fmt != "bf16")
+    want, bound = summed(w, idx, N), summed(bound, idx, N)
+    got = dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale)
+    assert dsa.device_status() == 0
+    assert bool(((got.double() - want).abs() <= bound + 2 * L * L * 2.0 ** -56).all()), float(((got.double() - want).abs() / bound).nan_to_num().max())
+    for _ in range(20):
+        assert torch.equal(dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale), got)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "q8", "q4"])
 def test_decode_of_many_short_sequences(dsa, fmt):
     g = gen(2)
