@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, kMoveBlocks) move_rows_kernel
         bytes[k] = mine ? p.bytes[i] : 0;
         paged[k] = mine && p.paged[i];
     }
-    struct Move {                                  // rows of the dense tensors and of the pools, -1: left out
+    struct Move {                                  // rows of the dense tensors and of the pools; from[0] -1: left out
         int from[2], to[2];
     };
     auto from = [](const Move& v, bool paged) { return paged ? v.from[1] : v.from[0]; };
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32, kMoveBlocks) move_rows_kernel
                     own.from[1] = (int)paged_row(p.pages, b, from);
                     own.to[1] = (int)paged_row(p.pages, b, to);
                     bad = own.from[1] < 0 || own.to[1] < 0;
-                    if (bad) own.from[1] = -1;     // the paged tensors are left out
+                    if (bad) own.from[0] = -1;     // in no tensor, so that a key's rows stay together
                 }
             }
             if (bad) raise_dev_error(p.status, DEV_ERR_BOUNDS);

@@ -539,7 +539,8 @@ dsa_status_t dsa_cache_evict_plan(const float *acc, const int32_t *pos, const in
  *   src, dst   int32 [B, moves] (device)
  *   tensors    host array of `count` device pointers (4-byte aligned); row_bytes: bytes of a row each, a
  *              multiple of 4; paged: 0 for [B, Nmax, ...] rows, 1 for a pool addressed through block_table
- * An entry >= Nmax or a page outside the pool is recorded as DSA_ERR_DEVICE_BOUNDS and not moved.
+ * An entry >= Nmax, or on a page outside the pool where a tensor is paged, is recorded as
+ * DSA_ERR_DEVICE_BOUNDS and moved in no tensor, the dense ones among them.
  * Errors (host): DSA_ERR_INVALID_ARG for a null pointer or a size < 1, row_bytes < 4, paged not 0 or 1;
  * DSA_ERR_UNSUPPORTED_SHAPE for count > 8, rows above 1 MB, B > 65535, products above 2^31 - 1, page
  * sizes as in the paged calls; DSA_ERR_MISALIGNED.

@@ -1,4 +1,5 @@
-"""The keys' weights where a CTA takes many queries and where the heads of a query differ in size, against float64.
+"""Eviction at its ends: the keys' weights where a CTA takes many queries and where the heads of a query differ in size, against
+float64; moves that are left out.
 
 Tolerances, from the arithmetic: those of test_gpu_evict.py (576 float32 additions of a score, off by at most 576 * 2^-24 of the
 sum S of its terms' absolute values, roundings of numbers up to S + |lse|, the exponential's and the sums'), but a head's own S
@@ -12,7 +13,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_evict import SCALE, choose, gen, make_cache, randn, values  # noqa: E402
+from test_gpu_evict import SCALE, choose, gen, i32, make_cache, randn, values  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -107,7 +108,7 @@ def test_decode_of_many_short_sequences(dsa, fmt):
     B, N, K = 1300, 140, 128
     lens = [(b * 7919) % (N + 1) for b in range(B)]
     cache, scale = make_cache(g, fmt, B * N)
-    idx, q, kv_len = choose(g, lens, N, K), sized_queries(g, B), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    idx, q, kv_len = choose(g, lens, N, K), sized_queries(g, B), i32(*lens)
     first = torch.arange(B, device="cuda")[:, None] * N
     at = torch.where(idx >= 0, idx + first, -1)
     kv = values(fmt, cache, scale)
@@ -119,3 +120,29 @@ def test_decode_of_many_short_sequences(dsa, fmt):
     assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).nan_to_num().max())
     for _ in range(20):
         assert torch.equal(dsa.mla_key_weights_decode(q, cache, kv_len, idx, lse, SCALE, cache_scale=scale), got)
+
+
+# ------------------------------------------------------------------------------------------------ moves
+
+def test_moves_of_dense_and_paged_tensors_leave_out_whole_entries(dsa):
+    """Where a page of either end lies outside the pool, no tensor moves, so that a key's weight stays with its rows."""
+    B, N, page = 2, 64, 16
+    g = gen(3)
+    acc, pos = torch.rand(B, N, generator=g, device="cuda"), torch.arange(B * N, device="cuda").int().view(B, N).contiguous()
+    wide = torch.randint(0, 256, (B, N, 48), generator=g, device="cuda").byte()
+    pool, keys = torch.randint(0, 256, (6 * page, 416), generator=g, device="cuda").byte(), randn(g, 6 * page, 128).bfloat16()
+    table = i32(0, 1, 2, 99, 3, 4, -1, 5).view(B, 4)
+    # of sequence 0: source on a page that is not there, destination on one, a good one, one behind the end, one unused; of 1 alike
+    src, dst = i32(50, 20, 21, 64, -1, 40, 50, 17, 51, 1).view(B, 5), i32(2, 49, 3, 5, 6, 3, 33, 4, 5, 64).view(B, 5)
+    good = [(0, 21, 3), (1, 17, 4), (1, 51, 5)]
+    row = lambda b, j: int(table[b, j // page]) * page + j % page  # noqa: E731
+    want = [t.clone() for t in (acc, pos, wide, pool, keys)]
+    for b, f, t in good:
+        for x, w in zip((acc, pos, wide), want[:3]):
+            w[b, t] = x[b, f]
+        for x, w in zip((pool, keys), want[3:]):
+            w[row(b, t)] = x[row(b, f)]
+    dsa.cache_move_rows(src, dst, dense=(acc, pos, wide), paged=(pool, keys), block_table=table, page_size=page)
+    assert dsa.device_status() == 7
+    for x, w in zip((acc, pos, wide, pool, keys), want):
+        assert torch.equal(x, w)
