@@ -810,7 +810,8 @@ def cache_evict_plan(acc: torch.Tensor, pos: torch.Tensor, kv_len: torch.Tensor,
     padded with -1, and the keys left [B].
 
     acc f32 [B, Nmax] (weights), pos int32 [B, Nmax] (positions), kv_len [B].  The `recent` latest positions and
-    those below `sink` stay, then the heaviest keys, equal ones the lower index first."""
+    those below `sink` stay, then the heaviest keys, equal ones the lower index first.
+    The places behind `left` keep their old weights and positions: a token appended there later starts with acc = 0."""
     dev = _current_device()
     if acc.dim() != 2:
         _bad("acc is f32 [B, Nmax]")

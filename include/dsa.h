@@ -469,6 +469,12 @@ dsa_status_t mla_sparse_attn_decode_q4_paged(const void *q, const void *cache, c
  * chooses the keys that stay, dsa_cache_move_rows closes the gaps in every tensor that holds a row a
  * key.  The order of a sequence's keys is not kept: its positions are a tensor of their own.  No
  * counterpart on the pages.
+ * After a cut to left[b] keys the places behind them hold what they held: dead or moved keys' weights,
+ * positions and rows.  No call clears them.  A token appended later is written whole: its rows, its position,
+ * and a weight of 0 (acc[b, place] = 0) before the first mla_key_weights_* call that accumulates.
+ * The other calls take places, not positions: a new token of sequence b at place kv_len[b] - 1 is query
+ * q_pos0[b] = kv_len[b] - 1 to dsa_indexer_scores and dsa_topk (a chunk's first place for a chunk), so that
+ * every key before it counts; positions only turn its query and key (dsa_indexer_norm_rope, mla_cache_write_*).
  */
 #define DSA_ROWS_BF16 0   /* 1152-byte rows, no cache_scale */
 #define DSA_ROWS_Q8 1     /* the 8-bit cache */

@@ -13,7 +13,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_evict import SCALE, choose, gen, i32, make_cache, randn, values  # noqa: E402
+from test_gpu_evict import SCALE, choose, gen, i32, make_cache, paged, plan_by_sorting, randn, values  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +146,77 @@ def test_moves_of_dense_and_paged_tensors_leave_out_whole_entries(dsa):
     assert dsa.device_status() == 7
     for x, w in zip((acc, pos, wide, pool, keys), want):
         assert torch.equal(x, w)
+
+
+# ------------------------------------------------------------------------------------------------ tokens after a cut
+
+@pytest.mark.parametrize("fmt,page", [("bf16", 0), ("q8", 64), ("q4", 16)])
+def test_tokens_appended_after_a_cut(dsa, fmt, page):
+    """A loop of decode steps that appends tokens and cuts the caches three times: indexer, top-k and attention over the cut
+    caches give what they give over the same keys in order, and the weights by which a cut goes are those each position
+    has received since it came."""
+    g = gen(5)
+    B, N, P, keep, K = 3, 160, 200, 60, 48
+    seq = torch.arange(B, device="cuda")
+    everything, every_scale = make_cache(g, fmt, B * P)                   # by positions
+    everything, every_scale = everything.view(B, P, -1), None if every_scale is None else every_scale.view(B, P)
+    index_keys = randn(g, B, P, 128).bfloat16()
+    start = [100, 59, 130]
+    kv_len, n_pos = i32(*start), torch.tensor(start, device="cuda")
+    if page:
+        cache, scale, table, _ = paged(g, everything[:, :N], None if every_scale is None else every_scale[:, :N], [N] * B, page)
+        kind = "_paged"
+        place = lambda at: table[seq, at // page].long() * page + at % page  # noqa: E731
+        paging = {"block_table": table, "page_size": page, "Nmax": N}
+    else:
+        cache, scale, kind, paging = everything[:, :N].clone(), None if every_scale is None else every_scale[:, :N].clone(), "", {}
+    keys = index_keys[:, :N].clone()
+    acc, pos = torch.zeros(B, N, device="cuda"), torch.arange(N, device="cuda").int()[None].repeat(B, 1).contiguous()
+    acc[:, 50:] = 1e9                                                     # places without a key hold anything
+    acc[torch.arange(N, device="cuda") < kv_len[:, None]] = 0.0
+    received = torch.zeros(B, P, device="cuda")                           # by positions
+    low = "" if fmt == "bf16" else "_" + fmt
+    rows = lambda c, s: (c,) if s is None else (c, s)  # noqa: E731
+    cuts = 0
+    for step in range(30):
+        at = kv_len.long()                                                # a token's place
+        pos[seq, at], acc[seq, at], keys[seq, at] = n_pos.int(), 0.0, index_keys[seq, n_pos]
+        if page:
+            cache[place(at)] = everything[seq, n_pos]
+            if scale is not None:
+                scale[place(at)] = every_scale[seq, n_pos]
+        else:
+            cache[seq, at] = everything[seq, n_pos]
+            if scale is not None:
+                scale[seq, at] = every_scale[seq, n_pos]
+        n_pos, kv_len = n_pos + 1, kv_len + 1
+        q, q_idx, w = randn(g, B, 64, 576).bfloat16(), randn(g, B, 1, 32, 128).bfloat16(), randn(g, B, 1, 32)
+        last = kv_len - 1
+        idx = dsa.topk(dsa.indexer_scores(q_idx, keys, w, last, kv_len), last, kv_len, N, K)[:, 0].contiguous()
+        named = torch.where(idx >= 0, pos.gather(1, idx.clamp(min=0).long()), -1).contiguous()
+        # the keys that are left, in the order of their positions
+        held = torch.where(torch.arange(N, device="cuda") < kv_len[:, None], pos, 1 << 20).sort(1).values
+        ordered = index_keys[seq[:, None], held.clamp(max=P - 1).long()].contiguous()
+        first = dsa.topk(dsa.indexer_scores(q_idx, ordered, w, last, kv_len), last, kv_len, N, K)[:, 0]
+        assert torch.equal(torch.where(first >= 0, held.gather(1, first.clamp(min=0).long()).int(), -1).sort(1).values, named.sort(1).values)
+        head = (q, *rows(cache, scale), kv_len) + ((table, page) if page else ()) + (idx, SCALE) + ((N,) if page else ())
+        out, lse = getattr(dsa, f"mla_sparse_attn_decode{low}{kind}")(*head, want_lse=True)
+        whole = getattr(dsa, f"mla_sparse_attn_decode{low}")(q, *rows(everything, every_scale), i32(*[P] * B), named, SCALE, want_lse=True)
+        assert torch.equal(out, whole[0]) and torch.equal(lse, whole[1])
+        dsa.mla_key_weights_decode(q, cache, kv_len, idx, lse, SCALE, acc=acc, cache_scale=scale, **paging)
+        received += dsa.mla_key_weights_decode(q, everything, i32(*[P] * B), named, lse, SCALE, cache_scale=every_scale)
+        mine = torch.arange(N, device="cuda") < kv_len[:, None]
+        tracked = received.gather(1, pos.long().clamp(0, P - 1))
+        assert torch.equal(acc[mine], tracked[mine])
+        if step % 10 == 7:
+            want = plan_by_sorting(tracked.cpu(), pos.cpu(), kv_len.cpu(), keep, 8, 2)
+            src, dst, left = dsa.cache_evict_plan(acc, pos, kv_len, keep, recent=8, sink=2)
+            assert all(torch.equal(x.cpu(), y) for x, y in zip((src, dst, left), want))
+            latent = [cache] + ([] if scale is None else [scale])
+            if page:
+                dsa.cache_move_rows(src, dst, dense=(acc, pos, keys), paged=latent, block_table=table, page_size=page)
+            else:
+                dsa.cache_move_rows(src, dst, dense=[acc, pos, keys] + latent)
+            kv_len, cuts = left, cuts + 1
+        assert dsa.device_status() == 0
+    assert cuts == 3
