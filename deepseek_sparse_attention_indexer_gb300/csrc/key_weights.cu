@@ -170,7 +170,10 @@ __device__ __forceinline__ void add_weight(const WeightParams& p, const Item& I,
         atomicAdd(p.acc + (int64_t)I.batch * p.Nmax + key, w);
 }
 
-// A copy of -lse log2(e) of the item's heads for the calling warp.
+// A copy of -lse log2(e) of the item's heads for the calling warp.  The exponent is s (scale log2(e)) - lse log2(e), both factors
+// rounded: up to 2^-23 (|scale s| + |lse|) of a weight, of the size of what the rounding of lse to float32 itself leaves open
+// (2^-24 |lse|).  (scale s - lse) log2(e) has one rounding of the difference; it took 4096 queries over 8-bit rows 704 -> 737 us and
+// over bf16 rows 758 -> 763, and left the error against float64 of 1024 queries at 3.5e-7 (bf16: the tensor core cuts sums) and 6e-8.
 __device__ __forceinline__ void stage_lse(const WeightParams& p, const Item& I, float2* nl, uint32_t lane) {
     const float* lse = p.lse + (int64_t)I.row * kH + 2 * lane;
     const float l0 = __ldg(lse), l1 = __ldg(lse + 1);

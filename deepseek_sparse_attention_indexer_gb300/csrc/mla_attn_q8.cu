@@ -10,8 +10,8 @@
 //     O^T = V^T . P^T (M = 128 keys / latent dims), the gathered tile is stored once with the 128-byte
 //     swizzle and read K-major by QK and MN-major by PV.
 //   * A bf16 query has 8 significant bits, an e4m3 number 4: a query is the sum of two e4m3 numbers,
-//     hi + lo / 16 (times a power of two a head), exactly so down to 2^-14 of the head's largest
-//     element and within 2^-22 of it below.  hi and lo of the 64 heads stand next to each other as one
+//     hi + lo / 16 (times a power of two a head), exactly so down to 2^-13 of the head's largest
+//     element and within 2^-21 of it below.  hi and lo of the 64 heads stand next to each other as one
 //     N = 128 operand, so QK over 32 dims is one MMA; the softmax adds the two halves.  The rope
 //     dims are a bf16 product of their own (their rows are not scaled).
 //   * The probabilities are split the same way, P' = hi + lo / 16, lo's factor applied by the

@@ -352,7 +352,7 @@ dsa_status_t mla_cache_read_q8_paged(const void *cache, const float *cache_scale
  * no matter.  Where that size is 0, NULL will do.  It depends on the current
  * device (0 where the library does not run) and is the same in every call.
  * Precision: products and sums are float32.  The query enters as two e4m3
- * numbers a value (exact for bf16 down to 2^-14 of a head's largest value), and
+ * numbers a value (exact for bf16 down to 2^-13 of a head's largest value), and
  * so do the probabilities, whose relative error is at most 2^-8 as in the bf16
  * calls; a probability (times its row's scale) below 2^-10.5 of the head's
  * largest is held to 2^-18.5 of that (rows of zeros of scale 1 or more, as
@@ -493,7 +493,11 @@ dsa_status_t mla_sparse_attn_decode_q4_paged(const void *q, const void *cache, c
  *   lse          f32 [L, 64] or [B, 64]; a lse of other keys than the selected (the log of the sum over
  *                several caches' parts) gives the weights relative to those
  *   acc          f32 [N], or [B, Nmax]: the sums of sequence b's keys; every key's is written with accumulate 0
- * Products are exact and accumulated in float32.  The weight of an entry of idx is at most 128 (64 heads'
+ * Scores are those of the attention over the same rows: over bf16 rows exact products, over 8-bit and 4-bit
+ * rows products with the query as two e4m3 numbers a latent dim (exact for dims down to 2^-13 of their head's
+ * largest, held to 2^-21 of that below: beside one far larger dim the others lose bits, in the attention and
+ * in its lse alike).  They are accumulated in float32, and the exponent's factors are rounded to float32:
+ * 2^-22 (|scale * s| + |lse|) of a weight.  The weight of an entry of idx is at most 128 (64 heads'
  * probabilities are at most 64); a NaN counts 0.  Entries of idx behind the cache are recorded as
  * DSA_ERR_DEVICE_BOUNDS and skipped, negative ones skipped; a key given twice in a query counts twice.
  * Prefill adds whole numbers of 2^-shift, L * 128 * 2^shift <= 2^62 (64 bits hold a key that every

@@ -4,7 +4,7 @@ float64; moves that are left out.
 Tolerances, from the arithmetic: those of test_gpu_evict.py (576 float32 additions of a score, off by at most 576 * 2^-24 of the
 sum S of its terms' absolute values, roundings of numbers up to S + |lse|, the exponential's and the sums'), but a head's own S
 and lse in place of the largest.  Over 8-bit and 4-bit rows the query's latent dims enter as hi + lo / 16 in e4m3, exact where
-a dim is 2^-14 of its head's largest or more; below, lo ends at steps of 2^-9, so a dim is off by at most 2^-10 / 16 beside a
+a dim is 2^-13 of its head's largest or more; below, lo ends at steps of 2^-9, so a dim is off by at most 2^-10 / 16 beside a
 largest of at least 224: 2^-21.8 of it, taken as 2^-21.  A score is off by that times scale * the sum of the key's |latent dims|.
 """
 import math
@@ -120,6 +120,89 @@ def test_decode_of_many_short_sequences(dsa, fmt):
     assert bool(((got.double() - want).abs() <= bound).all()), float(((got.double() - want).abs() / bound).nan_to_num().max())
     for _ in range(20):
         assert torch.equal(dsa.mla_key_weights_decode(q, cache, kv_len, idx, lse, SCALE, cache_scale=scale), got)
+
+
+# ------------------------------------------------------------------------------------------------ heads of one large dim
+
+F8 = torch.float8_e4m3fn
+
+
+def as_two_e4m3(q):
+    """Queries [.., 576] as they enter over 8-bit and 4-bit rows: latent dims hi + lo / 16 times a power of two a head, by which
+    the largest is in (224, 448]; both numbers nearest, from half precision."""
+    lat = q[..., :512].double()
+    top = lat.abs().amax(-1, keepdim=True)
+    step = torch.exp2(torch.ceil(torch.log2(top / 448.0)))
+    x = (lat / step).half()
+    hi = x.float().to(F8).float()
+    lo = ((x.float() - hi).half() * 16).float().to(F8).double()
+    out = (hi.double() + lo / 16) * step
+    assert bool(((out - lat).abs() <= 2.0 ** -21 * top).all())
+    assert bool(((out == lat) | (lat.abs() < 2.0 ** -13 * top)).all())    # exact from there on
+    return torch.cat([out, q[..., 512:].double()], -1)
+
+
+@pytest.mark.parametrize("power", [8, 14, 20])
+@pytest.mark.parametrize("fmt", ["bf16", "q8", "q4"])
+def test_weights_of_heads_with_one_large_dim(dsa, fmt, power):
+    """One dim of each head 2^power times the others, where the cache is zero: over bf16 rows nothing is lost, over the others
+    the weights are those of the query as two e4m3 numbers, which are the attention's own."""
+    g = gen(power)
+    L, N, K = 20, 500, 300
+    cache, scale = make_cache(g, fmt, N)
+    if fmt == "q4":
+        cache[:, 18] &= 0x8F                                              # dim 37: the fifth of group 4
+    else:
+        cache[:, 37] = 0
+    kv = values(fmt, cache, scale)
+    assert bool((kv[:, 37] == 0).all())
+    q, idx = randn(g, L, 64, 576).bfloat16(), choose(g, [N] * L, N, K)
+    q[:, :, 37] = torch.exp2(torch.tensor(float(power), device="cuda")) * (1.0 + torch.rand(L, 64, generator=g, device="cuda"))
+    held = q.double() if fmt == "bf16" else as_two_e4m3(q)
+    lse, w, bound = weights64(held, lambda s: kv[idx[s].long()], idx, False)
+    want, bound = summed(w, idx, N), summed(bound, idx, N)
+    got = dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale)
+    assert bool(((got.double() - want).abs() <= bound + 2 * L * L * 2.0 ** -56).all()), float(((got.double() - want).abs() / bound).max())
+    if fmt == "bf16":
+        _, own = dsa.mla_sparse_attn_prefill(q, cache, idx, SCALE, want_lse=True)
+    else:
+        _, own = getattr(dsa, f"mla_sparse_attn_prefill_{fmt}")(q, cache, scale, idx, SCALE, want_lse=True)
+    acc = dsa.mla_key_weights_prefill(q, cache, idx, own, SCALE, cache_scale=scale)
+    # the attention's lse is within 2^-12 of its own scores' (its tests' bound), a factor of every weight
+    assert abs(float(acc.double().sum()) - 64 * L) <= 64 * L * 2.0 ** -11
+    assert dsa.device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q8", "q4"])
+def test_weights_of_large_scores(dsa, fmt):
+    """Scores of 3000 and a lse next to them: the rounded factors of the exponent, and no more.  All numbers are multiples of 1/64
+    that float32 holds, so that nothing else is rounded but the exponential and the sums (below 2^-17 together)."""
+    R, N = 4, 64
+    j, h = torch.arange(N, device="cuda"), torch.arange(64, device="cuda")
+    q = torch.zeros(R, 64, 576, device="cuda")
+    q[..., 0], q[..., 512] = 8000.0, 2.0                                  # times 6 and -j: 48000 - 2 j
+    rope = torch.zeros(N, 64, device="cuda")
+    rope[:, 0] = -j.float()
+    if fmt == "bf16":
+        cache, scale = torch.zeros(N, 576, device="cuda").bfloat16(), None
+        cache[:, 0], cache[:, 512:] = 6.0, rope.bfloat16()
+    else:
+        cache, scale = torch.zeros(N, 640 if fmt == "q8" else 416, dtype=torch.uint8, device="cuda"), torch.ones(N, device="cuda")
+        if fmt == "q8":
+            cache[:, 0] = torch.tensor(6.0, device="cuda").to(F8).view(torch.uint8)
+        else:
+            cache[:, 0], cache[:, 256] = 7, 18                            # magnitude 6, block scale 1
+        cache[:, -128:] = rope.bfloat16().view(torch.uint8)
+    lse = (3000.0 + h / 64).repeat(R, 1).float()
+    idx = j.int().repeat(R, 1)
+    one = torch.exp(-j[:, None].double() / 8 - h.double() / 64).sum(1)
+    tol = math.expm1(2.0 ** -22 * (3000.0 + 3001.0)) + 2.0 ** -17
+    got = dsa.mla_key_weights_prefill(q.bfloat16(), cache, idx, lse, SCALE, cache_scale=scale)
+    assert bool(((got.double() / R - one).abs() <= tol * one).all()), float((got.double() / R / one - 1).abs().max())
+    got = dsa.mla_key_weights_decode(q[:1].bfloat16(), cache[None], i32(N), idx[:1], lse[:1], SCALE,
+                                     cache_scale=None if scale is None else scale[None])
+    assert bool(((got[0].double() - one).abs() <= tol * one).all()), float((got[0].double() / one - 1).abs().max())
+    assert dsa.device_status() == 0
 
 
 # ------------------------------------------------------------------------------------------------ moves
