@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_plan_kernel(const PlanParam
         if (rank == 0 && t == 0) p.left[b] = max(n, 0);
         return;
     }
-    const int part = (n + C - 1) / C;
-    const int j0 = min(n, rank * part), len = min(n, j0 + part) - j0;
+    const int part = (n - 1) / C + 1;              // n > keep >= 1, up to 2^31 - 1
+    const int j0 = (int)min((int64_t)n, (int64_t)rank * part), len = min(part, n - j0);
     const float* acc = p.acc + (int64_t)b * p.Nmax + j0;
     const int32_t* pos = p.pos + (int64_t)b * p.Nmax + j0;
 

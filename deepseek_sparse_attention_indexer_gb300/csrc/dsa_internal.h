@@ -61,7 +61,7 @@ struct PageTable {
     int num_pages;   // pages in the pool
 };
 
-inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+inline int ceil_div(int a, int b) { return a / b + (a % b != 0); }   // (a up to 2^31 - 1)
 inline size_t round_up(size_t n) { return (n + 255) / 256 * 256; }   // parts of a workspace
 
 // Launch entry points implemented in the kernel files.

@@ -231,6 +231,23 @@ def test_moves_of_dense_and_paged_tensors_leave_out_whole_entries(dsa):
         assert torch.equal(x, w)
 
 
+# ------------------------------------------------------------------------------------------------ plan
+
+def test_plan_of_as_many_keys_as_there_may_be(dsa):
+    """2^31 - 1 keys of one sequence: sums of places and of block sizes stay in 32 bits."""
+    N = 2 ** 31 - 1
+    acc, pos = torch.rand(1, N, generator=gen(6), device="cuda"), torch.arange(N, dtype=torch.int32, device="cuda")[None]
+    heavy = torch.tensor([3, 5, 2 ** 28 - 1, 2 ** 28, 2 ** 30 + 7, N - 9, N - 8, N - 2], device="cuda")
+    acc[0, heavy] = 2.0 + torch.arange(8, device="cuda")
+    src, dst, left = dsa.cache_evict_plan(acc, pos, i32(N), 9, recent=1)   # and the last position
+    assert src[0].tolist() == [2 ** 28 - 1, 2 ** 28, 2 ** 30 + 7, N - 9, N - 8, N - 2, N - 1, -1, -1]
+    assert dst[0].tolist() == [0, 1, 2, 4, 6, 7, 8, -1, -1] and int(left[0]) == 9
+    src, dst, left = dsa.cache_evict_plan(acc, pos, i32(N - 6), 7)
+    assert src[0].tolist() == [2 ** 28 - 1, 2 ** 28, 2 ** 30 + 7, N - 9, N - 8, -1, -1]
+    assert dst[0].tolist() == [0, 1, 2, 4, 6, -1, -1] and int(left[0]) == 7
+    assert dsa.device_status() == 0
+
+
 # ------------------------------------------------------------------------------------------------ tokens after a cut
 
 @pytest.mark.parametrize("fmt,page", [("bf16", 0), ("q8", 64), ("q4", 16)])
