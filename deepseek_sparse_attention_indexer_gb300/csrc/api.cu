@@ -399,7 +399,7 @@ dsa_status_t attn_prefill(bool q4, const void* q, const void* cache, const float
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace) ||
-        (q4 && !aligned32(workspace)))
+        (q4 && attn_q4_expands(L, top_k, N) && !aligned32(workspace)))
         return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
     if ((st = check_workspace(workspace, ws_bytes, q4 ? attn_q4_workspace(L, top_k, N) : attn_q8_workspace(L, top_k))) != DSA_OK)
@@ -418,7 +418,7 @@ dsa_status_t attn_prefill_paged(bool q4, const void* q, const void* cache, const
     const int stride = page_size > 0 ? (int)(((long long)N + page_size - 1) / page_size) : 0;
     if ((st = make_page_table(block_table, stride, page_size, num_pages, N, &pt)) != DSA_OK) return st;
     if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace) ||
-        (q4 && !aligned32(workspace)))
+        (q4 && attn_q4_expands(L, top_k, N) && !aligned32(workspace)))
         return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
     if ((st = check_workspace(workspace, ws_bytes, q4 ? attn_q4_workspace(L, top_k, N) : attn_q8_workspace(L, top_k))) != DSA_OK)

@@ -104,6 +104,7 @@ dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const floa
                                     const int32_t* idx, int L, int N, int top_k, float scale, void* out, int out_f32,
                                     float* lse, void* workspace, const PageTable& pages, cudaStream_t stream);
 size_t attn_q8_workspace(int rows, int top_k);
+bool attn_q4_expands(int rows, int top_k, int N);       // a prefill that holds its rows as 8-bit ones in the workspace
 size_t attn_q4_workspace(int rows, int top_k, int N);   // N: keys of a prefill's cache; decode 0
 // Merge of nsplit partial (normalised output, lse) pairs a sequence.
 dsa_status_t launch_decode_combine(const float* part_o, const float* part_lse, int B, int nsplit, void* out, int out_f32,

@@ -45,7 +45,7 @@
 //   * The same kernel over the 4-bit cache (Q4): every stored value is an e4m3 number, so only the gather differs.  The four
 //     latent warps expand chunks 0 and 1, the four rope warps 2 and 3 ahead of their rope rows, a lane its own row: codes in
 //     registers before their place comes free, a block's eight magnitudes from a table in shared memory, a byte selection
-//     a half word.  A prefill that selects each key several times expands the cache once instead (want_expanded) and
+//     a half word.  A prefill that selects each key several times expands the cache once instead (attn_q4_expands) and
 //     takes the 8-bit kernel's time, 4096 queries 1.13 ms.  Decode of 256 sequences of up to 8192 keys 145 us (104 over 8-bit
 //     rows), of 37 20.8, of one 13.7: the latent warps are never idle (a trace: of 8300 cycles a tile the L2 prefetch of 32
 //     rows takes 2000, lookups 900, expanding 2300, the loads' latency 1500).  The table in shared memory left out would give
@@ -1115,14 +1115,14 @@ dsa_status_t launch_rows(AttnQ8Params p, int rows, void* workspace, cudaStream_t
     return launch_decode_combine(p.part_o, p.part_lse, c.cut, c.splits, out, p.out_f32, lse, stream);
 }
 
+}  // namespace
+
 // A prefill over the 4-bit cache expands the cache's rows to 8-bit ones first, once for all its queries, where they
 // select each key three times or more: a selected key then costs 0.14 ns in place of 0.20, a key of the cache 0.2 ns and
 // the launch 2 us.  Direct / expanded, us: 8 queries of 2048 of 2k keys 15.1 / 15.7; 32 of 4k 26.2 / 24.3; 152 of 16k 65 / 51,
 // of 131k (2.4 times each) 69 / 74; 608 of 131k 279 / 209, of 524k (2.4) 295 / 275; 4096 of 16k 1717 / 1154, of 2M (4)
 // 2016 / 1593.
-bool want_expanded(int rows, int top_k, int N) { return (long long)rows * top_k >= 3LL * N + 24576; }
-
-}  // namespace
+bool attn_q4_expands(int rows, int top_k, int N) { return N > 0 && (long long)rows * top_k >= 3LL * N + 24576; }
 
 size_t attn_q8_workspace(int rows, int top_k) {
     const Cut c = cut_rows(rows, top_k);
@@ -1131,7 +1131,7 @@ size_t attn_q8_workspace(int rows, int top_k) {
 
 size_t attn_q4_workspace(int rows, int top_k, int N) {
     const size_t cut = attn_q8_workspace(rows, top_k);
-    if (N < 1 || !want_expanded(rows, top_k, N)) return cut;
+    if (!attn_q4_expands(rows, top_k, N)) return cut;
     return round_up(cut) + round_up((size_t)N * kQ8Row) + (size_t)N * sizeof(float);
 }
 
@@ -1141,7 +1141,7 @@ dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const floa
     AttnQ8Params p = base_params(q, cache, cache_scale, idx, N, top_k, scale, out, out_f32, lse, pages);
     p.prefill = 1;
     if (!q4) return launch_rows<false>(p, L, workspace, stream);
-    if (!want_expanded(L, top_k, N)) return launch_rows<true>(p, L, workspace, stream);
+    if (!attn_q4_expands(L, top_k, N)) return launch_rows<true>(p, L, workspace, stream);
     uint8_t* rows = static_cast<uint8_t*>(workspace) + round_up(attn_q8_workspace(L, top_k));
     float* scales = reinterpret_cast<float*>(rows + round_up((size_t)N * kQ8Row));
     const dsa_status_t st = launch_cache_expand_q4(cache, cache_scale, N, rows, scales, pages, stream);
