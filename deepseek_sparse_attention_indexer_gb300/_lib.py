@@ -526,7 +526,8 @@ def attn_q8_workspace_size(rows: int, top_k: int) -> int:
 
 
 def attn_q4_workspace_size(rows: int, top_k: int, N: int = 0) -> int:
-    """The same for a 4-bit cache; N: the keys of a prefill's cache, 0 for a decode call."""
+    """The same for a 4-bit cache; N: the keys of a prefill's cache, 0 for a decode call.  A prefill given a workspace of the
+    size for N = 0 holds no rows in it and reads the cache directly: slower where its queries select each key often."""
     return _q4_workspace_bytes(_current_device(), rows, top_k, N)
 
 
@@ -718,7 +719,8 @@ def _weights_cache(cache, cache_scale, dev):
 
 @functools.lru_cache(maxsize=4096)
 def key_weights_workspace_size(L: int, top_k: int, N: int, row_format: int = 0) -> int:
-    """Bytes mla_key_weights_prefill takes; row_format 0 bf16 rows, 1 8-bit, 2 4-bit."""
+    """Bytes mla_key_weights_prefill takes; row_format 0 bf16 rows, 1 8-bit, 2 4-bit.  (A prefill over 4-bit rows given the
+    size for bf16 rows holds no rows in it and reads the cache directly.)"""
     return int(load().mla_key_weights_workspace_size(row_format, L, N, top_k))
 
 

@@ -398,13 +398,14 @@ dsa_status_t attn_prefill(bool q4, const void* q, const void* cache, const float
                           void* workspace, size_t ws_bytes, void* stream) {
     dsa_status_t st = check_attn_q8(q, cache, cache_scale, idx, L, N, top_k, scale, out, out_dtype);
     if (st != DSA_OK) return st;
-    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace) ||
-        (q4 && attn_q4_expands(L, top_k, N) && !aligned32(workspace)))
+    // a workspace of the parts' size alone asks for the rows to be read as they are
+    const size_t parts = attn_q8_workspace(L, top_k);
+    const bool expand = q4 && attn_q4_expands(L, top_k, N) && ws_bytes != parts;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace) || (expand && !aligned32(workspace)))
         return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
-    if ((st = check_workspace(workspace, ws_bytes, q4 ? attn_q4_workspace(L, top_k, N) : attn_q8_workspace(L, top_k))) != DSA_OK)
-        return st;
-    return launch_attn_q8_prefill(q, cache, cache_scale, q4, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32,
+    if ((st = check_workspace(workspace, ws_bytes, expand ? attn_q4_workspace(L, top_k, N) : parts)) != DSA_OK) return st;
+    return launch_attn_q8_prefill(q, cache, cache_scale, q4, expand, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32,
                                   lse, workspace, PageTable{}, static_cast<cudaStream_t>(stream));
 }
 
@@ -417,13 +418,14 @@ dsa_status_t attn_prefill_paged(bool q4, const void* q, const void* cache, const
     PageTable pt;
     const int stride = page_size > 0 ? (int)(((long long)N + page_size - 1) / page_size) : 0;
     if ((st = make_page_table(block_table, stride, page_size, num_pages, N, &pt)) != DSA_OK) return st;
-    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace) ||
-        (q4 && attn_q4_expands(L, top_k, N) && !aligned32(workspace)))
+    // a workspace of the parts' size alone asks for the rows to be read as they are
+    const size_t parts = attn_q8_workspace(L, top_k);
+    const bool expand = q4 && attn_q4_expands(L, top_k, N) && ws_bytes != parts;
+    if (!aligned16(q) || !aligned32(cache) || !aligned16(out) || !aligned16(workspace) || (expand && !aligned32(workspace)))
         return DSA_ERR_MISALIGNED;
     if ((st = check_device()) != DSA_OK) return st;
-    if ((st = check_workspace(workspace, ws_bytes, q4 ? attn_q4_workspace(L, top_k, N) : attn_q8_workspace(L, top_k))) != DSA_OK)
-        return st;
-    return launch_attn_q8_prefill(q, cache, cache_scale, q4, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32,
+    if ((st = check_workspace(workspace, ws_bytes, expand ? attn_q4_workspace(L, top_k, N) : parts)) != DSA_OK) return st;
+    return launch_attn_q8_prefill(q, cache, cache_scale, q4, expand, idx, L, N, top_k, scale, out, out_dtype == DSA_OUT_F32,
                                   lse, workspace, pt, static_cast<cudaStream_t>(stream));
 }
 
@@ -657,7 +659,7 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 size_t mla_key_weights_workspace_size(int row_format, int L, int N, int top_k) {
     if (row_format < DSA_ROWS_BF16 || row_format > DSA_ROWS_Q4 || L < 1 || N < 1 || top_k < 1 || top_k > DSA_MAX_TOPK) return 0;
-    return key_weights_workspace(row_format, L, N, top_k);
+    return key_weights_workspace(key_weights_expands(row_format, L, N, top_k), N);
 }
 
 dsa_status_t mla_key_weights_prefill(const void* q, const void* cache, const float* cache_scale, int row_format,
@@ -670,9 +672,11 @@ dsa_status_t mla_key_weights_prefill(const void* q, const void* cache, const flo
     const int stride = page_size > 0 ? (int)(((long long)N + page_size - 1) / page_size) : 0;
     if (block_table && (st = make_page_table(block_table, stride, page_size, num_pages, N, &pt)) != DSA_OK) return st;
     if (!aligned16(q) || !aligned32(cache) || !aligned32(workspace)) return DSA_ERR_MISALIGNED;
-    if ((st = check_workspace(workspace, ws_bytes, key_weights_workspace(row_format, L, N, top_k))) != DSA_OK) return st;
+    // a workspace of the sums' size alone asks for the rows to be read as they are
+    const bool expand = key_weights_expands(row_format, L, N, top_k) && ws_bytes != key_weights_workspace(false, N);
+    if ((st = check_workspace(workspace, ws_bytes, key_weights_workspace(expand, N))) != DSA_OK) return st;
     if ((st = check_device()) != DSA_OK) return st;
-    return launch_key_weights_prefill(row_format, q, cache, cache_scale, idx, lse, L, N, top_k, scale, acc, accumulate,
+    return launch_key_weights_prefill(row_format, expand, q, cache, cache_scale, idx, lse, L, N, top_k, scale, acc, accumulate,
                                       workspace, pt, static_cast<cudaStream_t>(stream));
 }
 

@@ -99,12 +99,12 @@ dsa_status_t launch_cache_read_q4_paged(const void* cache, const float* cache_sc
 // Rows 0 .. N - 1 of a sequence of the 4-bit cache as rows of the 8-bit cache, dense.
 dsa_status_t launch_cache_expand_q4(const void* cache, const float* cache_scale, int N, void* out, float* out_scale,
                                     const PageTable& pages, cudaStream_t stream);
-// The attention over the 8-bit cache, or (q4) over the 4-bit one.
-dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, bool q4,
+// The attention over the 8-bit cache, or (q4) over the 4-bit one, whose rows a prefill may hold as 8-bit ones (expand).
+dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, bool q4, bool expand,
                                     const int32_t* idx, int L, int N, int top_k, float scale, void* out, int out_f32,
                                     float* lse, void* workspace, const PageTable& pages, cudaStream_t stream);
 size_t attn_q8_workspace(int rows, int top_k);
-bool attn_q4_expands(int rows, int top_k, int N);       // a prefill that holds its rows as 8-bit ones in the workspace
+bool attn_q4_expands(int rows, int top_k, int N);       // a prefill that holds its rows as 8-bit ones where it may
 size_t attn_q4_workspace(int rows, int top_k, int N);   // N: keys of a prefill's cache; decode 0
 // Merge of nsplit partial (normalised output, lse) pairs a sequence.
 dsa_status_t launch_decode_combine(const float* part_o, const float* part_lse, int B, int nsplit, void* out, int out_f32,
@@ -118,8 +118,9 @@ dsa_status_t launch_indexer_norm_rope(const void* q, int64_t q_stride, const voi
                                       float eps, const float* cos_sin, int max_pos, int interleave,
                                       const int32_t* pos, const int32_t* slots, int R, void* q_out, void* k_cache,
                                       int cache_rows, cudaStream_t stream);
-size_t key_weights_workspace(int format, int L, int N, int top_k);
-dsa_status_t launch_key_weights_prefill(int format, const void* q, const void* cache, const float* cache_scale,
+bool key_weights_expands(int format, int L, int N, int top_k);   // holds 4-bit rows as 8-bit ones where it may
+size_t key_weights_workspace(bool expand, int N);
+dsa_status_t launch_key_weights_prefill(int format, bool expand, const void* q, const void* cache, const float* cache_scale,
                                         const int32_t* idx, const float* lse, int L, int N, int top_k, float scale,
                                         float* acc, int accumulate, void* workspace, const PageTable& pages,
                                         cudaStream_t stream);

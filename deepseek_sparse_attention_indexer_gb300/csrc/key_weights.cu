@@ -832,22 +832,22 @@ WeightParams base_params(const void* q, const void* cache, const float* cache_sc
     return p;
 }
 
+}  // namespace
+
 // A prefill over the 4-bit cache expands its rows to 8-bit ones first where the queries select each key six times or more:
 // a selected key then costs 0.09 ns in place of 0.127, a key of the cache 0.2 ns and the launch 2 us.  Direct / expanded, us: 16
 // queries of 2048 of 2k keys 13.0 / 13.3, 32 17.6 / 16.0; 64 of 8k 26 / 22; 304 of 16k 79 / 58, of 65k (9.5 times each) 81 / 68;
 // 608 of 131k (9.5) 164 / 138; 2432 of 262k 690 / 506.
-bool want_expanded(int format, int L, int N, int top_k) {
+bool key_weights_expands(int format, int L, int N, int top_k) {
     return format == DSA_ROWS_Q4 && (long long)L * top_k >= 6LL * N + 49152;
 }
 
-}  // namespace
-
-size_t key_weights_workspace(int format, int L, int N, int top_k) {
+size_t key_weights_workspace(bool expand, int N) {
     const size_t sums = (size_t)N * 8;
-    return want_expanded(format, L, N, top_k) ? round_up(sums) + round_up((size_t)N * kQ8Row) + (size_t)N * sizeof(float) : sums;
+    return expand ? round_up(sums) + round_up((size_t)N * kQ8Row) + (size_t)N * sizeof(float) : sums;
 }
 
-dsa_status_t launch_key_weights_prefill(int format, const void* q, const void* cache, const float* cache_scale,
+dsa_status_t launch_key_weights_prefill(int format, bool expand, const void* q, const void* cache, const float* cache_scale,
                                         const int32_t* idx, const float* lse, int L, int N, int top_k, float scale,
                                         float* acc, int accumulate, void* workspace, const PageTable& pages,
                                         cudaStream_t stream) {
@@ -861,7 +861,7 @@ dsa_status_t launch_key_weights_prefill(int format, const void* q, const void* c
     split(p, L);
     if (cudaMemsetAsync(workspace, 0, (size_t)N * 8, stream) != cudaSuccess) return DSA_ERR_CUDA;
     dsa_status_t st = DSA_OK;
-    if (want_expanded(format, L, N, top_k)) {
+    if (expand) {
         uint8_t* rows = static_cast<uint8_t*>(workspace) + round_up((size_t)N * 8);
         float* scales = reinterpret_cast<float*>(rows + round_up((size_t)N * kQ8Row));
         if ((st = launch_cache_expand_q4(cache, cache_scale, N, rows, scales, pages, stream)) != DSA_OK) return st;

@@ -1135,13 +1135,13 @@ size_t attn_q4_workspace(int rows, int top_k, int N) {
     return round_up(cut) + round_up((size_t)N * kQ8Row) + (size_t)N * sizeof(float);
 }
 
-dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, bool q4,
+dsa_status_t launch_attn_q8_prefill(const void* q, const void* cache, const float* cache_scale, bool q4, bool expand,
                                     const int32_t* idx, int L, int N, int top_k, float scale, void* out, int out_f32,
                                     float* lse, void* workspace, const PageTable& pages, cudaStream_t stream) {
     AttnQ8Params p = base_params(q, cache, cache_scale, idx, N, top_k, scale, out, out_f32, lse, pages);
     p.prefill = 1;
     if (!q4) return launch_rows<false>(p, L, workspace, stream);
-    if (!attn_q4_expands(L, top_k, N)) return launch_rows<true>(p, L, workspace, stream);
+    if (!expand) return launch_rows<true>(p, L, workspace, stream);
     uint8_t* rows = static_cast<uint8_t*>(workspace) + round_up(attn_q8_workspace(L, top_k));
     float* scales = reinterpret_cast<float*>(rows + round_up((size_t)N * kQ8Row));
     const dsa_status_t st = launch_cache_expand_q4(cache, cache_scale, N, rows, scales, pages, stream);

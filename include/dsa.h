@@ -437,10 +437,12 @@ dsa_status_t mla_cache_read_q4_paged(const void *cache, const float *cache_scale
  * of the call over the 8-bit cache of the same name, and so are the bits of the result where both
  * caches hold the same values.  (Rows of zeros of scale 1 or more, which leave the others all of a
  * probability's range, are those whose codes are zeros; one whose block bytes make them zeros is
- * looked for only by a prefill whose queries select each key several times over.)
+ * looked for only where a prefill holds the rows as 8-bit ones.)
  * Workspace: as there, of mla_sparse_attn_q4_workspace_size(rows, top_k, N) bytes, N the keys of a
  * prefill's cache and 0 for a decode call.  A prefill whose queries select each key several times over
- * holds the N rows in it as 8-bit ones (644 bytes a key); its workspace is 32-byte aligned.
+ * holds the N rows in it as 8-bit ones (644 bytes a key); its workspace is 32-byte aligned.  A workspace
+ * of exactly the size for N = 0 (NULL where that is 0) asks for the rows to be read as they are instead:
+ * slower, with no memory of that kind.
  */
 size_t mla_sparse_attn_q4_workspace_size(int rows, int top_k, int N);
 dsa_status_t mla_sparse_attn_prefill_q4(const void *q, const void *cache, const float *cache_scale,
@@ -504,7 +506,8 @@ dsa_status_t mla_sparse_attn_decode_q4_paged(const void *q, const void *cache, c
  * query has up to four times, whatever lse; any that lse counts as often), in a workspace of
  * mla_key_weights_workspace_size(row_format, L, N, top_k) bytes (32-byte aligned): the sums do not depend
  * on any order, and so the same call gives the same bits.  (A prefill over the 4-bit cache whose queries
- * select each key many times holds the N rows there as 8-bit ones.)  Decode needs none, and has each
+ * select each key many times holds the N rows there as 8-bit ones; a workspace of exactly 8 N bytes, the
+ * size for bf16 rows, asks for them to be read as they are, with the same result.)  Decode needs none, and has each
  * sequence's keys once.
  * Errors (host): DSA_ERR_INVALID_ARG for a null pointer (a cache_scale with bf16 rows too), sizes < 1, a
  * scale that is not positive and finite, accumulate not 0 or 1; DSA_ERR_UNSUPPORTED_SHAPE for top_k and
