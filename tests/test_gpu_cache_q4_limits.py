@@ -3,7 +3,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_cache_q4 import SCALE, as_q8, choose, gen, make_cache, paged, randn  # noqa: E402
+from test_gpu_cache_q4 import SCALE, as_q8, attention64, choose, close, gen, i32, make_cache, paged, randn, values  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,52 @@ def test_key_weights_without_room_for_their_rows(dsa):
     for n in (small - 8, small + 8):
         with pytest.raises(dsa.DsaError):
             dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale, workspace=ws[:n])
+
+
+# ------------------------------------------------------------------------------------------------ many queries a CTA
+
+def short_selections(g, rows, N, K, every):
+    """Selections of none to K keys, -1 behind; every `every`-th at most a tile."""
+    many = torch.randint(0, K + 1, (rows, 1), generator=g, device="cuda")
+    many[::every] = many[::every] % 129
+    return choose(g, [N] * rows, N, K).masked_fill(torch.arange(K, device="cuda") >= many, -1)
+
+
+@pytest.mark.parametrize("direct", [True, False])
+def test_prefill_of_many_queries(dsa, direct):
+    """Five queries a CTA of none to three tiles, over the rows as they are and over expanded ones; both types of the output."""
+    g = gen(24)
+    L, N, K = 740, 900, 300
+    cache, scale = make_cache(g, N, exponents=2)
+    q, idx = randn(g, L, 64, 576).bfloat16(), short_selections(g, L, N, K, 3)
+    size = dsa.attn_q4_workspace_size(L, K, 0 if direct else N)
+    assert dsa.attn_q4_workspace_size(L, K, N) >= dsa.attn_q4_workspace_size(L, K) + 644 * N
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    out, lse = dsa.mla_sparse_attn_prefill_q4(q, cache, scale, idx, SCALE, want_lse=True, workspace=ws)
+    kv = values(cache, scale)
+    close(out, lse, attention64(q, lambda s: kv[idx[s].clamp(min=0).long()], idx >= 0, SCALE))
+    twin = dsa.mla_sparse_attn_prefill_q8(q, as_q8(cache), scale, idx, SCALE, want_lse=True)
+    assert torch.equal(out, twin[0]) and torch.equal(lse, twin[1])
+    for _ in range(20):
+        o16, l16 = dsa.mla_sparse_attn_prefill_q4(q, cache, scale, idx, SCALE, want_lse=True, workspace=ws, out_dtype=torch.bfloat16)
+        assert torch.equal(o16, out.bfloat16()) and torch.equal(l16, lse)   # the float32 result, rounded
+    assert dsa.device_status() == 0
+
+
+def test_decode_of_many_sequences(dsa):
+    """Five sequences a CTA, every length from none on."""
+    g = gen(25)
+    B, N, K = 740, 310, 300
+    cache, scale = make_cache(g, B * N, exponents=1)
+    cache, scale = cache.view(B, N, 416), scale.view(B, N)
+    lens = [(b * 7919) % (N + 1) for b in range(B)]
+    idx, q, kv_len = choose(g, lens, N, K), randn(g, B, 64, 576).bfloat16(), i32(*lens)
+    out, lse = dsa.mla_sparse_attn_decode_q4(q, cache, scale, kv_len, idx, SCALE, want_lse=True)
+    kv = values(cache, scale)
+    close(out, lse, attention64(q, lambda s: torch.stack([kv[b][idx[b].clamp(min=0).long()] for b in range(B)[s]]), idx >= 0, SCALE))
+    twin = dsa.mla_sparse_attn_decode_q8(q, as_q8(cache), scale, kv_len, idx, SCALE, want_lse=True)
+    assert torch.equal(out, twin[0]) and torch.equal(lse, twin[1])
+    for _ in range(20):
+        o16, l16 = dsa.mla_sparse_attn_decode_q4(q, cache, scale, kv_len, idx, SCALE, want_lse=True, out_dtype=torch.bfloat16)
+        assert torch.equal(o16, out.bfloat16()) and torch.equal(l16, lse)
+    assert dsa.device_status() == 0
