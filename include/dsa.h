@@ -415,7 +415,9 @@ dsa_status_t mla_sparse_attn_decode_q8_paged(const void *q, const void *cache, c
  *   M    = |u| / (S_b * 2^k) to the nearest, ties to the even index, saturating;  cache_scale = 2^k
  *
  * (u as a float32 rounded to odd, so that every comparison is as with u itself; below 2^-149 u is 0.)
- * Arguments, bounds and errors are those of mla_cache_write_q8 (rows of 416 bytes).
+ * Arguments, bounds and errors are those of mla_cache_write_q8 (rows of 416 bytes).  The format has no NaN
+ * and no infinity: a token whose latent dims are not finite leaves finite ones in its row, where the 8-bit
+ * row holds NaN, so that its queries do not show it.
  */
 dsa_status_t mla_cache_write_q4(const void *kv_a, int64_t kv_a_stride, const float *norm_w, float eps,
                                 const float *cos_sin, int max_pos, int interleave, const int32_t *pos,

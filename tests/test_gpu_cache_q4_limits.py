@@ -3,7 +3,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_cache_q4 import SCALE, as_q8, attention64, choose, close, gen, i32, make_cache, paged, randn, values  # noqa: E402
+from test_gpu_cache_q4 import SCALE, angles, as_q8, attention64, choose, close, gen, i32, make_cache, paged, randn, values  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -68,6 +68,31 @@ def test_key_weights_without_room_for_their_rows(dsa):
     for n in (small - 8, small + 8):
         with pytest.raises(dsa.DsaError):
             dsa.mla_key_weights_prefill(q, cache, idx, lse, SCALE, cache_scale=scale, workspace=ws[:n])
+
+
+# ------------------------------------------------------------------------------------------------ write
+
+def test_write_of_tokens_that_are_not_finite(dsa):
+    """NaN and infinite latent dims leave finite numbers in their token's row (the 8-bit row holds NaN), and no other row."""
+    g = gen(26)
+    R = 12
+    kv_a, w, cs, at = randn(g, R, 576).bfloat16(), torch.exp(0.3 * randn(g, 512)), angles(R), torch.arange(R, device="cuda").int()
+    bad = kv_a.clone()
+    bad[2, 7], bad[5, 500], bad[8, :512], bad[9, 30:60] = float("nan"), float("inf"), float("nan"), -float("inf")
+    odd = torch.zeros(R, dtype=torch.bool, device="cuda")
+    odd[[2, 5, 8, 9]] = True
+    rows = []
+    for x in (kv_a, bad):
+        cache, scale = torch.full((R, 416), 0xEE, dtype=torch.uint8, device="cuda"), torch.zeros(R, device="cuda")
+        dsa.mla_cache_write_q4(x, w, 1e-6, cs, at, at, cache, scale)
+        rows.append((cache, scale))
+        assert bool(torch.isfinite(dsa.mla_cache_read_q4(cache, scale, at).float()).all()) and bool(torch.isfinite(scale).all())
+    for x, y in zip(*rows):
+        assert torch.equal(x[~odd], y[~odd])
+    eight, scale = torch.zeros(R, 640, dtype=torch.uint8, device="cuda"), torch.zeros(R, device="cuda")
+    dsa.mla_cache_write_q8(bad, w, 1e-6, cs, at, at, eight, scale)
+    assert torch.equal(torch.isnan(dsa.mla_cache_read_q8(eight, scale, at).float()).any(1), odd)
+    assert dsa.device_status() == 0
 
 
 # ------------------------------------------------------------------------------------------------ many queries a CTA
