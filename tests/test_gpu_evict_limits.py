@@ -8,6 +8,7 @@ a dim is 2^-13 of its head's largest or more; below, lo ends at steps of 2^-9, s
 largest of at least 224: 2^-21.8 of it, taken as 2^-21.  A score is off by that times scale * the sum of the key's |latent dims|.
 """
 import math
+import threading
 
 import pytest
 
@@ -320,3 +321,49 @@ def test_tokens_appended_after_a_cut(dsa, fmt, page):
             kv_len, cuts = left, cuts + 1
         assert dsa.device_status() == 0
     assert cuts == 3
+
+
+# ------------------------------------------------------------------------------------------------ calls at once
+
+def test_calls_of_three_threads_at_once(dsa):
+    """Attention over the 4-bit cache, weights, plans and moves by three threads on a stream each give the bits of the same
+    calls one after the other."""
+    work = []
+    for t in range(3):
+        g = gen(40 + t)
+        L, B, N, K, keep = 170 + t, 5, 900 + 70 * t, 300, 400
+        cache, scale = make_cache(g, "q4", B * N)
+        q, idx = randn(g, L, 64, 576).bfloat16(), choose(g, [N] * L, N, K)
+        one, few, kv_len = randn(g, B, 64, 576).bfloat16(), choose(g, [N - 50 * b for b in range(B)], N, K), i32(*[N - 50 * b for b in range(B)])
+        acc, pos = torch.rand(B, N, generator=g, device="cuda"), torch.rand(B, N, generator=g, device="cuda").argsort(1).int()
+
+        def calls(cache=cache, scale=scale, q=q, idx=idx, one=one, few=few, kv_len=kv_len, acc=acc, pos=pos, B=B, N=N, keep=keep):
+            out, lse = dsa.mla_sparse_attn_prefill_q4(q, cache[:N], scale[:N], idx, SCALE, want_lse=True)
+            batch, bscale = cache.view(B, N, -1), scale.view(B, N)
+            out1, lse1 = dsa.mla_sparse_attn_decode_q4(one, batch, bscale, kv_len, few, SCALE, want_lse=True)
+            w = dsa.mla_key_weights_prefill(q, cache[:N], idx, lse, SCALE, cache_scale=scale[:N])
+            w1 = dsa.mla_key_weights_decode(one, batch, kv_len, few, lse1, SCALE, cache_scale=bscale)
+            src, dst, left = dsa.cache_evict_plan(acc, pos, kv_len, keep, recent=20, sink=2)
+            moved = [acc.clone(), pos.clone(), batch.clone(), bscale.clone()]
+            dsa.cache_move_rows(src, dst, dense=moved)
+            return [out, lse, out1, lse1, w, w1, src, dst, left] + moved
+
+        work.append((calls, calls()))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def repeat(calls, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(60):
+                    got = calls()
+                    wrong.extend(i for i, (x, y) in enumerate(zip(got, want)) if not torch.equal(x, y))
+        except Exception as error:                                        # for the thread that asserts
+            wrong.append(error)
+
+    threads = [threading.Thread(target=repeat, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and dsa.device_status() == 0
