@@ -9,8 +9,8 @@
 // are order-preserving 32-bit keys in shared memory, protected ones the largest; a radix select (11 + 11 + 10 bits,
 // the blocks' histograms summed through distributed shared memory) finds the last one that stays, and two scans give each
 // thread, which has a run of keys, the ranks of its equal keys, its gaps and its movers.  No sort, no atomics whose order
-// shows.  It is a chain of latencies: three histograms, four cluster barriers (8 sequences of 4096 keys 12.9 us, 64 of 16k
-// 18.9).
+// shows.  It is a chain of latencies: three histograms, four cluster barriers (8 sequences of 4096 keys 12.8 us, 64 of up to
+// 16k 19.5).
 //
 // Moves: all tensors of the call in one launch of as many warps as the SMs hold.  The rows lie apart in HBM, so it is bytes
 // in flight that count: 32 entries' indices and pages are looked up at once, a lane each, and a lane loads its pieces of two

@@ -804,7 +804,10 @@ dsa_status_t launch_format(int format, const WeightParams& p, cudaStream_t strea
                                    : launch<key_weights_e4m3_kernel<true>, low::kThreads, low::kSmemBytes>(p, stream);
 }
 
-// Parts of a query's tiles: whole queries where they fill the SMs, else so many parts that the items do.
+// Parts of a query's tiles: as many as give each SM one item at most; whole queries where they are more than half as many as the
+// SMs.  A cut costs another load of the query and no merge, so finer ones could even out what this leaves idle: half of the
+// SMs at 77 queries on 152, almost all of a second round at 153 (decode over bf16 / 8-bit / 4-bit rows, us: 77 sequences
+// 45 / 32 / 43, 152 65 / 44 / 51, 153 95 / 65 / 87, 304 123 / 79 / 96).
 void split(WeightParams& p, int rows) {
     const int sms = device_sm_count(), tiles = ceil_div(p.top_k, kTile);
     int parts = rows >= sms || sms < 1 ? 1 : sms / rows;
@@ -835,9 +838,9 @@ WeightParams base_params(const void* q, const void* cache, const float* cache_sc
 }  // namespace
 
 // A prefill over the 4-bit cache expands its rows to 8-bit ones first where the queries select each key six times or more:
-// a selected key then costs 0.09 ns in place of 0.127, a key of the cache 0.2 ns and the launch 2 us.  Direct / expanded, us: 16
-// queries of 2048 of 2k keys 13.0 / 13.3, 32 17.6 / 16.0; 64 of 8k 26 / 22; 304 of 16k 79 / 58, of 65k (9.5 times each) 81 / 68;
-// 608 of 131k (9.5) 164 / 138; 2432 of 262k 690 / 506.
+// a selected key then costs 0.085 ns in place of 0.125, a key of the cache 0.2 ns and the launch 2 us.  Direct / expanded, us: 16
+// queries of 2048 of 2k keys 13.0 / 13.0, 32 17.7 / 15.6; 64 of 8k 26 / 22; 304 of 16k 80 / 59, of 65k (9.5 times each) 82 / 68;
+// 608 of 131k (9.5) 167 / 138, of 262k (4.8) 183 / 168, of 524k (2.4) 196 / 222; 2432 of 262k 698 / 507; 4096 of 2M (4) 1391 / 1396.
 bool key_weights_expands(int format, int L, int N, int top_k) {
     return format == DSA_ROWS_Q4 && (long long)L * top_k >= 6LL * N + 49152;
 }

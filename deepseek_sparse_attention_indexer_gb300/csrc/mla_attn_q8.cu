@@ -38,16 +38,16 @@
 //     bf16 path's merge kernel.  Merging inside a thread-block cluster was slower: reading the other CTAs' parts from
 //     distributed shared memory took 13 thousand cycles, storing them there 20 thousand, and a cluster barrier
 //     with the parts in global memory made a call of 8 sequences 18.2 us, against 14.9 with the merge kernel.
-//   * Measured: 4096 queries of 2048 keys 1.13 ms (0.52 of the bf16 matrix peak for the 1088 products a key and
-//     head), decode of 256 sequences 102 us, of 8 14.3 us, of one 12.9 us.  About 5000 cycles a tile of 128 keys:
+//   * Measured: 4096 queries of 2048 keys 1.12 ms (0.52 of the bf16 matrix peak for the 1088 products a key and
+//     head), decode of 256 sequences 99 us, of 8 14.4 us, of one 12.9 us.  About 5000 cycles a tile of 128 keys:
 //     the loop copy, QK, softmax, PV of a stage is 10 thousand, and two stages fit.  Leaving out the vote and the
 //     softmax's reads of shared memory took 1.18 to 1.11 ms, half of PV or of QK 1.25 to 1.15.
 //   * The same kernel over the 4-bit cache (Q4): every stored value is an e4m3 number, so only the gather differs.  The four
 //     latent warps expand chunks 0 and 1, the four rope warps 2 and 3 ahead of their rope rows, a lane its own row: codes in
 //     registers before their place comes free, a block's eight magnitudes from a table in shared memory, a byte selection
 //     a half word.  A prefill that selects each key several times expands the cache once instead (attn_q4_expands) and
-//     takes the 8-bit kernel's time, 4096 queries 1.13 ms.  Decode of 256 sequences of up to 8192 keys 145 us (104 over 8-bit
-//     rows), of 37 20.8, of one 13.7: the latent warps are never idle (a trace: of 8300 cycles a tile the L2 prefetch of 32
+//     takes the 8-bit kernel's time, 4096 queries 1.13 ms.  Decode of 256 sequences of up to 8192 keys 145 us (99 over 8-bit
+//     rows), of 37 20.6, of one 13.4: the latent warps are never idle (a trace: of 8300 cycles a tile the L2 prefetch of 32
 //     rows takes 2000, lookups 900, expanding 2300, the loads' latency 1500).  The table in shared memory left out would give
 //     17 us, all of the expansion 24.
 #include <cuda.h>
@@ -1123,10 +1123,10 @@ dsa_status_t launch_rows(AttnQ8Params p, int rows, void* workspace, cudaStream_t
 }  // namespace
 
 // A prefill over the 4-bit cache expands the cache's rows to 8-bit ones first, once for all its queries, where they
-// select each key three times or more: a selected key then costs 0.14 ns in place of 0.20, a key of the cache 0.2 ns and
-// the launch 2 us.  Direct / expanded, us: 8 queries of 2048 of 2k keys 15.1 / 15.7; 32 of 4k 26.2 / 24.3; 152 of 16k 65 / 51,
-// of 131k (2.4 times each) 69 / 74; 608 of 131k 279 / 209, of 524k (2.4) 295 / 275; 4096 of 16k 1717 / 1154, of 2M (4)
-// 2016 / 1593.
+// select each key three times or more: a selected key then costs 0.13 ns in place of 0.19, a key of the cache 0.2 ns and
+// the launch 2 us.  Direct / expanded, us: 8 queries of 2048 of 2k keys 15.3 / 15.9; 32 of 4k 26.2 / 24.1; 152 of 16k 64 / 51,
+// of 131k (2.4 times each) 68 / 73; 608 of 131k 267 / 203, of 524k (2.4) 278 / 270; 4096 of 16k 1584 / 1111, of 2M (4)
+// 1891 / 1545.
 bool attn_q4_expands(int rows, int top_k, int N) { return N > 0 && (long long)rows * top_k >= 3LL * N + 24576; }
 
 size_t attn_q8_workspace(int rows, int top_k) {
