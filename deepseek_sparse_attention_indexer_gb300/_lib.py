@@ -838,7 +838,7 @@ def cache_move_rows(src: torch.Tensor, dst: torch.Tensor, dense=(), paged=(), bl
                     page_size: int = 0, stream=None) -> None:
     """Row dst[b, i] of sequence b becomes its row src[b, i] in every tensor given, in place: `dense` ones [B, Nmax, ...],
     `paged` ones pools [num_pages * page_size, ...] with block_table [B, pages].  At most 8 tensors, rows of a multiple
-    of 4 bytes."""
+    of 4 bytes.  A pair out of range, or on a page outside the pool, is moved in none of them."""
     dev = _current_device()
     if src.dim() != 2:
         _bad("src and dst are int32 [B, moves]")
